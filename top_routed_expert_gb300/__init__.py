@@ -6,5 +6,6 @@ include/moe_gb300.h (libmoe_gb300.so); `abi` is its thin ctypes binding and
 """
 from . import abi  # noqa: F401
 from .abi import (MoEError, moe_combine, moe_expert_ffn, moe_get_device_status,  # noqa: F401
-                  moe_layer_forward, moe_permute, moe_route, moe_status_str, moe_workspace_bytes)
+                  moe_kv_append, moe_layer_forward, moe_paged_attention, moe_paged_attention_ws_bytes, moe_permute,
+                  moe_route, moe_route_scores, moe_status_str, moe_workspace_bytes)
 from .build import build  # noqa: F401

@@ -33,10 +33,14 @@ STATUS = {
     8: "MOE_ERR_DEVICE_NONFINITE",
 }
 
-# Every symbol include/moe_gb300.h declares.
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 0, 1
+
+# Every symbol the headers under include/ declare.
 EXPORTS = ("moe_abi_version", "moe_status_str", "moe_workspace_bytes", "moe_route", "moe_permute",
            "moe_permute_noalloc", "moe_expert_ffn", "moe_combine", "moe_layer_forward", "moe_launch_count",
-           "moe_get_device_status", "moe_qk_norm_rope")
+           "moe_get_device_status", "moe_qk_norm_rope", "moe_route_scores", "moe_kv_append",
+           "moe_paged_attention", "moe_paged_attention_ws_bytes")
 
 
 class MoEError(RuntimeError):
@@ -55,6 +59,29 @@ class moe_config_t(ctypes.Structure):
 class moe_qk_rope_config_t(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("n_pos", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class moe_route_scores_config_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "n_experts", "top_k", "n_groups", "top_groups", "group_rank",
+                                              "score", "logit_dtype", "renormalise")]
+    _fields_ += [("scale", ctypes.c_float), ("logit_stride", ctypes.c_int64)]
+
+
+class moe_kv_cache_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table")]
+    _fields_ += [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim", "max_pages")]
+    _fields_ += [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")]
+
+
+class moe_kv_append_config_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "batch", "n_q_heads", "rot_dim", "rope_layout", "n_pos")]
+    _fields_ += [("eps", ctypes.c_float)]
+    _fields_ += [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")]
+
+
+class moe_paged_attention_config_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "batch", "n_q_heads", "max_q_len", "window", "n_sink")]
+    _fields_ += [("sm_scale", ctypes.c_float), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
 
 
 class moe_weights_t(ctypes.Structure):
@@ -90,6 +117,12 @@ def load(path: str = LIB) -> ctypes.CDLL:
         "moe_launch_count": (ctypes.c_uint64, []),
         "moe_get_device_status": (i32, [vp]),
         "moe_qk_norm_rope": (i32, [ctypes.POINTER(moe_qk_rope_config_t), vp, vp, vp, vp, vp, vp, vp]),
+        "moe_route_scores": (i32, [ctypes.POINTER(moe_route_scores_config_t), vp, vp, vp, vp, vp]),
+        "moe_kv_append": (i32, [ctypes.POINTER(moe_kv_append_config_t), ctypes.POINTER(moe_kv_cache_t)] + [vp] * 11),
+        "moe_paged_attention": (i32, [ctypes.POINTER(moe_paged_attention_config_t), ctypes.POINTER(moe_kv_cache_t)]
+                                + [vp] * 6 + [sz, vp]),
+        "moe_paged_attention_ws_bytes": (sz, [ctypes.POINTER(moe_paged_attention_config_t),
+                                              ctypes.POINTER(moe_kv_cache_t)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -186,6 +219,100 @@ def moe_qk_norm_rope(cfg, q, k, gamma_q, gamma_k, cos_sin, positions, stream=Non
     """Fused QK-norm + RoPE, in place on q [T, Hq, D] and k [T, Hkv, D] (bf16)."""
     _check(load().moe_qk_norm_rope(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
                                    _ptr(cos_sin), _ptr(positions), _stream(stream)), "moe_qk_norm_rope")
+
+
+def _need(cond: bool, what: str):
+    if not cond:
+        raise ValueError(what)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(t: torch.Tensor, stream):
+    """Address of the stream, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def make_route_scores_config(T, n_experts, top_k, n_groups=1, top_groups=1, group_rank=1, score=MOE_SCORE_SOFTMAX,
+                             logit_dtype=MOE_F32, renormalise=True, scale=1.0,
+                             logit_stride=None) -> moe_route_scores_config_t:
+    return moe_route_scores_config_t(T, n_experts, top_k, n_groups, top_groups, group_rank, score, logit_dtype,
+                                     int(renormalise), scale, n_experts if logit_stride is None else logit_stride)
+
+
+def moe_route_scores(cfg, logits, bias, topk_ids, topk_w, stream=None):
+    """Experts and weights from given logits (include/route_scores.h)."""
+    _check(load().moe_route_scores(cfg, logits.data_ptr(), _addr(bias), topk_ids.data_ptr(), topk_w.data_ptr(),
+                                   _raw_stream(logits, stream)), "moe_route_scores")
+
+
+def make_kv_cache(k, v, k_scale, v_scale, page_table) -> moe_kv_cache_t:
+    """A paged cache from its tensors: k, v [n_pages, n_kv_heads, page_size, D] of torch.float8_e4m3fn (or uint8
+    codes) in any stride order with contiguous D, the scales [n_pages, n_kv_heads] float32, page_table
+    [batch, max_pages] int32.  The tensors stay alive with the returned object."""
+    _need(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride(), "k and v: one 4-d shape, the same strides")
+    _need(k.element_size() == 1 and v.element_size() == 1 and k.stride(3) == 1, "k and v: 8-bit codes, contiguous heads")
+    n_pages, heads, page, D = k.shape
+    for s in (k_scale, v_scale):
+        _need(s.shape == (n_pages, heads) and s.dtype == torch.float32 and s.is_contiguous(),
+              "scales: contiguous float32 [n_pages, n_kv_heads]")
+    _need(page_table.dim() == 2 and page_table.dtype == torch.int32 and page_table.is_contiguous(),
+          "page_table: contiguous int32 [batch, max_pages]")
+    # a dimension of size 1 may carry any stride: give it one that the library takes
+    strides = [st if n > 1 else D for n, st in zip(k.shape[:3], k.stride()[:3])]
+    c = moe_kv_cache_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
+                       n_pages, page, heads, D, page_table.shape[1], *strides)
+    c.tensors = (k, v, k_scale, v_scale, page_table)
+    return c
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride of [T, heads, D] with contiguous heads."""
+    _need(t.dim() == 3 and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2]),
+          "rows of [T, heads, D] with contiguous heads")
+    _need(t.dtype == torch.bfloat16, "bf16 rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def make_kv_append_config(q, k, v, q_out, batch, rot_dim=0, n_pos=0, rope_layout=MOE_ROPE_HALF,
+                          eps=1e-6) -> moe_kv_append_config_t:
+    """Sizes and strides of an append from its tensors (q and q_out may be None)."""
+    _need(k.shape == v.shape and (q is None or (q.shape[0] == k.shape[0] and q.shape == q_out.shape)),
+          "q, k, v and q_out: the same rows")
+    return moe_kv_append_config_t(k.shape[0], batch, 0 if q is None else q.shape[1], rot_dim, rope_layout, n_pos, eps,
+                                  0 if q is None else _row_stride(q), _row_stride(k), _row_stride(v),
+                                  0 if q is None else _row_stride(q_out))
+
+
+def moe_kv_append(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream=None):
+    """Norm, rotation and append to the paged cache (include/paged_kv.h)."""
+    _check(load().moe_kv_append(cfg, cache, _addr(q), k.data_ptr(), v.data_ptr(), _addr(gamma_q), _addr(gamma_k),
+                                _addr(cos_sin), _addr(positions), cu.data_ptr(), kv_len.data_ptr(), _addr(q_out),
+                                _raw_stream(k, stream)), "moe_kv_append")
+
+
+def make_paged_attention_config(q, out, batch, max_q_len=0, window=0, n_sink=0,
+                                sm_scale=None) -> moe_paged_attention_config_t:
+    """Sizes and strides of an attention call from its tensors; sm_scale defaults to 1/sqrt(D)."""
+    _need(q.shape == out.shape, "q and out: the same shape")
+    return moe_paged_attention_config_t(q.shape[0], batch, q.shape[1], max_q_len, window, n_sink,
+                                        q.shape[2] ** -0.5 if sm_scale is None else sm_scale, _row_stride(q),
+                                        _row_stride(out))
+
+
+def moe_paged_attention_ws_bytes(cfg, cache) -> int:
+    return load().moe_paged_attention_ws_bytes(cfg, cache)
+
+
+def moe_paged_attention(cfg, cache, q, cu, kv_len, out, lse=None, ws=None, stream=None):
+    """Attention of the new tokens over the paged cache (include/paged_kv.h)."""
+    _check(load().moe_paged_attention(cfg, cache, q.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(),
+                                      _addr(lse), _addr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                      _raw_stream(q, stream)), "moe_paged_attention")
 
 
 def moe_launch_count() -> int:

@@ -42,7 +42,8 @@ def _stale(objs) -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(os.path.dirname(PKG), "include", "moe_gb300.h"))
+    include = os.path.join(os.path.dirname(PKG), "include")
+    deps += [os.path.join(include, f) for f in os.listdir(include)]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(p) > t for p in deps)
 
