@@ -28,11 +28,17 @@
 // scales: a key's scale multiplies its score; a value's scale goes into the
 // exponent of its weight, with a running maximum of its own, so that the
 // weights rounded to f16 stay at most 1 whatever the scales are.
+#include <climits>
+
 #include "paged_kv.cuh"
 #include "tc_ptx.cuh"
 #include "paged_attn.cuh"
 
 namespace moe {
+
+bool paged_attn_tc_supported(int D);
+cudaError_t launch_paged_attn_tc(const PaArgs& a, cudaStream_t s);
+
 namespace {
 
 constexpr int kWarps = 4;
@@ -414,24 +420,26 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
 // Joins the partial sums of the row tiles that more than one CTA worked on.
 // One block per (key head, place of a row tile, row); the places of a ragged
 // batch are found as moe_kv_append finds its pages: request b's row tiles
-// start at cu[b] group / 16 + b.
+// start at cu[b] group / 16 + b; where a request has at most rt_max of them
+// (rt_max > 0) they start at b rt_max.
 template <int D>
-__global__ void __launch_bounds__(128) paged_attn_join(PaArgs a, int n_ctas) {
+__global__ void __launch_bounds__(128) paged_attn_join(PaArgs a, int n_ctas, int rt_max) {
   using S = Shape<D>;
   __shared__ int64_t s_red[2][4];
   __shared__ float s_acc[4][D], s_st[4][3];
   pdl_enter();
   const int kvh = blockIdx.y, r = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = warp_find_request(a.cu, a.B, blockIdx.x, a.group, kRows, 1);
+  const int b = rt_max ? blockIdx.x / rt_max : warp_find_request(a.cu, a.B, blockIdx.x, a.group, kRows, 1);
   const Request rq = load_request(a.cu, a.kv_len, b, a.T);
-  const int rt = blockIdx.x - static_cast<int>(static_cast<int64_t>(rq.row0) * a.group / kRows + b);
+  const int rt = rt_max ? blockIdx.x % rt_max
+                        : blockIdx.x - static_cast<int>(static_cast<int64_t>(rq.row0) * a.group / kRows + b);
   const int rts = ceil_div(rq.n * a.group, kRows);
-  if (!rq.ok || rt < 0 || rt >= rts || rt * kRows + r >= rq.n * a.group) return;
+  if (!rq.ok || rq.n * a.group > a.tc_rows || rt < 0 || rt >= rts || rt * kRows + r >= rq.n * a.group) return;
   // units before request b, and in all
   int64_t before = 0, total = 0;
   for (int i = threadIdx.x; i < a.B; i += blockDim.x) {
     const Request x = load_request(a.cu, a.kv_len, i, a.T);
-    const int64_t n = static_cast<int64_t>(a.c.n_kv_heads) * ceil_div(x.n * a.group, kRows) * span_of(a, x, kUnit).units;
+    const int64_t n = units_of(a, x, kRows, kUnit);
     total += n;
     before += i < b ? n : 0;
   }
@@ -506,9 +514,11 @@ cudaError_t launch(const PaArgs& a, int num_sms, cudaStream_t s) {
   count_launches(2);
   err = launch_pdl(paged_attn_kernel<D>, ctas, kWarps * 32, smem, s, a);
   if (err != cudaSuccess) return err;
-  const int64_t places = static_cast<int64_t>(a.T) * a.group / kRows + a.B;
+  const int rt_max = a.tc_rows < INT_MAX ? ceil_div(a.tc_rows, kRows) : 0;
+  const int64_t places = rt_max ? static_cast<int64_t>(rt_max) * a.B : static_cast<int64_t>(a.T) * a.group / kRows + a.B;
   if (places > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_pdl(paged_attn_join<D>, dim3(static_cast<unsigned>(places), a.c.n_kv_heads, kRows), 128, 0, s, a, ctas);
+  return launch_pdl(paged_attn_join<D>, dim3(static_cast<unsigned>(places), a.c.n_kv_heads, kRows), 128, 0, s, a, ctas,
+                    rt_max);
 }
 
 }  // namespace
@@ -518,7 +528,17 @@ size_t paged_attn_ws_bytes(int D) {
   return static_cast<size_t>(ctas_for(D, kMaxSms)) * 2 * part;
 }
 
-cudaError_t launch_paged_attn(const PaArgs& a, int num_sms, cudaStream_t s) {
+// Requests with more rows than this go to the tcgen05 kernel.
+constexpr int kTcRows = 64;
+
+cudaError_t launch_paged_attn(PaArgs a, int max_q_len, int num_sms, cudaStream_t s) {
+  const int64_t most = static_cast<int64_t>(max_q_len > 0 ? std::min(max_q_len, a.T) : a.T) * a.group;
+  a.tc_rows = INT_MAX;
+  if (most > kTcRows && paged_attn_tc_supported(a.c.head_dim)) {
+    a.tc_rows = kTcRows;
+    const cudaError_t err = launch_paged_attn_tc(a, s);
+    if (err != cudaSuccess) return err;
+  }
   switch (a.c.head_dim) {
     case 64: return launch<64>(a, num_sms, s);
     case 128: return launch<128>(a, num_sms, s);
@@ -582,5 +602,5 @@ extern "C" moe_status_t moe_paged_attention(const moe_paged_attention_config_t* 
   a.window = cfg->window;
   a.n_sink = cfg->n_sink;
   a.sm_scale = cfg->sm_scale;
-  return launch_paged_attn(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_paged_attn(a, cfg->max_q_len, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -17,6 +17,7 @@ struct PaArgs {
   unsigned* status;
   int64_t qs, os;
   int T, B, group, window, n_sink;
+  int tc_rows;          // requests with more rows (tokens x heads of the group) go to paged_attn_tc.cu
   float sm_scale;
 };
 
@@ -58,9 +59,15 @@ __device__ __forceinline__ Span span_of(const PaArgs& a, const Request& r, int u
   return span_for(a, r.start, r.end - 1, unit);
 }
 
+// Units of a request: all its key heads and row tiles of `rows` rows.
+__device__ __forceinline__ int64_t units_of(const PaArgs& a, const Request& r, int rows, int unit) {
+  if (r.n * a.group > a.tc_rows) return 0;
+  return static_cast<int64_t>(a.c.n_kv_heads) * ceil_div(r.n * a.group, rows) * span_of(a, r, unit).units;
+}
+
 // Units of the call, request by request: start[b] units come before request
-// b (all its key heads and row tiles of ROWS rows), start[B] in all.  The
-// whole block calls; `status` records offsets that are out of order.
+// b, start[B] in all.  The whole block calls; `status` records offsets that
+// are out of order and lengths past the page table.
 template <int ROWS, int UNIT>
 __device__ __forceinline__ void build_unit_table(const PaArgs& a, int64_t* start, unsigned* status) {
   __shared__ int64_t s_warp[32];
@@ -72,7 +79,7 @@ __device__ __forceinline__ void build_unit_table(const PaArgs& a, int64_t* start
     if (b < a.B) {
       const Request r = load_request(a.cu, a.kv_len, b, a.T);
       if (!r.ok || r.end > a.c.max_pages * a.c.page_size) set_status(status, MOE_ERR_DEVICE_BOUNDS);
-      n = static_cast<int64_t>(a.c.n_kv_heads) * ceil_div(r.n * a.group, ROWS) * span_of(a, r, UNIT).units;
+      n = units_of(a, r, ROWS, UNIT);
     }
     int64_t sum = n;   // inclusive prefix over the warp, then over the warps
     for (int off = 1; off < 32; off <<= 1) {

@@ -1,0 +1,579 @@
+// Attention over the paged 8-bit cache for many query rows (prompts and
+// their chunks) on the 5th-generation tensor cores.
+//
+// The rows of one (request, key head) are its new tokens times the query
+// heads of the group (row r = token r / group, head r % group); a CTA takes
+// 256 of them as two tiles of 128 and walks the cached tokens that any of
+// them sees in steps of 128:
+//   S = Q K^T   (kind::f16, M = 128 rows, N = 128 tokens, both from shared
+//               memory)
+//   P = 2^(S k_scale .. - m), f16, written over S in tensor memory
+//   O += P V    (A = P from tensor memory, B = V^T from shared memory)
+// Warps 0-3 and 4-7 are the softmax of tile 0 and 1 (one thread a row), warps
+// 8-11 convert codes, warp 12 issues the MMAs (13-15 only lend registers): while one tile's softmax runs,
+// the tensor core works on the other's products.
+//
+// The cache's codes become f16 exactly on the way to shared memory (E4M3 fits
+// f16), one conversion for the 256 rows; the values are transposed there by
+// byte permutations before the conversion, so both products read K-major
+// operands.  Page scales stay out of the products: a score is multiplied by
+// its 16-token group's key scale, and the value scale is added to the
+// exponent (its logarithm, relative to the first page's), so that P V needs
+// no scaling and the sum of the weights is the group sums divided by the same
+// scale.
+//
+// The running maximum moves only when it grows by more than 2^8: the old
+// weights are then at most 2^8 times too large for f16's range (65504), the
+// result is the same after the division, and the accumulator is almost never
+// rescaled.
+#include "paged_attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+using namespace ptx;
+
+namespace {
+
+constexpr int kRowTile = 128;
+constexpr int kItemRows = 2 * kRowTile;
+constexpr int kTok = 128;                // tokens of a step
+constexpr int kGroups = kTok / 16;       // scale groups of a step
+constexpr int kThreads = 16 * 32;
+// Registers of a thread, by warpgroup: softmax, conversion, MMA issue.  The
+// launch has 128 for each of the 512 threads; 256 x 184 + 128 x 104 + 128 x 40
+// are the same 65536.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 184, kConvRegs = 104, kIssueRegs = 40;
+static_assert(2 * kSoftmaxRegs + kConvRegs + kIssueRegs <= 4 * kLaunchRegs, "setmaxnreg would wait forever");
+constexpr int kConvThreads = 128;
+constexpr int kScaleSlots = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.0f;            // log2 of the growth that moves the maximum
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 200000000ull;
+
+struct Ctrl {
+  uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], sc_full[kScaleSlots],
+      drain;
+  float4 scale[kScaleSlots][kGroups];    // key scale, log2 of the value scale, 1 / value scale (both relative)
+  float lref;                            // log2 of the reference value scale
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D> struct Tc {
+  static constexpr int kQ = kRowTile * D * 2;    // bytes of a row tile
+  static constexpr int kK = kTok * D * 2;        // of a step's keys, or values
+  static constexpr int kSmem = 2 * kQ + 4 * kK + 1024 + static_cast<int>(sizeof(Ctrl));
+  // tensor memory columns: two score tiles, two outputs
+  static constexpr int kS = 0, kO = 2 * kTok;
+};
+
+// Instruction descriptor of kind::f16 with f16 operands, both K-major, fp32
+// accumulator: D format [4,6) = 1, N >> 3 in [17,23), M >> 4 in [24,29).
+constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A from tensor memory: row i in lane i, two f16 of consecutive K in a column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t f16x2_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 t, u;\n mov.b32 {t, u}, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 t, u;\n mov.b32 {t, u}, %1;\n cvt.rn.f16x2.e4m3x2 %0, u;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16-byte chunk c of row r in a 128-byte-swizzled tile of 128-byte rows.
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// The CTA's work: up to 256 rows of one request and key head.
+struct Item {
+  Request rq;
+  int b, kvh, row0, rows;
+  Span sp;
+  bool any;
+};
+
+__device__ __forceinline__ Item item_of(const PaArgs& a) {
+  Item it;
+  const int place = static_cast<int>(gridDim.x - 1 - blockIdx.x);   // the later, longer rows of a request first
+  it.b = warp_find_request(a.cu, a.B, place, a.group, kItemRows, 1);
+  it.rq = load_request(a.cu, a.kv_len, it.b, a.T);
+  it.kvh = blockIdx.y;
+  const int all = it.rq.n * a.group;
+  const int64_t blk = place - (static_cast<int64_t>(it.rq.row0) * a.group / kItemRows + it.b);
+  it.any = it.rq.ok && blk >= 0 && blk * kItemRows < all && all > a.tc_rows;
+  it.row0 = it.any ? static_cast<int>(blk) * kItemRows : 0;
+  it.rows = min(kItemRows, all - it.row0);
+  it.sp = span_for(a, it.rq.start + it.row0 / a.group, it.rq.start + (it.row0 + max(it.rows, 1) - 1) / a.group, kTok);
+  return it;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
+  using L = Tc<D>;
+  constexpr int KB = D / 64;             // 64-element (128-byte) column blocks of a head
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctrl* c = reinterpret_cast<Ctrl*>(smem + 2 * L::kQ + 4 * L::kK);
+  const uint32_t s_q = smem_u32(smem), s_k = s_q + 2 * L::kQ, s_v = s_k + 2 * L::kK;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &c->abort;
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&c->q_full), 2 * kRowTile);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&c->k_full[i]), kConvThreads);
+      mbar_init(smem_u32(&c->v_full[i]), kConvThreads);
+      mbar_init(smem_u32(&c->k_free[i]), 1);
+      mbar_init(smem_u32(&c->v_free[i]), 1);
+      mbar_init(smem_u32(&c->s_full[i]), 1);
+      mbar_init(smem_u32(&c->p_full[i]), kRowTile);
+      mbar_init(smem_u32(&c->o_full[i]), 1);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&c->sc_full[i]), kGroups);
+    mbar_init(smem_u32(&c->drain), 1);
+    c->abort = 0;
+    c->lref = 0.f;
+    fence_barrier_init();
+  }
+  pdl_enter();
+  const Item it = item_of(a);
+  if (!it.any) return;   // the whole block; nothing is held yet
+  if (warp == 12) {
+    tmem_alloc(smem_u32(&c->tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem_base;
+  const Span sp = it.sp;
+  const int steps = sp.units;
+
+  if (warp < 8) {
+    // ---------------------------------------------------------- softmax
+    regs_up<kSoftmaxRegs>();
+    const int tile = warp >> 2, r = it.row0 + tile * kRowTile + (threadIdx.x & 127);
+    const bool live = r < it.row0 + it.rows;
+    const int tok = live ? r / a.group : 0, head = it.kvh * a.group + (live ? r % a.group : 0);
+    const int pos = live ? it.rq.start + tok : -1;
+    // this warp's live rows: first and last position
+    const int w0 = it.row0 + tile * kRowTile + (warp & 3) * 32;
+    const int w1 = min(w0 + 31, it.row0 + it.rows - 1);
+    const int pos_min = it.rq.start + w0 / a.group, pos_max = it.rq.start + max(w1, 0) / a.group;
+    float rf;
+    {
+      uint4 raw[D / 8];
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(it.rq.row0 + tok) * a.qs +
+                                                        static_cast<int64_t>(head) * D);
+      float amax = 0.f;
+      bool fin = true;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        raw[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+          fin = fin && lo < INFINITY && hi < INFINITY;
+          amax = fmaxf(amax, fmaxf(lo, hi));
+        }
+      }
+      const float f = q_factor(amax, fin);
+      rf = a.sm_scale * kLog2e / f;
+      const int row = threadIdx.x & 127;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          h[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+        sts128(s_q + tile * L::kQ + (i / 8) * (kRowTile * 128) + sw128(row, i % 8), h[0], h[1], h[2], h[3]);
+      }
+      fence_async();
+      mbar_arrive(smem_u32(&c->q_full));
+    }
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + L::kS + tile * kTok, t_o = tmem + lanes + L::kO + tile * D;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < steps; ++j) {
+      const int slot = j % kScaleSlots;
+      ok = mbar_wait(smem_u32(&c->s_full[tile]), j & 1, abort, kWaitNs) &&
+           mbar_wait(smem_u32(&c->sc_full[slot]), (j / kScaleSlots) & 1, abort, kWaitNs);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const int j0 = sp.block_of(j) * kTok;
+      const bool full = sp.all_see(j0, j0 + kTok - 1, pos_min, pos_max);
+      const float4* sc = c->scale[slot];
+      float top = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[2][32];
+        tmem_ld32x2(t_s + h * 64, t_s + h * 64 + 32, v[0], v[1]);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float4 s = sc[h * 4 + g];
+          const float f = s.x * rf;
+          float* x = v[g >> 1] + (g & 1) * 16;
+          if (full) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaf(x[i], f, s.y));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (sp.sees(pos, j0 + h * 64 + g * 16 + i)) top = fmaxf(top, fmaf(x[i], f, s.y));
+          }
+        }
+      }
+      if (j == 0) {
+        m = top;
+      } else {
+        const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
+        if (__any_sync(0xffffffffu, grow)) {
+          // s_full came after the product before: the accumulator is at rest
+          const float f = grow ? ex2(m - top) : 1.f;
+          if (grow) m = top;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            float v[2][16];
+            tmem_ld16x2(t_o + i * 32, t_o + i * 32 + 16, v[0], v[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[h][e] * f);
+              tmem_st16(t_o + i * 32 + h * 16, w);
+            }
+          }
+        }
+      }
+      const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[2][32];
+        tmem_ld32x2(t_s + h * 64, t_s + h * 64 + 32, v[0], v[1]);
+        uint32_t p[2][16];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float4 s = sc[h * 4 + g];
+          const float f = s.x * rf, shift = s.y - ms;
+          float* x = v[g >> 1] + (g & 1) * 16;
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float e = fmaf(x[i], f, shift);
+            if (!full && !sp.sees(pos, j0 + h * 64 + g * 16 + i)) e = -INFINITY;
+            x[i] = ex2(e);
+            sum += x[i];
+          }
+          l = fmaf(sum, s.z, l);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[g >> 1][(g & 1) * 8 + i] = pack_f16(x[2 * i], x[2 * i + 1]);
+        }
+        // over the first 64 score columns: chunk h's columns have been read
+        tmem_st16(t_s + h * 32, p[0]);
+        tmem_st16(t_s + h * 32 + 16, p[1]);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&c->p_full[tile]));
+    }
+    if (ok) ok = mbar_wait(smem_u32(&c->o_full[tile]), 0, abort, kWaitNs);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      const bool empty = l == 0.f;   // nothing visible (a NaN sum is not)
+      const float f = empty ? 0.f : exp2f(c->lref) / l;
+      uint16_t* dst = a.out + static_cast<int64_t>(it.rq.row0 + tok) * a.os + static_cast<int64_t>(head) * D;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        float v[2][16];
+        tmem_ld16x2(t_o + i * 32, t_o + i * 32 + 16, v[0], v[1]);
+        if (live) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float* x = v[q >> 1] + (q & 1) * 8;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * e] * f, x[2 * e + 1] * f);
+              w[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            *reinterpret_cast<uint4*>(dst + i * 32 + q * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (live && a.lse)
+        a.lse[static_cast<int64_t>(it.rq.row0 + tok) * (a.group * a.c.n_kv_heads) + head] =
+            empty ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      tc_fence_before();
+    }
+  } else if (warp < 12) {
+    // ---------------------------------------------------------- conversion
+    regs_down<kConvRegs>();
+    const int t = threadIdx.x - 256, cw = warp - 8;
+    constexpr int CPT = D / 16;                 // 16-byte chunks of a token
+    constexpr int KN = kTok * CPT / kConvThreads;   // key chunks of a thread
+    constexpr int KSTEP = kConvThreads / CPT;   // tokens between them
+    constexpr int VN = D / 32;                  // 32-byte column blocks of the values
+    const int32_t* table = a.c.page_table + static_cast<int64_t>(it.b) * a.c.max_pages;
+    const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + it.kvh * a.c.head_stride;
+    const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v) + it.kvh * a.c.head_stride;
+    const int64_t ts = a.c.token_stride;
+    const int ps = a.c.page_size, ps_log = 31 - __clz(ps);
+    // key token (+ i KSTEP) and chunk: eight neighbouring lanes have four chunks
+    // of two rows, which the swizzle puts in eight banks
+    const int kc = D == 128 ? (t & 3) | ((t >> 1) & 4) : t & 3;
+    const int kr = D == 128 ? ((t >> 2) & 1) | (t >> 4 << 1) : t >> 2;
+    // values: 8 tokens (an octet of the warp's 32) by 4 elements; the lane's
+    // bits are dealt so that eight neighbouring lanes store to eight banks
+    const int oct = (lane >> 1) & 3, vx = (lane & 1) | ((lane >> 3) << 1);
+    const int vt = cw * 32 + oct * 8;
+    // page of the token, -1: not there or not seen by any row
+    auto page_at = [&](int j, int first, int last) -> int {
+      if (!sp.any_seen(first, last)) return -1;
+      const int p = table[j >> ps_log];
+      if (p >= 0 && p < a.c.n_pages) return p;
+      set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      return -1;
+    };
+    int kp[KN], vp = -1, gp = -1;
+    auto load_pages = [&](int j) {
+      if (j >= steps) return;
+      const int j0 = sp.block_of(j) * kTok;
+#pragma unroll
+      for (int i = 0; i < KN; ++i) {
+        const int x = j0 + i * KSTEP + kr;
+        kp[i] = page_at(x, x, x);
+      }
+      vp = page_at(j0 + vt, j0 + vt, j0 + vt + 7);
+      if (t < kGroups) gp = page_at(j0 + t * 16, j0 + t * 16, j0 + t * 16 + 15);
+    };
+    uint4 kw[KN];
+    uint32_t vw[VN][8];
+    float g_ks = 0.f, g_vs = 1.f;
+    auto load_keys = [&](int j) {
+      const int j0 = sp.block_of(j) * kTok;
+#pragma unroll
+      for (int i = 0; i < KN; ++i) {
+        const int x = j0 + i * KSTEP + kr;
+        kw[i] = make_uint4(0, 0, 0, 0);
+        if (kp[i] >= 0)
+          kw[i] = __ldg(reinterpret_cast<const uint4*>(kbase + kp[i] * a.c.page_stride + (x & (ps - 1)) * ts + kc * 16));
+      }
+      if (t < kGroups && gp >= 0) {
+        g_ks = a.c.k_scale[static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh];
+        g_vs = a.c.v_scale[static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh];
+      }
+    };
+    auto load_values = [&](int j) {
+      const int j0 = sp.block_of(j) * kTok + vt;
+      const uint8_t* base = vbase + vp * a.c.page_stride + vx * 4;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool seen = vp >= 0 && sp.seen(j0 + k);
+        const uint8_t* row = base + ((j0 + k) & (ps - 1)) * ts;
+#pragma unroll
+        for (int d = 0; d < VN; ++d) vw[d][k] = seen ? __ldg(reinterpret_cast<const uint32_t*>(row + d * 32)) : 0u;
+      }
+    };
+    float lref = 0.f;
+    load_pages(0);
+    load_keys(0);
+    int gp0 = gp;
+    load_values(0);
+    load_pages(1);
+    for (int j = 0; j < steps; ++j) {
+      const int st = j & 1, ph = (j >> 1) & 1;
+      if (t < 32) {
+        // the groups' scales; a group without a page masks itself
+        const bool have = t < kGroups && gp0 >= 0;
+        const float lvs = have ? log2f(g_vs) : 0.f;
+        if (j == 0) {
+          const unsigned any = __ballot_sync(0xffffffffu, have);
+          lref = __shfl_sync(0xffffffffu, lvs, any ? __ffs(any) - 1 : 0);
+          if (t == 0) c->lref = lref;
+        }
+        if (t < kGroups) {
+          c->scale[j % kScaleSlots][t] = have ? make_float4(g_ks, lvs - lref, exp2f(lref - lvs), 0.f)
+                                              : make_float4(0.f, -INFINITY, 0.f, 0.f);
+          mbar_arrive(smem_u32(&c->sc_full[j % kScaleSlots]));
+        }
+      }
+      if (!mbar_wait(smem_u32(&c->k_free[st]), ph ^ 1, abort, kWaitNs)) break;
+#pragma unroll
+      for (int i = 0; i < KN; ++i) {
+        const int row = i * KSTEP + kr;
+        const uint32_t base = s_k + st * L::kK + (kc >> 2) * (kTok * 128);
+        const uint4 w = kw[i];
+        const int c0 = (kc & 3) * 2;
+        sts128(base + sw128(row, c0), f16x2_lo(w.x), f16x2_hi(w.x), f16x2_lo(w.y), f16x2_hi(w.y));
+        sts128(base + sw128(row, c0 + 1), f16x2_lo(w.z), f16x2_hi(w.z), f16x2_lo(w.w), f16x2_hi(w.w));
+      }
+      fence_async();
+      mbar_arrive(smem_u32(&c->k_full[st]));
+      if (j + 1 < steps) load_keys(j + 1);
+      gp0 = gp;
+      if (!mbar_wait(smem_u32(&c->v_free[st]), ph ^ 1, abort, kWaitNs)) break;
+#pragma unroll
+      for (int d = 0; d < VN; ++d) {
+        uint32_t lo[4], hi[4];   // token pairs of elements 0,1 and 2,3
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          lo[k] = __byte_perm(vw[d][2 * k], vw[d][2 * k + 1], 0x5140);
+          hi[k] = __byte_perm(vw[d][2 * k], vw[d][2 * k + 1], 0x7362);
+        }
+        const int row = d * 32 + vx * 4, ch = (vt & 63) >> 3;
+        const uint32_t base = s_v + st * L::kK + (vt >> 6) * (D * 128);
+        sts128(base + sw128(row, ch), f16x2_lo(lo[0]), f16x2_lo(lo[1]), f16x2_lo(lo[2]), f16x2_lo(lo[3]));
+        sts128(base + sw128(row + 1, ch), f16x2_hi(lo[0]), f16x2_hi(lo[1]), f16x2_hi(lo[2]), f16x2_hi(lo[3]));
+        sts128(base + sw128(row + 2, ch), f16x2_lo(hi[0]), f16x2_lo(hi[1]), f16x2_lo(hi[2]), f16x2_lo(hi[3]));
+        sts128(base + sw128(row + 3, ch), f16x2_hi(hi[0]), f16x2_hi(hi[1]), f16x2_hi(hi[2]), f16x2_hi(hi[3]));
+      }
+      fence_async();
+      mbar_arrive(smem_u32(&c->v_full[st]));
+      if (j + 1 < steps) load_values(j + 1);
+      load_pages(j + 2);
+    }
+  } else {
+    // ---------------------------------------------------------- MMA issue
+    regs_down<kIssueRegs>();
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t is = idesc_f16(kRowTile, kTok), io = idesc_f16(kRowTile, D);
+      auto scores = [&](int tile, int st) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const uint64_t da = desc_sw128(s_q + tile * L::kQ + kb * (kRowTile * 128));
+          const uint64_t db = desc_sw128(s_k + st * L::kK + kb * (kTok * 128));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss(tmem + L::kS + tile * kTok, da + 2 * kk, db + 2 * kk, is, (kb | kk) != 0);
+        }
+        mma_commit(smem_u32(&c->s_full[tile]));
+      };
+      auto output = [&](int tile, int st, bool first) {
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+          const uint64_t db = desc_sw128(s_v + st * L::kK + tb * (D * 128));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(tmem + L::kO + tile * D, tmem + L::kS + tile * kTok + tb * 32 + kk * 8, db + 2 * kk, io,
+                   !first || (tb | kk) != 0);
+        }
+      };
+      bool ok = mbar_wait(smem_u32(&c->q_full), 0, abort, kWaitNs) &&
+                mbar_wait(smem_u32(&c->k_full[0]), 0, abort, kWaitNs);
+      if (ok) {
+        tc_fence_after();
+        scores(0, 0);
+        scores(1, 0);
+        mma_commit(smem_u32(&c->k_free[0]));
+      }
+      for (int j = 0; ok && j < steps; ++j) {
+        const int st = j & 1, ph = (j >> 1) & 1, nst = st ^ 1, nph = ((j + 1) >> 1) & 1;
+        const bool more = j + 1 < steps;
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile) {
+          if (tile == 0) ok = mbar_wait(smem_u32(&c->v_full[st]), ph, abort, kWaitNs);
+          ok = ok && mbar_wait(smem_u32(&c->p_full[tile]), j & 1, abort, kWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          output(tile, st, j == 0);
+          if (!more) {
+            mma_commit(smem_u32(&c->o_full[tile]));
+          } else {
+            if (tile == 0) ok = mbar_wait(smem_u32(&c->k_full[nst]), nph, abort, kWaitNs);
+            if (!ok) break;
+            tc_fence_after();
+            scores(tile, nst);
+          }
+        }
+        if (!ok) break;
+        mma_commit(smem_u32(&c->v_free[st]));
+        if (more) mma_commit(smem_u32(&c->k_free[nst]));
+      }
+      // nothing is in flight when the tensor memory goes back
+      mma_commit(smem_u32(&c->drain));
+      int no_abort = 0;
+      mbar_wait(smem_u32(&c->drain), 0, &no_abort, kDrainNs);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0 && c->abort) set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const PaArgs& a, cudaStream_t s) {
+  const cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(paged_attn_tc_kernel<D>), Tc<D>::kSmem);
+  if (err != cudaSuccess) return err;
+  const int64_t places = static_cast<int64_t>(a.T) * a.group / kItemRows + a.B;
+  if (places > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  count_launches(1);
+  return launch_pdl(paged_attn_tc_kernel<D>, dim3(static_cast<unsigned>(places), a.c.n_kv_heads), kThreads,
+                    Tc<D>::kSmem, s, a);
+}
+
+}  // namespace
+
+bool paged_attn_tc_supported(int D) { return D == 64 || D == 128; }
+
+cudaError_t launch_paged_attn_tc(const PaArgs& a, cudaStream_t s) {
+  return a.c.head_dim == 64 ? launch<64>(a, s) : launch<128>(a, s);
+}
+
+}  // namespace moe
