@@ -26,6 +26,8 @@
 // weights are then at most 2^8 times too large for f16's range (65504), the
 // result is the same after the division, and the accumulator is almost never
 // rescaled.
+#include <climits>
+
 #include "paged_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -41,9 +43,9 @@ constexpr int kTok = 128;                // tokens of a step
 constexpr int kGroups = kTok / 16;       // scale groups of a step
 constexpr int kThreads = 16 * 32;
 // Registers of a thread, by warpgroup: softmax, conversion, MMA issue.  The
-// launch has 128 for each of the 512 threads; 256 x 184 + 128 x 104 + 128 x 40
+// launch has 128 for each of the 512 threads; 256 x 168 + 128 x 104 + 128 x 72
 // are the same 65536.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 184, kConvRegs = 104, kIssueRegs = 40;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kConvRegs = 104, kIssueRegs = 72;
 static_assert(2 * kSoftmaxRegs + kConvRegs + kIssueRegs <= 4 * kLaunchRegs, "setmaxnreg would wait forever");
 constexpr int kConvThreads = 128;
 constexpr int kScaleSlots = 4;
@@ -54,8 +56,9 @@ constexpr uint64_t kDrainNs = 200000000ull;
 
 struct Ctrl {
   uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], sc_full[kScaleSlots],
-      drain;
+      pl_full[kScaleSlots], drain;
   float4 scale[kScaleSlots][kGroups];    // key scale, log2 of the value scale, 1 / value scale (both relative)
+  int64_t place[kScaleSlots][kGroups];   // byte offset of a 16-token group in the cache, -1: none
   float lref;                            // log2 of the reference value scale
   uint32_t tmem_base;
   int abort;
@@ -129,6 +132,24 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // 16-byte chunk c of row r in a 128-byte-swizzled tile of 128-byte rows.
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
@@ -158,7 +179,6 @@ __device__ __forceinline__ Item item_of(const PaArgs& a) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
   using L = Tc<D>;
-  constexpr int KB = D / 64;             // 64-element (128-byte) column blocks of a head
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl* c = reinterpret_cast<Ctrl*>(smem + 2 * L::kQ + 4 * L::kK);
@@ -177,7 +197,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       mbar_init(smem_u32(&c->p_full[i]), kRowTile);
       mbar_init(smem_u32(&c->o_full[i]), 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&c->sc_full[i]), kGroups);
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(smem_u32(&c->sc_full[i]), kGroups);
+      mbar_init(smem_u32(&c->pl_full[i]), kGroups);
+    }
     mbar_init(smem_u32(&c->drain), 1);
     c->abort = 0;
     c->lref = 0.f;
@@ -255,24 +278,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       const int j0 = sp.block_of(j) * kTok;
       const bool full = sp.all_see(j0, j0 + kTok - 1, pos_min, pos_max);
       const float4* sc = c->scale[slot];
-      float top = -INFINITY;
+      if (!full) {
+        // scores that the row does not see become -infinity, in place: the
+        // passes below need no mask
+        const int hi = pos - j0, lo = sp.window ? hi - sp.window : INT_MIN, sink = sp.n_sink - j0;
+#pragma unroll 1
+        for (int q = 0; q < kTok; q += 16) {
+          float v[16];
+          uint32_t w[16];
+          tmem_ld16(t_s + q, v);
 #pragma unroll
+          for (int i = 0; i < 16; ++i)
+            w[i] = (q + i <= hi && (q + i > lo || q + i < sink)) ? __float_as_uint(v[i]) : 0xff800000u;
+          tmem_st16(t_s + q, w);
+        }
+        tmem_st_wait();
+      }
+      float top = -INFINITY;
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         float v[2][32];
         tmem_ld32x2(t_s + h * 64, t_s + h * 64 + 32, v[0], v[1]);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
+          // one positive factor for 16 columns: their largest product has the largest score
+          const float* x = v[g >> 1] + (g & 1) * 16;
+          float u = fmaxf(x[0], x[1]);
+#pragma unroll
+          for (int i = 2; i < 16; i += 2) u = fmaxf(u, fmaxf(x[i], x[i + 1]));
           const float4 s = sc[h * 4 + g];
-          const float f = s.x * rf;
-          float* x = v[g >> 1] + (g & 1) * 16;
-          if (full) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaf(x[i], f, s.y));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (sp.sees(pos, j0 + h * 64 + g * 16 + i)) top = fmaxf(top, fmaf(x[i], f, s.y));
-          }
+          top = fmaxf(top, fmaf(u, s.x * rf, s.y));
         }
       }
       if (j == 0) {
@@ -299,31 +334,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         }
       }
       const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         float v[2][32];
         tmem_ld32x2(t_s + h * 64, t_s + h * 64 + 32, v[0], v[1]);
-        uint32_t p[2][16];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float4 s = sc[h * 4 + g];
-          const float f = s.x * rf, shift = s.y - ms;
-          float* x = v[g >> 1] + (g & 1) * 16;
-          float sum = 0.f;
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float e = fmaf(x[i], f, shift);
-            if (!full && !sp.sees(pos, j0 + h * 64 + g * 16 + i)) e = -INFINITY;
-            x[i] = ex2(e);
-            sum += x[i];
+          for (int g = 0; g < 2; ++g) {
+            const float4 s = sc[h * 4 + q * 2 + g];
+            const float f = s.x * rf, shift = s.y - ms;
+            const float* x = v[q] + g * 16;
+            const uint64_t f2 = pair(f, f), shift2 = pair(shift, shift);
+            uint64_t sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float e0, e1;
+              unpair(fma2(pair(x[2 * i], x[2 * i + 1]), f2, shift2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum = add2(sum, pair(e0, e1));
+              p[g * 8 + i] = pack_f16(e0, e1);
+            }
+            float sum0, sum1;
+            unpair(sum, sum0, sum1);
+            l = fmaf(sum0 + sum1, s.z, l);
           }
-          l = fmaf(sum, s.z, l);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) p[g >> 1][(g & 1) * 8 + i] = pack_f16(x[2 * i], x[2 * i + 1]);
+          // over the first 64 score columns: what it covers has been read
+          tmem_st16(t_s + h * 32 + q * 16, p);
         }
-        // over the first 64 score columns: chunk h's columns have been read
-        tmem_st16(t_s + h * 32, p[0]);
-        tmem_st16(t_s + h * 32 + 16, p[1]);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -363,15 +403,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
     // ---------------------------------------------------------- conversion
     regs_down<kConvRegs>();
     const int t = threadIdx.x - 256, cw = warp - 8;
-    constexpr int CPT = D / 16;                 // 16-byte chunks of a token
+    constexpr int CPT = D / 16;                     // 16-byte chunks of a token
     constexpr int KN = kTok * CPT / kConvThreads;   // key chunks of a thread
-    constexpr int KSTEP = kConvThreads / CPT;   // tokens between them
-    constexpr int VN = D / 32;                  // 32-byte column blocks of the values
-    const int32_t* table = a.c.page_table + static_cast<int64_t>(it.b) * a.c.max_pages;
+    constexpr int KSTEP = kConvThreads / CPT;       // tokens between them
+    constexpr int VN = D / 32;                      // 32-byte column blocks of the values
     const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + it.kvh * a.c.head_stride;
     const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v) + it.kvh * a.c.head_stride;
     const int64_t ts = a.c.token_stride;
-    const int ps = a.c.page_size, ps_log = 31 - __clz(ps);
     // key token (+ i KSTEP) and chunk: eight neighbouring lanes have four chunks
     // of two rows, which the swizzle puts in eight banks
     const int kc = D == 128 ? (t & 3) | ((t >> 1) & 4) : t & 3;
@@ -380,77 +418,97 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
     // bits are dealt so that eight neighbouring lanes store to eight banks
     const int oct = (lane >> 1) & 3, vx = (lane & 1) | ((lane >> 3) << 1);
     const int vt = cw * 32 + oct * 8;
-    // page of the token, -1: not there or not seen by any row
-    auto page_at = [&](int j, int first, int last) -> int {
-      if (!sp.any_seen(first, last)) return -1;
-      const int p = table[j >> ps_log];
-      if (p >= 0 && p < a.c.n_pages) return p;
-      set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-      return -1;
+    const uint8_t* kmine = kbase + (kr & 15) * ts + kc * 16;
+    const uint8_t* vmine = vbase + (vt & 15) * ts + vx * 4;
+
+    // Eight threads look after a step's eight 16-token groups: the page id is
+    // asked for three steps ahead, the group's place in the cache (an offset
+    // for all converting threads, -1: none) and its scales follow from it.
+    constexpr int kNotSeen = INT_MIN;
+    const int32_t* table = a.c.page_table + static_cast<int64_t>(it.b) * a.c.max_pages;
+    const int ps = a.c.page_size, ps_log = 31 - __clz(ps);
+    int gp = kNotSeen;
+    bool have = false;
+    float g_ks = 0.f, g_vs = 1.f, lref = 0.f;
+    auto ask_page = [&](int j) {
+      if (t >= kGroups || j >= steps) return;
+      const int x = sp.block_of(j) * kTok + t * 16;
+      gp = sp.any_seen(x, x + 15) ? __ldg(table + (x >> ps_log)) : kNotSeen;
     };
-    int kp[KN], vp = -1, gp = -1;
-    auto load_pages = [&](int j) {
-      if (j >= steps) return;
-      const int j0 = sp.block_of(j) * kTok;
-#pragma unroll
-      for (int i = 0; i < KN; ++i) {
-        const int x = j0 + i * KSTEP + kr;
-        kp[i] = page_at(x, x, x);
+    auto place = [&](int j) {
+      if (t >= kGroups || j >= steps) return;
+      const int x = sp.block_of(j) * kTok + t * 16;
+      have = static_cast<unsigned>(gp) < static_cast<unsigned>(a.c.n_pages);
+      if (!have && gp != kNotSeen) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      c->place[j % kScaleSlots][t] = have ? gp * a.c.page_stride + (x & (ps - 1)) * ts : -1;
+      mbar_arrive(smem_u32(&c->pl_full[j % kScaleSlots]));
+      if (have) {
+        g_ks = __ldg(a.c.k_scale + static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh);
+        g_vs = __ldg(a.c.v_scale + static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh);
       }
-      vp = page_at(j0 + vt, j0 + vt, j0 + vt + 7);
-      if (t < kGroups) gp = page_at(j0 + t * 16, j0 + t * 16, j0 + t * 16 + 15);
+    };
+    auto publish_scales = [&](int j) {
+      if (t >= kGroups || j >= steps) return;
+      // a group without a page masks itself
+      const float lvs = log2f(g_vs) - lref;
+      c->scale[j % kScaleSlots][t] = have ? make_float4(g_ks, lvs, exp2f(-lvs), 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
+      mbar_arrive(smem_u32(&c->sc_full[j % kScaleSlots]));
     };
     uint4 kw[KN];
     uint32_t vw[VN][8];
-    float g_ks = 0.f, g_vs = 1.f;
+    // every token of the step is seen by some row
+    auto all_there = [&](int j0) { return j0 + kTok <= sp.end && (j0 >= sp.lo || j0 + kTok <= sp.n_sink); };
     auto load_keys = [&](int j) {
       const int j0 = sp.block_of(j) * kTok;
+      const bool all = all_there(j0);
 #pragma unroll
       for (int i = 0; i < KN; ++i) {
-        const int x = j0 + i * KSTEP + kr;
+        const int x = i * KSTEP + kr;
+        const int64_t off = c->place[j % kScaleSlots][x >> 4];
+        const bool ok = off >= 0 && (all || sp.seen(j0 + x));
         kw[i] = make_uint4(0, 0, 0, 0);
-        if (kp[i] >= 0)
-          kw[i] = __ldg(reinterpret_cast<const uint4*>(kbase + kp[i] * a.c.page_stride + (x & (ps - 1)) * ts + kc * 16));
-      }
-      if (t < kGroups && gp >= 0) {
-        g_ks = a.c.k_scale[static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh];
-        g_vs = a.c.v_scale[static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh];
+        if (ok) kw[i] = __ldg(reinterpret_cast<const uint4*>(kmine + off));
       }
     };
     auto load_values = [&](int j) {
-      const int j0 = sp.block_of(j) * kTok + vt;
-      const uint8_t* base = vbase + vp * a.c.page_stride + vx * 4;
+      const int j0 = sp.block_of(j) * kTok;
+      const bool all = all_there(j0);
+      const int64_t off = c->place[j % kScaleSlots][vt >> 4];
+      const uint8_t* row = vmine + off;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const bool seen = vp >= 0 && sp.seen(j0 + k);
-        const uint8_t* row = base + ((j0 + k) & (ps - 1)) * ts;
+        const bool ok = off >= 0 && (all || sp.seen(j0 + vt + k));
 #pragma unroll
-        for (int d = 0; d < VN; ++d) vw[d][k] = seen ? __ldg(reinterpret_cast<const uint32_t*>(row + d * 32)) : 0u;
+        for (int d = 0; d < VN; ++d) {
+          vw[d][k] = 0u;
+          if (ok) vw[d][k] = __ldg(reinterpret_cast<const uint32_t*>(row + d * 32));
+        }
+        row += ts;
       }
     };
-    float lref = 0.f;
-    load_pages(0);
-    load_keys(0);
-    int gp0 = gp;
-    load_values(0);
-    load_pages(1);
-    for (int j = 0; j < steps; ++j) {
+    auto placed = [&](int j) {
+      return mbar_wait(smem_u32(&c->pl_full[j % kScaleSlots]), (j / kScaleSlots) & 1, abort, kWaitNs);
+    };
+    ask_page(0);
+    place(0);
+    if (cw == 0) {
+      const float l0 = log2f(g_vs);
+      const unsigned any = __ballot_sync(0xffffffffu, have);
+      lref = any ? __shfl_sync(0xffffffffu, l0, __ffs(any) - 1) : 0.f;
+      if (t == 0) c->lref = lref;
+    }
+    publish_scales(0);
+    ask_page(1);
+    place(1);
+    ask_page(2);
+    const bool begin = placed(0);
+    if (begin) {
+      load_keys(0);
+      load_values(0);
+    }
+#pragma unroll 1
+    for (int j = 0; begin && j < steps; ++j) {
       const int st = j & 1, ph = (j >> 1) & 1;
-      if (t < 32) {
-        // the groups' scales; a group without a page masks itself
-        const bool have = t < kGroups && gp0 >= 0;
-        const float lvs = have ? log2f(g_vs) : 0.f;
-        if (j == 0) {
-          const unsigned any = __ballot_sync(0xffffffffu, have);
-          lref = __shfl_sync(0xffffffffu, lvs, any ? __ffs(any) - 1 : 0);
-          if (t == 0) c->lref = lref;
-        }
-        if (t < kGroups) {
-          c->scale[j % kScaleSlots][t] = have ? make_float4(g_ks, lvs - lref, exp2f(lref - lvs), 0.f)
-                                              : make_float4(0.f, -INFINITY, 0.f, 0.f);
-          mbar_arrive(smem_u32(&c->sc_full[j % kScaleSlots]));
-        }
-      }
       if (!mbar_wait(smem_u32(&c->k_free[st]), ph ^ 1, abort, kWaitNs)) break;
 #pragma unroll
       for (int i = 0; i < KN; ++i) {
@@ -463,8 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       }
       fence_async();
       mbar_arrive(smem_u32(&c->k_full[st]));
-      if (j + 1 < steps) load_keys(j + 1);
-      gp0 = gp;
+      const bool more = j + 1 < steps;
+      if (more) {
+        if (!placed(j + 1)) break;
+        load_keys(j + 1);
+      }
       if (!mbar_wait(smem_u32(&c->v_free[st]), ph ^ 1, abort, kWaitNs)) break;
 #pragma unroll
       for (int d = 0; d < VN; ++d) {
@@ -483,34 +544,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       }
       fence_async();
       mbar_arrive(smem_u32(&c->v_full[st]));
-      if (j + 1 < steps) load_values(j + 1);
-      load_pages(j + 2);
+      if (more) load_values(j + 1);
+      // The slot of step j+1's scales was last read for step j-3, which both
+      // softmax tiles left before k_free of step j-2 could complete.
+      publish_scales(j + 1);
+      place(j + 2);
+      ask_page(j + 3);
     }
   } else {
     // ---------------------------------------------------------- MMA issue
     regs_down<kIssueRegs>();
     if (warp == 12 && lane == 0) {
       constexpr uint32_t is = idesc_f16(kRowTile, kTok), io = idesc_f16(kRowTile, D);
+      // descriptors of the first tile and stage; the others lie a multiple of
+      // the operand's size (in 16-byte units) behind
+      const uint64_t dq = desc_sw128(s_q), dk = desc_sw128(s_k), dv = desc_sw128(s_v);
       auto scores = [&](int tile, int st) {
+        const uint64_t da = dq + tile * (L::kQ >> 4), db = dk + st * (L::kK >> 4);
+        const uint32_t d = tmem + L::kS + tile * kTok;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const uint64_t da = desc_sw128(s_q + tile * L::kQ + kb * (kRowTile * 128));
-          const uint64_t db = desc_sw128(s_k + st * L::kK + kb * (kTok * 128));
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ss(tmem + L::kS + tile * kTok, da + 2 * kk, db + 2 * kk, is, (kb | kk) != 0);
+        for (int k = 0; k < D / 16; ++k) {
+          const int o = (k >> 2) * (kRowTile * 128 >> 4) + 2 * (k & 3);   // 128-byte column block, 32-byte step
+          mma_ss(d, da + o, db + o, is, k != 0);
         }
         mma_commit(smem_u32(&c->s_full[tile]));
       };
       auto output = [&](int tile, int st, bool first) {
+        const uint64_t db = dv + st * (L::kK >> 4);
+        const uint32_t d = tmem + L::kO + tile * D, p = tmem + L::kS + tile * kTok;
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-          const uint64_t db = desc_sw128(s_v + st * L::kK + tb * (D * 128));
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts(tmem + L::kO + tile * D, tmem + L::kS + tile * kTok + tb * 32 + kk * 8, db + 2 * kk, io,
-                   !first || (tb | kk) != 0);
-        }
+        for (int k = 0; k < kTok / 16; ++k)
+          mma_ts(d, p + k * 8, db + (k >> 2) * (D * 128 >> 4) + 2 * (k & 3), io, !first || k != 0);
       };
       bool ok = mbar_wait(smem_u32(&c->q_full), 0, abort, kWaitNs) &&
                 mbar_wait(smem_u32(&c->k_full[0]), 0, abort, kWaitNs);
@@ -520,10 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         scores(1, 0);
         mma_commit(smem_u32(&c->k_free[0]));
       }
+#pragma unroll 1
       for (int j = 0; ok && j < steps; ++j) {
         const int st = j & 1, ph = (j >> 1) & 1, nst = st ^ 1, nph = ((j + 1) >> 1) & 1;
         const bool more = j + 1 < steps;
-#pragma unroll
+#pragma unroll 1
         for (int tile = 0; tile < 2; ++tile) {
           if (tile == 0) ok = mbar_wait(smem_u32(&c->v_full[st]), ph, abort, kWaitNs);
           ok = ok && mbar_wait(smem_u32(&c->p_full[tile]), j & 1, abort, kWaitNs);
