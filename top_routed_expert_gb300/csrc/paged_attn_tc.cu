@@ -10,8 +10,9 @@
 //   P = 2^(S k_scale .. - m), f16, written over S in tensor memory
 //   O += P V    (A = P from tensor memory, B = V^T from shared memory)
 // Warps 0-3 and 4-7 are the softmax of tile 0 and 1 (one thread a row), warps
-// 8-11 convert codes, warp 12 issues the MMAs (13-15 only lend registers): while one tile's softmax runs,
-// the tensor core works on the other's products.
+// 8-11 convert keys and 12-15 values, warp 16 issues the MMAs, warp 17 looks up
+// pages and scales some steps ahead (18 and 19 only lend registers): while one
+// tile's softmax runs, the tensor core works on the other's products.
 //
 // The cache's codes become f16 exactly on the way to shared memory (E4M3 fits
 // f16), one conversion for the 256 rows; the values are transposed there by
@@ -41,24 +42,26 @@ constexpr int kRowTile = 128;
 constexpr int kItemRows = 2 * kRowTile;
 constexpr int kTok = 128;                // tokens of a step
 constexpr int kGroups = kTok / 16;       // scale groups of a step
-constexpr int kThreads = 16 * 32;
-// Registers of a thread, by warpgroup: softmax, conversion, MMA issue.  The
-// launch has 128 for each of the 512 threads; 256 x 168 + 128 x 104 + 128 x 72
-// are the same 65536.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kConvRegs = 104, kIssueRegs = 72;
-static_assert(2 * kSoftmaxRegs + kConvRegs + kIssueRegs <= 4 * kLaunchRegs, "setmaxnreg would wait forever");
+constexpr int kThreads = 20 * 32;
+// Registers of a thread, by warpgroup: two of softmax, two of conversion, one
+// that plans and issues.  The launch has 96 for each of the 640 threads;
+// 256 x 144 + 256 x 64 + 128 x 64 are the same 61440.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 144, kConvRegs = 64, kIssueRegs = 64;
+static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kIssueRegs <= 5 * kLaunchRegs, "setmaxnreg would wait forever");
 constexpr int kConvThreads = 128;
-constexpr int kScaleSlots = 4;
+constexpr int kSlots = 8;              // steps that are planned ahead, at most
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.0f;            // log2 of the growth that moves the maximum
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 
 struct Ctrl {
-  uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], sc_full[kScaleSlots],
-      pl_full[kScaleSlots], drain;
-  float4 scale[kScaleSlots][kGroups];    // key scale, log2 of the value scale, 1 / value scale (both relative)
-  int64_t place[kScaleSlots][kGroups];   // byte offset of a 16-token group in the cache, -1: none
+  uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], plan_full[kSlots],
+      plan_free[kSlots], drain;
+  // of a step's eight 16-token groups: key scale, log2 of the value scale, 1 /
+  // value scale (both relative to lref); byte offset in the cache, -1: none
+  float4 scale[kSlots][kGroups];
+  int64_t place[kSlots][kGroups];
   float lref;                            // log2 of the reference value scale
   uint32_t tmem_base;
   int abort;
@@ -106,6 +109,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
 }
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -197,9 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       mbar_init(smem_u32(&c->p_full[i]), kRowTile);
       mbar_init(smem_u32(&c->o_full[i]), 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(smem_u32(&c->sc_full[i]), kGroups);
-      mbar_init(smem_u32(&c->pl_full[i]), kGroups);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&c->plan_full[i]), kGroups);
+      mbar_init(smem_u32(&c->plan_free[i]), 1);
     }
     mbar_init(smem_u32(&c->drain), 1);
     c->abort = 0;
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
   pdl_enter();
   const Item it = item_of(a);
   if (!it.any) return;   // the whole block; nothing is held yet
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(smem_u32(&c->tmem_base), 512);
     tmem_relinquish();
   }
@@ -269,9 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < steps; ++j) {
-      const int slot = j % kScaleSlots;
+      const int slot = j % kSlots;
       ok = mbar_wait(smem_u32(&c->s_full[tile]), j & 1, abort, kWaitNs) &&
-           mbar_wait(smem_u32(&c->sc_full[slot]), (j / kScaleSlots) & 1, abort, kWaitNs);
+           mbar_wait(smem_u32(&c->plan_full[slot]), (j / kSlots) & 1, abort, kWaitNs);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -399,217 +408,222 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
             empty ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       tc_fence_before();
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ---------------------------------------------------------- conversion
     regs_down<kConvRegs>();
-    const int t = threadIdx.x - 256, cw = warp - 8;
-    constexpr int CPT = D / 16;                     // 16-byte chunks of a token
-    constexpr int KN = kTok * CPT / kConvThreads;   // key chunks of a thread
-    constexpr int KSTEP = kConvThreads / CPT;       // tokens between them
-    constexpr int VN = D / 32;                      // 32-byte column blocks of the values
-    const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + it.kvh * a.c.head_stride;
-    const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v) + it.kvh * a.c.head_stride;
+    const int t = threadIdx.x & 127;
     const int64_t ts = a.c.token_stride;
-    // key token (+ i KSTEP) and chunk: eight neighbouring lanes have four chunks
-    // of two rows, which the swizzle puts in eight banks
-    const int kc = D == 128 ? (t & 3) | ((t >> 1) & 4) : t & 3;
-    const int kr = D == 128 ? ((t >> 2) & 1) | (t >> 4 << 1) : t >> 2;
-    // values: 8 tokens (an octet of the warp's 32) by 4 elements; the lane's
-    // bits are dealt so that eight neighbouring lanes store to eight banks
-    const int oct = (lane >> 1) & 3, vx = (lane & 1) | ((lane >> 3) << 1);
-    const int vt = cw * 32 + oct * 8;
-    const uint8_t* kmine = kbase + (kr & 15) * ts + kc * 16;
-    const uint8_t* vmine = vbase + (vt & 15) * ts + vx * 4;
-
-    // Eight threads look after a step's eight 16-token groups: the page id is
-    // asked for three steps ahead, the group's place in the cache (an offset
-    // for all converting threads, -1: none) and its scales follow from it.
-    constexpr int kNotSeen = INT_MIN;
-    const int32_t* table = a.c.page_table + static_cast<int64_t>(it.b) * a.c.max_pages;
-    const int ps = a.c.page_size, ps_log = 31 - __clz(ps);
-    int gp = kNotSeen;
-    bool have = false;
-    float g_ks = 0.f, g_vs = 1.f, lref = 0.f;
-    auto ask_page = [&](int j) {
-      if (t >= kGroups || j >= steps) return;
-      const int x = sp.block_of(j) * kTok + t * 16;
-      gp = sp.any_seen(x, x + 15) ? __ldg(table + (x >> ps_log)) : kNotSeen;
+    auto planned = [&](int j) {
+      return mbar_wait(smem_u32(&c->plan_full[j % kSlots]), (j / kSlots) & 1, abort, kWaitNs);
     };
-    auto place = [&](int j) {
-      if (t >= kGroups || j >= steps) return;
-      const int x = sp.block_of(j) * kTok + t * 16;
-      have = static_cast<unsigned>(gp) < static_cast<unsigned>(a.c.n_pages);
-      if (!have && gp != kNotSeen) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-      c->place[j % kScaleSlots][t] = have ? gp * a.c.page_stride + (x & (ps - 1)) * ts : -1;
-      mbar_arrive(smem_u32(&c->pl_full[j % kScaleSlots]));
-      if (have) {
-        g_ks = __ldg(a.c.k_scale + static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh);
-        g_vs = __ldg(a.c.v_scale + static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh);
-      }
-    };
-    auto publish_scales = [&](int j) {
-      if (t >= kGroups || j >= steps) return;
-      // a group without a page masks itself
-      const float lvs = log2f(g_vs) - lref;
-      c->scale[j % kScaleSlots][t] = have ? make_float4(g_ks, lvs, exp2f(-lvs), 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
-      mbar_arrive(smem_u32(&c->sc_full[j % kScaleSlots]));
-    };
-    uint4 kw[KN];
-    uint32_t vw[VN][8];
     // every token of the step is seen by some row
     auto all_there = [&](int j0) { return j0 + kTok <= sp.end && (j0 >= sp.lo || j0 + kTok <= sp.n_sink); };
-    auto load_keys = [&](int j) {
-      const int j0 = sp.block_of(j) * kTok;
-      const bool all = all_there(j0);
+    if (warp < 12) {
+      // keys: token (+ i KSTEP) and 16-byte chunk; eight neighbouring lanes have
+      // four chunks of two rows, which the swizzle puts in eight banks
+      constexpr int CPT = D / 16, KN = kTok * CPT / kConvThreads, KSTEP = kConvThreads / CPT;
+      const int kc = D == 128 ? (t & 3) | ((t >> 1) & 4) : t & 3;
+      const int kr = D == 128 ? ((t >> 2) & 1) | (t >> 4 << 1) : t >> 2;
+      const uint8_t* mine = static_cast<const uint8_t*>(a.c.k) + it.kvh * a.c.head_stride + (kr & 15) * ts + kc * 16;
+      uint4 kw[KN];
+      auto load = [&](int j) {
+        const int j0 = sp.block_of(j) * kTok;
+        const bool all = all_there(j0);
 #pragma unroll
-      for (int i = 0; i < KN; ++i) {
-        const int x = i * KSTEP + kr;
-        const int64_t off = c->place[j % kScaleSlots][x >> 4];
-        const bool ok = off >= 0 && (all || sp.seen(j0 + x));
-        kw[i] = make_uint4(0, 0, 0, 0);
-        if (ok) kw[i] = __ldg(reinterpret_cast<const uint4*>(kmine + off));
+        for (int i = 0; i < KN; ++i) {
+          const int x = i * KSTEP + kr;
+          const int64_t off = c->place[j % kSlots][x >> 4];
+          kw[i] = make_uint4(0, 0, 0, 0);
+          if (off >= 0 && (all || sp.seen(j0 + x))) kw[i] = __ldg(reinterpret_cast<const uint4*>(mine + off));
+        }
+      };
+      bool ok = planned(0);
+      if (ok) load(0);
+#pragma unroll 1
+      for (int j = 0; ok && j < steps; ++j) {
+        const int st = j & 1, ph = (j >> 1) & 1;
+        if (!mbar_wait(smem_u32(&c->k_free[st]), ph ^ 1, abort, kWaitNs)) break;
+        const uint32_t base = s_k + st * L::kK + (kc >> 2) * (kTok * 128);
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
+          const int row = i * KSTEP + kr, c0 = (kc & 3) * 2;
+          const uint4 w = kw[i];
+          sts128(base + sw128(row, c0), f16x2_lo(w.x), f16x2_hi(w.x), f16x2_lo(w.y), f16x2_hi(w.y));
+          sts128(base + sw128(row, c0 + 1), f16x2_lo(w.z), f16x2_hi(w.z), f16x2_lo(w.w), f16x2_hi(w.w));
+        }
+        fence_async();
+        mbar_arrive(smem_u32(&c->k_full[st]));
+        if (j + 1 < steps) {
+          ok = planned(j + 1);
+          if (ok) load(j + 1);
+        }
       }
-    };
-    auto load_values = [&](int j) {
-      const int j0 = sp.block_of(j) * kTok;
-      const bool all = all_there(j0);
-      const int64_t off = c->place[j % kScaleSlots][vt >> 4];
-      const uint8_t* row = vmine + off;
+    } else {
+      // values: 8 tokens (an octet of the warp's 32) by 4 elements; the lane's
+      // bits are dealt so that eight neighbouring lanes store to eight banks
+      constexpr int VN = D / 32;   // 32-byte column blocks
+      const int vx = (lane & 1) | ((lane >> 3) << 1), vt = (warp & 3) * 32 + ((lane >> 1) & 3) * 8;
+      const uint8_t* mine = static_cast<const uint8_t*>(a.c.v) + it.kvh * a.c.head_stride + (vt & 15) * ts + vx * 4;
+      uint32_t vw[VN][8];
+      auto load = [&](int j) {
+        const int j0 = sp.block_of(j) * kTok;
+        const bool all = all_there(j0);
+        const int64_t off = c->place[j % kSlots][vt >> 4];
+        const uint8_t* row = mine + off;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const bool ok = off >= 0 && (all || sp.seen(j0 + vt + k));
+        for (int k = 0; k < 8; ++k) {
+          const bool there = off >= 0 && (all || sp.seen(j0 + vt + k));
+#pragma unroll
+          for (int d = 0; d < VN; ++d) {
+            vw[d][k] = 0u;
+            if (there) vw[d][k] = __ldg(reinterpret_cast<const uint32_t*>(row + d * 32));
+          }
+          row += ts;
+        }
+      };
+      bool ok = planned(0);
+      if (ok) load(0);
+#pragma unroll 1
+      for (int j = 0; ok && j < steps; ++j) {
+        const int st = j & 1, ph = (j >> 1) & 1;
+        if (!mbar_wait(smem_u32(&c->v_free[st]), ph ^ 1, abort, kWaitNs)) break;
+        const uint32_t base = s_v + st * L::kK + (vt >> 6) * (D * 128);
+        const int ch = (vt & 63) >> 3;
 #pragma unroll
         for (int d = 0; d < VN; ++d) {
-          vw[d][k] = 0u;
-          if (ok) vw[d][k] = __ldg(reinterpret_cast<const uint32_t*>(row + d * 32));
+          uint32_t lo[4], hi[4];   // token pairs of elements 0,1 and 2,3
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            lo[k] = __byte_perm(vw[d][2 * k], vw[d][2 * k + 1], 0x5140);
+            hi[k] = __byte_perm(vw[d][2 * k], vw[d][2 * k + 1], 0x7362);
+          }
+          const int row = d * 32 + vx * 4;
+          sts128(base + sw128(row, ch), f16x2_lo(lo[0]), f16x2_lo(lo[1]), f16x2_lo(lo[2]), f16x2_lo(lo[3]));
+          sts128(base + sw128(row + 1, ch), f16x2_hi(lo[0]), f16x2_hi(lo[1]), f16x2_hi(lo[2]), f16x2_hi(lo[3]));
+          sts128(base + sw128(row + 2, ch), f16x2_lo(hi[0]), f16x2_lo(hi[1]), f16x2_lo(hi[2]), f16x2_lo(hi[3]));
+          sts128(base + sw128(row + 3, ch), f16x2_hi(hi[0]), f16x2_hi(hi[1]), f16x2_hi(hi[2]), f16x2_hi(hi[3]));
         }
-        row += ts;
-      }
-    };
-    auto placed = [&](int j) {
-      return mbar_wait(smem_u32(&c->pl_full[j % kScaleSlots]), (j / kScaleSlots) & 1, abort, kWaitNs);
-    };
-    ask_page(0);
-    place(0);
-    if (cw == 0) {
-      const float l0 = log2f(g_vs);
-      const unsigned any = __ballot_sync(0xffffffffu, have);
-      lref = any ? __shfl_sync(0xffffffffu, l0, __ffs(any) - 1) : 0.f;
-      if (t == 0) c->lref = lref;
-    }
-    publish_scales(0);
-    ask_page(1);
-    place(1);
-    ask_page(2);
-    const bool begin = placed(0);
-    if (begin) {
-      load_keys(0);
-      load_values(0);
-    }
-#pragma unroll 1
-    for (int j = 0; begin && j < steps; ++j) {
-      const int st = j & 1, ph = (j >> 1) & 1;
-      if (!mbar_wait(smem_u32(&c->k_free[st]), ph ^ 1, abort, kWaitNs)) break;
-#pragma unroll
-      for (int i = 0; i < KN; ++i) {
-        const int row = i * KSTEP + kr;
-        const uint32_t base = s_k + st * L::kK + (kc >> 2) * (kTok * 128);
-        const uint4 w = kw[i];
-        const int c0 = (kc & 3) * 2;
-        sts128(base + sw128(row, c0), f16x2_lo(w.x), f16x2_hi(w.x), f16x2_lo(w.y), f16x2_hi(w.y));
-        sts128(base + sw128(row, c0 + 1), f16x2_lo(w.z), f16x2_hi(w.z), f16x2_lo(w.w), f16x2_hi(w.w));
-      }
-      fence_async();
-      mbar_arrive(smem_u32(&c->k_full[st]));
-      const bool more = j + 1 < steps;
-      if (more) {
-        if (!placed(j + 1)) break;
-        load_keys(j + 1);
-      }
-      if (!mbar_wait(smem_u32(&c->v_free[st]), ph ^ 1, abort, kWaitNs)) break;
-#pragma unroll
-      for (int d = 0; d < VN; ++d) {
-        uint32_t lo[4], hi[4];   // token pairs of elements 0,1 and 2,3
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          lo[k] = __byte_perm(vw[d][2 * k], vw[d][2 * k + 1], 0x5140);
-          hi[k] = __byte_perm(vw[d][2 * k], vw[d][2 * k + 1], 0x7362);
+        fence_async();
+        mbar_arrive(smem_u32(&c->v_full[st]));
+        if (j + 1 < steps) {
+          ok = planned(j + 1);
+          if (ok) load(j + 1);
         }
-        const int row = d * 32 + vx * 4, ch = (vt & 63) >> 3;
-        const uint32_t base = s_v + st * L::kK + (vt >> 6) * (D * 128);
-        sts128(base + sw128(row, ch), f16x2_lo(lo[0]), f16x2_lo(lo[1]), f16x2_lo(lo[2]), f16x2_lo(lo[3]));
-        sts128(base + sw128(row + 1, ch), f16x2_hi(lo[0]), f16x2_hi(lo[1]), f16x2_hi(lo[2]), f16x2_hi(lo[3]));
-        sts128(base + sw128(row + 2, ch), f16x2_lo(hi[0]), f16x2_lo(hi[1]), f16x2_lo(hi[2]), f16x2_lo(hi[3]));
-        sts128(base + sw128(row + 3, ch), f16x2_hi(hi[0]), f16x2_hi(hi[1]), f16x2_hi(hi[2]), f16x2_hi(hi[3]));
       }
-      fence_async();
-      mbar_arrive(smem_u32(&c->v_full[st]));
-      if (more) load_values(j + 1);
-      // The slot of step j+1's scales was last read for step j-3, which both
-      // softmax tiles left before k_free of step j-2 could complete.
-      publish_scales(j + 1);
-      place(j + 2);
-      ask_page(j + 3);
     }
   } else {
-    // ---------------------------------------------------------- MMA issue
     regs_down<kIssueRegs>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 17) {
+      // -------------------------------------------------------- planning
+      // Four steps at a time, a lane for each 16-token group: page id, place in
+      // the cache, scales.
+      constexpr int kNotSeen = INT_MIN;
+      const int32_t* table = a.c.page_table + static_cast<int64_t>(it.b) * a.c.max_pages;
+      const int ps = a.c.page_size, ps_log = 31 - __clz(ps), grp = lane & 7;
+      float lref = 0.f;
+      bool ok = true;
+#pragma unroll 1
+      for (int j0 = 0; ok && j0 < steps; j0 += 4) {
+        const int j = j0 + (lane >> 3), slot = j % kSlots;
+        const bool mine = j < steps;
+        const int x = mine ? sp.block_of(j) * kTok + grp * 16 : 0;
+        const int gp = mine && sp.any_seen(x, x + 15) ? __ldg(table + (x >> ps_log)) : kNotSeen;
+        const bool have = static_cast<unsigned>(gp) < static_cast<unsigned>(a.c.n_pages);
+        if (!have && gp != kNotSeen) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+        float ks = 0.f, lvs = 0.f;
+        if (have) {
+          const int64_t s = static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh;
+          ks = __ldg(a.c.k_scale + s);
+          lvs = log2f(__ldg(a.c.v_scale + s));
+        }
+        if (j0 == 0) {
+          const unsigned any = __ballot_sync(0xffffffffu, have);
+          lref = __shfl_sync(0xffffffffu, lvs, any ? __ffs(any) - 1 : 0);
+          if (lane == 0) c->lref = lref;
+        }
+        if (mine && j >= kSlots)
+          ok = mbar_wait(smem_u32(&c->plan_free[slot]), ((j / kSlots) - 1) & 1, abort, kWaitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (mine && ok) {
+          // a group without a page masks itself
+          c->place[slot][grp] = have ? gp * a.c.page_stride + (x & (ps - 1)) * a.c.token_stride : -1;
+          c->scale[slot][grp] =
+              have ? make_float4(ks, lvs - lref, exp2f(lref - lvs), 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
+          mbar_arrive(smem_u32(&c->plan_full[slot]));
+        }
+      }
+    }
+    // ---------------------------------------------------------- MMA issue
+    // The whole warp walks the loop, so that descriptors stay in uniform
+    // registers (per-thread ones cost an MMA's time to move); one lane issues.
+    if (warp == 16) {
       constexpr uint32_t is = idesc_f16(kRowTile, kTok), io = idesc_f16(kRowTile, D);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       // descriptors of the first tile and stage; the others lie a multiple of
       // the operand's size (in 16-byte units) behind
       const uint64_t dq = desc_sw128(s_q), dk = desc_sw128(s_k), dv = desc_sw128(s_v);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort, kWaitNs)) != 0;
+      };
       auto scores = [&](int tile, int st) {
         const uint64_t da = dq + tile * (L::kQ >> 4), db = dk + st * (L::kK >> 4);
-        const uint32_t d = tmem + L::kS + tile * kTok;
+        const uint32_t d = tm + L::kS + tile * kTok;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const int o = (k >> 2) * (kRowTile * 128 >> 4) + 2 * (k & 3);   // 128-byte column block, 32-byte step
-          mma_ss(d, da + o, db + o, is, k != 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const int o = (k >> 2) * (kRowTile * 128 >> 4) + 2 * (k & 3);   // 128-byte column block, 32-byte step
+            mma_ss(d, da + o, db + o, is, k != 0);
+          }
+          mma_commit(smem_u32(&c->s_full[tile]));
         }
-        mma_commit(smem_u32(&c->s_full[tile]));
+        __syncwarp();
       };
       auto output = [&](int tile, int st, bool first) {
         const uint64_t db = dv + st * (L::kK >> 4);
-        const uint32_t d = tmem + L::kO + tile * D, p = tmem + L::kS + tile * kTok;
+        const uint32_t d = tm + L::kO + tile * D, p = tm + L::kS + tile * kTok;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTok / 16; ++k)
-          mma_ts(d, p + k * 8, db + (k >> 2) * (D * 128 >> 4) + 2 * (k & 3), io, !first || k != 0);
+          for (int k = 0; k < kTok / 16; ++k)
+            mma_ts(d, p + k * 8, db + (k >> 2) * (D * 128 >> 4) + 2 * (k & 3), io, !first || k != 0);
+        }
+        __syncwarp();
       };
-      bool ok = mbar_wait(smem_u32(&c->q_full), 0, abort, kWaitNs) &&
-                mbar_wait(smem_u32(&c->k_full[0]), 0, abort, kWaitNs);
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) mma_commit(smem_u32(bar));
+        __syncwarp();
+      };
+      bool ok = wait(&c->q_full, 0) && wait(&c->k_full[0], 0);
       if (ok) {
         tc_fence_after();
         scores(0, 0);
         scores(1, 0);
-        mma_commit(smem_u32(&c->k_free[0]));
+        commit(&c->k_free[0]);
       }
 #pragma unroll 1
       for (int j = 0; ok && j < steps; ++j) {
         const int st = j & 1, ph = (j >> 1) & 1, nst = st ^ 1, nph = ((j + 1) >> 1) & 1;
         const bool more = j + 1 < steps;
+        if (!(ok = wait(&c->v_full[st], ph))) break;
 #pragma unroll 1
         for (int tile = 0; tile < 2; ++tile) {
-          if (tile == 0) ok = mbar_wait(smem_u32(&c->v_full[st]), ph, abort, kWaitNs);
-          ok = ok && mbar_wait(smem_u32(&c->p_full[tile]), j & 1, abort, kWaitNs);
-          if (!ok) break;
+          if (!(ok = wait(&c->p_full[tile], j & 1))) break;
           tc_fence_after();
           output(tile, st, j == 0);
           if (!more) {
-            mma_commit(smem_u32(&c->o_full[tile]));
+            commit(&c->o_full[tile]);
           } else {
-            if (tile == 0) ok = mbar_wait(smem_u32(&c->k_full[nst]), nph, abort, kWaitNs);
-            if (!ok) break;
+            if (tile == 0 && !(ok = wait(&c->k_full[nst], nph))) break;
             tc_fence_after();
             scores(tile, nst);
           }
         }
         if (!ok) break;
-        mma_commit(smem_u32(&c->v_free[st]));
-        if (more) mma_commit(smem_u32(&c->k_free[nst]));
+        commit(&c->v_free[st]);
+        commit(&c->plan_free[j % kSlots]);   // both softmax tiles and the converters are past step j
+        if (more) commit(&c->k_free[nst]);
       }
       // nothing is in flight when the tensor memory goes back
-      mma_commit(smem_u32(&c->drain));
+      commit(&c->drain);
       int no_abort = 0;
       mbar_wait(smem_u32(&c->drain), 0, &no_abort, kDrainNs);
     }
@@ -619,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0 && c->abort) set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 template <int D>
