@@ -23,10 +23,10 @@
 // no scaling and the sum of the weights is the group sums divided by the same
 // scale.
 //
-// The running maximum moves only when it grows by more than 2^8: the old
-// weights are then at most 2^8 times too large for f16's range (65504), the
-// result is the same after the division, and the accumulator is almost never
-// rescaled.
+// The running maximum moves only when it grows by more than 2^14: weights
+// relative to an older maximum stay within f16's range (65504) until then, the
+// quotient is the same, the scores are read once, and the accumulator is almost
+// never rescaled.
 #include <climits>
 
 #include "paged_attn.cuh"
@@ -51,7 +51,7 @@ static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kIssueRegs <= 5 * kLaunchRegs, 
 constexpr int kConvThreads = 128;
 constexpr int kSlots = 8;              // steps that are planned ahead, at most
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kGrow = 8.0f;            // log2 of the growth that moves the maximum
+constexpr float kGrow = 14.0f;           // log2 of the growth that moves the maximum
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -98,12 +98,53 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, 
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+// 16 consecutive fp32 columns of this thread's lane.  The values may be used
+// after the wait; it names them, so that no use moves before it.
+__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, float (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_wait(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+// 32 consecutive fp32 columns of this thread's lane.  The values may be used
+// after the wait; it names them, so that no use moves before it.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20,"
+      " %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
+      "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
+      "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
       : "memory");
 }
 
@@ -157,6 +198,32 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// Weights 2^(score - m) of a 16-token group as f16 (s: its scales), the
+// largest score into `top`; returns `l` plus the weights' sum.
+__device__ __forceinline__ float weigh(const float (&x)[16], const float4& s, float rf, float m, float* p, float& top,
+                                       float l) {
+  const float f = s.x * rf, shift = s.y - m;
+  // one positive factor for the group: its largest product has the largest score
+  float u = fmaxf(x[0], x[1]);
+#pragma unroll
+  for (int i = 2; i < 16; i += 2) u = fmaxf(u, fmaxf(x[i], x[i + 1]));
+  top = fmaxf(top, fmaf(u, f, s.y));
+  const uint64_t f2 = pair(f, f), shift2 = pair(shift, shift);
+  uint64_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float e0, e1;
+    unpair(fma2(pair(x[2 * i], x[2 * i + 1]), f2, shift2), e0, e1);
+    e0 = ex2(e0);
+    e1 = ex2(e1);
+    sum = add2(sum, pair(e0, e1));
+    p[i] = __uint_as_float(pack_f16(e0, e1));
+  }
+  float sum0, sum1;
+  unpair(sum, sum0, sum1);
+  return fmaf(sum0 + sum1, s.z, l);
 }
 
 // 16-byte chunk c of row r in a 128-byte-swizzled tile of 128-byte rows.
@@ -288,92 +355,67 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       const bool full = sp.all_see(j0, j0 + kTok - 1, pos_min, pos_max);
       const float4* sc = c->scale[slot];
       if (!full) {
-        // scores that the row does not see become -infinity, in place: the
-        // passes below need no mask
+        // scores that the row does not see become -infinity, in place: what
+        // follows needs no mask
         const int hi = pos - j0, lo = sp.window ? hi - sp.window : INT_MIN, sink = sp.n_sink - j0;
 #pragma unroll 1
-        for (int q = 0; q < kTok; q += 16) {
-          float v[16];
-          uint32_t w[16];
-          tmem_ld16(t_s + q, v);
+        for (int q = 0; q < kTok; q += 32) {
+          if (sp.all_see(j0 + q, j0 + q + 31, pos_min, pos_max)) continue;   // the same for the whole warp
+          float v[32];
+          tmem_ld32_issue(t_s + q, v);
+          tmem_ld32_wait(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            w[i] = (q + i <= hi && (q + i > lo || q + i < sink)) ? __float_as_uint(v[i]) : 0xff800000u;
-          tmem_st16(t_s + q, w);
+          for (int i = 0; i < 32; ++i)
+            if (q + i > hi || (q + i <= lo && q + i >= sink)) v[i] = -INFINITY;
+          tmem_st32(t_s + q, v);
         }
         tmem_st_wait();
       }
-      float top = -INFINITY;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float v[2][32];
-        tmem_ld32x2(t_s + h * 64, t_s + h * 64 + 32, v[0], v[1]);
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          // one positive factor for 16 columns: their largest product has the largest score
-          const float* x = v[g >> 1] + (g & 1) * 16;
-          float u = fmaxf(x[0], x[1]);
-#pragma unroll
-          for (int i = 2; i < 16; i += 2) u = fmaxf(u, fmaxf(x[i], x[i + 1]));
-          const float4 s = sc[h * 4 + g];
-          top = fmaxf(top, fmaf(u, s.x * rf, s.y));
-        }
-      }
-      if (j == 0) {
-        m = top;
-      } else {
-        const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
-        if (__any_sync(0xffffffffu, grow)) {
-          // s_full came after the product before: the accumulator is at rest
-          const float f = grow ? ex2(m - top) : 1.f;
-          if (grow) m = top;
-          l *= f;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            float v[2][16];
-            tmem_ld16x2(t_o + i * 32, t_o + i * 32 + 16, v[0], v[1]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[h][e] * f);
-              tmem_st16(t_o + i * 32 + h * 16, w);
-            }
-          }
-        }
-      }
+      // Weights with the maximum so far, the scores read once.  The row's new
+      // maximum comes out beside them; it hardly ever asks for a second look.
+      float top = -INFINITY, lnew = l;
+      float p[2][32];   // f16 pairs: the first and the last 64 tokens
       const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float v[2][32];
-        tmem_ld32x2(t_s + h * 64, t_s + h * 64 + 32, v[0], v[1]);
+      {
+        float v[2][16];
+        tmem_ld16_issue(t_s, v[0]);
+        tmem_ld16_wait(v[0]);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t p[16];
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float4 s = sc[h * 4 + q * 2 + g];
-            const float f = s.x * rf, shift = s.y - ms;
-            const float* x = v[q] + g * 16;
-            const uint64_t f2 = pair(f, f), shift2 = pair(shift, shift);
-            uint64_t sum = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float e0, e1;
-              unpair(fma2(pair(x[2 * i], x[2 * i + 1]), f2, shift2), e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum = add2(sum, pair(e0, e1));
-              p[g * 8 + i] = pack_f16(e0, e1);
-            }
-            float sum0, sum1;
-            unpair(sum, sum0, sum1);
-            l = fmaf(sum0 + sum1, s.z, l);
-          }
-          // over the first 64 score columns: what it covers has been read
-          tmem_st16(t_s + h * 32 + q * 16, p);
+        for (int g = 0; g < kGroups; ++g) {
+          if (g + 1 < kGroups) tmem_ld16_issue(t_s + (g + 1) * 16, v[(g + 1) & 1]);
+          lnew = weigh(v[g & 1], sc[g], rf, ms, p[g >> 2] + (g & 3) * 8, top, lnew);
+          if (g + 1 < kGroups) tmem_ld16_wait(v[(g + 1) & 1]);
         }
       }
+      const bool grow = m == -INFINITY ? top > m : top > m + kGrow;
+      if (__any_sync(0xffffffffu, grow)) {
+        // s_full came after the product before: the accumulator is at rest
+        const float f = grow ? ex2(m - top) : 1.f;
+        if (grow) m = top;
+        if (j > 0) {
+#pragma unroll 1
+          for (int i = 0; i < D; i += 32) {
+            float v[32];
+            tmem_ld32_issue(t_o + i, v);
+            tmem_ld32_wait(v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= f;
+            tmem_st32(t_o + i, v);
+          }
+        }
+        lnew = l * f;
+        const float mg = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          float v[16];
+          tmem_ld16_issue(t_s + g * 16, v);
+          tmem_ld16_wait(v);
+          lnew = weigh(v, sc[g], rf, mg, p[g >> 2] + (g & 3) * 8, top, lnew);
+        }
+      }
+      l = lnew;
+      tmem_st32(t_s, p[0]);
+      tmem_st32(t_s + 32, p[1]);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(smem_u32(&c->p_full[tile]));
