@@ -418,7 +418,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
 }
 
 // Joins the partial sums of the row tiles that more than one CTA worked on.
-// One block per (key head, place of a row tile, row); the places of a ragged
+// One block per key head, place of a row tile and row (all rows beside the
+// tcgen05 kernel, where few requests or none are left for it); the places of a ragged
 // batch are found as moe_kv_append finds its pages: request b's row tiles
 // start at cu[b] group / 16 + b; where a request has at most rt_max of them
 // (rt_max > 0) they start at b rt_max.
@@ -428,13 +429,14 @@ __global__ void __launch_bounds__(128) paged_attn_join(PaArgs a, int n_ctas, int
   __shared__ int64_t s_red[2][4];
   __shared__ float s_acc[4][D], s_st[4][3];
   pdl_enter();
-  const int kvh = blockIdx.y, r = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int kvh = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = rt_max ? blockIdx.x / rt_max : warp_find_request(a.cu, a.B, blockIdx.x, a.group, kRows, 1);
   const Request rq = load_request(a.cu, a.kv_len, b, a.T);
   const int rt = rt_max ? blockIdx.x % rt_max
                         : blockIdx.x - static_cast<int>(static_cast<int64_t>(rq.row0) * a.group / kRows + b);
   const int rts = ceil_div(rq.n * a.group, kRows);
-  if (!rq.ok || rq.n * a.group > a.tc_rows || rt < 0 || rt >= rts || rt * kRows + r >= rq.n * a.group) return;
+  if (!rq.ok || rq.n * a.group > a.tc_rows || rt < 0 || rt >= rts) return;
+  const int rows = min(kRows, rq.n * a.group - rt * kRows);
   // units before request b, and in all
   int64_t before = 0, total = 0;
   for (int i = threadIdx.x; i < a.B; i += blockDim.x) {
@@ -459,43 +461,46 @@ __global__ void __launch_bounds__(128) paged_attn_join(PaArgs a, int n_ctas, int
   const int64_t start = before + (static_cast<int64_t>(kvh) * rts + rt) * units, end = start + units;
   const int c0 = static_cast<int>(start / piece), c1 = static_cast<int>((end - 1) / piece);
   if (c0 == c1) return;   // one CTA did all of it
-  float m = -INFINITY, m2 = -INFINITY;
   auto part_of = [&](int c) {
     const int slot = (c == c0 && start != c0 * piece) ? 1 : 0;
     return a.part + (static_cast<int64_t>(c) * 2 + slot) * S::kPart;
   };
-  for (int c = c0; c <= c1; ++c) {
-    const float* p = part_of(c) + kRows * D + r;
-    m = fmaxf(m, p[0]);
-    m2 = fmaxf(m2, p[kRows]);
-  }
-  float sum = 0.f;
-  constexpr int PER = D / 32;   // columns of a lane
-  float acc[PER] = {};
-  for (int c = c0 + warp; c <= c1; c += 4) {
-    const float* p = part_of(c);
-    sum += p[kRows * D + 2 * kRows + r] * ex2_from(p[kRows * D + r], m);
-    const float f = ex2_from(p[kRows * D + kRows + r], m2);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] += p[r * D + lane + 32 * i] * f;
-  }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) s_acc[warp][lane + 32 * i] = acc[i];
-  if (lane == 0) s_st[warp][0] = sum;
-  __syncthreads();
-  sum = s_st[0][0] + s_st[1][0] + s_st[2][0] + s_st[3][0];
-  const int row = rt * kRows + r, tok = row / a.group, head = kvh * a.group + row % a.group;
-  const int d = threadIdx.x * 4;
-  if (d < D) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      x.x += s_acc[w][d];
-      x.y += s_acc[w][d + 1];
-      x.z += s_acc[w][d + 2];
-      x.w += s_acc[w][d + 3];
+  for (int r = blockIdx.z; r < rows; r += gridDim.z) {
+    float m = -INFINITY, m2 = -INFINITY;
+    for (int c = c0; c <= c1; ++c) {
+      const float* p = part_of(c) + kRows * D + r;
+      m = fmaxf(m, p[0]);
+      m2 = fmaxf(m2, p[kRows]);
     }
-    store_row4(a, rq.row0 + tok, head, D, d, x, m, m2, sum);
+    float sum = 0.f;
+    constexpr int PER = D / 32;   // columns of a lane
+    float acc[PER] = {};
+    for (int c = c0 + warp; c <= c1; c += 4) {
+      const float* p = part_of(c);
+      sum += p[kRows * D + 2 * kRows + r] * ex2_from(p[kRows * D + r], m);
+      const float f = ex2_from(p[kRows * D + kRows + r], m2);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] += p[r * D + lane + 32 * i] * f;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s_acc[warp][lane + 32 * i] = acc[i];
+    if (lane == 0) s_st[warp][0] = sum;
+    __syncthreads();
+    sum = s_st[0][0] + s_st[1][0] + s_st[2][0] + s_st[3][0];
+    const int row = rt * kRows + r, tok = row / a.group, head = kvh * a.group + row % a.group;
+    const int d = threadIdx.x * 4;
+    if (d < D) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        x.x += s_acc[w][d];
+        x.y += s_acc[w][d + 1];
+        x.z += s_acc[w][d + 2];
+        x.w += s_acc[w][d + 3];
+      }
+      store_row4(a, rq.row0 + tok, head, D, d, x, m, m2, sum);
+    }
+    __syncthreads();
   }
 }
 
@@ -517,8 +522,8 @@ cudaError_t launch(const PaArgs& a, int num_sms, cudaStream_t s) {
   const int rt_max = a.tc_rows < INT_MAX ? ceil_div(a.tc_rows, kRows) : 0;
   const int64_t places = rt_max ? static_cast<int64_t>(rt_max) * a.B : static_cast<int64_t>(a.T) * a.group / kRows + a.B;
   if (places > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_pdl(paged_attn_join<D>, dim3(static_cast<unsigned>(places), a.c.n_kv_heads, kRows), 128, 0, s, a, ctas,
-                    rt_max);
+  return launch_pdl(paged_attn_join<D>, dim3(static_cast<unsigned>(places), a.c.n_kv_heads, rt_max ? 1 : kRows),
+                    128, 0, s, a, ctas, rt_max);
 }
 
 }  // namespace

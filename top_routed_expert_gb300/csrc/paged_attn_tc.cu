@@ -23,10 +23,11 @@
 // no scaling and the sum of the weights is the group sums divided by the same
 // scale.
 //
-// The running maximum moves only when it grows by more than 2^14: weights
-// relative to an older maximum stay within f16's range (65504) until then, the
-// quotient is the same, the scores are read once, and the accumulator is almost
-// never rescaled.
+// A row's weights are taken relative to the maximum of the first step that it
+// sees something in, and that reference moves only when a group of 16 weights
+// sums to over 2^15: until then they fit f16 (65504), and the quotient is the
+// same.  So the scores are read once, no maximum is taken in the ordinary step,
+// and the accumulator is almost never rescaled.
 #include <climits>
 
 #include "paged_attn.cuh"
@@ -45,13 +46,13 @@ constexpr int kGroups = kTok / 16;       // scale groups of a step
 constexpr int kThreads = 20 * 32;
 // Registers of a thread, by warpgroup: two of softmax, two of conversion, one
 // that plans and issues.  The launch has 96 for each of the 640 threads;
-// 256 x 144 + 256 x 64 + 128 x 64 are the same 61440.
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 144, kConvRegs = 64, kIssueRegs = 64;
+// 256 x 136 + 256 x 72 + 128 x 64 are the same 61440.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kConvRegs = 72, kIssueRegs = 64;
 static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kIssueRegs <= 5 * kLaunchRegs, "setmaxnreg would wait forever");
 constexpr int kConvThreads = 128;
 constexpr int kSlots = 8;              // steps that are planned ahead, at most
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kGrow = 14.0f;           // log2 of the growth that moves the maximum
+constexpr float kMostSum = 32768.0f;     // sum of 16 weights that moves the maximum: none is over f16's 65504
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -200,16 +201,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Weights 2^(score - m) of a 16-token group as f16 (s: its scales), the
-// largest score into `top`; returns `l` plus the weights' sum.
-__device__ __forceinline__ float weigh(const float (&x)[16], const float4& s, float rf, float m, float* p, float& top,
+// Weights 2^(score - m) of a 16-token group as f16 (s: its scales); their sum
+// goes into the largest so far and, divided by the value scale, to `l`.
+__device__ __forceinline__ float weigh(const float (&x)[16], const float4& s, float rf, float m, float* p, float& most,
                                        float l) {
   const float f = s.x * rf, shift = s.y - m;
-  // one positive factor for the group: its largest product has the largest score
-  float u = fmaxf(x[0], x[1]);
-#pragma unroll
-  for (int i = 2; i < 16; i += 2) u = fmaxf(u, fmaxf(x[i], x[i + 1]));
-  top = fmaxf(top, fmaf(u, f, s.y));
   const uint64_t f2 = pair(f, f), shift2 = pair(shift, shift);
   uint64_t sum = 0;
 #pragma unroll
@@ -223,7 +219,14 @@ __device__ __forceinline__ float weigh(const float (&x)[16], const float4& s, fl
   }
   float sum0, sum1;
   unpair(sum, sum0, sum1);
-  return fmaf(sum0 + sum1, s.z, l);
+  sum0 += sum1;
+  most = fmaxf(most, sum0);
+  return fmaf(sum0, s.z, l);
+}
+
+// The lowest n bits (n may be negative or over 32).
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
 // 16-byte chunk c of row r in a 128-byte-swizzled tile of 128-byte rows.
@@ -342,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
     }
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + L::kS + tile * kTok, t_o = tmem + lanes + L::kO + tile * D;
-    float m = -INFINITY, l = 0.f;
+    // a row that sees nothing at all needs no reference
+    float m = pos >= 0 ? -INFINITY : 0.f, l = 0.f;
     bool ok = true;
     for (int j = 0; j < steps; ++j) {
       const int slot = j % kSlots;
@@ -361,38 +365,56 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
 #pragma unroll 1
         for (int q = 0; q < kTok; q += 32) {
           if (sp.all_see(j0 + q, j0 + q + 31, pos_min, pos_max)) continue;   // the same for the whole warp
+          const uint32_t see = first_bits(hi + 1 - q) & (~first_bits(lo == INT_MIN ? 0 : lo + 1 - q) | first_bits(sink - q));
           float v[32];
           tmem_ld32_issue(t_s + q, v);
           tmem_ld32_wait(v);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (q + i > hi || (q + i <= lo && q + i >= sink)) v[i] = -INFINITY;
+            if (!(see & (1u << i))) v[i] = -INFINITY;
           tmem_st32(t_s + q, v);
         }
         tmem_st_wait();
       }
-      // Weights with the maximum so far, the scores read once.  The row's new
-      // maximum comes out beside them; it hardly ever asks for a second look.
-      float top = -INFINITY, lnew = l;
+      // Weights relative to the maximum so far, the scores read once.  A sum
+      // that grows too large for f16, or a row without a maximum yet, asks for
+      // a second look.
       float p[2][32];   // f16 pairs: the first and the last 64 tokens
-      const float ms = m == -INFINITY ? 0.f : m;
-      {
+      float lnew = l, most = 0.f;
+      bool again = m == -INFINITY;
+      if (!__any_sync(0xffffffffu, again)) {
         float v[2][16];
         tmem_ld16_issue(t_s, v[0]);
         tmem_ld16_wait(v[0]);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           if (g + 1 < kGroups) tmem_ld16_issue(t_s + (g + 1) * 16, v[(g + 1) & 1]);
-          lnew = weigh(v[g & 1], sc[g], rf, ms, p[g >> 2] + (g & 3) * 8, top, lnew);
+          lnew = weigh(v[g & 1], sc[g], rf, m, p[g >> 2] + (g & 3) * 8, most, lnew);
           if (g + 1 < kGroups) tmem_ld16_wait(v[(g + 1) & 1]);
         }
+        again = most > kMostSum;
       }
-      const bool grow = m == -INFINITY ? top > m : top > m + kGrow;
-      if (__any_sync(0xffffffffu, grow)) {
-        // s_full came after the product before: the accumulator is at rest
-        const float f = grow ? ex2(m - top) : 1.f;
-        if (grow) m = top;
+      if (__any_sync(0xffffffffu, again)) {
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < kTok; q += 32) {
+          float v[32];
+          tmem_ld32_issue(t_s + q, v);
+          tmem_ld32_wait(v);
+          // one positive factor for a group: its largest product has the largest score
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float u = fmaxf(v[16 * g], v[16 * g + 1]);
+#pragma unroll
+            for (int i = 2; i < 16; i += 2) u = fmaxf(u, fmaxf(v[16 * g + i], v[16 * g + i + 1]));
+            const float4 s = sc[q / 16 + g];
+            top = fmaxf(top, fmaf(u, s.x * rf, s.y));
+          }
+        }
+        const float to = fmaxf(m, top), f = m == -INFINITY ? 0.f : ex2(m - to);
+        m = to;
         if (j > 0) {
+          // s_full came after the product before: the accumulator is at rest
 #pragma unroll 1
           for (int i = 0; i < D; i += 32) {
             float v[32];
@@ -410,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
           float v[16];
           tmem_ld16_issue(t_s + g * 16, v);
           tmem_ld16_wait(v);
-          lnew = weigh(v, sc[g], rf, mg, p[g >> 2] + (g & 3) * 8, top, lnew);
+          lnew = weigh(v, sc[g], rf, mg, p[g >> 2] + (g & 3) * 8, most, lnew);
         }
       }
       l = lnew;
