@@ -37,7 +37,7 @@
 namespace moe {
 
 bool paged_attn_tc_supported(int D);
-cudaError_t launch_paged_attn_tc(const PaArgs& a, cudaStream_t s);
+cudaError_t launch_paged_attn_tc(const PaArgs& a, int num_sms, cudaStream_t s);
 
 namespace {
 
@@ -117,6 +117,86 @@ template <int D> __device__ __forceinline__ uint32_t chunk_at(int row, int chunk
   return row * D + ((chunk ^ ((row & 3) << 1) ^ (((row >> 2) & 1) << 2)) << 4);
 }
 
+// Lists the row blocks of the requests that go to paged_attn_tc.cu, the longest
+// first (a counting sort by 256 classes of length; the order inside a class
+// does not matter to the results).  One block; `first`: B + 1 ints, `scratch`:
+// the block's other shared memory.
+__device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* scratch) {
+  int* bins = reinterpret_cast<int*>(scratch);            // [256]
+  int* s_max = bins + 256;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int s_warp[kWarps];
+  for (int i = threadIdx.x; i < 256; i += kWarps * 32) bins[i] = 0;
+  if (threadIdx.x == 0) *s_max = 0;
+  __syncthreads();
+  auto blocks_of = [&](const Request& r) { return r.n * a.group > a.tc_rows ? ceil_div(r.n * a.group, kTcItemRows) : 0; };
+  auto length = [&](const Request& r, int blk) {
+    const int row0 = blk * kTcItemRows, row1 = min(row0 + kTcItemRows, r.n * a.group) - 1;
+    return span_for(a, r.start + row0 / a.group, r.start + row1 / a.group, kTcStep).units;
+  };
+  int base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
+    const int b = b0 + threadIdx.x;
+    int n = 0;
+    if (b < a.B) {
+      const Request r = load_request(a.cu, a.kv_len, b, a.T);
+      n = blocks_of(r);
+      if (n > 0) atomicMax(s_max, length(r, n - 1));
+    }
+    int sum = n;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += x;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    int all = 0, below = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      all += s_warp[w];
+      below += w < warp ? s_warp[w] : 0;
+    }
+    if (b < a.B) first[b] = base + below + sum - n;
+    base += all;
+    __syncthreads();
+  }
+  const int total = base;
+  const int64_t widest = *s_max + 1;
+  auto look = [&](int i, int2& e) {   // the i-th block and its class
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    e = make_int2(lo, i - first[lo]);
+    const int units = length(load_request(a.cu, a.kv_len, lo, a.T), e.y);
+    return 255 - static_cast<int>(min(static_cast<int64_t>(255), units * 256 / widest));
+  };
+  int2 e;
+  for (int i = threadIdx.x; i < total; i += kWarps * 32) atomicAdd(&bins[look(i, e)], 1);
+  __syncthreads();
+  if (warp == 0) {   // exclusive prefix over the classes
+    int sum = 0, mine[8];
+    for (int i = 0; i < 8; ++i) {
+      mine[i] = sum;
+      sum += bins[lane * 8 + i];
+    }
+    int before = sum;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, before, off);
+      if (lane >= off) before += x;
+    }
+    before -= sum;
+    for (int i = 0; i < 8; ++i) bins[lane * 8 + i] = before + mine[i];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < total; i += kWarps * 32) {
+    const int at = atomicAdd(&bins[look(i, e)], 1);
+    a.tc_list[1 + at] = e;
+  }
+  if (threadIdx.x == 0) a.tc_list[0] = make_int2(total, 0);
+  __syncthreads();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kernel(PaArgs a) {
   using S = Shape<D>;
@@ -128,6 +208,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
   __shared__ float s_scale[kWarps][kStages][4];
   int64_t* s_start = reinterpret_cast<int64_t*>(smem + kWarps * S::kRing);
   pdl_enter();
+  // the last CTA has the least to do here, often nothing
+  if (a.tc_rows < INT_MAX && blockIdx.x == gridDim.x - 1) list_tc_items(a, reinterpret_cast<int*>(s_start), smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   build_unit_table<kRows, kUnit>(a, s_start, blockIdx.x == 0 ? a.status : nullptr);
   const int64_t total = s_start[a.B];
@@ -538,17 +620,15 @@ constexpr int kTcRows = 64;
 
 cudaError_t launch_paged_attn(PaArgs a, int max_q_len, int num_sms, cudaStream_t s) {
   const int64_t most = static_cast<int64_t>(max_q_len > 0 ? std::min(max_q_len, a.T) : a.T) * a.group;
-  a.tc_rows = INT_MAX;
-  if (most > kTcRows && paged_attn_tc_supported(a.c.head_dim)) {
-    a.tc_rows = kTcRows;
-    const cudaError_t err = launch_paged_attn_tc(a, s);
-    if (err != cudaSuccess) return err;
-  }
+  const bool tc = most > kTcRows && paged_attn_tc_supported(a.c.head_dim);
+  a.tc_rows = tc ? kTcRows : INT_MAX;
+  cudaError_t err;
   switch (a.c.head_dim) {
-    case 64: return launch<64>(a, num_sms, s);
-    case 128: return launch<128>(a, num_sms, s);
-    default: return launch<256>(a, num_sms, s);
+    case 64: err = launch<64>(a, num_sms, s); break;
+    case 128: err = launch<128>(a, num_sms, s); break;
+    default: err = launch<256>(a, num_sms, s); break;
   }
+  return err == cudaSuccess && tc ? launch_paged_attn_tc(a, num_sms, s) : err;
 }
 
 namespace {
@@ -571,7 +651,11 @@ bool attention_config_ok(const moe_paged_attention_config_t* c, const moe_kv_cac
 extern "C" size_t moe_paged_attention_ws_bytes(const moe_paged_attention_config_t* cfg, const moe_kv_cache_t* cache) {
   using namespace moe;
   if (!attention_config_ok(cfg, cache)) return 0;
-  return align_up(paged_attn_ws_bytes(cache->head_dim), 256);
+  PaArgs a;
+  a.T = cfg->T;
+  a.B = cfg->batch;
+  a.group = cfg->n_q_heads / cache->n_kv_heads;
+  return align_up(paged_attn_ws_bytes(cache->head_dim), 256) + align_up((tc_places(a) + 1) * sizeof(int2), 256);
 }
 
 extern "C" moe_status_t moe_paged_attention(const moe_paged_attention_config_t* cfg, const moe_kv_cache_t* cache,
@@ -597,6 +681,7 @@ extern "C" moe_status_t moe_paged_attention(const moe_paged_attention_config_t* 
   a.cu = cu;
   a.kv_len = kv_len;
   a.part = static_cast<float*>(ws);
+  a.tc_list = reinterpret_cast<int2*>(static_cast<char*>(ws) + align_up(paged_attn_ws_bytes(cache->head_dim), 256));
   a.c = *cache;
   a.status = status;
   a.qs = cfg->q_stride;

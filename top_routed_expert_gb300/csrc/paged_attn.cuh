@@ -12,7 +12,8 @@ struct PaArgs {
   float* lse;
   const int32_t* cu;
   const int32_t* kv_len;
-  float* part;          // workspace
+  float* part;          // workspace: partial sums ...
+  int2* tc_list;        // ... and the row blocks for paged_attn_tc.cu: [0].x of them, (request, block) from [1] on
   moe_kv_cache_t c;
   unsigned* status;
   int64_t qs, os;
@@ -20,6 +21,12 @@ struct PaArgs {
   int tc_rows;          // requests with more rows (tokens x heads of the group) go to paged_attn_tc.cu
   float sm_scale;
 };
+
+constexpr int kTcItemRows = 256;   // rows of an item of paged_attn_tc.cu
+constexpr int kTcStep = 128;       // cached tokens of its steps
+
+// The most row blocks that the requests can have, for one key head.
+inline int64_t tc_places(const PaArgs& a) { return static_cast<int64_t>(a.T) * a.group / kTcItemRows + a.B; }
 
 // Cached tokens that the new tokens of a request can see, in blocks of `unit`
 // tokens: the blocks with the first visible positions of a window's sinks,

@@ -2,9 +2,9 @@
 // their chunks) on the 5th-generation tensor cores.
 //
 // The rows of one (request, key head) are its new tokens times the query
-// heads of the group (row r = token r / group, head r % group); a CTA takes
-// 256 of them as two tiles of 128 and walks the cached tokens that any of
-// them sees in steps of 128:
+// heads of the group (row r = token r / group, head r % group); an item is 256
+// of them, two tiles of 128, and walks the cached tokens that any of them sees
+// in steps of 128:
 //   S = Q K^T   (kind::f16, M = 128 rows, N = 128 tokens, both from shared
 //               memory)
 //   P = 2^(S k_scale .. - m), f16, written over S in tensor memory
@@ -12,7 +12,9 @@
 // Warps 0-3 and 4-7 are the softmax of tile 0 and 1 (one thread a row), warps
 // 8-11 convert keys and 12-15 values, warp 16 issues the MMAs, warp 17 looks up
 // pages and scales some steps ahead (18 and 19 only lend registers): while one
-// tile's softmax runs, the tensor core works on the other's products.
+// tile's softmax runs, the tensor core works on the other's products.  The CTAs
+// are persistent, one on an SM, and take items from a list that paged_attn.cu
+// has sorted by length; steps of the next item start beside the last of this.
 //
 // The cache's codes become f16 exactly on the way to shared memory (E4M3 fits
 // f16), one conversion for the 256 rows; the values are transposed there by
@@ -40,8 +42,8 @@ using namespace ptx;
 namespace {
 
 constexpr int kRowTile = 128;
-constexpr int kItemRows = 2 * kRowTile;
-constexpr int kTok = 128;                // tokens of a step
+static_assert(kTcItemRows == 2 * kRowTile, "two row tiles");
+constexpr int kTok = kTcStep;            // tokens of a step
 constexpr int kGroups = kTok / 16;       // scale groups of a step
 constexpr int kThreads = 20 * 32;
 // Registers of a thread, by warpgroup: two of softmax, two of conversion, one
@@ -51,19 +53,37 @@ constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kConvRegs = 72, kIssueRegs =
 static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kIssueRegs <= 5 * kLaunchRegs, "setmaxnreg would wait forever");
 constexpr int kConvThreads = 128;
 constexpr int kSlots = 8;              // steps that are planned ahead, at most
+constexpr int kItems = 16;             // items that are announced ahead; more than kSlots, as an item has a step or more
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMostSum = 32768.0f;     // sum of 16 weights that moves the maximum: none is over f16's 65504
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr long long kWaitCycles = 3000000000ll;
 constexpr uint64_t kDrainNs = 200000000ull;
 
+// A row block's work: up to 256 rows of one request and key head; rows = 0:
+// there is no more.
+struct Item {
+  int b, kvh, token0, n, end, row0, rows;   // token0, n, end: the request's rows and length
+  float lref;                               // log2 of the reference value scale
+  __device__ __forceinline__ Span span(const PaArgs& a) const {
+    const int start = end - n;
+    return span_for(a, start + row0 / a.group, start + (row0 + rows - 1) / a.group, kTok);
+  }
+};
+
 struct Ctrl {
-  uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], plan_full[kSlots],
-      plan_free[kSlots], drain;
+  // s_full[tile][step & 1] is the one signal that the MMA warp gives in a step:
+  // it says that the tile's scores are there and, the products running in
+  // order, that everything issued before them is done.  The converters take
+  // their free stages from tile 1's.  (Two barriers in turn, so that none can
+  // run a phase ahead of a waiter; a signal of its own for each stage made the
+  // issuing warp the bottleneck.)  Steps are counted through all items.
+  uint64_t q_full, k_full[2], v_full[2], s_full[2][2], p_full[2], o_full[2], plan_full[kSlots], plan_free[kSlots],
+      item_full[kItems], drain;
   // of a step's eight 16-token groups: key scale, log2 of the value scale, 1 /
   // value scale (both relative to lref); byte offset in the cache, -1: none
   float4 scale[kSlots][kGroups];
   int64_t place[kSlots][kGroups];
-  float lref;                            // log2 of the reference value scale
+  Item item[kItems];
   uint32_t tmem_base;
   int abort;
 };
@@ -229,31 +249,28 @@ __device__ __forceinline__ uint32_t first_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
+// Waits for the phase of `bar` with the given parity, bounded like mbar_wait.
+// A hand-over between two warps is on the critical path here, and a read of
+// the wall clock takes longer than one: the limit is in cycles (about a second
+// and a half) and is looked at now and then.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t at = smem_u32(bar);
+  if (mbar_try_wait(at, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(at, parity)) return true;
+    if ((i & 63) == 0) {
+      if (*abort) return false;
+      if (clock64() - t0 > kWaitCycles) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // 16-byte chunk c of row r in a 128-byte-swizzled tile of 128-byte rows.
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
-
-// The CTA's work: up to 256 rows of one request and key head.
-struct Item {
-  Request rq;
-  int b, kvh, row0, rows;
-  Span sp;
-  bool any;
-};
-
-__device__ __forceinline__ Item item_of(const PaArgs& a) {
-  Item it;
-  const int place = static_cast<int>(gridDim.x - 1 - blockIdx.x);   // the later, longer rows of a request first
-  it.b = warp_find_request(a.cu, a.B, place, a.group, kItemRows, 1);
-  it.rq = load_request(a.cu, a.kv_len, it.b, a.T);
-  it.kvh = blockIdx.y;
-  const int all = it.rq.n * a.group;
-  const int64_t blk = place - (static_cast<int64_t>(it.rq.row0) * a.group / kItemRows + it.b);
-  it.any = it.rq.ok && blk >= 0 && blk * kItemRows < all && all > a.tc_rows;
-  it.row0 = it.any ? static_cast<int>(blk) * kItemRows : 0;
-  it.rows = min(kItemRows, all - it.row0);
-  it.sp = span_for(a, it.rq.start + it.row0 / a.group, it.rq.start + (it.row0 + max(it.rows, 1) - 1) / a.group, kTok);
-  return it;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
@@ -270,9 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&c->k_full[i]), kConvThreads);
       mbar_init(smem_u32(&c->v_full[i]), kConvThreads);
-      mbar_init(smem_u32(&c->k_free[i]), 1);
-      mbar_init(smem_u32(&c->v_free[i]), 1);
-      mbar_init(smem_u32(&c->s_full[i]), 1);
+      mbar_init(smem_u32(&c->s_full[i][0]), 1);
+      mbar_init(smem_u32(&c->s_full[i][1]), 1);
       mbar_init(smem_u32(&c->p_full[i]), kRowTile);
       mbar_init(smem_u32(&c->o_full[i]), 1);
     }
@@ -280,14 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       mbar_init(smem_u32(&c->plan_full[i]), kGroups);
       mbar_init(smem_u32(&c->plan_free[i]), 1);
     }
+    for (int i = 0; i < kItems; ++i) mbar_init(smem_u32(&c->item_full[i]), 1);
     mbar_init(smem_u32(&c->drain), 1);
     c->abort = 0;
-    c->lref = 0.f;
     fence_barrier_init();
   }
-  pdl_enter();
-  const Item it = item_of(a);
-  if (!it.any) return;   // the whole block; nothing is held yet
   if (warp == 16) {
     tmem_alloc(smem_u32(&c->tmem_base), 512);
     tmem_relinquish();
@@ -295,218 +308,268 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_enter();
   const uint32_t tmem = c->tmem_base;
-  const Span sp = it.sp;
-  const int steps = sp.units;
+  // item k, once the planning warp has announced it
+  auto next_item = [&](int k) { return wait_phase(&c->item_full[k % kItems], (k / kItems) & 1, abort); };
 
   if (warp < 8) {
     // ---------------------------------------------------------- softmax
     regs_up<kSoftmaxRegs>();
-    const int tile = warp >> 2, r = it.row0 + tile * kRowTile + (threadIdx.x & 127);
-    const bool live = r < it.row0 + it.rows;
-    const int tok = live ? r / a.group : 0, head = it.kvh * a.group + (live ? r % a.group : 0);
-    const int pos = live ? it.rq.start + tok : -1;
-    // this warp's live rows: first and last position
-    const int w0 = it.row0 + tile * kRowTile + (warp & 3) * 32;
-    const int w1 = min(w0 + 31, it.row0 + it.rows - 1);
-    const int pos_min = it.rq.start + w0 / a.group, pos_max = it.rq.start + max(w1, 0) / a.group;
-    float rf;
-    {
-      uint4 raw[D / 8];
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(it.rq.row0 + tok) * a.qs +
-                                                        static_cast<int64_t>(head) * D);
-      float amax = 0.f;
-      bool fin = true;
+    const int tile = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + L::kS + tile * kTok, t_o = tmem + lanes + L::kO + tile * D;
+    // q travels in whole rows: D/8 neighbouring lanes have one, 16 bytes each
+    constexpr int LPR = D / 8, RPI = 32 / LPR;   // lanes of a row, rows at a time
+    const int lr = lane % LPR, lq = lane / LPR;
+    // Rows of item `it` into the tile's q as f16, each scaled by a power of two;
+    // returns this thread's row's factor for the scores.
+    auto load_q = [&](const Item& it) {
+      const int r = it.row0 + tile * kRowTile + (threadIdx.x & 127);
+      int64_t mine = -1;   // element of this thread's row
+      if (r < it.row0 + it.rows)
+        mine = (it.token0 + r / a.group) * a.qs + static_cast<int64_t>(it.kvh * a.group + r % a.group) * D;
+      static_assert(32 / RPI == LPR, "as many rows for a lane as lanes for a row");
+      uint4 raw[LPR];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        raw[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      for (int i = 0; i < LPR; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, mine, i * RPI + lq);
+        raw[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + at + lr * 8)) : make_uint4(0, 0, 0, 0);
+      }
+      // The largest size of each row as bits (a NaN's are above infinity's).
+      // LPR rows in LPR lanes: each exchange halves the rows that a lane keeps,
+      // until lane lr has the maximum of its group's row lr.
+      uint32_t top[LPR];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-          fin = fin && lo < INFINITY && hi < INFINITY;
-          amax = fmaxf(amax, fmaxf(lo, hi));
+      for (int i = 0; i < LPR; ++i) {
+        uint32_t x = __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu);
+        x = __vmaxu2(x, __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
+        top[i] = max(x & 0xffffu, x >> 16);
+      }
+#pragma unroll
+      for (int half = LPR / 2; half > 0; half >>= 1) {
+        const bool upper = lr & half;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+          const uint32_t keep = upper ? top[i + half] : top[i], give = upper ? top[i] : top[i + half];
+          top[i] = max(keep, __shfl_xor_sync(0xffffffffu, give, half));
         }
       }
-      const float f = q_factor(amax, fin);
-      rf = a.sm_scale * kLog2e / f;
-      const int row = threadIdx.x & 127;
+      const float factor = q_factor(__uint_as_float(top[0] << 16), top[0] < 0x7f80u);   // of row lr * RPI + lq
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
+      for (int i = 0; i < LPR; ++i) {
+        const float f = __shfl_sync(0xffffffffu, factor, lq * LPR + i);
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
         uint32_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           h[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
-        sts128(s_q + tile * L::kQ + (i / 8) * (kRowTile * 128) + sw128(row, i % 8), h[0], h[1], h[2], h[3]);
+        const int row = (warp & 3) * 32 + i * RPI + lq;
+        sts128(s_q + tile * L::kQ + (lr / 8) * (kRowTile * 128) + sw128(row, lr % 8), h[0], h[1], h[2], h[3]);
       }
+      const float rf = a.sm_scale * kLog2e / __shfl_sync(0xffffffffu, factor, (lane % RPI) * LPR + lane / RPI);
       fence_async();
       mbar_arrive(smem_u32(&c->q_full));
-    }
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + L::kS + tile * kTok, t_o = tmem + lanes + L::kO + tile * D;
-    // a row that sees nothing at all needs no reference
-    float m = pos >= 0 ? -INFINITY : 0.f, l = 0.f;
-    bool ok = true;
-    for (int j = 0; j < steps; ++j) {
-      const int slot = j % kSlots;
-      ok = mbar_wait(smem_u32(&c->s_full[tile]), j & 1, abort, kWaitNs) &&
-           mbar_wait(smem_u32(&c->plan_full[slot]), (j / kSlots) & 1, abort, kWaitNs);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const int j0 = sp.block_of(j) * kTok;
-      const bool full = sp.all_see(j0, j0 + kTok - 1, pos_min, pos_max);
-      const float4* sc = c->scale[slot];
-      if (!full) {
-        // scores that the row does not see become -infinity, in place: what
-        // follows needs no mask
-        const int hi = pos - j0, lo = sp.window ? hi - sp.window : INT_MIN, sink = sp.n_sink - j0;
+      return rf;
+    };
+    int g = 0;   // step, over all items
+    bool ok = __all_sync(0xffffffffu, next_item(0));
+    float rf = ok && c->item[0].rows > 0 ? load_q(c->item[0]) : 0.f;
 #pragma unroll 1
-        for (int q = 0; q < kTok; q += 32) {
-          if (sp.all_see(j0 + q, j0 + q + 31, pos_min, pos_max)) continue;   // the same for the whole warp
-          const uint32_t see = first_bits(hi + 1 - q) & (~first_bits(lo == INT_MIN ? 0 : lo + 1 - q) | first_bits(sink - q));
-          float v[32];
-          tmem_ld32_issue(t_s + q, v);
-          tmem_ld32_wait(v);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(see & (1u << i))) v[i] = -INFINITY;
-          tmem_st32(t_s + q, v);
-        }
-        tmem_st_wait();
-      }
-      // Weights relative to the maximum so far, the scores read once.  A sum
-      // that grows too large for f16, or a row without a maximum yet, asks for
-      // a second look.
-      float p[2][32];   // f16 pairs: the first and the last 64 tokens
-      float lnew = l, most = 0.f;
-      bool again = m == -INFINITY;
-      if (!__any_sync(0xffffffffu, again)) {
-        float v[2][16];
-        tmem_ld16_issue(t_s, v[0]);
-        tmem_ld16_wait(v[0]);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          if (g + 1 < kGroups) tmem_ld16_issue(t_s + (g + 1) * 16, v[(g + 1) & 1]);
-          lnew = weigh(v[g & 1], sc[g], rf, m, p[g >> 2] + (g & 3) * 8, most, lnew);
-          if (g + 1 < kGroups) tmem_ld16_wait(v[(g + 1) & 1]);
-        }
-        again = most > kMostSum;
-      }
-      if (__any_sync(0xffffffffu, again)) {
-        float top = -INFINITY;
+    for (int k = 0; ok; ++k) {
+      const Item& it = c->item[k % kItems];
+      if (it.rows == 0) break;
+      const Span sp = it.span(a);
+      const int steps = sp.units, start = it.end - it.n;
+      // this thread's row, and the first and last position of the warp's live rows
+      const int w0 = it.row0 + tile * kRowTile + (warp & 3) * 32, r = w0 + lane;
+      const int w1 = min(w0 + 31, it.row0 + it.rows - 1);
+      const bool live = r <= w1;
+      const int pos = live ? start + r / a.group : -1;
+      const int pos_min = start + w0 / a.group, pos_max = start + max(w1, 0) / a.group;
+      // a row that sees nothing at all needs no reference
+      float m = pos >= 0 ? -INFINITY : 0.f, l = 0.f;
 #pragma unroll 1
-        for (int q = 0; q < kTok; q += 32) {
-          float v[32];
-          tmem_ld32_issue(t_s + q, v);
-          tmem_ld32_wait(v);
-          // one positive factor for a group: its largest product has the largest score
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float u = fmaxf(v[16 * g], v[16 * g + 1]);
-#pragma unroll
-            for (int i = 2; i < 16; i += 2) u = fmaxf(u, fmaxf(v[16 * g + i], v[16 * g + i + 1]));
-            const float4 s = sc[q / 16 + g];
-            top = fmaxf(top, fmaf(u, s.x * rf, s.y));
-          }
-        }
-        const float to = fmaxf(m, top), f = m == -INFINITY ? 0.f : ex2(m - to);
-        m = to;
-        if (j > 0) {
-          // s_full came after the product before: the accumulator is at rest
+      for (int j = 0; j < steps; ++j, ++g) {
+        const int slot = g % kSlots;
+        ok = wait_phase(&c->s_full[tile][g & 1], (g >> 1) & 1, abort) &&
+             wait_phase(&c->plan_full[slot], (g / kSlots) & 1, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const int j0 = sp.block_of(j) * kTok;
+        const float4* sc = c->scale[slot];
+        if (!sp.all_see(j0, j0 + kTok - 1, pos_min, pos_max)) {
+          // scores that the row does not see become -infinity, in place: what
+          // follows needs no mask
+          const int hi = pos - j0, lo = sp.window ? hi - sp.window : INT_MIN, sink = sp.n_sink - j0;
 #pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
+          for (int q = 0; q < kTok; q += 32) {
+            if (sp.all_see(j0 + q, j0 + q + 31, pos_min, pos_max)) continue;   // the same for the whole warp
+            const uint32_t see = first_bits(hi + 1 - q) & (~first_bits(lo == INT_MIN ? 0 : lo + 1 - q) | first_bits(sink - q));
             float v[32];
-            tmem_ld32_issue(t_o + i, v);
+            tmem_ld32_issue(t_s + q, v);
             tmem_ld32_wait(v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= f;
-            tmem_st32(t_o + i, v);
+            for (int i = 0; i < 32; ++i)
+              if (!(see & (1u << i))) v[i] = -INFINITY;
+            tmem_st32(t_s + q, v);
           }
+          tmem_st_wait();
         }
-        lnew = l * f;
-        const float mg = m == -INFINITY ? 0.f : m;
+        // Weights relative to the maximum so far, the scores read once.  A sum
+        // that grows too large for f16, or a row without a maximum yet, takes the
+        // maximum first and moves the accumulator to it.
+        float p[2][32];   // f16 pairs: the first and the last 64 tokens
+        float lnew = l;
+        bool move = m == -INFINITY;
+#pragma unroll 1
+        for (int look = 0; look < 2; ++look) {
+          if (__any_sync(0xffffffffu, move)) {
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < kTok; q += 32) {
+              float v[32];
+              tmem_ld32_issue(t_s + q, v);
+              tmem_ld32_wait(v);
+              // one positive factor for a group: its largest product has the largest score
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          float v[16];
-          tmem_ld16_issue(t_s + g * 16, v);
-          tmem_ld16_wait(v);
-          lnew = weigh(v, sc[g], rf, mg, p[g >> 2] + (g & 3) * 8, most, lnew);
+              for (int h = 0; h < 2; ++h) {
+                float u = fmaxf(v[16 * h], v[16 * h + 1]);
+#pragma unroll
+                for (int i = 2; i < 16; i += 2) u = fmaxf(u, fmaxf(v[16 * h + i], v[16 * h + i + 1]));
+                const float4 s = sc[q / 16 + h];
+                top = fmaxf(top, fmaf(u, s.x * rf, s.y));
+              }
+            }
+            const float to = fmaxf(m, top), f = m == -INFINITY ? 0.f : ex2(m - to);
+            m = to;
+            l *= f;
+            if (j > 0) {
+              // the scores came after the product before: the accumulator is at rest
+#pragma unroll 1
+              for (int i = 0; i < D; i += 32) {
+                float v[32];
+                tmem_ld32_issue(t_o + i, v);
+                tmem_ld32_wait(v);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] *= f;
+                tmem_st32(t_o + i, v);
+              }
+            }
+          }
+          lnew = l;
+          const float ms = m == -INFINITY ? 0.f : m;
+          float most = 0.f;
+          float v[2][16];
+          tmem_ld16_issue(t_s, v[0]);
+          tmem_ld16_wait(v[0]);
+#pragma unroll
+          for (int h = 0; h < kGroups; ++h) {
+            if (h + 1 < kGroups) tmem_ld16_issue(t_s + (h + 1) * 16, v[(h + 1) & 1]);
+            lnew = weigh(v[h & 1], sc[h], rf, ms, p[h >> 2] + (h & 3) * 8, most, lnew);
+            if (h + 1 < kGroups) tmem_ld16_wait(v[(h + 1) & 1]);
+          }
+          move = most > kMostSum;
+          if (!__any_sync(0xffffffffu, move)) break;
         }
+        l = lnew;
+        tmem_st32(t_s, p[0]);
+        tmem_st32(t_s + 32, p[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&c->p_full[tile]));
       }
-      l = lnew;
-      tmem_st32(t_s, p[0]);
-      tmem_st32(t_s + 32, p[1]);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&c->p_full[tile]));
-    }
-    if (ok) ok = mbar_wait(smem_u32(&c->o_full[tile]), 0, abort, kWaitNs);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
+      if (!ok) break;
+      // The next item's q goes in while the last product runs (the tile's q is
+      // free: its last scores are there), so that its first scores are computed
+      // beside this item's output.
+      ok = __all_sync(0xffffffffu, next_item(k + 1));
+      if (!ok) break;
+      float rf_next = 0.f;
+      if (c->item[(k + 1) % kItems].rows > 0) rf_next = load_q(c->item[(k + 1) % kItems]);
+      ok = __all_sync(0xffffffffu, wait_phase(&c->o_full[tile], k & 1, abort));
+      if (!ok) break;
       tc_fence_after();
       const bool empty = l == 0.f;   // nothing visible (a NaN sum is not)
-      const float f = empty ? 0.f : exp2f(c->lref) / l;
-      uint16_t* dst = a.out + static_cast<int64_t>(it.rq.row0 + tok) * a.os + static_cast<int64_t>(head) * D;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        float v[2][16];
-        tmem_ld16x2(t_o + i * 32, t_o + i * 32 + 16, v[0], v[1]);
+      const float f = empty ? 0.f : exp2f(it.lref) / l;
+      const int head = it.kvh * a.group + r % a.group, token = it.token0 + r / a.group;
+      uint16_t* dst = a.out + static_cast<int64_t>(token) * a.os + static_cast<int64_t>(head) * D;
+#pragma unroll 1
+      for (int i = 0; i < D; i += 32) {
+        float v[32];
+        tmem_ld32_issue(t_o + i, v);
+        tmem_ld32_wait(v);
         if (live) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float* x = v[q >> 1] + (q & 1) * 8;
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * e] * f, x[2 * e + 1] * f);
+              const __nv_bfloat162 y = __floats2bfloat162_rn(v[8 * q + 2 * e] * f, v[8 * q + 2 * e + 1] * f);
               w[e] = *reinterpret_cast<const uint32_t*>(&y);
             }
-            *reinterpret_cast<uint4*>(dst + i * 32 + q * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + i + q * 8) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
       if (live && a.lse)
-        a.lse[static_cast<int64_t>(it.rq.row0 + tok) * (a.group * a.c.n_kv_heads) + head] =
+        a.lse[static_cast<int64_t>(token) * (a.group * a.c.n_kv_heads) + head] =
             empty ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       tc_fence_before();
+      rf = rf_next;
     }
   } else if (warp < 16) {
     // ---------------------------------------------------------- conversion
     regs_down<kConvRegs>();
     const int t = threadIdx.x & 127;
     const int64_t ts = a.c.token_stride;
-    auto planned = [&](int j) {
-      return mbar_wait(smem_u32(&c->plan_full[j % kSlots]), (j / kSlots) & 1, abort, kWaitNs);
+    // walks the steps of all items; false: there are no more
+    int k = -1, j = 0, g = -1, steps = 0, j0 = 0;
+    bool all = false;
+    Span sp = {};
+    int64_t head_at = 0;
+    auto next_step = [&] {
+      ++g;
+      if (++j >= steps) {
+        if (!next_item(++k)) return false;
+        const Item& it = c->item[k % kItems];
+        if (it.rows == 0) return false;
+        sp = it.span(a);
+        steps = sp.units;
+        head_at = it.kvh * a.c.head_stride;
+        j = 0;
+      }
+      j0 = sp.block_of(j) * kTok;
+      // every token of the step is seen by some row
+      all = j0 + kTok <= sp.end && (j0 >= sp.lo || j0 + kTok <= sp.n_sink);
+      return wait_phase(&c->plan_full[g % kSlots], (g / kSlots) & 1, abort);
     };
-    // every token of the step is seen by some row
-    auto all_there = [&](int j0) { return j0 + kTok <= sp.end && (j0 >= sp.lo || j0 + kTok <= sp.n_sink); };
     if (warp < 12) {
       // keys: token (+ i KSTEP) and 16-byte chunk; eight neighbouring lanes have
       // four chunks of two rows, which the swizzle puts in eight banks
       constexpr int CPT = D / 16, KN = kTok * CPT / kConvThreads, KSTEP = kConvThreads / CPT;
       const int kc = D == 128 ? (t & 3) | ((t >> 1) & 4) : t & 3;
       const int kr = D == 128 ? ((t >> 2) & 1) | (t >> 4 << 1) : t >> 2;
-      const uint8_t* mine = static_cast<const uint8_t*>(a.c.k) + it.kvh * a.c.head_stride + (kr & 15) * ts + kc * 16;
+      const uint8_t* mine = static_cast<const uint8_t*>(a.c.k) + (kr & 15) * ts + kc * 16;
       uint4 kw[KN];
-      auto load = [&](int j) {
-        const int j0 = sp.block_of(j) * kTok;
-        const bool all = all_there(j0);
+      auto load = [&] {
+        const uint8_t* from = mine + head_at;
 #pragma unroll
         for (int i = 0; i < KN; ++i) {
           const int x = i * KSTEP + kr;
-          const int64_t off = c->place[j % kSlots][x >> 4];
+          const int64_t off = c->place[g % kSlots][x >> 4];
           kw[i] = make_uint4(0, 0, 0, 0);
-          if (off >= 0 && (all || sp.seen(j0 + x))) kw[i] = __ldg(reinterpret_cast<const uint4*>(mine + off));
+          if (off >= 0 && (all || sp.seen(j0 + x))) kw[i] = __ldg(reinterpret_cast<const uint4*>(from + off));
         }
       };
-      bool ok = planned(0);
-      if (ok) load(0);
+      bool more = next_step();
+      if (more) load();
 #pragma unroll 1
-      for (int j = 0; ok && j < steps; ++j) {
-        const int st = j & 1, ph = (j >> 1) & 1;
-        if (!mbar_wait(smem_u32(&c->k_free[st]), ph ^ 1, abort, kWaitNs)) break;
+      while (more) {
+        // the stage is free when the scores of two steps before are there
+        const int st = g & 1;
+        if (g >= 2 && !wait_phase(&c->s_full[1][st], ((g - 2) >> 1) & 1, abort)) break;
         const uint32_t base = s_k + st * L::kK + (kc >> 2) * (kTok * 128);
 #pragma unroll
         for (int i = 0; i < KN; ++i) {
@@ -517,49 +580,51 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         }
         fence_async();
         mbar_arrive(smem_u32(&c->k_full[st]));
-        if (j + 1 < steps) {
-          ok = planned(j + 1);
-          if (ok) load(j + 1);
-        }
+        more = next_step();
+        if (more) load();
       }
     } else {
       // values: 8 tokens (an octet of the warp's 32) by 4 elements; the lane's
       // bits are dealt so that eight neighbouring lanes store to eight banks
       constexpr int VN = D / 32;   // 32-byte column blocks
       const int vx = (lane & 1) | ((lane >> 3) << 1), vt = (warp & 3) * 32 + ((lane >> 1) & 3) * 8;
-      const uint8_t* mine = static_cast<const uint8_t*>(a.c.v) + it.kvh * a.c.head_stride + (vt & 15) * ts + vx * 4;
+      const uint8_t* mine = static_cast<const uint8_t*>(a.c.v) + (vt & 15) * ts + vx * 4;
       uint32_t vw[VN][8];
-      auto load = [&](int j) {
-        const int j0 = sp.block_of(j) * kTok;
-        const bool all = all_there(j0);
-        const int64_t off = c->place[j % kSlots][vt >> 4];
-        const uint8_t* row = mine + off;
+      auto load = [&] {
+        const int64_t off = c->place[g % kSlots][vt >> 4];
+        const uint8_t* row = mine + head_at + off;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const bool there = off >= 0 && (all || sp.seen(j0 + vt + k));
+        for (int i = 0; i < 8; ++i) {
+          const bool there = off >= 0 && (all || sp.seen(j0 + vt + i));
 #pragma unroll
           for (int d = 0; d < VN; ++d) {
-            vw[d][k] = 0u;
-            if (there) vw[d][k] = __ldg(reinterpret_cast<const uint32_t*>(row + d * 32));
+            vw[d][i] = 0u;
+            if (there) vw[d][i] = __ldg(reinterpret_cast<const uint32_t*>(row + d * 32));
           }
           row += ts;
         }
       };
-      bool ok = planned(0);
-      if (ok) load(0);
+      bool more = next_step();
+      if (more) load();
 #pragma unroll 1
-      for (int j = 0; ok && j < steps; ++j) {
-        const int st = j & 1, ph = (j >> 1) & 1;
-        if (!mbar_wait(smem_u32(&c->v_free[st]), ph ^ 1, abort, kWaitNs)) break;
+      while (more) {
+        // the stage is free when the products of two steps before are done, which
+        // the scores of one step before say; both softmax tiles are past that
+        // step then, and its plan is free
+        const int st = g & 1;
+        if (g >= 2) {
+          if (!wait_phase(&c->s_full[1][st ^ 1], ((g - 1) >> 1) & 1, abort)) break;
+          if (t == 0) mbar_arrive(smem_u32(&c->plan_free[(g - 2) % kSlots]));
+        }
         const uint32_t base = s_v + st * L::kK + (vt >> 6) * (D * 128);
         const int ch = (vt & 63) >> 3;
 #pragma unroll
         for (int d = 0; d < VN; ++d) {
           uint32_t lo[4], hi[4];   // token pairs of elements 0,1 and 2,3
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            lo[k] = __byte_perm(vw[d][2 * k], vw[d][2 * k + 1], 0x5140);
-            hi[k] = __byte_perm(vw[d][2 * k], vw[d][2 * k + 1], 0x7362);
+          for (int i = 0; i < 4; ++i) {
+            lo[i] = __byte_perm(vw[d][2 * i], vw[d][2 * i + 1], 0x5140);
+            hi[i] = __byte_perm(vw[d][2 * i], vw[d][2 * i + 1], 0x7362);
           }
           const int row = d * 32 + vx * 4;
           sts128(base + sw128(row, ch), f16x2_lo(lo[0]), f16x2_lo(lo[1]), f16x2_lo(lo[2]), f16x2_lo(lo[3]));
@@ -569,52 +634,76 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         }
         fence_async();
         mbar_arrive(smem_u32(&c->v_full[st]));
-        if (j + 1 < steps) {
-          ok = planned(j + 1);
-          if (ok) load(j + 1);
-        }
+        more = next_step();
+        if (more) load();
       }
     }
   } else {
     regs_down<kIssueRegs>();
     if (warp == 17) {
       // -------------------------------------------------------- planning
-      // Four steps at a time, a lane for each 16-token group: page id, place in
-      // the cache, scales.
+      // Takes this CTA's items from the list (the longest come first; the CTAs
+      // take them forth and back), announces them, and looks up their steps:
+      // four at a time, a lane for each 16-token group: page id, place in the
+      // cache, scales.
       constexpr int kNotSeen = INT_MIN;
-      const int32_t* table = a.c.page_table + static_cast<int64_t>(it.b) * a.c.max_pages;
       const int ps = a.c.page_size, ps_log = 31 - __clz(ps), grp = lane & 7;
-      float lref = 0.f;
+      const int64_t total = static_cast<int64_t>(a.tc_list[0].x) * a.c.n_kv_heads;
       bool ok = true;
+      int g = 0;
 #pragma unroll 1
-      for (int j0 = 0; ok && j0 < steps; j0 += 4) {
-        const int j = j0 + (lane >> 3), slot = j % kSlots;
-        const bool mine = j < steps;
-        const int x = mine ? sp.block_of(j) * kTok + grp * 16 : 0;
-        const int gp = mine && sp.any_seen(x, x + 15) ? __ldg(table + (x >> ps_log)) : kNotSeen;
-        const bool have = static_cast<unsigned>(gp) < static_cast<unsigned>(a.c.n_pages);
-        if (!have && gp != kNotSeen) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-        float ks = 0.f, lvs = 0.f;
-        if (have) {
-          const int64_t s = static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh;
-          ks = __ldg(a.c.k_scale + s);
-          lvs = log2f(__ldg(a.c.v_scale + s));
+      for (int k = 0; ok; ++k) {
+        const int64_t at = static_cast<int64_t>(k) * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        Item it = {};
+        if (at < total) {
+          const int2 e = a.tc_list[1 + at / a.c.n_kv_heads];
+          const Request rq = load_request(a.cu, a.kv_len, e.x, a.T);
+          it.b = e.x;
+          it.kvh = static_cast<int>(at % a.c.n_kv_heads);
+          it.token0 = rq.row0;
+          it.n = rq.n;
+          it.end = rq.end;
+          it.row0 = e.y * kTcItemRows;
+          it.rows = min(kTcItemRows, rq.n * a.group - it.row0);
         }
-        if (j0 == 0) {
-          const unsigned any = __ballot_sync(0xffffffffu, have);
-          lref = __shfl_sync(0xffffffffu, lvs, any ? __ffs(any) - 1 : 0);
-          if (lane == 0) c->lref = lref;
+        if (lane == 0) {
+          c->item[k % kItems] = it;
+          mbar_arrive(smem_u32(&c->item_full[k % kItems]));
         }
-        if (mine && j >= kSlots)
-          ok = mbar_wait(smem_u32(&c->plan_free[slot]), ((j / kSlots) - 1) & 1, abort, kWaitNs);
-        ok = __all_sync(0xffffffffu, ok);
-        if (mine && ok) {
-          // a group without a page masks itself
-          c->place[slot][grp] = have ? gp * a.c.page_stride + (x & (ps - 1)) * a.c.token_stride : -1;
-          c->scale[slot][grp] =
-              have ? make_float4(ks, lvs - lref, exp2f(lref - lvs), 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
-          mbar_arrive(smem_u32(&c->plan_full[slot]));
+        if (it.rows == 0) break;
+        const Span sp = it.span(a);
+        const int32_t* table = a.c.page_table + static_cast<int64_t>(it.b) * a.c.max_pages;
+        float lref = 0.f;
+#pragma unroll 1
+        for (int jb = 0; ok && jb < sp.units; jb += 4) {
+          const int j = jb + (lane >> 3), s = g + j, slot = s % kSlots;
+          const bool mine = j < sp.units;
+          const int x = mine ? sp.block_of(j) * kTok + grp * 16 : 0;
+          const int gp = mine && sp.any_seen(x, x + 15) ? __ldg(table + (x >> ps_log)) : kNotSeen;
+          const bool have = static_cast<unsigned>(gp) < static_cast<unsigned>(a.c.n_pages);
+          if (!have && gp != kNotSeen) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+          float ks = 0.f, lvs = 0.f;
+          if (have) {
+            const int64_t sa = static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh;
+            ks = __ldg(a.c.k_scale + sa);
+            lvs = log2f(__ldg(a.c.v_scale + sa));
+          }
+          if (jb == 0) {
+            const unsigned any = __ballot_sync(0xffffffffu, have);
+            lref = __shfl_sync(0xffffffffu, lvs, any ? __ffs(any) - 1 : 0);
+            if (lane == 0) c->item[k % kItems].lref = lref;
+          }
+          if (mine && s >= kSlots) ok = wait_phase(&c->plan_free[slot], ((s / kSlots) - 1) & 1, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (mine && ok) {
+            // a group without a page masks itself
+            c->place[slot][grp] = have ? gp * a.c.page_stride + (x & (ps - 1)) * a.c.token_stride : -1;
+            c->scale[slot][grp] =
+                have ? make_float4(ks, lvs - lref, exp2f(lref - lvs), 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
+            mbar_arrive(smem_u32(&c->plan_full[slot]));
+          }
         }
+        g += sp.units;
       }
     }
     // ---------------------------------------------------------- MMA issue
@@ -627,18 +716,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       // the operand's size (in 16-byte units) behind
       const uint64_t dq = desc_sw128(s_q), dk = desc_sw128(s_k), dv = desc_sw128(s_v);
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort, kWaitNs)) != 0;
+        return __all_sync(0xffffffffu, wait_phase(bar, parity, abort)) != 0;
       };
-      auto scores = [&](int tile, int st) {
+      auto scores = [&](int tile, int st) {   // st: step & 1
         const uint64_t da = dq + tile * (L::kQ >> 4), db = dk + st * (L::kK >> 4);
         const uint32_t d = tm + L::kS + tile * kTok;
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const int o = (k >> 2) * (kRowTile * 128 >> 4) + 2 * (k & 3);   // 128-byte column block, 32-byte step
-            mma_ss(d, da + o, db + o, is, k != 0);
+          for (int i = 0; i < D / 16; ++i) {
+            const int o = (i >> 2) * (kRowTile * 128 >> 4) + 2 * (i & 3);   // 128-byte column block, 32-byte step
+            mma_ss(d, da + o, db + o, is, i != 0);
           }
-          mma_commit(smem_u32(&c->s_full[tile]));
+          mma_commit(smem_u32(&c->s_full[tile][st]));
         }
         __syncwarp();
       };
@@ -647,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         const uint32_t d = tm + L::kO + tile * D, p = tm + L::kS + tile * kTok;
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTok / 16; ++k)
-            mma_ts(d, p + k * 8, db + (k >> 2) * (D * 128 >> 4) + 2 * (k & 3), io, !first || k != 0);
+          for (int i = 0; i < kTok / 16; ++i)
+            mma_ts(d, p + i * 8, db + (i >> 2) * (D * 128 >> 4) + 2 * (i & 3), io, !first || i != 0);
         }
         __syncwarp();
       };
@@ -656,35 +745,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         if (elect_one()) mma_commit(smem_u32(bar));
         __syncwarp();
       };
-      bool ok = wait(&c->q_full, 0) && wait(&c->k_full[0], 0);
-      if (ok) {
+      int g = 0;   // step, over all items
+      bool ok = true;
+#pragma unroll 1
+      for (int k = 0; ok; ++k) {
+        if (!(ok = __all_sync(0xffffffffu, next_item(k)))) break;
+        const Item& it = c->item[k % kItems];
+        if (it.rows == 0) break;
+        const int steps = it.span(a).units;
+        if (!(ok = wait(&c->q_full, k & 1) && wait(&c->k_full[g & 1], (g >> 1) & 1))) break;
         tc_fence_after();
-        scores(0, 0);
-        scores(1, 0);
-        commit(&c->k_free[0]);
-      }
+        scores(0, g & 1);
+        scores(1, g & 1);
 #pragma unroll 1
-      for (int j = 0; ok && j < steps; ++j) {
-        const int st = j & 1, ph = (j >> 1) & 1, nst = st ^ 1, nph = ((j + 1) >> 1) & 1;
-        const bool more = j + 1 < steps;
-        if (!(ok = wait(&c->v_full[st], ph))) break;
+        for (int j = 0; j < steps; ++j, ++g) {
+          const int st = g & 1, nst = st ^ 1;
+          const bool more = j + 1 < steps;
+          if (!(ok = wait(&c->v_full[st], (g >> 1) & 1))) break;
 #pragma unroll 1
-        for (int tile = 0; tile < 2; ++tile) {
-          if (!(ok = wait(&c->p_full[tile], j & 1))) break;
-          tc_fence_after();
-          output(tile, st, j == 0);
-          if (!more) {
-            commit(&c->o_full[tile]);
-          } else {
-            if (tile == 0 && !(ok = wait(&c->k_full[nst], nph))) break;
+          for (int tile = 0; tile < 2; ++tile) {
+            if (!(ok = wait(&c->p_full[tile], g & 1))) break;
             tc_fence_after();
-            scores(tile, nst);
+            output(tile, st, j == 0);
+            if (!more) {
+              commit(&c->o_full[tile]);
+            } else {
+              if (tile == 0 && !(ok = wait(&c->k_full[nst], ((g + 1) >> 1) & 1))) break;
+              tc_fence_after();
+              scores(tile, nst);
+            }
           }
+          if (!ok) break;
         }
-        if (!ok) break;
-        commit(&c->v_free[st]);
-        commit(&c->plan_free[j % kSlots]);   // both softmax tiles and the converters are past step j
-        if (more) commit(&c->k_free[nst]);
       }
       // nothing is in flight when the tensor memory goes back
       commit(&c->drain);
@@ -701,13 +793,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
 }
 
 template <int D>
-cudaError_t launch(const PaArgs& a, cudaStream_t s) {
+cudaError_t launch(const PaArgs& a, int num_sms, cudaStream_t s) {
   const cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(paged_attn_tc_kernel<D>), Tc<D>::kSmem);
   if (err != cudaSuccess) return err;
-  const int64_t places = static_cast<int64_t>(a.T) * a.group / kItemRows + a.B;
-  if (places > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const int64_t items = tc_places(a) * a.c.n_kv_heads;
   count_launches(1);
-  return launch_pdl(paged_attn_tc_kernel<D>, dim3(static_cast<unsigned>(places), a.c.n_kv_heads), kThreads,
+  return launch_pdl(paged_attn_tc_kernel<D>, static_cast<unsigned>(std::min<int64_t>(num_sms, items)), kThreads,
                     Tc<D>::kSmem, s, a);
 }
 
@@ -715,8 +806,8 @@ cudaError_t launch(const PaArgs& a, cudaStream_t s) {
 
 bool paged_attn_tc_supported(int D) { return D == 64 || D == 128; }
 
-cudaError_t launch_paged_attn_tc(const PaArgs& a, cudaStream_t s) {
-  return a.c.head_dim == 64 ? launch<64>(a, s) : launch<128>(a, s);
+cudaError_t launch_paged_attn_tc(const PaArgs& a, int num_sms, cudaStream_t s) {
+  return a.c.head_dim == 64 ? launch<64>(a, num_sms, s) : launch<128>(a, num_sms, s);
 }
 
 }  // namespace moe
