@@ -48,8 +48,8 @@ constexpr int kGroups = kTok / 16;       // scale groups of a step
 constexpr int kThreads = 20 * 32;
 // Registers of a thread, by warpgroup: two of softmax, two of conversion, one
 // that plans and issues.  The launch has 96 for each of the 640 threads;
-// 256 x 136 + 256 x 72 + 128 x 64 are the same 61440.
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kConvRegs = 72, kIssueRegs = 64;
+// 256 x 128 + 256 x 72 + 128 x 80 are the same 61440.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 128, kConvRegs = 72, kIssueRegs = 80;
 static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kIssueRegs <= 5 * kLaunchRegs, "setmaxnreg would wait forever");
 constexpr int kConvThreads = 128;
 constexpr int kSlots = 8;              // steps that are planned ahead, at most
