@@ -28,8 +28,9 @@ extern "C" {
 typedef struct {
   void* k;                   /* E4M3 codes of the keys, page 0                    */
   void* v;                   /* E4M3 codes of the values, same strides            */
-  float* k_scale;            /* [n_pages][n_kv_heads], positive and finite        */
-  float* v_scale;            /* [n_pages][n_kv_heads], likewise                   */
+  float* k_scale;            /* [n_pages][n_kv_heads], 2^-100 to 2^100            */
+  float* v_scale;            /* [n_pages][n_kv_heads], likewise, and those of     */
+                             /*   one request and head within 2^80 of each other  */
   const int32_t* page_table; /* [batch][max_pages]                                */
   int32_t n_pages;           /* pages in the cache, >= 1                          */
   int32_t page_size;         /* tokens in a page: 16, 32, 64 or 128               */

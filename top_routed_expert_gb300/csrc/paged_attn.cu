@@ -24,10 +24,12 @@
 //    consecutive codes of four tokens, and one byte permutation pairs two
 //    tokens' codes for the conversion;
 //  - the first product's result registers are the second's A operand.
-// The row maximum and sum are kept per warp and joined at the end.  Page
-// scales: a key's scale multiplies its score; a value's scale goes into the
-// exponent of its weight, with a running maximum of its own, so that the
-// weights rounded to f16 stay at most 1 whatever the scales are.
+// Sums and references are kept per warp and joined at the end.  Page scales: a
+// key's scale multiplies its score; a value's scale goes into the exponent of
+// its weight, and the weights' sum takes it out again.  A row's weights are
+// relative to the maximum of the first tile that it sees something in; that
+// reference moves only when weights grow over 2^15 (f16 holds 65504), so the
+// ordinary tile takes no maximum and rescales nothing.
 #include <climits>
 
 #include "paged_kv.cuh"
@@ -44,13 +46,15 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kRows = 16;
 constexpr int kUnit = 64;        // tokens of a unit
+constexpr int kJoinThreads = 512, kJoinRows = 4;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMostSum = 32768.0f;   // sum of a lane's four weights that moves the reference: f16 holds 65504
 
 template <int D> struct Shape {
   static constexpr int kTile = 16 * D;                  // bytes of 16 tokens' keys (or values)
   static constexpr int kStages = D == 256 ? 3 : 4;      // what lets two or three CTAs share an SM
   static constexpr int kRing = kStages * 2 * kTile;     // per warp
-  static constexpr int kPart = kRows * D + 3 * kRows;   // floats of a partial: sums, m, m', l
+  static constexpr int kPart = kRows * D + 2 * kRows;   // floats of a partial: outputs, references, sums
 };
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -63,8 +67,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // 16 bytes, or zeros when !valid (the source is not read then).
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
   constexpr int NT = D / 8;       // column tiles of the output
   constexpr int kStages = S::kStages;
   extern __shared__ __align__(128) char smem[];
-  __shared__ float s_m[kWarps][kRows], s_m2[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ float s_scale[kWarps][kStages][4];
   int64_t* s_start = reinterpret_cast<int64_t*>(smem + kWarps * S::kRing);
   pdl_enter();
@@ -212,11 +219,18 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
   if (a.tc_rows < INT_MAX && blockIdx.x == gridDim.x - 1) list_tc_items(a, reinterpret_cast<int*>(s_start), smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   build_unit_table<kRows, kUnit>(a, s_start, blockIdx.x == 0 ? a.status : nullptr);
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= a.B; i += kWarps * 32) a.starts[i] = s_start[i];
   const int64_t total = s_start[a.B];
   const int64_t piece = piece_of(total, gridDim.x);
   const int64_t first = piece * blockIdx.x, last = min(total, first + piece);
   const uint32_t ring = ptx::smem_u32(smem) + warp * S::kRing;
-  const int ps = a.c.page_size;
+  const int ps = a.c.page_size, ps_log = 31 - __clz(ps);
+  const int64_t ts = a.c.token_stride;
+  // this lane's 16-byte chunks of a tile: token (+ RSTEP each) and chunk
+  constexpr int CPR = D / 16, RSTEP = 32 / CPR, COPIES = 16 / RSTEP;
+  const int crow = lane / CPR, cchunk = lane % CPR;
+  const int64_t lane_off = crow * ts + cchunk * 16;
 
   for (int64_t at = first; at < last;) {
     // the row tile at `at`, and the piece of it that is this CTA's
@@ -225,47 +239,56 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
     const Span sp = span_of(a, rq, kUnit);
     const int64_t in_b = at - s_start[b];
     const int tile = static_cast<int>(in_b / sp.units);      // (key head, row tile)
-    const int u0 = static_cast<int>(in_b % sp.units);
+    const int u0 = static_cast<int>(in_b - static_cast<int64_t>(tile) * sp.units);
     const int u1 = static_cast<int>(min(static_cast<int64_t>(sp.units), u0 + (last - at)));
     const int rts = ceil_div(rq.n * a.group, kRows);
-    const int kvh = tile / rts, row0 = tile % rts * kRows;
+    const int kvh = tile / rts, row0 = (tile - kvh * rts) * kRows;
     const int rows = min(kRows, rq.n * a.group - row0);
     const bool whole = u0 == 0 && u1 == sp.units;
     const int slot = at == first ? 0 : 1;
     at += u1 - u0;
 
     const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + kvh * a.c.head_stride;
-    const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v) + kvh * a.c.head_stride;
+    const int64_t v_minus_k = static_cast<const uint8_t*>(a.c.v) - static_cast<const uint8_t*>(a.c.k);
     const int32_t* table = a.c.page_table + static_cast<int64_t>(b) * a.c.max_pages;
     auto tile_base = [&](int u) { return sp.block_of(u) * kUnit + warp * 16; };
+    // Page ids are asked for a tile ahead of the copies and looked at there.
+    constexpr int kNothing = INT_MIN;
     auto page_id = [&](int u) -> int {
       const int j = tile_base(u);
-      if (u >= u1 || !sp.any_seen(j, j + 15)) return -2;      // nothing to fetch
-      const int p = j / ps;
-      return p < a.c.max_pages ? table[p] : -1;
+      return u < u1 && sp.any_seen(j, j + 15) ? __ldg(table + (j >> ps_log)) : kNothing;
     };
     auto issue = [&](int u, int pid, int stage) {
-      const uint32_t kd = ring + stage * 2 * S::kTile, vd = kd + S::kTile;
-      float* sc = s_scale[warp][stage];
-      if (pid == -2) return;
+      if (pid == kNothing) return;
       const int j0 = tile_base(u);
-      const bool ok = pid >= 0 && pid < a.c.n_pages;
-      if (!ok && lane == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      float* sc = s_scale[warp][stage];
+      const bool ok = static_cast<unsigned>(pid) < static_cast<unsigned>(a.c.n_pages);
       if (lane == 0) sc[2] = ok ? 1.f : 0.f;
-      const int64_t page = ok ? pid : 0;
-      if (lane < 2) {
-        const float* src = (lane ? a.c.v_scale : a.c.k_scale) + page * a.c.n_kv_heads + kvh;
-        cp4(ptx::smem_u32(sc + lane), src);
+      if (!ok) {
+        if (lane == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+        return;
       }
-      const int64_t off = page * a.c.page_stride + (j0 % ps) * a.c.token_stride;
-      constexpr int CPR = D / 16;   // chunks of a token
+      if (lane < 2)
+        cp4(ptx::smem_u32(sc + lane), (lane ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(pid) * a.c.n_kv_heads + kvh);
+      const uint8_t* src = kbase + (pid * a.c.page_stride + (j0 & (ps - 1)) * ts + lane_off);
+      const uint32_t kd = ring + stage * 2 * S::kTile, vd = kd + S::kTile;
+      if (sp.all_seen(j0, j0 + 15)) {
 #pragma unroll
-      for (int i = 0; i < 16 * CPR / 32; ++i) {
-        const int c = i * 32 + lane, row = c / CPR, chunk = c % CPR;
-        const bool valid = ok && sp.seen(j0 + row);
-        const int64_t o = off + row * a.c.token_stride + chunk * 16;
-        cp16(kd + chunk_at<D>(row, chunk), valid ? kbase + o : kbase, valid);
-        cp16(vd + chunk_at<D>(row, chunk), valid ? vbase + o : vbase, valid);
+        for (int i = 0; i < COPIES; ++i) {
+          const uint32_t d = chunk_at<D>(i * RSTEP + crow, cchunk);
+          cp16(kd + d, src);
+          cp16(vd + d, src + v_minus_k);
+          src += RSTEP * ts;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const uint32_t d = chunk_at<D>(i * RSTEP + crow, cchunk);
+          const bool seen = sp.seen(j0 + i * RSTEP + crow);
+          cp16_or_zero(kd + d, seen ? src : kbase, seen);
+          cp16_or_zero(vd + d, seen ? src + v_minus_k : kbase, seen);
+          src += RSTEP * ts;
+        }
       }
     };
 
@@ -290,25 +313,19 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
       pos[h] = live ? rq.start + tok : -1;
       const uint16_t* src = a.q + static_cast<int64_t>(rq.row0 + tok) * a.qs + static_cast<int64_t>(head) * D;
       uint4 raw[KC][2];
-      float amax = 0.f;
-      bool fin = true;
+      uint32_t top = 0;   // the largest size as bits: a NaN's are above infinity's
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          raw[c][i] = live ? *reinterpret_cast<const uint4*>(src + c * 64 + t * 16 + i * 8) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {raw[c][i].x, raw[c][i].y, raw[c][i].z, raw[c][i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-            fin = fin && lo < INFINITY && hi < INFINITY;
-            amax = fmaxf(amax, fmaxf(lo, hi));
-          }
+          raw[c][i] = live ? __ldg(reinterpret_cast<const uint4*>(src + c * 64 + t * 16 + i * 8)) : make_uint4(0, 0, 0, 0);
+          top = __vmaxu2(top, __vmaxu2(raw[c][i].x & 0x7fff7fffu, raw[c][i].y & 0x7fff7fffu));
+          top = __vmaxu2(top, __vmaxu2(raw[c][i].z & 0x7fff7fffu, raw[c][i].w & 0x7fff7fffu));
         }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      fin = ((__ballot_sync(0xffffffffu, fin) >> (lane & ~3)) & 0xfu) == 0xfu;
-      const float f = q_factor(amax, fin);
+      top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float f = q_factor(__uint_as_float(top << 16), top < 0x7f80u);
       rf[h] = a.sm_scale * kLog2e / f;
 #pragma unroll
       for (int c = 0; c < KC; ++c)
@@ -322,16 +339,18 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
         }
     }
     const int pos_min = rq.start + row0 / a.group, pos_max = rq.start + (row0 + rows - 1) / a.group;
+    const bool low_only = rows <= 8;   // rows 8..15 are not there
 
     float o[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, m2[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // a row that sees nothing at all needs no reference
+    float m[2] = {pos[0] >= 0 ? -INFINITY : 0.f, pos[1] >= 0 ? -INFINITY : 0.f}, l[2] = {0.f, 0.f};
 
-    for (int u = u0; u < u1; ++u) {
-      const int stage = (u - u0) % kStages;
+#pragma unroll 1
+    for (int u = u0, stage = 0; u < u1; ++u, stage = stage + 1 == kStages ? 0 : stage + 1) {
       cp_wait<kStages - 2>();
       __syncwarp();
       const int j0 = tile_base(u);
@@ -350,52 +369,56 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
             for (int e = 0; e < 4; ++e) mma16816(s[j], qf[c][e], f16x2_of(w[e]), f16x2_of_hi(w[e]));
           }
         }
-        const float ks = sc[0], lvs = log2f(sc[1]);
-        const bool full = sp.all_see(j0, j0 + 15, pos_min, pos_max);
-        float top[2] = {-INFINITY, -INFINITY};
+        const float ks = sc[0], lvs = __log2f(sc[1]), ivs = __frcp_rn(sc[1]);
+        if (!sp.all_see(j0, j0 + 15, pos_min, pos_max)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int h = e >> 1;
-            s[j][e] *= ks * rf[h];
-            if (!full && !sp.sees(pos[h], j0 + token_of(j, 2 * t + (e & 1)))) s[j][e] = -INFINITY;
-            top[h] = fmaxf(top[h], s[j][e]);
-          }
-        bool grew = false;
-        float drop[2] = {1.f, 1.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-          if (top[h] > m[h]) {
-            l[h] *= ex2(m[h] - top[h]);
-            m[h] = top[h];
-          }
-          const float top2 = top[h] + lvs;
-          if (top2 > m2[h]) {
-            drop[h] = ex2(m2[h] - top2);
-            m2[h] = top2;
-            grew = true;
-          }
+            for (int e = 0; e < 4; ++e)
+              if (!sp.sees(pos[e >> 1], j0 + token_of(j, 2 * t + (e & 1)))) s[j][e] = -INFINITY;
         }
-        if (__any_sync(0xffffffffu, grew)) {
+        // weights relative to the reference so far; a sum too large for f16, or
+        // a row without a reference, takes the row's maximum first
+        float e[2][4], sum[2];
+        auto weigh = [&](int h) {
+          const float f = score_factor(ks, rf[h]), shift = lvs - (m[h] == -INFINITY ? 0.f : m[h]);
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+          for (int j = 0; j < 2; ++j) {
+            e[j][2 * h] = ex2(fmaf(s[j][2 * h], f, shift));
+            e[j][2 * h + 1] = ex2(fmaf(s[j][2 * h + 1], f, shift));
+          }
+          sum[h] = (e[0][2 * h] + e[0][2 * h + 1]) + (e[1][2 * h] + e[1][2 * h + 1]);
+        };
+        weigh(0);
+        if (low_only) {
+          sum[1] = e[0][2] = e[0][3] = e[1][2] = e[1][3] = 0.f;
+        } else {
+          weigh(1);
+        }
+        if (__any_sync(0xffffffffu, m[0] == -INFINITY || m[1] == -INFINITY || sum[0] > kMostSum || sum[1] > kMostSum)) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] *= drop[e >> 1];
+          for (int h = 0; h < 2; ++h) {
+            float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+            top = fmaf(top, score_factor(ks, rf[h]), lvs);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float to = fmaxf(m[h], top), f = m[h] == -INFINITY ? 0.f : ex2(m[h] - to);
+            m[h] = to;
+            l[h] *= f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              o[i][2 * h] *= f;
+              o[i][2 * h + 1] *= f;
+            }
+            weigh(h);
+          }
         }
         uint32_t p[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float ms = m[h] == -INFINITY ? 0.f : m[h];
-          const float shift = m2[h] == -INFINITY ? -INFINITY : lvs - m2[h];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float s0 = s[j][2 * h], s1 = s[j][2 * h + 1];
-            l[h] += ex2(s0 - ms) + ex2(s1 - ms);
-            p[2 * j + h] = pack_f16(ex2(s0 + shift), ex2(s1 + shift));
-          }
+          l[h] = fmaf(sum[h], ivs, l[h]);
+          p[h] = pack_f16(e[0][2 * h], e[0][2 * h + 1]);
+          p[2 + h] = pack_f16(e[1][2 * h], e[1][2 * h + 1]);
         }
         // values: words of tokens t, t+4 | t+8, t+12
         constexpr int VW = D >= 128 ? 4 : 2;     // words of a lane's run of codes
@@ -430,7 +453,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
       }
       __syncwarp();
       const int next = page_id(u + kStages);
-      issue(u + kStages - 1, pid, (stage + kStages - 1) % kStages);
+      issue(u + kStages - 1, pid, stage == 0 ? kStages - 1 : stage - 1);
       cp_commit();
       pid = next;
     }
@@ -444,7 +467,6 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       if (t == 0) {
         s_m[warp][g + 8 * h] = m[h];
-        s_m2[warp][g + 8 * h] = m2[h];
         s_l[warp][g + 8 * h] = l[h];
       }
     }
@@ -453,29 +475,28 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
     constexpr int RUN = D >= 128 ? 16 : 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
+      if (h == 0 || !low_only) {
 #pragma unroll
-      for (int i = 0; i < NT; i += 4)
+        for (int i = 0; i < NT; i += 4)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int col = i / 16 * 128 + RUN * (2 * t + e) + i % 16;
-          *reinterpret_cast<float4*>(mine + (g + 8 * h) * D + (D == 64 ? RUN * (2 * t + e) + i : col)) =
-              make_float4(o[i][2 * h + e], o[i + 1][2 * h + e], o[i + 2][2 * h + e], o[i + 3][2 * h + e]);
-        }
+          for (int e = 0; e < 2; ++e) {
+            const int col = D == 64 ? RUN * (2 * t + e) + i : i / 16 * 128 + RUN * (2 * t + e) + i % 16;
+            *reinterpret_cast<float4*>(mine + (g + 8 * h) * D + col) =
+                make_float4(o[i][2 * h + e], o[i + 1][2 * h + e], o[i + 2][2 * h + e], o[i + 3][2 * h + e]);
+          }
+      }
     __syncthreads();
     for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
-      float mm = -INFINITY, mm2 = -INFINITY;
+      float mm = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        mm = fmaxf(mm, s_m[w][r]);
-        mm2 = fmaxf(mm2, s_m2[w][r]);
-      }
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
       float sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        sum += s_l[w][r] * ex2_from(s_m[w][r], mm);
-        const float f = ex2_from(s_m2[w][r], mm2);
+        const float f = ex2_from(s_m[w][r], mm);
+        sum += s_l[w][r] * f;
         const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + w * (S::kRing / 4) + r * D + d);
         acc.x += x.x * f;
         acc.y += x.y * f;
@@ -484,14 +505,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
       }
       if (whole) {
         const int tok = (row0 + r) / a.group, head = kvh * a.group + (row0 + r) % a.group;
-        store_row4(a, rq.row0 + tok, head, D, d, acc, mm, mm2, sum);
+        store_row4(a, rq.row0 + tok, head, D, d, acc, mm, sum);
       } else {
         float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::kPart;
         *reinterpret_cast<float4*>(part + r * D + d) = acc;
         if (d == 0) {
           part[kRows * D + r] = mm;
-          part[kRows * D + kRows + r] = mm2;
-          part[kRows * D + 2 * kRows + r] = sum;
+          part[kRows * D + kRows + r] = sum;
         }
       }
     }
@@ -499,91 +519,77 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
   }
 }
 
-// Joins the partial sums of the row tiles that more than one CTA worked on.
-// One block per key head, place of a row tile and row (all rows beside the
-// tcgen05 kernel, where few requests or none are left for it); the places of a ragged
-// batch are found as moe_kv_append finds its pages: request b's row tiles
-// start at cu[b] group / 16 + b; where a request has at most rt_max of them
-// (rt_max > 0) they start at b rt_max.
+// Joins the partial sums of the row tiles that more than one CTA worked on: a
+// block for the end of each CTA's piece (but the last) and each group of rows.
+// A tile with several ends inside belongs to the first of them.
 template <int D>
-__global__ void __launch_bounds__(128) paged_attn_join(PaArgs a, int n_ctas, int rt_max) {
+__global__ void __launch_bounds__(kJoinThreads) paged_attn_join(PaArgs a, int n_ctas) {
   using S = Shape<D>;
-  __shared__ int64_t s_red[2][4];
-  __shared__ float s_acc[4][D], s_st[4][3];
+  constexpr int LANES = D / 4;                          // threads of a row, four columns each
+  constexpr int SHARES = kJoinThreads / (kJoinRows * LANES);   // threads that share a row's parts
+  __shared__ float4 s_acc[SHARES][kJoinRows][LANES];
+  __shared__ float s_sum[SHARES][kJoinRows];
+  __shared__ int s_b;
   pdl_enter();
-  const int kvh = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = rt_max ? blockIdx.x / rt_max : warp_find_request(a.cu, a.B, blockIdx.x, a.group, kRows, 1);
-  const Request rq = load_request(a.cu, a.kv_len, b, a.T);
-  const int rt = rt_max ? blockIdx.x % rt_max
-                        : blockIdx.x - static_cast<int>(static_cast<int64_t>(rq.row0) * a.group / kRows + b);
-  const int rts = ceil_div(rq.n * a.group, kRows);
-  if (!rq.ok || rq.n * a.group > a.tc_rows || rt < 0 || rt >= rts) return;
-  const int rows = min(kRows, rq.n * a.group - rt * kRows);
-  // units before request b, and in all
-  int64_t before = 0, total = 0;
-  for (int i = threadIdx.x; i < a.B; i += blockDim.x) {
-    const Request x = load_request(a.cu, a.kv_len, i, a.T);
-    const int64_t n = units_of(a, x, kRows, kUnit);
-    total += n;
-    before += i < b ? n : 0;
-  }
-  for (int off = 16; off > 0; off >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, off);
-    total += __shfl_xor_sync(0xffffffffu, total, off);
-  }
-  if (lane == 0) {
-    s_red[0][warp] = before;
-    s_red[1][warp] = total;
-  }
+  const int64_t total = a.starts[a.B], piece = piece_of(total, n_ctas);
+  const int64_t end = piece * (blockIdx.x + 1);         // the piece's end: this CTA's last unit is end - 1
+  if (end >= total) return;
+  // the request that unit end - 1 belongs to
+  for (int i = threadIdx.x; i < a.B; i += kJoinThreads)
+    if (a.starts[i] <= end - 1 && end - 1 < a.starts[i + 1]) s_b = i;
   __syncthreads();
-  before = s_red[0][0] + s_red[0][1] + s_red[0][2] + s_red[0][3];
-  total = s_red[1][0] + s_red[1][1] + s_red[1][2] + s_red[1][3];
-  const int64_t piece = piece_of(total, n_ctas);
+  const int b = s_b;
+  const Request rq = load_request(a.cu, a.kv_len, b, a.T);
   const int units = span_of(a, rq, kUnit).units;
-  const int64_t start = before + (static_cast<int64_t>(kvh) * rts + rt) * units, end = start + units;
-  const int c0 = static_cast<int>(start / piece), c1 = static_cast<int>((end - 1) / piece);
-  if (c0 == c1) return;   // one CTA did all of it
+  const int64_t base = a.starts[b];
+  const int64_t tile = (end - 1 - base) / units, begin = base + tile * units, stop = begin + units;
+  // not split here, or an earlier end inside it has it
+  if (stop == end || (begin < end - piece && blockIdx.x > 0)) return;
+  const int rts = ceil_div(rq.n * a.group, kRows);
+  const int kvh = static_cast<int>(tile / rts), row0 = static_cast<int>(tile - static_cast<int64_t>(kvh) * rts) * kRows;
+  const int rows = min(kRows, rq.n * a.group - row0);
+  const int c0 = blockIdx.x, c1 = static_cast<int>((stop - 1) / piece);
+  const int lane = threadIdx.x % LANES, rl = threadIdx.x / LANES % kJoinRows, share = threadIdx.x / (LANES * kJoinRows);
+  const int r = blockIdx.y * kJoinRows + rl;
+  if (blockIdx.y * kJoinRows >= rows) return;
   auto part_of = [&](int c) {
-    const int slot = (c == c0 && start != c0 * piece) ? 1 : 0;
+    const int slot = (c == c0 && begin != c0 * piece) ? 1 : 0;
     return a.part + (static_cast<int64_t>(c) * 2 + slot) * S::kPart;
   };
-  for (int r = blockIdx.z; r < rows; r += gridDim.z) {
-    float m = -INFINITY, m2 = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
-      const float* p = part_of(c) + kRows * D + r;
-      m = fmaxf(m, p[0]);
-      m2 = fmaxf(m2, p[kRows]);
-    }
-    float sum = 0.f;
-    constexpr int PER = D / 32;   // columns of a lane
-    float acc[PER] = {};
-    for (int c = c0 + warp; c <= c1; c += 4) {
+  float m = -INFINITY;
+  if (r < rows)
+    for (int c = c0; c <= c1; ++c) m = fmaxf(m, part_of(c)[kRows * D + r]);
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < rows)
+#pragma unroll 4
+    for (int c = c0 + share; c <= c1; c += SHARES) {
       const float* p = part_of(c);
-      sum += p[kRows * D + 2 * kRows + r] * ex2_from(p[kRows * D + r], m);
-      const float f = ex2_from(p[kRows * D + kRows + r], m2);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] += p[r * D + lane + 32 * i] * f;
+      const float f = ex2_from(p[kRows * D + r], m);
+      const float4 x = *reinterpret_cast<const float4*>(p + r * D + lane * 4);
+      sum += p[kRows * D + kRows + r] * f;
+      acc.x += x.x * f;
+      acc.y += x.y * f;
+      acc.z += x.z * f;
+      acc.w += x.w * f;
     }
+  s_acc[share][rl][lane] = acc;
+  if (lane == 0) s_sum[share][rl] = sum;
+  __syncthreads();
+  if (share > 0 || r >= rows) return;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) s_acc[warp][lane + 32 * i] = acc[i];
-    if (lane == 0) s_st[warp][0] = sum;
-    __syncthreads();
-    sum = s_st[0][0] + s_st[1][0] + s_st[2][0] + s_st[3][0];
-    const int row = rt * kRows + r, tok = row / a.group, head = kvh * a.group + row % a.group;
-    const int d = threadIdx.x * 4;
-    if (d < D) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        x.x += s_acc[w][d];
-        x.y += s_acc[w][d + 1];
-        x.z += s_acc[w][d + 2];
-        x.w += s_acc[w][d + 3];
-      }
-      store_row4(a, rq.row0 + tok, head, D, d, x, m, m2, sum);
-    }
-    __syncthreads();
+  for (int i = 1; i < SHARES; ++i) {
+    const float4 x = s_acc[i][rl][lane];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
   }
+  sum = s_sum[0][rl];
+#pragma unroll
+  for (int i = 1; i < SHARES; ++i) sum += s_sum[i][rl];
+  const int tok = (row0 + r) / a.group, head = kvh * a.group + (row0 + r) % a.group;
+  store_row4(a, rq.row0 + tok, head, D, lane * 4, acc, m, sum);
 }
 
 // Persistent CTAs: what the SMs hold at once (registers and ring).  The
@@ -601,17 +607,13 @@ cudaError_t launch(const PaArgs& a, int num_sms, cudaStream_t s) {
   count_launches(2);
   err = launch_pdl(paged_attn_kernel<D>, ctas, kWarps * 32, smem, s, a);
   if (err != cudaSuccess) return err;
-  const int rt_max = a.tc_rows < INT_MAX ? ceil_div(a.tc_rows, kRows) : 0;
-  const int64_t places = rt_max ? static_cast<int64_t>(rt_max) * a.B : static_cast<int64_t>(a.T) * a.group / kRows + a.B;
-  if (places > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_pdl(paged_attn_join<D>, dim3(static_cast<unsigned>(places), a.c.n_kv_heads, rt_max ? 1 : kRows),
-                    128, 0, s, a, ctas, rt_max);
+  return launch_pdl(paged_attn_join<D>, dim3(std::max(1, ctas - 1), kRows / kJoinRows), kJoinThreads, 0, s, a, ctas);
 }
 
 }  // namespace
 
 size_t paged_attn_ws_bytes(int D) {
-  const size_t part = (static_cast<size_t>(kRows) * D + 3 * kRows) * sizeof(float);
+  const size_t part = (static_cast<size_t>(kRows) * D + 2 * kRows) * sizeof(float);
   return static_cast<size_t>(ctas_for(D, kMaxSms)) * 2 * part;
 }
 
@@ -632,6 +634,19 @@ cudaError_t launch_paged_attn(PaArgs a, int max_q_len, int num_sms, cudaStream_t
 }
 
 namespace {
+
+// Workspace: partial sums, the requests' first units, the list of row blocks.
+struct Workspace {
+  size_t starts, tc_list, total;
+};
+
+Workspace plan_workspace(const PaArgs& a, int D) {
+  Workspace w;
+  w.starts = align_up(paged_attn_ws_bytes(D), 256);
+  w.tc_list = w.starts + align_up((a.B + 1) * sizeof(int64_t), 256);
+  w.total = w.tc_list + align_up((tc_places(a) + 1) * sizeof(int2), 256);
+  return w;
+}
 
 bool attention_config_ok(const moe_paged_attention_config_t* c, const moe_kv_cache_t* cache) {
   if (!c || !kv_cache_shape_ok(cache)) return false;
@@ -655,7 +670,7 @@ extern "C" size_t moe_paged_attention_ws_bytes(const moe_paged_attention_config_
   a.T = cfg->T;
   a.B = cfg->batch;
   a.group = cfg->n_q_heads / cache->n_kv_heads;
-  return align_up(paged_attn_ws_bytes(cache->head_dim), 256) + align_up((tc_places(a) + 1) * sizeof(int2), 256);
+  return plan_workspace(a, cache->head_dim).total;
 }
 
 extern "C" moe_status_t moe_paged_attention(const moe_paged_attention_config_t* cfg, const moe_kv_cache_t* cache,
@@ -680,8 +695,6 @@ extern "C" moe_status_t moe_paged_attention(const moe_paged_attention_config_t* 
   a.lse = lse;
   a.cu = cu;
   a.kv_len = kv_len;
-  a.part = static_cast<float*>(ws);
-  a.tc_list = reinterpret_cast<int2*>(static_cast<char*>(ws) + align_up(paged_attn_ws_bytes(cache->head_dim), 256));
   a.c = *cache;
   a.status = status;
   a.qs = cfg->q_stride;
@@ -692,5 +705,9 @@ extern "C" moe_status_t moe_paged_attention(const moe_paged_attention_config_t* 
   a.window = cfg->window;
   a.n_sink = cfg->n_sink;
   a.sm_scale = cfg->sm_scale;
+  const Workspace w = plan_workspace(a, cache->head_dim);
+  a.part = static_cast<float*>(ws);
+  a.starts = reinterpret_cast<int64_t*>(static_cast<char*>(ws) + w.starts);
+  a.tc_list = reinterpret_cast<int2*>(static_cast<char*>(ws) + w.tc_list);
   return launch_paged_attn(a, cfg->max_q_len, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

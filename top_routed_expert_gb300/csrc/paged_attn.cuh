@@ -12,8 +12,9 @@ struct PaArgs {
   float* lse;
   const int32_t* cu;
   const int32_t* kv_len;
-  float* part;          // workspace: partial sums ...
-  int2* tc_list;        // ... and the row blocks for paged_attn_tc.cu: [0].x of them, (request, block) from [1] on
+  float* part;          // workspace: partial sums,
+  int64_t* starts;      // the first unit of each request, their total,
+  int2* tc_list;        // and the row blocks for paged_attn_tc.cu: [0].x of them, (request, block) from [1] on
   moe_kv_cache_t c;
   unsigned* status;
   int64_t qs, os;
@@ -39,6 +40,8 @@ struct Span {
   __device__ __forceinline__ bool seen(int j) const { return j < end && (j >= lo || j < n_sink); }
   // ... and any position of [j0, j1]
   __device__ __forceinline__ bool any_seen(int j0, int j1) const { return j0 < end && (j1 >= lo || j0 < n_sink); }
+  // ... and all of them
+  __device__ __forceinline__ bool all_seen(int j0, int j1) const { return j1 < end && (j0 >= lo || j1 < n_sink); }
   // the row at position p
   __device__ __forceinline__ bool sees(int p, int j) const {
     return j <= p && (window == 0 || j > p - window || j < n_sink);
@@ -126,6 +129,10 @@ __device__ __forceinline__ int64_t piece_of(int64_t total, int ctas) {
 // 2^(m - top) for the join of partial maxima; m = -infinity: an empty part.
 __device__ __forceinline__ float ex2_from(float m, float top) { return m == -INFINITY ? 0.f : exp2f(m - top); }
 
+// A key scale times a row's factor, kept above 0: a masked score is -infinity
+// and has to stay so (a product that small leaves no score to speak of).
+__device__ __forceinline__ float score_factor(float k_scale, float rf) { return fmaxf(k_scale * rf, 1e-37f); }
+
 // Factor that brings a head's largest |q| into [2^14, 2^15), a power of two;
 // NaN when the head holds a non-finite element (its row becomes NaN).
 __device__ __forceinline__ float q_factor(float amax, bool finite) {
@@ -136,12 +143,12 @@ __device__ __forceinline__ float q_factor(float amax, bool finite) {
   return __uint_as_float(static_cast<uint32_t>(f + 127) << 23);
 }
 
-// Four columns of a finished row: sums acc relative to 2^m2, weights' sum
-// relative to 2^m (both in powers of two of the scaled scores).
+// Four columns of a finished row: outputs `acc` and the weights' sum, both
+// relative to 2^m.
 __device__ __forceinline__ void store_row4(const PaArgs& a, int row, int head, int D, int d, const float4& acc, float m,
-                                           float m2, float sum) {
+                                           float sum) {
   const bool empty = sum == 0.f;   // nothing visible (a NaN sum is not)
-  const float f = empty ? 0.f : exp2f(m2 - m) / sum;
+  const float f = empty ? 0.f : 1.0f / sum;
   const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * f, acc.y * f), y = __floats2bfloat162_rn(acc.z * f, acc.w * f);
   *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(row) * a.os + static_cast<int64_t>(head) * D + d) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));

@@ -21,9 +21,8 @@
 // byte permutations before the conversion, so both products read K-major
 // operands.  Page scales stay out of the products: a score is multiplied by
 // its 16-token group's key scale, and the value scale is added to the
-// exponent (its logarithm, relative to the first page's), so that P V needs
-// no scaling and the sum of the weights is the group sums divided by the same
-// scale.
+// exponent (its logarithm), so that P V needs no scaling and the sum of the
+// weights is the group sums divided by the same scale.
 //
 // A row's weights are taken relative to the maximum of the first step that it
 // sees something in, and that reference moves only when a group of 16 weights
@@ -63,7 +62,6 @@ constexpr uint64_t kDrainNs = 200000000ull;
 // there is no more.
 struct Item {
   int b, kvh, token0, n, end, row0, rows;   // token0, n, end: the request's rows and length
-  float lref;                               // log2 of the reference value scale
   __device__ __forceinline__ Span span(const PaArgs& a) const {
     const int start = end - n;
     return span_for(a, start + row0 / a.group, start + (row0 + rows - 1) / a.group, kTok);
@@ -80,7 +78,7 @@ struct Ctrl {
   uint64_t q_full, k_full[2], v_full[2], s_full[2][2], p_full[2], o_full[2], plan_full[kSlots], plan_free[kSlots],
       item_full[kItems], drain;
   // of a step's eight 16-token groups: key scale, log2 of the value scale, 1 /
-  // value scale (both relative to lref); byte offset in the cache, -1: none
+  // value scale; byte offset in the cache, -1: none
   float4 scale[kSlots][kGroups];
   int64_t place[kSlots][kGroups];
   Item item[kItems];
@@ -225,7 +223,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // goes into the largest so far and, divided by the value scale, to `l`.
 __device__ __forceinline__ float weigh(const float (&x)[16], const float4& s, float rf, float m, float* p, float& most,
                                        float l) {
-  const float f = s.x * rf, shift = s.y - m;
+  const float f = score_factor(s.x, rf), shift = s.y - m;
   const uint64_t f2 = pair(f, f), shift2 = pair(shift, shift);
   uint64_t sum = 0;
 #pragma unroll
@@ -439,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
 #pragma unroll
                 for (int i = 2; i < 16; i += 2) u = fmaxf(u, fmaxf(v[16 * h + i], v[16 * h + i + 1]));
                 const float4 s = sc[q / 16 + h];
-                top = fmaxf(top, fmaf(u, s.x * rf, s.y));
+                top = fmaxf(top, fmaf(u, score_factor(s.x, rf), s.y));
               }
             }
             const float to = fmaxf(m, top), f = m == -INFINITY ? 0.f : ex2(m - to);
@@ -492,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       if (!ok) break;
       tc_fence_after();
       const bool empty = l == 0.f;   // nothing visible (a NaN sum is not)
-      const float f = empty ? 0.f : exp2f(it.lref) / l;
+      const float f = empty ? 0.f : 1.0f / l;
       const int head = it.kvh * a.group + r % a.group, token = it.token0 + r / a.group;
       uint16_t* dst = a.out + static_cast<int64_t>(token) * a.os + static_cast<int64_t>(head) * D;
 #pragma unroll 1
@@ -673,7 +671,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         if (it.rows == 0) break;
         const Span sp = it.span(a);
         const int32_t* table = a.c.page_table + static_cast<int64_t>(it.b) * a.c.max_pages;
-        float lref = 0.f;
 #pragma unroll 1
         for (int jb = 0; ok && jb < sp.units; jb += 4) {
           const int j = jb + (lane >> 3), s = g + j, slot = s % kSlots;
@@ -682,16 +679,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
           const int gp = mine && sp.any_seen(x, x + 15) ? __ldg(table + (x >> ps_log)) : kNotSeen;
           const bool have = static_cast<unsigned>(gp) < static_cast<unsigned>(a.c.n_pages);
           if (!have && gp != kNotSeen) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-          float ks = 0.f, lvs = 0.f;
+          float ks = 0.f, vs = 1.f;
           if (have) {
             const int64_t sa = static_cast<int64_t>(gp) * a.c.n_kv_heads + it.kvh;
             ks = __ldg(a.c.k_scale + sa);
-            lvs = log2f(__ldg(a.c.v_scale + sa));
-          }
-          if (jb == 0) {
-            const unsigned any = __ballot_sync(0xffffffffu, have);
-            lref = __shfl_sync(0xffffffffu, lvs, any ? __ffs(any) - 1 : 0);
-            if (lane == 0) c->item[k % kItems].lref = lref;
+            vs = __ldg(a.c.v_scale + sa);
           }
           if (mine && s >= kSlots) ok = wait_phase(&c->plan_free[slot], ((s / kSlots) - 1) & 1, abort);
           ok = __all_sync(0xffffffffu, ok);
@@ -699,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
             // a group without a page masks itself
             c->place[slot][grp] = have ? gp * a.c.page_stride + (x & (ps - 1)) * a.c.token_stride : -1;
             c->scale[slot][grp] =
-                have ? make_float4(ks, lvs - lref, exp2f(lref - lvs), 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
+                have ? make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
             mbar_arrive(smem_u32(&c->plan_full[slot]));
           }
         }
