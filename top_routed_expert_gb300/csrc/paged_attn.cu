@@ -4,26 +4,29 @@
 // not take.
 //
 // The rows of one (request, key head) are its new tokens times the query
-// heads of the group, row r = token r / group, head r % group; 16 rows make a
-// row tile.  The work of a row tile is cut into units of 64 cached tokens.
+// heads of the group, row r = token r / group, head r % group; 8 or 16 rows make
+// a row tile.  The work of a row tile is cut into units of 64 cached tokens.
 // All units of the call stand in one line (request, key head, row tile,
 // token), and the persistent CTAs take equal pieces of that line, so a batch
 // of mixed lengths keeps every SM busy to the end.  A piece may end inside a
-// row tile; then both CTAs leave partial sums and paged_attn_join adds them in
-// order (a fixed order: the same bits every time).
+// row tile; then all its CTAs leave partial sums and paged_attn_join adds them
+// in order (a fixed order: the same bits every time).
 //
 // A CTA has four warps; in a unit each has 16 tokens of its own, fetched by
 // cp.async into a ring that only this warp uses (no block barrier in the
-// loop).  Both products run on the tensor cores as m16n8k16 with f16 operands:
-// the 16 rows are M, so the codes, converted exactly to f16 in registers, are
-// the B operand of both, loaded straight from the stored rows:
-//  - the order of the head's elements inside a product's K is free if q uses
-//    the same: a lane takes 16 consecutive codes of a key and calls them its
-//    elements of four K steps;
-//  - so is the order of the tokens in the second product: a lane takes 16
+// loop).  Both products run on the tensor cores as m16n8k16 with f16 operands
+// and the rows as N, so that the eight heads of a group fill it:
+//   S^T = K Q^T (M = 16 tokens),  O^T = V^T P^T (M = 16 elements of the head)
+// The codes are the A operands, converted exactly to f16 in registers, straight
+// from the stored rows:
+//  - the order of the head's elements inside the first product's K is free if q
+//    uses the same: a lane takes 16 consecutive codes of a key and calls them
+//    its elements of four K steps;
+//  - so is the order of the elements in the second product's M: a lane takes 16
 //    consecutive codes of four tokens, and one byte permutation pairs two
 //    tokens' codes for the conversion;
-//  - the first product's result registers are the second's A operand.
+//  - the weights become the second product's B operand by a transposition of
+//    8x8 blocks between the lanes.
 // Sums and references are kept per warp and joined at the end.  Page scales: a
 // key's scale multiplies its score; a value's scale goes into the exponent of
 // its weight, and the weights' sum takes it out again.  A row's weights are
@@ -44,15 +47,21 @@ cudaError_t launch_paged_attn_tc(const PaArgs& a, int num_sms, cudaStream_t s);
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kRows = 16;
 constexpr int kUnit = 64;        // tokens of a unit
-constexpr int kJoinThreads = 512, kJoinRows = 4;
+// What a row tile costs beside its units (finding it, q, the join of the
+// warps), in units.
+constexpr int kTileCost = 4;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMostSum = 32768.0f;   // sum of a lane's four weights that moves the reference: f16 holds 65504
+constexpr float kMostSum = 32768.0f;   // sum of a lane's two weights that moves the reference: f16 holds 65504
 
-template <int D> struct Shape {
+// D: elements of a head, NB: blocks of eight rows in a row tile.
+template <int D, int NB> struct Shape {
+  static constexpr int kRows = 8 * NB;
   static constexpr int kTile = 16 * D;                  // bytes of 16 tokens' keys (or values)
-  static constexpr int kStages = D == 256 ? 3 : 4;      // what lets two or three CTAs share an SM
+  // CTAs on an SM, by registers (O takes D NB / 4 of a thread's, q D NB / 8),
+  // and the stages of the ring that fit then
+  static constexpr int kCtas = D * NB == 64 ? 5 : D * NB == 128 ? 4 : D * NB == 256 ? 3 : 2;
+  static constexpr int kStages = D == 256 ? 2 : D * NB == 128 && D == 128 ? 3 : 4;
   static constexpr int kRing = kStages * 2 * kTile;     // per warp
   static constexpr int kPart = kRows * D + 2 * kRows;   // floats of a partial: outputs, references, sums
 };
@@ -109,19 +118,22 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Token of a 16-token tile that column n of score tile j stands for: lanes t
-// then read tokens t, t+4, t+8, t+12 as values.
-__device__ __forceinline__ int token_of(int j, int n) { return (n >> 1) + 4 * (n & 1) + 8 * j; }
+// An 8x8 block of f16, a row in four lanes (two columns each), transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
 // Where a 16-byte chunk of token `row` lies in a tile: no bank conflicts for
-// the copies (whole rows), the key reads (rows r and r+4, chunks of 64 bytes)
-// and the value reads (rows r..r+3, one or two chunks).
+// the copies (whole rows), the key reads (two neighbouring rows, 64 bytes of
+// each) and the value reads (four rows two apart, one or two chunks of each).
 template <int D> __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
   if (D == 64) {
-    const int slot = (row & ~1) | ((row ^ (row >> 2)) & 1);
-    return slot * 64 + ((chunk ^ (((row >> 1) & 1) << 1)) << 4);
+    const int slot = (row & ~1) | ((row ^ (row >> 1)) & 1);
+    return slot * 64 + ((chunk ^ (((row >> 2) & 1) << 1)) << 4);
   }
-  return row * D + ((chunk ^ ((row & 3) << 1) ^ (((row >> 2) & 1) << 2)) << 4);
+  return row * D + ((chunk ^ (((row >> 1) & 3) << 1) ^ ((row & 1) << 2)) << 4);
 }
 
 // Lists the row blocks of the requests that go to paged_attn_tc.cu, the longest
@@ -204,12 +216,12 @@ __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* sc
   __syncthreads();
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kernel(PaArgs a) {
-  using S = Shape<D>;
+template <int D, int NB>
+__global__ void __launch_bounds__(kWarps * 32, Shape<D, NB>::kCtas) paged_attn_kernel(PaArgs a) {
+  using S = Shape<D, NB>;
   constexpr int KC = D / 64;      // 64-element chunks of a head
-  constexpr int NT = D / 8;       // column tiles of the output
-  constexpr int kStages = S::kStages;
+  constexpr int MT = D / 16;      // 16-element tiles of the output
+  constexpr int kStages = S::kStages, kRows = S::kRows;
   extern __shared__ __align__(128) char smem[];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ float s_scale[kWarps][kStages][4];
@@ -218,9 +230,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
   // the last CTA has the least to do here, often nothing
   if (a.tc_rows < INT_MAX && blockIdx.x == gridDim.x - 1) list_tc_items(a, reinterpret_cast<int*>(s_start), smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  build_unit_table<kRows, kUnit>(a, s_start, blockIdx.x == 0 ? a.status : nullptr);
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= a.B; i += kWarps * 32) a.starts[i] = s_start[i];
+  build_unit_table<kRows, kUnit, kTileCost>(a, s_start, blockIdx.x == 0 ? a.status : nullptr);
   const int64_t total = s_start[a.B];
   const int64_t piece = piece_of(total, gridDim.x);
   const int64_t first = piece * blockIdx.x, last = min(total, first + piece);
@@ -231,22 +241,50 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
   constexpr int CPR = D / 16, RSTEP = 32 / CPR, COPIES = 16 / RSTEP;
   const int crow = lane / CPR, cchunk = lane % CPR;
   const int64_t lane_off = crow * ts + cchunk * 16;
+  JoinTile cut = {};   // the row tile that this CTA begins and others go on with
 
+  int b = -1;
+  Request rq = {};
   for (int64_t at = first; at < last;) {
     // the row tile at `at`, and the piece of it that is this CTA's
-    const int b = find_entry(s_start, a.B, at);
-    const Request rq = load_request(a.cu, a.kv_len, b, a.T);
+    const int b_now = find_entry(s_start, a.B, at);
+    if (b_now != b) {
+      b = b_now;
+      rq = load_request(a.cu, a.kv_len, b, a.T);
+    }
     const Span sp = span_of(a, rq, kUnit);
     const int64_t in_b = at - s_start[b];
-    const int tile = static_cast<int>(in_b / sp.units);      // (key head, row tile)
-    const int u0 = static_cast<int>(in_b - static_cast<int64_t>(tile) * sp.units);
-    const int u1 = static_cast<int>(min(static_cast<int64_t>(sp.units), u0 + (last - at)));
+    const int width = sp.units + kTileCost;
+    int tile;   // (key head, row tile)
+    if (in_b <= 0x7fffffff) tile = static_cast<int>(in_b) / width;
+    else tile = static_cast<int>(in_b / width);
+    const int v0 = static_cast<int>(in_b - static_cast<int64_t>(tile) * width);
+    const int v1 = static_cast<int>(min(static_cast<int64_t>(width), v0 + (last - at)));
+    const int u0 = max(v0 - kTileCost, 0), u1 = v1 - kTileCost;
+    const int64_t tile_end = at + (width - v0);
+    const int slot = at == first ? 0 : 1;
+    at += v1 - v0;
+    if (u1 <= u0) continue;   // the next CTA begins it
     const int rts = ceil_div(rq.n * a.group, kRows);
     const int kvh = tile / rts, row0 = (tile - kvh * rts) * kRows;
     const int rows = min(kRows, rq.n * a.group - row0);
     const bool whole = u0 == 0 && u1 == sp.units;
-    const int slot = at == first ? 0 : 1;
-    at += u1 - u0;
+    if (u0 == 0 && !whole) cut = JoinTile{rows, rq.row0, row0, kvh, slot, static_cast<int>((tile_end - 1) / piece)};
+
+    // q of this lane's row g of each block, on its way while the rest starts
+    uint4 raw[NB][KC][2];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int r = row0 + 8 * n + g;
+      const bool live = 8 * n + g < rows;
+      const uint16_t* src = a.q + static_cast<int64_t>(rq.row0 + (live ? r / a.group : 0)) * a.qs +
+                            static_cast<int64_t>(kvh * a.group + (live ? r % a.group : 0)) * D + t * 16;
+#pragma unroll
+      for (int c = 0; c < KC; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          raw[n][c][i] = live ? __ldg(reinterpret_cast<const uint4*>(src + c * 64 + i * 8)) : make_uint4(0, 0, 0, 0);
+    }
 
     const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + kvh * a.c.head_stride;
     const int64_t v_minus_k = static_cast<const uint8_t*>(a.c.v) - static_cast<const uint8_t*>(a.c.k);
@@ -301,53 +339,55 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
       pid = next;
     }
 
-    // this lane's rows g and g+8: position, q as f16 scaled by a power of two
-    uint32_t qf[KC][4][4];
-    float rf[2];
-    int pos[2];
+    // q as f16, each head scaled by a power of two; the lane's score columns are
+    // rows 2t and 2t+1 of each block
+    uint32_t qf[NB][KC][4][2];
+    float rf[NB][2], m[NB][2], l[NB][2];
+    int pos[NB][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = row0 + g + 8 * h;
-      const bool live = g + 8 * h < rows;
-      const int tok = live ? r / a.group : 0, head = kvh * a.group + (live ? r % a.group : 0);
-      pos[h] = live ? rq.start + tok : -1;
-      const uint16_t* src = a.q + static_cast<int64_t>(rq.row0 + tok) * a.qs + static_cast<int64_t>(head) * D;
-      uint4 raw[KC][2];
+    for (int n = 0; n < NB; ++n) {
       uint32_t top = 0;   // the largest size as bits: a NaN's are above infinity's
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          raw[c][i] = live ? __ldg(reinterpret_cast<const uint4*>(src + c * 64 + t * 16 + i * 8)) : make_uint4(0, 0, 0, 0);
-          top = __vmaxu2(top, __vmaxu2(raw[c][i].x & 0x7fff7fffu, raw[c][i].y & 0x7fff7fffu));
-          top = __vmaxu2(top, __vmaxu2(raw[c][i].z & 0x7fff7fffu, raw[c][i].w & 0x7fff7fffu));
+          const uint4 w = raw[n][c][i];
+          top = __vmaxu2(top, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
+          top = __vmaxu2(top, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
         }
       top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const float f = q_factor(__uint_as_float(top << 16), top < 0x7f80u);
-      rf[h] = a.sm_scale * kLog2e / f;
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t w[4] = {raw[c][i].x, raw[c][i].y, raw[c][i].z, raw[c][i].w};
+          const uint32_t w[4] = {raw[n][c][i].x, raw[n][c][i].y, raw[n][c][i].z, raw[n][c][i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            qf[c][2 * i + (e >> 1)][h + 2 * (e & 1)] =
+            qf[n][c][2 * i + (e >> 1)][e & 1] =
                 pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
         }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 8 * n + 2 * t + h;
+        rf[n][h] = a.sm_scale * kLog2e / __shfl_sync(0xffffffffu, f, (2 * t + h) * 4);
+        pos[n][h] = r < rows ? rq.start + (row0 + r) / a.group : -1;
+        // a row that sees nothing at all needs no reference
+        m[n][h] = pos[n][h] >= 0 ? -INFINITY : 0.f;
+        l[n][h] = 0.f;
+      }
     }
     const int pos_min = rq.start + row0 / a.group, pos_max = rq.start + (row0 + rows - 1) / a.group;
-    const bool low_only = rows <= 8;   // rows 8..15 are not there
 
-    float o[NT][4];
+    float o[NB][MT][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    // a row that sees nothing at all needs no reference
-    float m[2] = {pos[0] >= 0 ? -INFINITY : 0.f, pos[1] >= 0 ? -INFINITY : 0.f}, l[2] = {0.f, 0.f};
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
 
 #pragma unroll 1
     for (int u = u0, stage = 0; u < u1; ++u, stage = stage + 1 == kStages ? 0 : stage + 1) {
@@ -357,82 +397,86 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
       const float* sc = s_scale[warp][stage];
       if (sp.any_seen(j0, j0 + 15) && sc[2] != 0.f) {
         const uint32_t kd = ring + stage * 2 * S::kTile, vd = kd + S::kTile;
-        float s[2][4] = {};
+        // scores: tokens g and g+8 (e >> 1) by rows 2t and 2t+1 (e & 1)
+        float s[NB][4] = {};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int row = token_of(j, g);
+        for (int c = 0; c < KC; ++c) {
+          const uint4 klo = lds128(kd + chunk_at<D>(g, 4 * c + t)), khi = lds128(kd + chunk_at<D>(g + 8, 4 * c + t));
+          const uint32_t lo[4] = {klo.x, klo.y, klo.z, klo.w}, hi[4] = {khi.x, khi.y, khi.z, khi.w};
 #pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const uint4 kw = lds128(kd + chunk_at<D>(row, 4 * c + t));
-            const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t ka[4] = {f16x2_of(lo[e]), f16x2_of(hi[e]), f16x2_of_hi(lo[e]), f16x2_of_hi(hi[e])};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mma16816(s[j], qf[c][e], f16x2_of(w[e]), f16x2_of_hi(w[e]));
+            for (int n = 0; n < NB; ++n) mma16816(s[n], ka, qf[n][c][e][0], qf[n][c][e][1]);
           }
         }
         const float ks = sc[0], lvs = __log2f(sc[1]), ivs = __frcp_rn(sc[1]);
         if (!sp.all_see(j0, j0 + 15, pos_min, pos_max)) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (!sp.sees(pos[e >> 1], j0 + token_of(j, 2 * t + (e & 1)))) s[j][e] = -INFINITY;
+              if (!sp.sees(pos[n][e & 1], j0 + g + 8 * (e >> 1))) s[n][e] = -INFINITY;
         }
-        // weights relative to the reference so far; a sum too large for f16, or
-        // a row without a reference, takes the row's maximum first
-        float e[2][4], sum[2];
-        auto weigh = [&](int h) {
-          const float f = score_factor(ks, rf[h]), shift = lvs - (m[h] == -INFINITY ? 0.f : m[h]);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            e[j][2 * h] = ex2(fmaf(s[j][2 * h], f, shift));
-            e[j][2 * h + 1] = ex2(fmaf(s[j][2 * h + 1], f, shift));
-          }
-          sum[h] = (e[0][2 * h] + e[0][2 * h + 1]) + (e[1][2 * h] + e[1][2 * h + 1]);
+        // weights relative to the reference so far
+        float w[NB][4];
+        bool move = false;
+        auto weigh = [&](int n, int h) {
+          const float f = score_factor(ks, rf[n][h]), shift = lvs - (m[n][h] == -INFINITY ? 0.f : m[n][h]);
+          w[n][h] = ex2(fmaf(s[n][h], f, shift));
+          w[n][2 + h] = ex2(fmaf(s[n][2 + h], f, shift));
+          return m[n][h] == -INFINITY || w[n][h] + w[n][2 + h] > kMostSum;
         };
-        weigh(0);
-        if (low_only) {
-          sum[1] = e[0][2] = e[0][3] = e[1][2] = e[1][3] = 0.f;
-        } else {
-          weigh(1);
-        }
-        if (__any_sync(0xffffffffu, m[0] == -INFINITY || m[1] == -INFINITY || sum[0] > kMostSum || sum[1] > kMostSum)) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-            top = fmaf(top, score_factor(ks, rf[h]), lvs);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float to = fmaxf(m[h], top), f = m[h] == -INFINITY ? 0.f : ex2(m[h] - to);
-            m[h] = to;
-            l[h] *= f;
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              o[i][2 * h] *= f;
-              o[i][2 * h + 1] *= f;
+          for (int h = 0; h < 2; ++h) move |= weigh(n, h);
+        if (__any_sync(0xffffffffu, move)) {
+          // rows whose weights are too large for f16, or that have no reference
+          // yet, take their maximum
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const unsigned of_row = __ballot_sync(0xffffffffu, weigh(n, h)) & (0x11111111u << t);
+              float top = fmaf(fmaxf(s[n][h], s[n][2 + h]), score_factor(ks, rf[n][h]), lvs);
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+              if (of_row) {
+                const float to = fmaxf(m[n][h], top), f = m[n][h] == -INFINITY ? 0.f : ex2(m[n][h] - to);
+                m[n][h] = to;
+                l[n][h] *= f;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                  o[n][i][h] *= f;
+                  o[n][i][2 + h] *= f;
+                }
+                weigh(n, h);
+              }
             }
-            weigh(h);
-          }
         }
-        uint32_t p[4];
+        uint32_t p[NB][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          l[h] = fmaf(sum[h], ivs, l[h]);
-          p[h] = pack_f16(e[0][2 * h], e[0][2 * h + 1]);
-          p[2 + h] = pack_f16(e[1][2 * h], e[1][2 * h + 1]);
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) l[n][h] = fmaf(w[n][h] + w[n][2 + h], ivs, l[n][h]);
+          p[n][0] = transpose8x8(pack_f16(w[n][0], w[n][1]));
+          p[n][1] = transpose8x8(pack_f16(w[n][2], w[n][3]));
         }
-        // values: words of tokens t, t+4 | t+8, t+12
+        // values: words of tokens 2t, 2t+1 | 2t+8, 2t+9
         constexpr int VW = D >= 128 ? 4 : 2;     // words of a lane's run of codes
 #pragma unroll
         for (int c = 0; c < (D + 127) / 128; ++c) {
           uint32_t vw[4][VW];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
+            const int row = 2 * t + (i & 1) + 8 * (i >> 1);
             if (D == 64) {
-              const uint2 x = lds64(vd + chunk_at<D>(t + 4 * i, g >> 1) + (g & 1) * 8);
+              const uint2 x = lds64(vd + chunk_at<D>(row, g >> 1) + (g & 1) * 8);
               vw[i][0] = x.x;
               vw[i][1] = x.y;
             } else {
-              const uint4 x = lds128(vd + chunk_at<D>(t + 4 * i, 8 * c + g));
+              const uint4 x = lds128(vd + chunk_at<D>(row, 8 * c + g));
               vw[i][0] = x.x;
               vw[i][1] = x.y;
               vw[i][VW - 2] = x.z;
@@ -440,14 +484,16 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
             }
           }
 #pragma unroll
-          for (int w = 0; w < VW; ++w) {
-            const uint32_t a01 = __byte_perm(vw[0][w], vw[1][w], 0x5140), a23 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-            const uint32_t b01 = __byte_perm(vw[2][w], vw[3][w], 0x5140), b23 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-            float(*oc)[4] = &o[c * 16 + 4 * w];
-            mma16816(oc[0], p, f16x2_of(a01), f16x2_of(b01));
-            mma16816(oc[1], p, f16x2_of_hi(a01), f16x2_of_hi(b01));
-            mma16816(oc[2], p, f16x2_of(a23), f16x2_of(b23));
-            mma16816(oc[3], p, f16x2_of_hi(a23), f16x2_of_hi(b23));
+          for (int i = 0; i < VW; ++i) {
+            const uint32_t a01 = __byte_perm(vw[0][i], vw[1][i], 0x5140), a23 = __byte_perm(vw[0][i], vw[1][i], 0x7362);
+            const uint32_t b01 = __byte_perm(vw[2][i], vw[3][i], 0x5140), b23 = __byte_perm(vw[2][i], vw[3][i], 0x7362);
+            const uint32_t lo[4] = {f16x2_of(a01), f16x2_of_hi(a01), f16x2_of(b01), f16x2_of_hi(b01)};
+            const uint32_t hi[4] = {f16x2_of(a23), f16x2_of_hi(a23), f16x2_of(b23), f16x2_of_hi(b23)};
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              mma16816(o[n][c * 8 + 2 * i], lo, p[n][0], p[n][1]);
+              mma16816(o[n][c * 8 + 2 * i + 1], hi, p[n][0], p[n][1]);
+            }
           }
         }
       }
@@ -461,29 +507,27 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
     __syncthreads();   // every warp is done with its ring
 
     // join the four warps' sums
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if (t == 0) {
-        s_m[warp][g + 8 * h] = m[h];
-        s_l[warp][g + 8 * h] = l[h];
-      }
-    }
-    // the lane's columns: D = 128c + 16 (2t + (e & 1)) + i for tile 16c + i (D = 64: 8 (2t + (e & 1)) + i)
     float* mine = reinterpret_cast<float*>(smem) + warp * (S::kRing / 4);
-    constexpr int RUN = D >= 128 ? 16 : 8;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (h == 0 || !low_only) {
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int i = 0; i < NT; i += 4)
+      for (int h = 0; h < 2; ++h) {
+        const int r = 8 * n + 2 * t + h;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int col = D == 64 ? RUN * (2 * t + e) + i : i / 16 * 128 + RUN * (2 * t + e) + i % 16;
-            *reinterpret_cast<float4*>(mine + (g + 8 * h) * D + col) =
-                make_float4(o[i][2 * h + e], o[i + 1][2 * h + e], o[i + 2][2 * h + e], o[i + 3][2 * h + e]);
-          }
+        for (int off = 4; off < 32; off <<= 1) l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], off);
+        if (g == 0) {
+          s_m[warp][r] = m[n][h];
+          s_l[warp][r] = l[n][h];
+        }
+        // the lane's columns: tiles 2i and 2i+1 of a 128-element chunk have
+        // elements 4i, 4i+1 and 4i+2, 4i+3 of its run of codes
+        constexpr int RUN = D >= 128 ? 16 : 8;
+#pragma unroll
+        for (int i = 0; i < MT / 2; ++i) {
+          const int col = D == 64 ? RUN * g + 4 * i : i / 4 * 128 + RUN * g + i % 4 * 4;
+          *reinterpret_cast<float4*>(mine + r * D + (col ^ ((r & 7) << 2))) =
+              make_float4(o[n][2 * i][h], o[n][2 * i][2 + h], o[n][2 * i + 1][h], o[n][2 * i + 1][2 + h]);
+        }
       }
     __syncthreads();
     for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
@@ -497,7 +541,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2_from(s_m[w][r], mm);
         sum += s_l[w][r] * f;
-        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + w * (S::kRing / 4) + r * D + d);
+        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + w * (S::kRing / 4) + r * D +
+                                                          (d ^ ((r & 7) << 2)));
         acc.x += x.x * f;
         acc.y += x.y * f;
         acc.z += x.z * f;
@@ -517,104 +562,113 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) paged_attn_kern
     }
     __syncthreads();   // the ring is free again
   }
+  if (threadIdx.x == 0) a.joins[blockIdx.x] = cut;
 }
 
 // Joins the partial sums of the row tiles that more than one CTA worked on: a
-// block for the end of each CTA's piece (but the last) and each group of rows.
-// A tile with several ends inside belongs to the first of them.
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_attn_join(PaArgs a, int n_ctas) {
-  using S = Shape<D>;
-  constexpr int LANES = D / 4;                          // threads of a row, four columns each
-  constexpr int SHARES = kJoinThreads / (kJoinRows * LANES);   // threads that share a row's parts
-  __shared__ float4 s_acc[SHARES][kJoinRows][LANES];
-  __shared__ float s_sum[SHARES][kJoinRows];
-  __shared__ int s_b;
+// block for each CTA that may have begun one, and for each JR of its rows.  JR =
+// a whole row tile where there are about as many row tiles as CTAs (two or three
+// parts each), fewer where few row tiles have many parts.
+template <int D, int NB, int JR, int THREADS>
+__global__ void __launch_bounds__(THREADS) paged_attn_join(PaArgs a) {
+  using S = Shape<D, NB>;
+  constexpr int kRows = S::kRows;
+  constexpr int LANES = D / 4;                     // threads of a row, four columns each
+  constexpr int RPP = THREADS / LANES < JR ? THREADS / LANES : JR;   // rows at a time
+  constexpr int SHARES = THREADS / (RPP * LANES);  // threads that share a row's parts
+  __shared__ float4 s_acc[SHARES][RPP][LANES];
+  __shared__ float s_sum[SHARES][RPP];
   pdl_enter();
-  const int64_t total = a.starts[a.B], piece = piece_of(total, n_ctas);
-  const int64_t end = piece * (blockIdx.x + 1);         // the piece's end: this CTA's last unit is end - 1
-  if (end >= total) return;
-  // the request that unit end - 1 belongs to
-  for (int i = threadIdx.x; i < a.B; i += kJoinThreads)
-    if (a.starts[i] <= end - 1 && end - 1 < a.starts[i + 1]) s_b = i;
-  __syncthreads();
-  const int b = s_b;
-  const Request rq = load_request(a.cu, a.kv_len, b, a.T);
-  const int units = span_of(a, rq, kUnit).units;
-  const int64_t base = a.starts[b];
-  const int64_t tile = (end - 1 - base) / units, begin = base + tile * units, stop = begin + units;
-  // not split here, or an earlier end inside it has it
-  if (stop == end || (begin < end - piece && blockIdx.x > 0)) return;
-  const int rts = ceil_div(rq.n * a.group, kRows);
-  const int kvh = static_cast<int>(tile / rts), row0 = static_cast<int>(tile - static_cast<int64_t>(kvh) * rts) * kRows;
-  const int rows = min(kRows, rq.n * a.group - row0);
-  const int c0 = blockIdx.x, c1 = static_cast<int>((stop - 1) / piece);
-  const int lane = threadIdx.x % LANES, rl = threadIdx.x / LANES % kJoinRows, share = threadIdx.x / (LANES * kJoinRows);
-  const int r = blockIdx.y * kJoinRows + rl;
-  if (blockIdx.y * kJoinRows >= rows) return;
-  auto part_of = [&](int c) {
-    const int slot = (c == c0 && begin != c0 * piece) ? 1 : 0;
-    return a.part + (static_cast<int64_t>(c) * 2 + slot) * S::kPart;
-  };
-  float m = -INFINITY;
-  if (r < rows)
-    for (int c = c0; c <= c1; ++c) m = fmaxf(m, part_of(c)[kRows * D + r]);
-  float sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (r < rows)
+  const JoinTile tile = a.joins[blockIdx.x];
+  const int c0 = blockIdx.x, c1 = tile.last;
+  const int lane = threadIdx.x % LANES, rl = threadIdx.x / LANES % RPP, share = threadIdx.x / (LANES * RPP);
+  for (int r0 = blockIdx.y * JR; r0 < min(tile.rows, static_cast<int>(blockIdx.y + 1) * JR); r0 += RPP) {
+    const int r = r0 + rl;
+    const bool live = r < tile.rows;
+    auto part_of = [&](int c) { return a.part + (static_cast<int64_t>(c) * 2 + (c == c0 ? tile.slot : 0)) * S::kPart; };
+    float m = -INFINITY;
+    if (live)
 #pragma unroll 4
-    for (int c = c0 + share; c <= c1; c += SHARES) {
-      const float* p = part_of(c);
-      const float f = ex2_from(p[kRows * D + r], m);
-      const float4 x = *reinterpret_cast<const float4*>(p + r * D + lane * 4);
-      sum += p[kRows * D + kRows + r] * f;
-      acc.x += x.x * f;
-      acc.y += x.y * f;
-      acc.z += x.z * f;
-      acc.w += x.w * f;
+      for (int c = c0; c <= c1; ++c) m = fmaxf(m, part_of(c)[kRows * D + r]);
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live)
+#pragma unroll 4
+      for (int c = c0 + share; c <= c1; c += SHARES) {
+        const float* p = part_of(c);
+        const float f = ex2_from(p[kRows * D + r], m);
+        const float4 x = *reinterpret_cast<const float4*>(p + r * D + lane * 4);
+        sum += p[kRows * D + kRows + r] * f;
+        acc.x += x.x * f;
+        acc.y += x.y * f;
+        acc.z += x.z * f;
+        acc.w += x.w * f;
+      }
+    if (SHARES > 1) {
+      s_acc[share][rl][lane] = acc;
+      if (lane == 0) s_sum[share][rl] = sum;
+      __syncthreads();
+      if (share == 0) {
+#pragma unroll
+        for (int i = 1; i < SHARES; ++i) {
+          const float4 x = s_acc[i][rl][lane];
+          acc.x += x.x;
+          acc.y += x.y;
+          acc.z += x.z;
+          acc.w += x.w;
+          sum += s_sum[i][rl];
+        }
+      }
+      __syncthreads();
     }
-  s_acc[share][rl][lane] = acc;
-  if (lane == 0) s_sum[share][rl] = sum;
-  __syncthreads();
-  if (share > 0 || r >= rows) return;
-#pragma unroll
-  for (int i = 1; i < SHARES; ++i) {
-    const float4 x = s_acc[i][rl][lane];
-    acc.x += x.x;
-    acc.y += x.y;
-    acc.z += x.z;
-    acc.w += x.w;
+    if (share == 0 && live) {
+      const int tok = (tile.row0 + r) / a.group, head = tile.kvh * a.group + (tile.row0 + r) % a.group;
+      store_row4(a, tile.token0 + tok, head, D, lane * 4, acc, m, sum);
+    }
   }
-  sum = s_sum[0][rl];
-#pragma unroll
-  for (int i = 1; i < SHARES; ++i) sum += s_sum[i][rl];
-  const int tok = (row0 + r) / a.group, head = kvh * a.group + (row0 + r) % a.group;
-  store_row4(a, rq.row0 + tok, head, D, lane * 4, acc, m, sum);
 }
 
-// Persistent CTAs: what the SMs hold at once (registers and ring).  The
-// workspace is sized for kMaxSms SMs, so that its size needs no device.
+// Persistent CTAs: what the SMs hold at once.  The workspace is sized for
+// kMaxSms SMs, so that its size needs no device.
 constexpr int kMaxSms = 160;
-int ctas_for(int D, int num_sms) { return std::min(num_sms, kMaxSms) * (D == 256 ? 2 : 3); }
+template <int D, int NB> int ctas_for(int num_sms) { return std::min(num_sms, kMaxSms) * Shape<D, NB>::kCtas; }
 
-template <int D>
+template <int D, int NB>
 cudaError_t launch(const PaArgs& a, int num_sms, cudaStream_t s) {
-  using S = Shape<D>;
+  using S = Shape<D, NB>;
   const size_t smem = kWarps * S::kRing + sizeof(int64_t) * (a.B + 1);
-  cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(paged_attn_kernel<D>), static_cast<int>(smem));
+  cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(paged_attn_kernel<D, NB>), static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  const int ctas = ctas_for(D, num_sms);
+  const int ctas = ctas_for<D, NB>(num_sms);
   count_launches(2);
-  err = launch_pdl(paged_attn_kernel<D>, ctas, kWarps * 32, smem, s, a);
+  err = launch_pdl(paged_attn_kernel<D, NB>, ctas, kWarps * 32, smem, s, a);
   if (err != cudaSuccess) return err;
-  return launch_pdl(paged_attn_join<D>, dim3(std::max(1, ctas - 1), kRows / kJoinRows), kJoinThreads, 0, s, a, ctas);
+  // no fewer row tiles than half the CTAs: about two parts each
+  const int64_t tiles = (static_cast<int64_t>(a.T) * a.group / S::kRows + a.B) * a.c.n_kv_heads;
+  if (2 * tiles >= ctas) return launch_pdl(paged_attn_join<D, NB, S::kRows, 128>, ctas, 128, 0, s, a);
+  return launch_pdl(paged_attn_join<D, NB, 2, 512>, dim3(ctas, S::kRows / 2), 512, 0, s, a);
+}
+
+// Row tiles of eight where no request has more rows: half the registers, more
+// warps (measured at 64 requests of one token, 8 heads: see above).
+template <int D>
+cudaError_t launch(const PaArgs& a, int64_t most_rows, int num_sms, cudaStream_t s) {
+  if (D == 256 || most_rows <= 8) return launch<D, 1>(a, num_sms, s);
+  return launch<D == 256 ? 128 : D, 2>(a, num_sms, s);
+}
+
+template <int D, int NB> size_t part_bytes() {
+  return static_cast<size_t>(ctas_for<D, NB>(kMaxSms)) * 2 * Shape<D, NB>::kPart * sizeof(float);
 }
 
 }  // namespace
 
-size_t paged_attn_ws_bytes(int D) {
-  const size_t part = (static_cast<size_t>(kRows) * D + 2 * kRows) * sizeof(float);
-  return static_cast<size_t>(ctas_for(D, kMaxSms)) * 2 * part;
+size_t paged_attn_part_bytes(int D) {
+  switch (D) {
+    case 64: return std::max(part_bytes<64, 1>(), part_bytes<64, 2>());
+    case 128: return std::max(part_bytes<128, 1>(), part_bytes<128, 2>());
+    default: return part_bytes<256, 1>();
+  }
 }
 
 // Requests with more rows than this go to the tcgen05 kernel.
@@ -626,24 +680,24 @@ cudaError_t launch_paged_attn(PaArgs a, int max_q_len, int num_sms, cudaStream_t
   a.tc_rows = tc ? kTcRows : INT_MAX;
   cudaError_t err;
   switch (a.c.head_dim) {
-    case 64: err = launch<64>(a, num_sms, s); break;
-    case 128: err = launch<128>(a, num_sms, s); break;
-    default: err = launch<256>(a, num_sms, s); break;
+    case 64: err = launch<64>(a, std::min<int64_t>(most, a.tc_rows), num_sms, s); break;
+    case 128: err = launch<128>(a, std::min<int64_t>(most, a.tc_rows), num_sms, s); break;
+    default: err = launch<256>(a, most, num_sms, s); break;
   }
   return err == cudaSuccess && tc ? launch_paged_attn_tc(a, num_sms, s) : err;
 }
 
 namespace {
 
-// Workspace: partial sums, the requests' first units, the list of row blocks.
+// Workspace: partial sums, the row tiles to join, the list of row blocks.
 struct Workspace {
-  size_t starts, tc_list, total;
+  size_t joins, tc_list, total;
 };
 
 Workspace plan_workspace(const PaArgs& a, int D) {
   Workspace w;
-  w.starts = align_up(paged_attn_ws_bytes(D), 256);
-  w.tc_list = w.starts + align_up((a.B + 1) * sizeof(int64_t), 256);
+  w.joins = align_up(paged_attn_part_bytes(D), 256);
+  w.tc_list = w.joins + align_up(kMaxSms * 5 * sizeof(JoinTile), 256);
   w.total = w.tc_list + align_up((tc_places(a) + 1) * sizeof(int2), 256);
   return w;
 }
@@ -707,7 +761,7 @@ extern "C" moe_status_t moe_paged_attention(const moe_paged_attention_config_t* 
   a.sm_scale = cfg->sm_scale;
   const Workspace w = plan_workspace(a, cache->head_dim);
   a.part = static_cast<float*>(ws);
-  a.starts = reinterpret_cast<int64_t*>(static_cast<char*>(ws) + w.starts);
+  a.joins = reinterpret_cast<JoinTile*>(static_cast<char*>(ws) + w.joins);
   a.tc_list = reinterpret_cast<int2*>(static_cast<char*>(ws) + w.tc_list);
   return launch_paged_attn(a, cfg->max_q_len, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -6,6 +6,12 @@
 
 namespace moe {
 
+// A row tile whose partial sums several CTAs left: rows (0: none), where they
+// lie, the first CTA's slot and the last CTA.
+struct JoinTile {
+  int rows, token0, row0, kvh, slot, last;
+};
+
 struct PaArgs {
   const uint16_t* q;
   uint16_t* out;
@@ -13,7 +19,7 @@ struct PaArgs {
   const int32_t* cu;
   const int32_t* kv_len;
   float* part;          // workspace: partial sums,
-  int64_t* starts;      // the first unit of each request, their total,
+  JoinTile* joins;      // the row tile that each CTA leaves to others to finish,
   int2* tc_list;        // and the row blocks for paged_attn_tc.cu: [0].x of them, (request, block) from [1] on
   moe_kv_cache_t c;
   unsigned* status;
@@ -69,16 +75,17 @@ __device__ __forceinline__ Span span_of(const PaArgs& a, const Request& r, int u
   return span_for(a, r.start, r.end - 1, unit);
 }
 
-// Units of a request: all its key heads and row tiles of `rows` rows.
-__device__ __forceinline__ int64_t units_of(const PaArgs& a, const Request& r, int rows, int unit) {
+// Units of a request: all its key heads and row tiles of `rows` rows, each with
+// `cost` units more than its tokens make.
+__device__ __forceinline__ int64_t units_of(const PaArgs& a, const Request& r, int rows, int unit, int cost) {
   if (r.n * a.group > a.tc_rows) return 0;
-  return static_cast<int64_t>(a.c.n_kv_heads) * ceil_div(r.n * a.group, rows) * span_of(a, r, unit).units;
+  return static_cast<int64_t>(a.c.n_kv_heads) * ceil_div(r.n * a.group, rows) * (span_of(a, r, unit).units + cost);
 }
 
 // Units of the call, request by request: start[b] units come before request
 // b, start[B] in all.  The whole block calls; `status` records offsets that
 // are out of order and lengths past the page table.
-template <int ROWS, int UNIT>
+template <int ROWS, int UNIT, int COST>
 __device__ __forceinline__ void build_unit_table(const PaArgs& a, int64_t* start, unsigned* status) {
   __shared__ int64_t s_warp[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -89,7 +96,7 @@ __device__ __forceinline__ void build_unit_table(const PaArgs& a, int64_t* start
     if (b < a.B) {
       const Request r = load_request(a.cu, a.kv_len, b, a.T);
       if (!r.ok || r.end > a.c.max_pages * a.c.page_size) set_status(status, MOE_ERR_DEVICE_BOUNDS);
-      n = units_of(a, r, ROWS, UNIT);
+      n = units_of(a, r, ROWS, UNIT, COST);
     }
     int64_t sum = n;   // inclusive prefix over the warp, then over the warps
     for (int off = 1; off < 32; off <<= 1) {

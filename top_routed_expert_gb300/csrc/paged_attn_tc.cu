@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
                 top = fmaxf(top, fmaf(u, score_factor(s.x, rf), s.y));
               }
             }
-            const float to = fmaxf(m, top), f = m == -INFINITY ? 0.f : ex2(m - to);
+            const float to = move ? fmaxf(m, top) : m, f = m == -INFINITY ? 0.f : ex2(m - to);
             m = to;
             l *= f;
             if (j > 0) {
