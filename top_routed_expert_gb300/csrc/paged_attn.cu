@@ -565,65 +565,110 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB>::kCtas) paged_attn_k
   if (threadIdx.x == 0) a.joins[blockIdx.x] = cut;
 }
 
-// Joins the partial sums of the row tiles that more than one CTA worked on: a
-// block for each CTA that may have begun one, and for each JR of its rows.  JR =
-// a whole row tile where there are about as many row tiles as CTAs (two or three
-// parts each), fewer where few row tiles have many parts.
-template <int D, int NB, int JR, int THREADS>
-__global__ void __launch_bounds__(THREADS) paged_attn_join(PaArgs a) {
+// Joins the partial sums of the row tiles that more than one CTA worked on.  A
+// block looks at the tiles that a few CTAs may have begun (one block on an SM:
+// most have one or two or none to join), and its warps take their rows; where
+// that leaves warps over, several share a row's parts.  The kernel is a chain of
+// latencies, its own instructions' among them, so it is kept short: a lane
+// fetches the reference and sum of one part each, then the parts' columns
+// follow, eight parts under way at a time.
+constexpr int kJoinWarps = 32;
+
+template <int D, int NB>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join(PaArgs a, int n_ctas) {
   using S = Shape<D, NB>;
   constexpr int kRows = S::kRows;
-  constexpr int LANES = D / 4;                     // threads of a row, four columns each
-  constexpr int RPP = THREADS / LANES < JR ? THREADS / LANES : JR;   // rows at a time
-  constexpr int SHARES = THREADS / (RPP * LANES);  // threads that share a row's parts
-  __shared__ float4 s_acc[SHARES][RPP][LANES];
-  __shared__ float s_sum[SHARES][RPP];
+  constexpr int VEC = D / 64;   // pairs of columns of a lane
+  constexpr int kMost = 8;      // CTAs that a block looks at
+  __shared__ JoinTile s_tile[kMost];
+  __shared__ float2 s_acc[kJoinWarps][VEC][32];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   pdl_enter();
-  const JoinTile tile = a.joins[blockIdx.x];
-  const int c0 = blockIdx.x, c1 = tile.last;
-  const int lane = threadIdx.x % LANES, rl = threadIdx.x / LANES % RPP, share = threadIdx.x / (LANES * RPP);
-  for (int r0 = blockIdx.y * JR; r0 < min(tile.rows, static_cast<int>(blockIdx.y + 1) * JR); r0 += RPP) {
-    const int r = r0 + rl;
-    const bool live = r < tile.rows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int mine = (n_ctas - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x;   // at most kMost
+  if (threadIdx.x < mine) s_tile[threadIdx.x] = a.joins[blockIdx.x + threadIdx.x * gridDim.x];
+  __syncthreads();
+  int items = 0;
+  for (int i = 0; i < mine; ++i) items += s_tile[i].rows;
+  if (items == 0) return;
+  int shares = 1;
+  while (shares * 2 * items <= kJoinWarps) shares *= 2;
+  const int share = warp % shares;
+#pragma unroll 1
+  for (int base = 0; base < items; base += kJoinWarps / shares) {
+    const int item = base + warp / shares;
+    const bool live = item < items;
+    int x = 0, r = item;
+    while (live && r >= s_tile[x].rows) r -= s_tile[x++].rows;
+    const JoinTile tile = s_tile[x];
+    const int c0 = blockIdx.x + x * gridDim.x;
     auto part_of = [&](int c) { return a.part + (static_cast<int64_t>(c) * 2 + (c == c0 ? tile.slot : 0)) * S::kPart; };
-    float m = -INFINITY;
-    if (live)
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) m = fmaxf(m, part_of(c)[kRows * D + r]);
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live)
-#pragma unroll 4
-      for (int c = c0 + share; c <= c1; c += SHARES) {
-        const float* p = part_of(c);
-        const float f = ex2_from(p[kRows * D + r], m);
-        const float4 x = *reinterpret_cast<const float4*>(p + r * D + lane * 4);
-        sum += p[kRows * D + kRows + r] * f;
-        acc.x += x.x * f;
-        acc.y += x.y * f;
-        acc.z += x.z * f;
-        acc.w += x.w * f;
+    float m = -INFINITY, sum = 0.f;
+    float2 acc[VEC] = {};
+    // this share's parts, 32 at a time
+#pragma unroll 1
+    for (int c = c0 + share; live && c <= tile.last; c += 32 * shares) {
+      const int n = min(32, (tile.last - c) / shares + 1);
+      float pm = -INFINITY, pl = 0.f;
+      if (lane < n) {
+        const float* p = part_of(c + lane * shares) + kRows * D + r;
+        pm = p[0];
+        pl = p[kRows];
       }
-    if (SHARES > 1) {
-      s_acc[share][rl][lane] = acc;
-      if (lane == 0) s_sum[share][rl] = sum;
+      float to = fmaxf(m, pm);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
+      const float old = ex2_from(m, to), w = ex2_from(pm, to);
+      m = to;
+      pl *= w;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) pl += __shfl_xor_sync(0xffffffffu, pl, off);
+      sum = sum * old + pl;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = make_float2(acc[e].x * old, acc[e].y * old);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float2* p = reinterpret_cast<const float2*>(part_of(c + i * shares) + r * D);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float2 v = p[e * 32 + lane];
+          acc[e].x += v.x * wi;
+          acc[e].y += v.y * wi;
+        }
+      }
+    }
+    if (shares > 1) {
+      if (lane == 0) {
+        s_m[warp] = m;
+        s_l[warp] = sum;
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s_acc[warp][e][lane] = acc[e];
       __syncthreads();
       if (share == 0) {
+#pragma unroll 1
+        for (int i = 1; i < shares; ++i) {
+          const float to = fmaxf(m, s_m[warp + i]), f = ex2_from(m, to), w = ex2_from(s_m[warp + i], to);
+          m = to;
+          sum = sum * f + s_l[warp + i] * w;
 #pragma unroll
-        for (int i = 1; i < SHARES; ++i) {
-          const float4 x = s_acc[i][rl][lane];
-          acc.x += x.x;
-          acc.y += x.y;
-          acc.z += x.z;
-          acc.w += x.w;
-          sum += s_sum[i][rl];
+          for (int e = 0; e < VEC; ++e) {
+            const float2 v = s_acc[warp + i][e][lane];
+            acc[e] = make_float2(acc[e].x * f + v.x * w, acc[e].y * f + v.y * w);
+          }
         }
       }
       __syncthreads();
     }
-    if (share == 0 && live) {
+    if (live && share == 0) {
       const int tok = (tile.row0 + r) / a.group, head = tile.kvh * a.group + (tile.row0 + r) % a.group;
-      store_row4(a, tile.token0 + tok, head, D, lane * 4, acc, m, sum);
+      const float f = sum == 0.f ? 0.f : 1.0f / sum;   // nothing visible (a NaN sum is not)
+      __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + static_cast<int64_t>(tile.token0 + tok) * a.os +
+                                                              static_cast<int64_t>(head) * D);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) out[e * 32 + lane] = __floats2bfloat162_rn(acc[e].x * f, acc[e].y * f);
+      if (a.lse && lane == 0) store_lse(a, tile.token0 + tok, head, m, sum);
     }
   }
 }
@@ -643,10 +688,8 @@ cudaError_t launch(const PaArgs& a, int num_sms, cudaStream_t s) {
   count_launches(2);
   err = launch_pdl(paged_attn_kernel<D, NB>, ctas, kWarps * 32, smem, s, a);
   if (err != cudaSuccess) return err;
-  // no fewer row tiles than half the CTAs: about two parts each
-  const int64_t tiles = (static_cast<int64_t>(a.T) * a.group / S::kRows + a.B) * a.c.n_kv_heads;
-  if (2 * tiles >= ctas) return launch_pdl(paged_attn_join<D, NB, S::kRows, 128>, ctas, 128, 0, s, a);
-  return launch_pdl(paged_attn_join<D, NB, 2, 512>, dim3(ctas, S::kRows / 2), 512, 0, s, a);
+  static_assert(Shape<D, NB>::kCtas <= 8, "CTAs that a block of the join looks at");
+  return launch_pdl(paged_attn_join<D, NB>, ctas / Shape<D, NB>::kCtas, kJoinWarps * 32, 0, s, a, ctas);
 }
 
 // Row tiles of eight where no request has more rows: half the registers, more

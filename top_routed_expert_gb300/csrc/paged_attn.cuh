@@ -150,6 +150,11 @@ __device__ __forceinline__ float q_factor(float amax, bool finite) {
   return __uint_as_float(static_cast<uint32_t>(f + 127) << 23);
 }
 
+__device__ __forceinline__ void store_lse(const PaArgs& a, int row, int head, float m, float sum) {
+  a.lse[static_cast<int64_t>(row) * (a.group * a.c.n_kv_heads) + head] =
+      sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+}
+
 // Four columns of a finished row: outputs `acc` and the weights' sum, both
 // relative to 2^m.
 __device__ __forceinline__ void store_row4(const PaArgs& a, int row, int head, int D, int d, const float4& acc, float m,
@@ -159,9 +164,7 @@ __device__ __forceinline__ void store_row4(const PaArgs& a, int row, int head, i
   const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * f, acc.y * f), y = __floats2bfloat162_rn(acc.z * f, acc.w * f);
   *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(row) * a.os + static_cast<int64_t>(head) * D + d) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  if (a.lse && d == 0)
-    a.lse[static_cast<int64_t>(row) * (a.group * a.c.n_kv_heads) + head] =
-        empty ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+  if (a.lse && d == 0) store_lse(a, row, head, m, sum);
 }
 
 }  // namespace moe

@@ -511,9 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
           }
         }
       }
-      if (live && a.lse)
-        a.lse[static_cast<int64_t>(token) * (a.group * a.c.n_kv_heads) + head] =
-            empty ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      if (live && a.lse) store_lse(a, token, head, m, l);
       tc_fence_before();
       rf = rf_next;
     }
