@@ -565,32 +565,53 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB>::kCtas) paged_attn_k
   if (threadIdx.x == 0) a.joins[blockIdx.x] = cut;
 }
 
-// Joins the partial sums of the row tiles that more than one CTA worked on.  A
-// block looks at the tiles that a few CTAs may have begun (one block on an SM:
-// most have one or two or none to join), and its warps take their rows; where
-// that leaves warps over, several share a row's parts.  The kernel is a chain of
-// latencies, its own instructions' among them, so it is kept short: a lane
-// fetches the reference and sum of one part each, then the parts' columns
-// follow, eight parts under way at a time.
+// Joins the partial sums of the row tiles that more than one CTA worked on.  The
+// rows to join are dealt to all blocks (one on an SM) and their warps; where that
+// leaves warps over, several share a row's parts.  The kernel is a chain of
+// latencies, so what a row needs is under way at once: eight parts' columns, and
+// their references and sums, one part a lane.
 constexpr int kJoinWarps = 32;
+// The workspace is sized for kMaxSms SMs, so that its size needs no device.
+constexpr int kMaxSms = 160, kMaxCtas = kMaxSms * 5;
 
 template <int D, int NB>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join(PaArgs a, int n_ctas) {
   using S = Shape<D, NB>;
   constexpr int kRows = S::kRows;
   constexpr int VEC = D / 64;   // pairs of columns of a lane
-  constexpr int kMost = 8;      // CTAs that a block looks at
-  __shared__ JoinTile s_tile[kMost];
+  __shared__ int s_first[kJoinWarps * 32];   // rows to join before CTA i's
+  __shared__ JoinTile s_tile[kMaxCtas];
+  __shared__ int s_warp[kJoinWarps];
   __shared__ float2 s_acc[kJoinWarps][VEC][32];
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   pdl_enter();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int mine = (n_ctas - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x;   // at most kMost
-  if (threadIdx.x < mine) s_tile[threadIdx.x] = a.joins[blockIdx.x + threadIdx.x * gridDim.x];
+  int rows = 0;
+  if (threadIdx.x < n_ctas) {
+    const JoinTile tile = a.joins[threadIdx.x];
+    rows = tile.rows;
+    s_tile[threadIdx.x] = tile;
+  }
+  int before = rows;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, off);
+    if (lane >= off) before += v;
+  }
+  if (lane == 31) s_warp[warp] = before;
   __syncthreads();
-  int items = 0;
-  for (int i = 0; i < mine; ++i) items += s_tile[i].rows;
-  if (items == 0) return;
+  int in_warps = s_warp[lane];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, in_warps, off);
+    if (lane >= off) in_warps += v;
+  }
+  const int total = __shfl_sync(0xffffffffu, in_warps, 31);
+  const int prior = __shfl_sync(0xffffffffu, in_warps, max(warp - 1, 0));
+  s_first[threadIdx.x] = before - rows + (warp > 0 ? prior : 0);
+  __syncthreads();
+  const int items = (total - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x;   // this block's rows
+  if (items <= 0) return;
   int shares = 1;
   while (shares * 2 * items <= kJoinWarps) shares *= 2;
   const int share = warp % shares;
@@ -598,22 +619,33 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join(PaArgs a, int
   for (int base = 0; base < items; base += kJoinWarps / shares) {
     const int item = base + warp / shares;
     const bool live = item < items;
-    int x = 0, r = item;
-    while (live && r >= s_tile[x].rows) r -= s_tile[x++].rows;
-    const JoinTile tile = s_tile[x];
-    const int c0 = blockIdx.x + x * gridDim.x;
+    // the CTA that began the row's tile: the last that has no more rows before it
+    const int at = blockIdx.x + (live ? item : 0) * gridDim.x;
+    int c0 = 0;
+#pragma unroll
+    for (int step = kJoinWarps * 16; step > 0; step >>= 1)
+      if (c0 + step < n_ctas && s_first[c0 + step] <= at) c0 += step;
+    const int r = at - s_first[c0];
+    const JoinTile tile = s_tile[c0];
     auto part_of = [&](int c) { return a.part + (static_cast<int64_t>(c) * 2 + (c == c0 ? tile.slot : 0)) * S::kPart; };
     float m = -INFINITY, sum = 0.f;
     float2 acc[VEC] = {};
-    // this share's parts, 32 at a time
+    // this share's parts
+    constexpr int BATCH = D == 256 ? 4 : 8;
 #pragma unroll 1
-    for (int c = c0 + share; live && c <= tile.last; c += 32 * shares) {
-      const int n = min(32, (tile.last - c) / shares + 1);
+    for (int c = c0 + share; live && c <= tile.last; c += BATCH * shares) {
+      float2 v[BATCH][VEC];
       float pm = -INFINITY, pl = 0.f;
-      if (lane < n) {
+      if (lane < BATCH && c + lane * shares <= tile.last) {
         const float* p = part_of(c + lane * shares) + kRows * D + r;
         pm = p[0];
         pl = p[kRows];
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const float2* p = reinterpret_cast<const float2*>(part_of(c + i * shares) + r * D) + lane;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[i][e] = c + i * shares <= tile.last ? p[e * 32] : make_float2(0.f, 0.f);
       }
       float to = fmaxf(m, pm);
 #pragma unroll
@@ -626,15 +658,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join(PaArgs a, int
       sum = sum * old + pl;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) acc[e] = make_float2(acc[e].x * old, acc[e].y * old);
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
         const float wi = __shfl_sync(0xffffffffu, w, i);
-        const float2* p = reinterpret_cast<const float2*>(part_of(c + i * shares) + r * D);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float2 v = p[e * 32 + lane];
-          acc[e].x += v.x * wi;
-          acc[e].y += v.y * wi;
+          acc[e].x += v[i][e].x * wi;
+          acc[e].y += v[i][e].y * wi;
         }
       }
     }
@@ -647,15 +677,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join(PaArgs a, int
       for (int e = 0; e < VEC; ++e) s_acc[warp][e][lane] = acc[e];
       __syncthreads();
       if (share == 0) {
-#pragma unroll 1
-        for (int i = 1; i < shares; ++i) {
-          const float to = fmaxf(m, s_m[warp + i]), f = ex2_from(m, to), w = ex2_from(s_m[warp + i], to);
-          m = to;
-          sum = sum * f + s_l[warp + i] * w;
+        const float pm = lane < shares ? s_m[warp + lane] : -INFINITY;
+        float to = pm;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
+        const float w = ex2_from(pm, to);
+        m = to;
+        sum = lane < shares ? s_l[warp + lane] * w : 0.f;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < shares; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
             const float2 v = s_acc[warp + i][e][lane];
-            acc[e] = make_float2(acc[e].x * f + v.x * w, acc[e].y * f + v.y * w);
+            acc[e].x += v.x * wi;
+            acc[e].y += v.y * wi;
           }
         }
       }
@@ -673,9 +713,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join(PaArgs a, int
   }
 }
 
-// Persistent CTAs: what the SMs hold at once.  The workspace is sized for
-// kMaxSms SMs, so that its size needs no device.
-constexpr int kMaxSms = 160;
+// Persistent CTAs: what the SMs hold at once.
 template <int D, int NB> int ctas_for(int num_sms) { return std::min(num_sms, kMaxSms) * Shape<D, NB>::kCtas; }
 
 template <int D, int NB>
@@ -688,7 +726,7 @@ cudaError_t launch(const PaArgs& a, int num_sms, cudaStream_t s) {
   count_launches(2);
   err = launch_pdl(paged_attn_kernel<D, NB>, ctas, kWarps * 32, smem, s, a);
   if (err != cudaSuccess) return err;
-  static_assert(Shape<D, NB>::kCtas <= 8, "CTAs that a block of the join looks at");
+  static_assert(kMaxSms * Shape<D, NB>::kCtas <= kMaxCtas && kMaxCtas <= kJoinWarps * 32, "a thread of the join for each CTA");
   return launch_pdl(paged_attn_join<D, NB>, ctas / Shape<D, NB>::kCtas, kJoinWarps * 32, 0, s, a, ctas);
 }
 
@@ -740,7 +778,7 @@ struct Workspace {
 Workspace plan_workspace(const PaArgs& a, int D) {
   Workspace w;
   w.joins = align_up(paged_attn_part_bytes(D), 256);
-  w.tc_list = w.joins + align_up(kMaxSms * 5 * sizeof(JoinTile), 256);
+  w.tc_list = w.joins + align_up(kMaxCtas * sizeof(JoinTile), 256);
   w.total = w.tc_list + align_up((tc_places(a) + 1) * sizeof(int2), 256);
   return w;
 }
