@@ -72,10 +72,11 @@ struct Place {
   bool rotates;
 };
 
-__device__ __forceinline__ Place place_of(int lane_in_row, int rot, bool half) {
+template <bool HALF>
+__device__ __forceinline__ Place place_of(int lane_in_row, int rot) {
   Place p;
   p.rotates = lane_in_row * 8 < rot;
-  if (half && p.rotates) {
+  if (HALF && p.rotates) {
     p.oa = lane_in_row * 4;
     p.ob = rot / 2 + p.oa;
   } else {
@@ -85,45 +86,60 @@ __device__ __forceinline__ Place place_of(int lane_in_row, int rot, bool half) {
   return p;
 }
 
+struct Raw {
+  uint2 a, b;
+};
+
+// (Plain loads: the queries may be turned in place.)
+__device__ __forceinline__ Raw load_raw(const uint16_t* row, const Place& p) {
+  return Raw{*reinterpret_cast<const uint2*>(row + p.oa), *reinterpret_cast<const uint2*>(row + p.ob)};
+}
+
 // (cos, sin) of the thread's four pairs: frequencies oa..oa+3 of the half
 // layout, (oa/2, oa/2+1, ob/2, ob/2+1) of the interleaved one; both are four
 // consecutive table entries.
-__device__ __forceinline__ void load_cs(const float2* __restrict__ row, const Place& p, bool half, float2 (&cs)[4]) {
-  const float4* f = reinterpret_cast<const float4*>(row + (half ? p.oa : p.oa / 2));
-  const float4 x = f[0], y = f[1];
+template <bool HALF>
+__device__ __forceinline__ void load_cs(const float2* __restrict__ row, const Place& p, float2 (&cs)[4]) {
+  const float4* f = reinterpret_cast<const float4*>(row + (HALF ? p.oa : p.oa / 2));
+  const float4 x = __ldg(f), y = __ldg(f + 1);
   cs[0] = make_float2(x.x, x.y);
   cs[1] = make_float2(x.z, x.w);
   cs[2] = make_float2(y.x, y.y);
   cs[3] = make_float2(y.z, y.w);
 }
 
-// Norm (gamma != NULL) and rotation of the thread's eight elements, in place.
-// The products and sums of the rotation are rounded one by one: a value next
-// to an E4M3 rounding boundary then does not depend on how the compiler
-// contracts them.  TPR = D/8 threads of a row, all of them call.
-template <int TPR>
-__device__ __forceinline__ void norm_rotate(float (&x)[8], const float* __restrict__ gamma, const Place& p,
-                                            const float2 (&cs)[4], float eps, bool half) {
-  if (gamma) {
+struct Gamma {
+  float g[8];
+};
+
+__device__ __forceinline__ Gamma load_gamma(const float* __restrict__ gamma, const Place& p) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(gamma + p.oa)), b = __ldg(reinterpret_cast<const float4*>(gamma + p.ob));
+  return Gamma{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+
+// Norm and rotation of the thread's eight elements, in place.  TPR = D/8
+// threads of a row, all of them call.
+template <int TPR, bool HALF>
+__device__ __forceinline__ void norm_rotate(float (&x)[8], bool norm, const Gamma& gamma, const Place& p,
+                                            const float2 (&cs)[4], float eps) {
+  if (norm) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
     for (int off = TPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(TPR * 8) + eps);
-    const float4 ga = *reinterpret_cast<const float4*>(gamma + p.oa);
-    const float4 gb = *reinterpret_cast<const float4*>(gamma + p.ob);
-    const float g[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
+    const float rstd = rsqrtf(ss * (1.0f / static_cast<float>(TPR * 8)) + eps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * rstd * g[i];
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * rstd * gamma.g[i];
   }
   if (!p.rotates) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int ia = half ? i : 2 * i, ib = half ? i + 4 : 2 * i + 1;
+    constexpr int step = HALF ? 1 : 2;
+    const int ia = i * step, ib = HALF ? i + 4 : 2 * i + 1;
     const float a = x[ia], b = x[ib];
-    x[ia] = __fsub_rn(__fmul_rn(a, cs[i].x), __fmul_rn(b, cs[i].y));
-    x[ib] = __fadd_rn(__fmul_rn(b, cs[i].x), __fmul_rn(a, cs[i].y));
+    x[ia] = fmaf(a, cs[i].x, -b * cs[i].y);
+    x[ib] = fmaf(b, cs[i].x, a * cs[i].y);
   }
 }
 
@@ -135,6 +151,13 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(e << 23);
 }
 
+// The larger of two sizes, NaN if either is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Row of the frequency table of a token, or -1.
 __device__ __forceinline__ int table_row(const KaArgs& a, int t, int pos) {
   const int p = a.positions ? a.positions[t] : pos;
@@ -143,11 +166,11 @@ __device__ __forceinline__ int table_row(const KaArgs& a, int t, int pos) {
 
 // One page, one head, keys or values.  PASSES rows per thread group; the
 // block covers the page's slots in PASSES rounds of blockDim / TPR rows.
-template <int D, int PASSES>
-__device__ __forceinline__ void append_block(const KaArgs& a, int item, int head, bool is_v) {
+template <int D, int PASSES, bool HALF, bool IS_V>
+__device__ __forceinline__ void append_block(const KaArgs& a, int item, int head) {
   constexpr int TPR = D / 8;
   __shared__ float s_amax[32];
-  const int ps = a.c.page_size;
+  const int ps = a.c.page_size, ps_log = 31 - __clz(ps);
   const int b = warp_find_request(a.cu, a.B, item, 1, ps, 2);
   const Request r = load_request(a.cu, a.kv_len, b, a.T);
   if (!r.ok || r.start < 0) {
@@ -155,75 +178,94 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
     return;
   }
   if (r.n == 0) return;
-  const int at = item - (r.row0 / ps + 2 * b);
-  const int page = r.start / ps + at;
-  const int base = page * ps;
+  const int at = item - ((r.row0 >> ps_log) + 2 * b);
+  const int page = (r.start >> ps_log) + at;
+  const int base = page << ps_log;
   if (at < 0 || base >= r.end) return;   // one block too many, or before the first request
   int pid = -1;
   if (page < a.c.max_pages) pid = a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page];
-  if (pid < 0 || pid >= a.c.n_pages) {
-    if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-    return;
-  }
   const int lr = threadIdx.x % TPR, grp = threadIdx.x / TPR, rows = blockDim.x / TPR;
-  const bool rotates = !is_v && a.rot > 0;
-  const float* gamma = is_v ? nullptr : a.gamma_k;
-  const Place p = place_of(lr, is_v ? 0 : a.rot, a.half);
-  const uint16_t* src = (is_v ? a.v : a.k) + static_cast<int64_t>(head) * D;
-  const int64_t stride = is_v ? a.vs : a.ks;
-  float x[PASSES][8];
-  bool take[PASSES];
-  float amax = 0.f;
-  bool bad = false, outside = false;
+  const bool rotates = !IS_V && a.rot > 0, norm = !IS_V && a.gamma_k;
+  const Place p = place_of<HALF>(lr, IS_V ? 0 : a.rot);
+  const uint16_t* src = (IS_V ? a.v : a.k) + static_cast<int64_t>(head) * D;
+  const int64_t stride = IS_V ? a.vs : a.ks;
+  const int t0 = r.row0 - r.start;         // row of position 0
+  Gamma gamma = {};
+  if (norm) gamma = load_gamma(a.gamma_k, p);
+  Raw raw[PASSES];
+  float2 cs[PASSES][4];
+  bool take[PASSES], outside = false;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int j = base + i * rows + grp;
     take[i] = j >= r.start && j < r.end && j < base + ps;
-    const int t = r.row0 + (j - r.start);
-    int f = -1;
-    if (take[i] && rotates) {
-      f = table_row(a, t, j);
-      if (f < 0) { outside = true; take[i] = false; }
-    }
-    uint2 va = make_uint2(0, 0), vb = make_uint2(0, 0);
-    float2 cs[4] = {};
-    if (take[i]) {
-      const uint16_t* row = src + t * stride;
-      va = *reinterpret_cast<const uint2*>(row + p.oa);
-      vb = *reinterpret_cast<const uint2*>(row + p.ob);
-      if (p.rotates) load_cs(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), p, a.half, cs);
-    }
-    unpack4(va, x[i]);
-    unpack4(vb, x[i] + 4);
-    norm_rotate<TPR>(x[i], gamma, p, cs, a.eps, a.half);
+    raw[i] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
+    if (take[i]) raw[i] = load_raw(src + (t0 + j) * stride, p);
+  }
+  if (rotates) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float m = fabsf(x[i][e]);
-      if (take[i] && !(m < INFINITY)) bad = true;
-      else if (take[i]) amax = fmaxf(amax, m);
+    for (int i = 0; i < PASSES; ++i) {
+      const int j = base + i * rows + grp;
+      if (!take[i]) continue;
+      const int f = table_row(a, t0 + j, j);
+      if (f < 0) {
+        outside = true;
+        take[i] = false;
+      } else if (p.rotates) {
+        load_cs<HALF>(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), p, cs[i]);
+      }
+    }
+  }
+  if (pid < 0 || pid >= a.c.n_pages) {
+    if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  float* scale_at = (IS_V ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(pid) * a.c.n_kv_heads + head;
+  const bool had = r.start > base;
+  const float old = had ? *scale_at : 0.f;
+  float x[PASSES][8], amax = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    unpack4(raw[i].a, x[i]);
+    unpack4(raw[i].b, x[i] + 4);
+    if (!IS_V) norm_rotate<TPR, HALF>(x[i], norm, gamma, p, cs[i], a.eps);
+    float top = 0.f;   // a NaN or an infinity makes it one of them
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max_or_nan(top, fabsf(x[i][e]));
+    if (!take[i]) continue;
+    if (top < INFINITY) {
+      amax = fmaxf(amax, top);
+    } else {
+      bad = true;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (fabsf(x[i][e]) < INFINITY) amax = fmaxf(amax, fabsf(x[i][e]));
     }
   }
   if (bad) set_status(a.status, MOE_ERR_DEVICE_NONFINITE);
   if (outside && lr == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  // sizes order like their bits
+  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
   if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = amax;
-  float* scale_at = (is_v ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(pid) * a.c.n_kv_heads + head;
-  const bool had = r.start > base;
-  const float old = had ? *scale_at : 0.f;
   __syncthreads();   // also: every thread has read the old scale
   for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) amax = fmaxf(amax, s_amax[w]);
   const float scale = fmaxf(scale_for(amax), old);
   if (threadIdx.x == 0) *scale_at = scale;
   const float inv = 1.0f / scale;
-  uint8_t* codes = static_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + pid * a.c.page_stride + head * a.c.head_stride;
+  uint8_t* codes = static_cast<uint8_t*>(IS_V ? a.c.v : a.c.k) + pid * a.c.page_stride + head * a.c.head_stride;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int j = base + i * rows + grp;
     uint8_t* row = codes + (j - base) * a.c.token_stride;
     if (take[i]) {
-      *reinterpret_cast<uint32_t*>(row + p.oa) = codes4(x[i], inv);
-      *reinterpret_cast<uint32_t*>(row + p.ob) = codes4(x[i] + 4, inv);
+      const uint32_t lo = codes4(x[i], inv), hi = codes4(x[i] + 4, inv);
+      if (p.ob == p.oa + 4) {
+        *reinterpret_cast<uint2*>(row + p.oa) = make_uint2(lo, hi);
+      } else {
+        *reinterpret_cast<uint32_t*>(row + p.oa) = lo;
+        *reinterpret_cast<uint32_t*>(row + p.ob) = hi;
+      }
     } else if (had && scale > old && j < r.start) {
       uint32_t* wa = reinterpret_cast<uint32_t*>(row + p.oa);
       uint32_t* wb = reinterpret_cast<uint32_t*>(row + p.ob);
@@ -233,12 +275,28 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
   }
 }
 
-// All query heads of one token.
-template <int D>
+// All query heads of one token.  The first rows are on their way while the
+// token's request, position and angles are looked up.
+template <int D, bool HALF>
 __device__ __forceinline__ void query_block(const KaArgs& a, int t) {
-  constexpr int TPR = D / 8;
+  constexpr int TPR = D / 8, ILP = 4;
   const int lr = threadIdx.x % TPR, grp = threadIdx.x / TPR, groups = blockDim.x / TPR;
-  const Place p = place_of(lr, a.rot, a.half);
+  const Place p = place_of<HALF>(lr, a.rot);
+  const uint16_t* src = a.q + t * a.qs;
+  uint16_t* dst = a.q_out + t * a.qos;
+  Raw raw[ILP];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < ILP; ++i) {
+      const int h = h0 + i * groups + grp;
+      raw[i] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
+      if (h < a.Hq) raw[i] = load_raw(src + h * D, p);
+    }
+  };
+  load(0);
+  const bool norm = a.gamma_q;
+  Gamma gamma = {};
+  if (norm) gamma = load_gamma(a.gamma_q, p);
   float2 cs[4] = {};
   const int b = warp_find_request(a.cu, a.B, t, 1, 1, 0);
   const Request r = load_request(a.cu, a.kv_len, b, a.T);
@@ -249,59 +307,61 @@ __device__ __forceinline__ void query_block(const KaArgs& a, int t) {
       if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
       return;
     }
-    if (p.rotates) load_cs(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), p, a.half, cs);
+    if (p.rotates) load_cs<HALF>(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), p, cs);
   }
-  const uint16_t* src = a.q + t * a.qs;
-  uint16_t* dst = a.q_out + t * a.qos;
   // every thread makes the same number of rounds: the norm's shuffles need all lanes
-  for (int h0 = 0; h0 < a.Hq; h0 += groups) {
-    const int h = h0 + grp;
-    uint2 va = make_uint2(0, 0), vb = make_uint2(0, 0);
-    if (h < a.Hq) {
-      va = *reinterpret_cast<const uint2*>(src + h * D + p.oa);
-      vb = *reinterpret_cast<const uint2*>(src + h * D + p.ob);
-    }
-    float x[8];
-    unpack4(va, x);
-    unpack4(vb, x + 4);
-    norm_rotate<TPR>(x, a.gamma_q, p, cs, a.eps, a.half);
-    if (h < a.Hq) {
-      *reinterpret_cast<uint2*>(dst + h * D + p.oa) = pack4(x);
-      *reinterpret_cast<uint2*>(dst + h * D + p.ob) = pack4(x + 4);
+  for (int h0 = 0; h0 < a.Hq; h0 += ILP * groups) {
+    if (h0 > 0) load(h0);
+#pragma unroll
+    for (int i = 0; i < ILP; ++i) {
+      const int h = h0 + i * groups + grp;
+      float x[8];
+      unpack4(raw[i].a, x);
+      unpack4(raw[i].b, x + 4);
+      norm_rotate<TPR, HALF>(x, norm, gamma, p, cs, a.eps);
+      if (h < a.Hq) {
+        *reinterpret_cast<uint2*>(dst + h * D + p.oa) = pack4(x);
+        *reinterpret_cast<uint2*>(dst + h * D + p.ob) = pack4(x + 4);
+      }
     }
   }
 }
 
 // Blocks [0, 2 Hkv items): cache blocks; the rest: one query block per token.
-template <int D, int PASSES>
-__global__ void __launch_bounds__(1024) kv_append_kernel(KaArgs a) {
+template <int D, int PASSES, bool HALF, int THREADS>
+__global__ void __launch_bounds__(THREADS) kv_append_kernel(KaArgs a) {
   pdl_enter();
   const int n_cache = 2 * a.c.n_kv_heads * a.items;
   int i = blockIdx.x;
   if (i < n_cache) {
     const bool is_v = i & 1;
     i >>= 1;
-    append_block<D, PASSES>(a, i / a.c.n_kv_heads, i % a.c.n_kv_heads, is_v);
+    const int item = i / a.c.n_kv_heads, head = i - item * a.c.n_kv_heads;
+    if (is_v) append_block<D, PASSES, HALF, true>(a, item, head);
+    else append_block<D, PASSES, HALF, false>(a, item, head);
   } else {
-    query_block<D>(a, i - n_cache);
+    query_block<D, HALF>(a, i - n_cache);
   }
 }
 
-template <int D, int PASSES>
+template <int D, int PASSES, int THREADS>
 cudaError_t launch(const KaArgs& a, int threads, cudaStream_t s) {
   const int64_t blocks = int64_t(2) * a.c.n_kv_heads * a.items + (a.q ? a.T : 0);
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   count_launches(1);
-  return launch_pdl(kv_append_kernel<D, PASSES>, static_cast<unsigned>(blocks), threads, 0, s, a);
+  const unsigned n = static_cast<unsigned>(blocks);
+  return a.half ? launch_pdl(kv_append_kernel<D, PASSES, true, THREADS>, n, threads, 0, s, a)
+                : launch_pdl(kv_append_kernel<D, PASSES, false, THREADS>, n, threads, 0, s, a);
 }
 
 template <int D>
 cudaError_t launch_d(const KaArgs& a, cudaStream_t s) {
   // rows of eight elements a thread, at most four a thread
-  const int work = a.c.page_size * (D / 8);
-  if (work <= kQueryThreads) return launch<D, 1>(a, kQueryThreads, s);
-  if (work <= 2 * kQueryThreads) return launch<D, 2>(a, kQueryThreads, s);
-  return launch<D, 4>(a, std::max(kQueryThreads, work / 4), s);
+  const int work = a.c.page_size * (D / 8), threads = std::max(kQueryThreads, work / 4);
+  if (work <= kQueryThreads) return launch<D, 1, kQueryThreads>(a, kQueryThreads, s);
+  if (work <= 2 * kQueryThreads) return launch<D, 2, kQueryThreads>(a, kQueryThreads, s);
+  if (threads <= 256) return launch<D, 4, 256>(a, threads, s);
+  return launch<D, 4, D == 256 ? 1024 : 512>(a, threads, s);
 }
 
 bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
