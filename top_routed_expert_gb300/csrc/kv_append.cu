@@ -2,9 +2,10 @@
 // norm, rotation, page scale and E4M3 codes in one launch.
 //
 // Two kinds of blocks.  A cache block owns one page of one request for one
-// head, keys or values: all new tokens of the page pass through its
-// registers, so the page's scale is one block reduction and every code is
-// written once.  A query block owns one token and turns all its query heads.
+// head, keys and values: all new tokens of the page pass through its
+// registers, so the page's scales are one block reduction and every code is
+// written once.  A query block owns a token, or a few where a token has few
+// heads, and turns all query heads.
 //
 // Which pages a ragged batch touches is known on the device only.  A request
 // of n new tokens touches at most n/page + 2 pages, so request b's blocks
@@ -32,7 +33,7 @@ struct KaArgs {
   moe_kv_cache_t c;
   unsigned* status;
   int64_t qs, ks, vs, qos;
-  int T, B, Hq, rot, n_pos, items;   // items: page blocks per head, keys or values
+  int T, B, Hq, rot, n_pos, items;   // items: page blocks per head
   float eps;
   bool half;
 };
@@ -164,12 +165,44 @@ __device__ __forceinline__ int table_row(const KaArgs& a, int t, int pos) {
   return (p >= 0 && p < a.n_pos) ? p : -1;
 }
 
-// One page, one head, keys or values.  PASSES rows per thread group; the
-// block covers the page's slots in PASSES rounds of blockDim / TPR rows.
-template <int D, int PASSES, bool HALF, bool IS_V>
+// The new codes of a thread's eight elements, or the old ones rounded to a scale
+// that has grown.
+__device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, const float (&x)[8], float inv) {
+  const uint32_t lo = codes4(x, inv), hi = codes4(x + 4, inv);
+  if (p.ob == p.oa + 4) {
+    *reinterpret_cast<uint2*>(row + p.oa) = make_uint2(lo, hi);
+  } else {
+    *reinterpret_cast<uint32_t*>(row + p.oa) = lo;
+    *reinterpret_cast<uint32_t*>(row + p.ob) = hi;
+  }
+}
+__device__ __forceinline__ void rescale_codes(uint8_t* row, const Place& p, float f) {
+  uint32_t* wa = reinterpret_cast<uint32_t*>(row + p.oa);
+  uint32_t* wb = reinterpret_cast<uint32_t*>(row + p.ob);
+  *wa = rescale4(*wa, f);
+  *wb = rescale4(*wb, f);
+}
+
+// Largest finite size of eight elements; bad: one of them is not finite.
+__device__ __forceinline__ float largest(const float (&x)[8], bool& bad) {
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max_or_nan(top, fabsf(x[e]));
+  if (top < INFINITY) return top;
+  bad = true;
+  top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (fabsf(x[e]) < INFINITY) top = fmaxf(top, fabsf(x[e]));
+  return top;
+}
+
+// One page, one head.  PASSES rows per thread group; the block covers the
+// page's slots in PASSES rounds of blockDim / TPR rows.
+template <int D, int PASSES, bool HALF>
 __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head) {
   constexpr int TPR = D / 8;
-  __shared__ float s_amax[32];
+  __shared__ float s_amax[2][32];
   const int ps = a.c.page_size, ps_log = 31 - __clz(ps);
   const int b = warp_find_request(a.cu, a.B, item, 1, ps, 2);
   const Request r = load_request(a.cu, a.kv_len, b, a.T);
@@ -185,24 +218,27 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
   int pid = -1;
   if (page < a.c.max_pages) pid = a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page];
   const int lr = threadIdx.x % TPR, grp = threadIdx.x / TPR, rows = blockDim.x / TPR;
-  const bool rotates = !IS_V && a.rot > 0, norm = !IS_V && a.gamma_k;
-  const Place p = place_of<HALF>(lr, IS_V ? 0 : a.rot);
-  const uint16_t* src = (IS_V ? a.v : a.k) + static_cast<int64_t>(head) * D;
-  const int64_t stride = IS_V ? a.vs : a.ks;
+  const bool norm = a.gamma_k;
+  const Place p = place_of<HALF>(lr, a.rot), pv = place_of<HALF>(lr, 0);
   const int t0 = r.row0 - r.start;         // row of position 0
   Gamma gamma = {};
   if (norm) gamma = load_gamma(a.gamma_k, p);
-  Raw raw[PASSES];
+  Raw rk[PASSES];
+  uint4 rv[PASSES];
   float2 cs[PASSES][4];
   bool take[PASSES], outside = false;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int j = base + i * rows + grp;
     take[i] = j >= r.start && j < r.end && j < base + ps;
-    raw[i] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
-    if (take[i]) raw[i] = load_raw(src + (t0 + j) * stride, p);
+    rk[i] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
+    rv[i] = make_uint4(0, 0, 0, 0);
+    if (take[i]) {
+      rk[i] = load_raw(a.k + (t0 + j) * a.ks + static_cast<int64_t>(head) * D, p);
+      rv[i] = *reinterpret_cast<const uint4*>(a.v + (t0 + j) * a.vs + static_cast<int64_t>(head) * D + pv.oa);
+    }
   }
-  if (rotates) {
+  if (a.rot > 0) {
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int j = base + i * rows + grp;
@@ -211,6 +247,7 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
       if (f < 0) {
         outside = true;
         take[i] = false;
+        rv[i] = make_uint4(0, 0, 0, 0);
       } else if (p.rotates) {
         load_cs<HALF>(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), p, cs[i]);
       }
@@ -220,133 +257,169 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
     if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     return;
   }
-  float* scale_at = (IS_V ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(pid) * a.c.n_kv_heads + head;
+  const int64_t scale_at = static_cast<int64_t>(pid) * a.c.n_kv_heads + head;
   const bool had = r.start > base;
-  const float old = had ? *scale_at : 0.f;
-  float x[PASSES][8], amax = 0.f;
+  const float old_k = had ? a.c.k_scale[scale_at] : 0.f, old_v = had ? a.c.v_scale[scale_at] : 0.f;
+  float x[PASSES][8], top_k = 0.f;
+  uint32_t bits_v = 0;   // the largest size among the values as bf16 bits
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    unpack4(raw[i].a, x[i]);
-    unpack4(raw[i].b, x[i] + 4);
-    if (!IS_V) norm_rotate<TPR, HALF>(x[i], norm, gamma, p, cs[i], a.eps);
-    float top = 0.f;   // a NaN or an infinity makes it one of them
+    unpack4(rk[i].a, x[i]);
+    unpack4(rk[i].b, x[i] + 4);
+    norm_rotate<TPR, HALF>(x[i], norm, gamma, p, cs[i], a.eps);
+    if (take[i]) top_k = fmaxf(top_k, largest(x[i], bad));
+    const uint32_t w = __vmaxu2(__vmaxu2(rv[i].x & 0x7fff7fffu, rv[i].y & 0x7fff7fffu),
+                                __vmaxu2(rv[i].z & 0x7fff7fffu, rv[i].w & 0x7fff7fffu));
+    bits_v = __vmaxu2(bits_v, w);
+  }
+  bits_v = max(bits_v & 0xffffu, bits_v >> 16);
+  float top_v = __uint_as_float(bits_v << 16);
+  if (bits_v >= 0x7f80u) {   // an infinity or a NaN among them
+    top_v = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max_or_nan(top, fabsf(x[i][e]));
-    if (!take[i]) continue;
-    if (top < INFINITY) {
-      amax = fmaxf(amax, top);
-    } else {
-      bad = true;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (fabsf(x[i][e]) < INFINITY) amax = fmaxf(amax, fabsf(x[i][e]));
+    for (int i = 0; i < PASSES; ++i) {
+      float y[8];
+      unpack4(make_uint2(rv[i].x, rv[i].y), y);
+      unpack4(make_uint2(rv[i].z, rv[i].w), y + 4);
+      top_v = fmaxf(top_v, largest(y, bad));
     }
   }
   if (bad) set_status(a.status, MOE_ERR_DEVICE_NONFINITE);
   if (outside && lr == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
   // sizes order like their bits
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-  if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = amax;
-  __syncthreads();   // also: every thread has read the old scale
-  for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) amax = fmaxf(amax, s_amax[w]);
-  const float scale = fmaxf(scale_for(amax), old);
-  if (threadIdx.x == 0) *scale_at = scale;
-  const float inv = 1.0f / scale;
-  uint8_t* codes = static_cast<uint8_t*>(IS_V ? a.c.v : a.c.k) + pid * a.c.page_stride + head * a.c.head_stride;
+  top_k = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_k)));
+  top_v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_v)));
+  if ((threadIdx.x & 31) == 0) {
+    s_amax[0][threadIdx.x >> 5] = top_k;
+    s_amax[1][threadIdx.x >> 5] = top_v;
+  }
+  __syncthreads();   // also: every thread has read the old scales
+  for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) {
+    top_k = fmaxf(top_k, s_amax[0][w]);
+    top_v = fmaxf(top_v, s_amax[1][w]);
+  }
+  const float sk = fmaxf(scale_for(top_k), old_k), sv = fmaxf(scale_for(top_v), old_v);
+  if (threadIdx.x == 0) {
+    a.c.k_scale[scale_at] = sk;
+    a.c.v_scale[scale_at] = sv;
+  }
+  const float inv_k = 1.0f / sk, inv_v = 1.0f / sv;
+  const int64_t page_at = pid * a.c.page_stride + head * a.c.head_stride;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int j = base + i * rows + grp;
-    uint8_t* row = codes + (j - base) * a.c.token_stride;
+    const int64_t row = page_at + (j - base) * a.c.token_stride;
+    uint8_t* kc = static_cast<uint8_t*>(a.c.k) + row;
+    uint8_t* vc = static_cast<uint8_t*>(a.c.v) + row;
     if (take[i]) {
-      const uint32_t lo = codes4(x[i], inv), hi = codes4(x[i] + 4, inv);
-      if (p.ob == p.oa + 4) {
-        *reinterpret_cast<uint2*>(row + p.oa) = make_uint2(lo, hi);
-      } else {
-        *reinterpret_cast<uint32_t*>(row + p.oa) = lo;
-        *reinterpret_cast<uint32_t*>(row + p.ob) = hi;
-      }
-    } else if (had && scale > old && j < r.start) {
-      uint32_t* wa = reinterpret_cast<uint32_t*>(row + p.oa);
-      uint32_t* wb = reinterpret_cast<uint32_t*>(row + p.ob);
-      *wa = rescale4(*wa, old * inv);
-      *wb = rescale4(*wb, old * inv);
+      store_codes(kc, p, x[i], inv_k);
+      float y[8];
+      unpack4(make_uint2(rv[i].x, rv[i].y), y);
+      unpack4(make_uint2(rv[i].z, rv[i].w), y + 4);
+      store_codes(vc, pv, y, inv_v);
+    } else if (had && j < r.start) {
+      if (sk > old_k) rescale_codes(kc, p, old_k * inv_k);
+      if (sv > old_v) rescale_codes(vc, pv, old_v * inv_v);
     }
   }
 }
 
-// All query heads of one token.  The first rows are on their way while the
-// token's request, position and angles are looked up.
-template <int D, bool HALF>
+// All query heads of TOKENS tokens from t on.  The first rows are on their way
+// while the tokens' requests, positions and angles are looked up.
+template <int D, bool HALF, int TOKENS>
 __device__ __forceinline__ void query_block(const KaArgs& a, int t) {
-  constexpr int TPR = D / 8, ILP = 4;
+  constexpr int TPR = D / 8, HEADS = 4 / TOKENS;   // heads that a thread has under way for each token
   const int lr = threadIdx.x % TPR, grp = threadIdx.x / TPR, groups = blockDim.x / TPR;
   const Place p = place_of<HALF>(lr, a.rot);
-  const uint16_t* src = a.q + t * a.qs;
-  uint16_t* dst = a.q_out + t * a.qos;
-  Raw raw[ILP];
+  Raw raw[TOKENS][HEADS];
   auto load = [&](int h0) {
 #pragma unroll
-    for (int i = 0; i < ILP; ++i) {
-      const int h = h0 + i * groups + grp;
-      raw[i] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
-      if (h < a.Hq) raw[i] = load_raw(src + h * D, p);
-    }
+    for (int n = 0; n < TOKENS; ++n)
+#pragma unroll
+      for (int i = 0; i < HEADS; ++i) {
+        const int h = h0 + i * groups + grp;
+        raw[n][i] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
+        if (h < a.Hq && t + n < a.T) raw[n][i] = load_raw(a.q + (t + n) * a.qs + h * D, p);
+      }
   };
   load(0);
   const bool norm = a.gamma_q;
   Gamma gamma = {};
   if (norm) gamma = load_gamma(a.gamma_q, p);
-  float2 cs[4] = {};
-  const int b = warp_find_request(a.cu, a.B, t, 1, 1, 0);
-  const Request r = load_request(a.cu, a.kv_len, b, a.T);
-  if (!r.ok || r.start < 0 || t < r.row0 || t >= r.row0 + r.n) return;   // recorded by the cache blocks, or no request's row
-  if (a.rot > 0) {
-    const int f = table_row(a, t, r.start + (t - r.row0));
-    if (f < 0) {
-      if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-      return;
+  float2 cs[TOKENS][4] = {};
+  bool live[TOKENS];
+  int b = warp_find_request(a.cu, a.B, t, 1, 1, 0);
+  Request r = load_request(a.cu, a.kv_len, b, a.T);
+#pragma unroll
+  for (int n = 0; n < TOKENS; ++n) {
+    while (TOKENS > 1 && r.ok && t + n >= r.row0 + r.n && b + 1 < a.B) r = load_request(a.cu, a.kv_len, ++b, a.T);
+    // not live: recorded by the cache blocks, or no request's row
+    live[n] = r.ok && r.start >= 0 && t + n >= r.row0 && t + n < r.row0 + r.n;
+    if (live[n] && a.rot > 0) {
+      const int f = table_row(a, t + n, r.start + (t + n - r.row0));
+      live[n] = f >= 0;
+      if (f < 0 && threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      if (f >= 0 && p.rotates) load_cs<HALF>(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), p, cs[n]);
     }
-    if (p.rotates) load_cs<HALF>(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), p, cs);
   }
   // every thread makes the same number of rounds: the norm's shuffles need all lanes
-  for (int h0 = 0; h0 < a.Hq; h0 += ILP * groups) {
+  for (int h0 = 0; h0 < a.Hq; h0 += HEADS * groups) {
     if (h0 > 0) load(h0);
 #pragma unroll
-    for (int i = 0; i < ILP; ++i) {
-      const int h = h0 + i * groups + grp;
-      float x[8];
-      unpack4(raw[i].a, x);
-      unpack4(raw[i].b, x + 4);
-      norm_rotate<TPR, HALF>(x, norm, gamma, p, cs, a.eps);
-      if (h < a.Hq) {
-        *reinterpret_cast<uint2*>(dst + h * D + p.oa) = pack4(x);
-        *reinterpret_cast<uint2*>(dst + h * D + p.ob) = pack4(x + 4);
+    for (int n = 0; n < TOKENS; ++n)
+#pragma unroll
+      for (int i = 0; i < HEADS; ++i) {
+        const int h = h0 + i * groups + grp;
+        float x[8];
+        unpack4(raw[n][i].a, x);
+        unpack4(raw[n][i].b, x + 4);
+        norm_rotate<TPR, HALF>(x, norm, gamma, p, cs[n], a.eps);
+        if (h < a.Hq && live[n]) {
+          uint16_t* dst = a.q_out + (t + n) * a.qos + h * D;
+          *reinterpret_cast<uint2*>(dst + p.oa) = pack4(x);
+          *reinterpret_cast<uint2*>(dst + p.ob) = pack4(x + 4);
+        }
       }
-    }
   }
 }
 
-// Blocks [0, 2 Hkv items): cache blocks; the rest: one query block per token.
+// Tokens of a query block: four heads a thread in all.
+template <int D> __host__ __device__ __forceinline__ int query_tokens(int Hq, int threads) {
+  const int groups = threads / (D / 8);
+  return Hq <= groups ? 4 : Hq <= 2 * groups ? 2 : 1;
+}
+
+// Blocks [0, Hkv items): cache blocks; the rest: query blocks.
+// Blocks on an SM that the registers are cut for: more of them hide more of the
+// look-ups' latency (prefill of 32 x 256 tokens, two rows a thread: 37.4 us with
+// the compiler's choice of 5, 32.6 us with 7; ragged prompts with four rows a
+// thread: 67.6 and 58.7 us).
+template <int PASSES, int THREADS> constexpr int blocks_on_sm() {
+  return THREADS == 128 ? (PASSES < 4 ? 7 : 6) : THREADS == 256 ? 3 : 1;
+}
+
 template <int D, int PASSES, bool HALF, int THREADS>
-__global__ void __launch_bounds__(THREADS) kv_append_kernel(KaArgs a) {
+__global__ void __launch_bounds__(THREADS, blocks_on_sm<PASSES, THREADS>()) kv_append_kernel(KaArgs a) {
   pdl_enter();
-  const int n_cache = 2 * a.c.n_kv_heads * a.items;
-  int i = blockIdx.x;
+  const int n_cache = a.c.n_kv_heads * a.items, i = blockIdx.x;
   if (i < n_cache) {
-    const bool is_v = i & 1;
-    i >>= 1;
-    const int item = i / a.c.n_kv_heads, head = i - item * a.c.n_kv_heads;
-    if (is_v) append_block<D, PASSES, HALF, true>(a, item, head);
-    else append_block<D, PASSES, HALF, false>(a, item, head);
-  } else {
-    query_block<D, HALF>(a, i - n_cache);
+    const int item = i / a.c.n_kv_heads;
+    append_block<D, PASSES, HALF>(a, item, i - item * a.c.n_kv_heads);
+    return;
+  }
+  const int q = i - n_cache;
+  switch (query_tokens<D>(a.Hq, blockDim.x)) {
+    case 4: query_block<D, HALF, 4>(a, 4 * q); break;
+    case 2: query_block<D, HALF, 2>(a, 2 * q); break;
+    default: query_block<D, HALF, 1>(a, q); break;
   }
 }
 
 template <int D, int PASSES, int THREADS>
 cudaError_t launch(const KaArgs& a, int threads, cudaStream_t s) {
-  const int64_t blocks = int64_t(2) * a.c.n_kv_heads * a.items + (a.q ? a.T : 0);
+  int64_t blocks = int64_t(a.c.n_kv_heads) * a.items;
+  if (a.q) blocks += ceil_div(a.T, query_tokens<D>(a.Hq, threads));
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   count_launches(1);
   const unsigned n = static_cast<unsigned>(blocks);
@@ -360,6 +433,7 @@ cudaError_t launch_d(const KaArgs& a, cudaStream_t s) {
   const int work = a.c.page_size * (D / 8), threads = std::max(kQueryThreads, work / 4);
   if (work <= kQueryThreads) return launch<D, 1, kQueryThreads>(a, kQueryThreads, s);
   if (work <= 2 * kQueryThreads) return launch<D, 2, kQueryThreads>(a, kQueryThreads, s);
+  if (threads <= kQueryThreads) return launch<D, 4, kQueryThreads>(a, threads, s);
   if (threads <= 256) return launch<D, 4, 256>(a, threads, s);
   return launch<D, 4, D == 256 ? 1024 : 512>(a, threads, s);
 }
