@@ -1,9 +1,19 @@
 // Expert selection from given logits (include/route_scores.h): scores, bias,
-// groups, top-k and weights of one token in one warp.
+// groups, top-k and weights of one token in one warp; a warp takes tokens in
+// turn and keeps the bias in registers.
 //
 // Lane l holds the EPL consecutive experts l*EPL .. l*EPL+EPL-1, so a token's
 // logits are one vector load per lane, a group of experts is a run of lanes,
 // and among lanes with equal values the lowest lane has the lowest expert.
+//
+// The choice is bound by instructions, not by bytes (a token of 256 experts is
+// 512 or 1024 bytes), so it is made of few:
+//  - each lane sorts its keys once (19 compare-exchanges of eight keys, each a
+//    minimum and a maximum; no index travels with them);
+//  - a round of the top-k is one warp maximum of the lanes' heads and one
+//    ballot; the lowest lane that holds it gives its head up;
+//  - which expert a key belongs to is looked up at the end, for the chosen ones
+//    alone, by the lane of their slot.
 #include <cmath>
 
 #include "common.cuh"
@@ -22,7 +32,7 @@ constexpr float kMasked = -INFINITY;
 // +0).  -infinity maps to 0x007fffff, so 0 is free to mark "not available".
 __device__ __forceinline__ uint32_t value_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 constexpr uint32_t kMaskedKey = 0x007fffffu;
 
@@ -35,12 +45,8 @@ struct RsArgs {
   int64_t stride;
   int T, E, k, G, tg, rank;
   float scale;
-  bool bf16, sigmoid, renorm;
+  bool sigmoid, renorm, vectors;   // vectors: rows can be read EPL elements at a time
 };
-
-__device__ __forceinline__ float load_logit(const RsArgs& a, int64_t i) {
-  return a.bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.logits)[i]) : static_cast<const float*>(a.logits)[i];
-}
 
 // Larger of two (largest, second largest) pairs' union.
 __device__ __forceinline__ void merge_top2(float& t1, float& t2, float u1, float u2) {
@@ -48,127 +54,252 @@ __device__ __forceinline__ void merge_top2(float& t1, float& t2, float u1, float
   t1 = fmaxf(t1, u1);
 }
 
-template <int EPL>
-__global__ void __launch_bounds__(kRsWarps * 32) route_scores_kernel(RsArgs a) {
-  __shared__ float sval[kRsWarps][32 * EPL];
-  pdl_enter();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kRsWarps + warp;
-  if (t >= a.T) return;
-  float L[EPL], s[EPL], c[EPL];
-  bool bad = false;
-  float top = kMasked;
+// Descending order of N keys (N a power of two): Batcher's odd-even merge sort.
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&k)[N]) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane * EPL + i;
-    L[i] = e < a.E ? load_logit(a, t * a.stride + e) : kMasked;
-    if (!(L[i] < INFINITY)) { bad = true; L[i] = kMasked; }   // NaN or +infinity
-    top = fmaxf(top, L[i]);
-  }
-  // scores; numer keeps the softmax numerators
-  float numer[EPL];
-  if (a.sigmoid) {
+  for (int p = 1; p < N; p *= 2)
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) numer[i] = s[i] = 1.0f / (1.0f + expf(-L[i]));
-  } else {
+    for (int q = p; q > 0; q /= 2)
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (top == kMasked) top = 0.f;   // every expert masked
+      for (int j = q % p; j + q < N; j += 2 * q)
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) numer[i] = expf(L[i] - top);
-    // The denominator is a compensated sum (a two-term fp32 value, about 2^-45
-    // relative), so that its rounding, and with it the order of nearly equal
-    // biased scores, does not depend on the order of the addition.
-    float hi = 0.f, lo = 0.f;
-    auto add = [&](float x, float xlo) {
-      const float y = __fadd_rn(hi, x);
-      const float z = __fsub_rn(y, hi);
-      lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(y, z)), __fsub_rn(x, z)) + xlo;
-      hi = y;
-    };
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t a = k[i + j], b = k[i + j + q];
+            k[i + j] = max(a, b);
+            k[i + j + q] = min(a, b);
+          }
+}
+
+// The lane's EPL logits of a token as they lie in memory.
+template <int EPL, bool BF16> struct RawLogits {
+  static constexpr int kWords = BF16 ? (EPL + 1) / 2 : EPL;
+  uint32_t w[kWords];
+};
+
+template <int EPL, bool BF16>
+__device__ __forceinline__ RawLogits<EPL, BF16> load_logits(const RsArgs& a, int t, int lane) {
+  RawLogits<EPL, BF16> r;
+  constexpr int N = RawLogits<EPL, BF16>::kWords;
+  if (a.vectors) {
+    const uint32_t* p = static_cast<const uint32_t*>(a.logits) + (BF16 ? t * a.stride / 2 : t * a.stride) + lane * N;
+    if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) add(numer[i], 0.f);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) add(__shfl_xor_sync(0xffffffffu, hi, off), __shfl_xor_sync(0xffffffffu, lo, off));
-    const float Z = hi + lo;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) s[i] = Z > 0.f ? numer[i] / Z : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane * EPL + i;
-    if (a.bias && e < a.E) {
-      const float b = a.bias[e];
-      if (!(b < INFINITY)) bad = true;
-      c[i] = (b < INFINITY && L[i] > kMasked) ? __fadd_rn(s[i], b) : kMasked;
+      for (int i = 0; i < N; i += 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + i));
+        r.w[i] = v.x;
+        r.w[i + 1] = v.y;
+        r.w[i + 2] = v.z;
+        r.w[i + 3] = v.w;
+      }
     } else {
-      c[i] = L[i];
-    }
-  }
-  // groups
-  uint32_t keep = 0xffffffffu;
-  const int gs = a.E / a.G;
-  if (a.tg < a.G) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) sval[warp][lane * EPL + i] = (!a.bias && a.rank == 2) ? numer[i] : c[i];
-    __syncwarp();
-    float value = kMasked;
-    if (lane < a.G) {
-      float t1 = kMasked, t2 = kMasked;
-      for (int i = 0; i < gs; ++i) merge_top2(t1, t2, sval[warp][lane * gs + i], kMasked);
-      value = (a.rank == 2 && gs > 1) ? t1 + t2 : t1;
+      for (int i = 0; i < N; ++i) r.w[i] = __ldg(p + i);
     }
-    int better = 0;
-    for (int g = 0; g < a.G; ++g) {
-      const float v = __shfl_sync(0xffffffffu, value, g);
-      better += (v > value || (v == value && g < lane)) ? 1 : 0;
-    }
-    keep = __ballot_sync(0xffffffffu, lane < a.G && better < a.tg);
-  }
-  uint32_t key[EPL];
+  } else {
+    constexpr uint32_t none = BF16 ? 0xff80u : 0xff800000u;   // -infinity behind the last expert
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane * EPL + i;
-    key[i] = (e < a.E && ((keep >> (e / gs)) & 1u)) ? value_key(c[i]) : 0u;
-  }
-  // k rounds: the warp's largest key, the lowest expert that holds it
-  float my_s = 0.f, sum = 0.f;
-  int my_e = 0;
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t bk = 0u;
-    int bi = 0;
-    float bs = 0.f;
+    for (int i = 0; i < N; ++i) r.w[i] = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const bool better = key[i] > bk;
-      bk = better ? key[i] : bk;
-      bi = better ? i : bi;
-      bs = better ? s[i] : bs;
+      const int e = lane * EPL + i;
+      const int64_t at = t * a.stride + e;
+      if (BF16) r.w[i / 2] |= static_cast<uint32_t>(e < a.E ? __ldg(static_cast<const uint16_t*>(a.logits) + at) : none) << (16 * (i & 1));
+      else r.w[i] = e < a.E ? __ldg(static_cast<const uint32_t*>(a.logits) + at) : none;
     }
-    const uint32_t wk = __reduce_max_sync(0xffffffffu, bk);
-    const int src = __ffs(__ballot_sync(0xffffffffu, bk == wk)) - 1;
-    const int e = src * EPL + __shfl_sync(0xffffffffu, bi, src);
-    float v = __shfl_sync(0xffffffffu, bs, src);
-    if (wk <= kMaskedKey) v = 0.f;
-    if (lane == src) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) key[i] = i == bi ? 0u : key[i];
-    }
-    sum += v;
-    if (lane == j) { my_s = v; my_e = e; }
   }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(a.status, MOE_ERR_DEVICE_NONFINITE);
-  if (lane < a.k) {
-    const float w = a.renorm ? (sum > 0.f ? my_s / sum : 0.f) : my_s;
-    a.ids[static_cast<int64_t>(t) * a.k + lane] = my_e;
-    a.w[static_cast<int64_t>(t) * a.k + lane] = w * a.scale;
+  return r;
+}
+
+template <int EPL, bool BF16>
+__global__ void __launch_bounds__(kRsWarps * 32) route_scores_kernel(RsArgs a) {
+  // per warp: a token's keys (first the values that rank groups) and scores
+  __shared__ __align__(16) uint32_t s_key[kRsWarps][32 * EPL];
+  __shared__ __align__(16) float s_score[kRsWarps][32 * EPL];
+  pdl_enter();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = gridDim.x * kRsWarps;
+  int t = blockIdx.x * kRsWarps + warp;
+  if (t >= a.T) return;
+  RawLogits<EPL, BF16> raw = load_logits<EPL, BF16>(a, t, lane);
+  float bias[EPL];
+  bool bad_bias = false;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane * EPL + i;
+    bias[i] = a.bias && e < a.E ? a.bias[e] : 0.f;
+    if (!(bias[i] < INFINITY)) {   // NaN or +infinity: a mask
+      bad_bias = true;
+      bias[i] = kMasked;
+    }
+  }
+  const int gs = a.E / a.G;
+  // groups that are a power of two of whole lanes are ranked by shuffles
+  const int lpg = gs / EPL;
+  const bool by_lanes = gs == lpg * EPL && (lpg & (lpg - 1)) == 0;
+  const int my_group = lane * EPL / gs;   // by_lanes
+
+  while (true) {
+    float L[EPL], s[EPL], c[EPL];
+    bool bad = bad_bias;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      if (BF16) L[i] = __uint_as_float(i & 1 ? raw.w[i / 2] & 0xffff0000u : raw.w[i / 2] << 16);
+      else L[i] = __uint_as_float(raw.w[i]);
+      if (!(L[i] < INFINITY)) {   // NaN or +infinity: a mask
+        bad = true;
+        L[i] = kMasked;
+      }
+    }
+    const int next = t + warps;
+    if (next < a.T) raw = load_logits<EPL, BF16>(a, next, lane);
+    // scores; numer keeps the softmax numerators
+    float numer[EPL];
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) numer[i] = s[i] = __frcp_rn(1.0f + expf(-L[i]));
+    } else {
+      float top = kMasked;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) top = fmaxf(top, L[i]);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      if (top == kMasked) top = 0.f;   // every expert masked
+      // The denominator is a compensated sum (a two-term fp32 value, about 2^-45
+      // relative), so that its rounding, and with it the order of nearly equal
+      // biased scores, does not depend on the order of the addition.
+      float hi = 0.f, lo = 0.f;
+      auto add = [&](float x, float xlo) {
+        const float y = __fadd_rn(hi, x);
+        const float z = __fsub_rn(y, hi);
+        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(y, z)), __fsub_rn(x, z)) + xlo;
+        hi = y;
+      };
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        numer[i] = expf(L[i] - top);
+        add(numer[i], 0.f);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+        add(__shfl_xor_sync(0xffffffffu, hi, off), __shfl_xor_sync(0xffffffffu, lo, off));
+      const float Z = hi + lo;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) s[i] = Z > 0.f ? __fdiv_rn(numer[i], Z) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = !a.bias ? L[i] : L[i] > kMasked ? __fadd_rn(s[i], bias[i]) : kMasked;
+    // groups
+    uint32_t keep = 0xffffffffu;   // by_lanes: of this lane; else a bit a group
+    if (a.tg < a.G) {
+      const bool use_numer = !a.bias && a.rank == 2;
+      float t1 = kMasked, t2 = kMasked;
+      int better = 0;
+      if (by_lanes) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) merge_top2(t1, t2, use_numer ? numer[i] : c[i], kMasked);
+        for (int off = 1; off < lpg; off <<= 1) {
+          const float u1 = __shfl_xor_sync(0xffffffffu, t1, off), u2 = __shfl_xor_sync(0xffffffffu, t2, off);
+          merge_top2(t1, t2, u1, u2);
+        }
+        const float value = (a.rank == 2 && gs > 1) ? t1 + t2 : t1;
+        for (int g = 0; g < a.G; ++g) {
+          const float v = __shfl_sync(0xffffffffu, value, g * lpg);
+          better += (v > value || (v == value && g < my_group)) ? 1 : 0;
+        }
+        keep = better < a.tg ? 0xffffffffu : 0u;
+      } else {
+        float* val = reinterpret_cast<float*>(s_key[warp]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) val[lane * EPL + i] = use_numer ? numer[i] : c[i];
+        __syncwarp();
+        if (lane < a.G)
+          for (int i = 0; i < gs; ++i) merge_top2(t1, t2, val[lane * gs + i], kMasked);
+        const float value = (a.rank == 2 && gs > 1) ? t1 + t2 : t1;
+        for (int g = 0; g < a.G; ++g) {
+          const float v = __shfl_sync(0xffffffffu, value, g);
+          better += (v > value || (v == value && g < lane)) ? 1 : 0;
+        }
+        const unsigned bits = __ballot_sync(0xffffffffu, lane < a.G && better < a.tg);
+        keep = 0u;   // a bit for each of this lane's experts
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) keep |= ((bits >> ((lane * EPL + i) / gs)) & 1u) << i;
+        __syncwarp();
+      }
+    }
+    uint32_t key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane * EPL + i;
+      key[i] = (e < a.E && ((keep >> i) & 1u)) ? value_key(c[i]) : 0u;
+      s_key[warp][e] = key[i];
+      s_score[warp][e] = s[i];
+    }
+    // k rounds: the warp's largest key, from the lowest lane that holds it
+    sort_descending<EPL>(key);
+    uint32_t my_key = 0u;
+    int my_src = 0;
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t wk = __reduce_max_sync(0xffffffffu, key[0]);
+      const int src = __ffs(__ballot_sync(0xffffffffu, key[0] == wk)) - 1;
+      if (lane == src) {
+#pragma unroll
+        for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
+        key[EPL - 1] = 0u;
+      }
+      if (lane == j) {
+        my_key = wk;
+        my_src = src;
+      }
+    }
+    // The expert of slot `lane`: the lane that gave the key gives equal ones one
+    // after the other, lowest expert first.
+    const uint32_t before_key = __shfl_up_sync(0xffffffffu, my_key, 1);
+    const int before_src = __shfl_up_sync(0xffffffffu, my_src, 1);
+    const unsigned starts = __ballot_sync(0xffffffffu, lane == 0 || before_key != my_key || before_src != my_src);
+    int nth = lane - (31 - __clz(starts & (0xffffffffu >> (31 - lane))));
+    int my_e = my_src * EPL;
+    __syncwarp();
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const bool hit = !found && s_key[warp][my_src * EPL + i] == my_key;
+      if (hit && nth == 0) {
+        my_e = my_src * EPL + i;
+        found = true;
+      }
+      if (hit) --nth;
+    }
+    float my_s = lane < a.k && my_key > kMaskedKey ? s_score[warp][my_e] : 0.f;
+    float sum = my_s;
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);   // k <= 16 slots
+    if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(a.status, MOE_ERR_DEVICE_NONFINITE);
+    if (lane < a.k) {
+      if (a.renorm) my_s = sum > 0.f ? my_s / sum : 0.f;
+      a.ids[static_cast<int64_t>(t) * a.k + lane] = my_e;
+      a.w[static_cast<int64_t>(t) * a.k + lane] = my_s * a.scale;
+    }
+    if (next >= a.T) return;
+    t = next;
+    __syncwarp();   // the token's keys and scores have been read
   }
 }
 
+// Blocks on an SM at most; a long batch's warps then take several tokens each.
+constexpr int kRsBlocks = 8;
+
 template <int EPL>
-cudaError_t launch(const RsArgs& a, cudaStream_t s) {
+cudaError_t launch(RsArgs a, bool bf16, int num_sms, cudaStream_t s) {
+  const uintptr_t base = reinterpret_cast<uintptr_t>(a.logits);
+  const int row_bytes = EPL * (bf16 ? 2 : 4);   // a lane's
+  const size_t align = row_bytes >= 16 ? 16 : 4;
+  a.vectors = a.E == 32 * EPL && row_bytes % 4 == 0 && base % align == 0 && a.stride * (bf16 ? 2 : 4) % align == 0;
+  const int blocks = std::min(ceil_div(a.T, kRsWarps), num_sms * kRsBlocks);
   count_launches(1);
-  return launch_pdl(route_scores_kernel<EPL>, ceil_div(a.T, kRsWarps), kRsWarps * 32, 0, s, a);
+  return bf16 ? launch_pdl(route_scores_kernel<EPL, true>, blocks, kRsWarps * 32, 0, s, a)
+              : launch_pdl(route_scores_kernel<EPL, false>, blocks, kRsWarps * 32, 0, s, a);
 }
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -198,14 +329,28 @@ extern "C" moe_status_t moe_route_scores(const moe_route_scores_config_t* c, con
   int sms = 0;
   const moe_status_t st = current_device(&status, &sms);
   if (st != MOE_OK) return st;
-  const RsArgs a = {logits,  bias,      topk_ids,        topk_w,          status,   c->logit_stride,
-                    c->T,    c->n_experts, c->top_k,     c->n_groups,     c->top_groups, c->group_rank,
-                    c->scale, esz == 2,  c->score == MOE_SCORE_SIGMOID, c->renormalise != 0};
+  RsArgs a;
+  a.logits = logits;
+  a.bias = bias;
+  a.ids = topk_ids;
+  a.w = topk_w;
+  a.status = status;
+  a.stride = c->logit_stride;
+  a.T = c->T;
+  a.E = c->n_experts;
+  a.k = c->top_k;
+  a.G = c->n_groups;
+  a.tg = c->top_groups;
+  a.rank = c->group_rank;
+  a.scale = c->scale;
+  a.sigmoid = c->score == MOE_SCORE_SIGMOID;
+  a.renorm = c->renormalise != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = c->logit_dtype == MOE_BF16;
   cudaError_t err;
-  if (a.E <= 32) err = launch<1>(a, s);
-  else if (a.E <= 64) err = launch<2>(a, s);
-  else if (a.E <= 128) err = launch<4>(a, s);
-  else err = launch<8>(a, s);
+  if (a.E <= 32) err = launch<1>(a, bf16, sms, s);
+  else if (a.E <= 64) err = launch<2>(a, bf16, sms, s);
+  else if (a.E <= 128) err = launch<4>(a, bf16, sms, s);
+  else err = launch<8>(a, bf16, sms, s);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
