@@ -48,10 +48,43 @@ struct RsArgs {
   bool sigmoid, renorm, vectors;   // vectors: rows can be read EPL elements at a time
 };
 
-// Larger of two (largest, second largest) pairs' union.
-__device__ __forceinline__ void merge_top2(float& t1, float& t2, float u1, float u2) {
-  t2 = fmaxf(fminf(t1, u1), fmaxf(t2, u2));
-  t1 = fmaxf(t1, u1);
+// The two largest of two (largest, second largest) pairs.
+struct Top2 {
+  float first, second;
+};
+__device__ __forceinline__ Top2 merge(const Top2& a, const Top2& b) {
+  return Top2{fmaxf(a.first, b.first), fmaxf(fmaxf(fminf(a.first, b.first), a.second), b.second)};
+}
+// The two largest of N values (N a power of two).
+template <int N>
+__device__ __forceinline__ Top2 top2_of(const float (&v)[N]) {
+  Top2 t[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = Top2{v[i], kMasked};
+#pragma unroll
+  for (int n = N / 2; n > 0; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; ++i) t[i] = merge(t[i], t[i + n]);
+  return t[0];
+}
+
+// The larger of two values, NaN if either is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// N words of a lane into shared memory, 16 bytes at a time where there are as many.
+template <int N>
+__device__ __forceinline__ void put(uint32_t* to, const uint32_t (&v)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(to + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) to[i] = v[i];
+  }
 }
 
 // Descending order of N keys (N a power of two): Batcher's odd-even merge sort.
@@ -112,8 +145,12 @@ __device__ __forceinline__ RawLogits<EPL, BF16> load_logits(const RsArgs& a, int
   return r;
 }
 
-template <int EPL, bool BF16>
-__global__ void __launch_bounds__(kRsWarps * 32) route_scores_kernel(RsArgs a) {
+// Blocks on an SM (64 registers a thread); a long batch's warps take several
+// tokens each.
+constexpr int kRsBlocks = 8;
+
+template <int EPL, bool BF16, bool SIGMOID, bool BIAS>
+__global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(RsArgs a) {
   // per warp: a token's keys (first the values that rank groups) and scores
   __shared__ __align__(16) uint32_t s_key[kRsWarps][32 * EPL];
   __shared__ __align__(16) float s_score[kRsWarps][32 * EPL];
@@ -127,7 +164,7 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scores_kernel(RsArgs a) {
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane * EPL + i;
-    bias[i] = a.bias && e < a.E ? a.bias[e] : 0.f;
+    bias[i] = BIAS && e < a.E ? a.bias[e] : 0.f;
     if (!(bias[i] < INFINITY)) {   // NaN or +infinity: a mask
       bad_bias = true;
       bias[i] = kMasked;
@@ -146,22 +183,27 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scores_kernel(RsArgs a) {
     for (int i = 0; i < EPL; ++i) {
       if (BF16) L[i] = __uint_as_float(i & 1 ? raw.w[i / 2] & 0xffff0000u : raw.w[i / 2] << 16);
       else L[i] = __uint_as_float(raw.w[i]);
-      if (!(L[i] < INFINITY)) {   // NaN or +infinity: a mask
-        bad = true;
-        L[i] = kMasked;
+    }
+    float top = L[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) top = max_or_nan(top, L[i]);
+    if (!(top < INFINITY)) {   // a NaN or +infinity among them: a mask
+      bad = true;
+      top = kMasked;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (!(L[i] < INFINITY)) L[i] = kMasked;
+        top = fmaxf(top, L[i]);
       }
     }
     const int next = t + warps;
     if (next < a.T) raw = load_logits<EPL, BF16>(a, next, lane);
     // scores; numer keeps the softmax numerators
     float numer[EPL];
-    if (a.sigmoid) {
+    if (SIGMOID) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) numer[i] = s[i] = __frcp_rn(1.0f + expf(-L[i]));
     } else {
-      float top = kMasked;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) top = fmaxf(top, L[i]);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
       if (top == kMasked) top = 0.f;   // every expert masked
@@ -188,38 +230,37 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scores_kernel(RsArgs a) {
       for (int i = 0; i < EPL; ++i) s[i] = Z > 0.f ? __fdiv_rn(numer[i], Z) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = !a.bias ? L[i] : L[i] > kMasked ? __fadd_rn(s[i], bias[i]) : kMasked;
+    for (int i = 0; i < EPL; ++i) c[i] = !BIAS ? L[i] : L[i] > kMasked ? __fadd_rn(s[i], bias[i]) : kMasked;
     // groups
     uint32_t keep = 0xffffffffu;   // by_lanes: of this lane; else a bit a group
     if (a.tg < a.G) {
-      const bool use_numer = !a.bias && a.rank == 2;
-      float t1 = kMasked, t2 = kMasked;
+      // what ranks the groups: the values, or without a bias the scores where two are added
+      float v[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = !BIAS && a.rank == 2 ? numer[i] : c[i];
       int better = 0;
       if (by_lanes) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) merge_top2(t1, t2, use_numer ? numer[i] : c[i], kMasked);
-        for (int off = 1; off < lpg; off <<= 1) {
-          const float u1 = __shfl_xor_sync(0xffffffffu, t1, off), u2 = __shfl_xor_sync(0xffffffffu, t2, off);
-          merge_top2(t1, t2, u1, u2);
-        }
-        const float value = (a.rank == 2 && gs > 1) ? t1 + t2 : t1;
+        Top2 two = top2_of<EPL>(v);
+        for (int off = 1; off < lpg; off <<= 1)
+          two = merge(two, Top2{__shfl_xor_sync(0xffffffffu, two.first, off), __shfl_xor_sync(0xffffffffu, two.second, off)});
+        const float value = (a.rank == 2 && gs > 1) ? two.first + two.second : two.first;
         for (int g = 0; g < a.G; ++g) {
-          const float v = __shfl_sync(0xffffffffu, value, g * lpg);
-          better += (v > value || (v == value && g < my_group)) ? 1 : 0;
+          const float u = __shfl_sync(0xffffffffu, value, g * lpg);
+          better += (u > value || (u == value && g < my_group)) ? 1 : 0;
         }
         keep = better < a.tg ? 0xffffffffu : 0u;
       } else {
-        float* val = reinterpret_cast<float*>(s_key[warp]);
-        __syncwarp();
+        float* val = s_score[warp];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) val[lane * EPL + i] = use_numer ? numer[i] : c[i];
+        for (int i = 0; i < EPL; ++i) val[lane * EPL + i] = v[i];
         __syncwarp();
+        Top2 two = {kMasked, kMasked};
         if (lane < a.G)
-          for (int i = 0; i < gs; ++i) merge_top2(t1, t2, val[lane * gs + i], kMasked);
-        const float value = (a.rank == 2 && gs > 1) ? t1 + t2 : t1;
+          for (int i = 0; i < gs; ++i) two = merge(two, Top2{val[lane * gs + i], kMasked});
+        const float value = (a.rank == 2 && gs > 1) ? two.first + two.second : two.first;
         for (int g = 0; g < a.G; ++g) {
-          const float v = __shfl_sync(0xffffffffu, value, g);
-          better += (v > value || (v == value && g < lane)) ? 1 : 0;
+          const float u = __shfl_sync(0xffffffffu, value, g);
+          better += (u > value || (u == value && g < lane)) ? 1 : 0;
         }
         const unsigned bits = __ballot_sync(0xffffffffu, lane < a.G && better < a.tg);
         keep = 0u;   // a bit for each of this lane's experts
@@ -228,14 +269,14 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scores_kernel(RsArgs a) {
         __syncwarp();
       }
     }
-    uint32_t key[EPL];
+    uint32_t key[EPL], score_bits[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = lane * EPL + i;
-      key[i] = (e < a.E && ((keep >> i) & 1u)) ? value_key(c[i]) : 0u;
-      s_key[warp][e] = key[i];
-      s_score[warp][e] = s[i];
+      key[i] = (lane * EPL + i < a.E && ((keep >> i) & 1u)) ? value_key(c[i]) : 0u;
+      score_bits[i] = __float_as_uint(s[i]);
     }
+    put(s_key[warp] + lane * EPL, key);
+    put(reinterpret_cast<uint32_t*>(s_score[warp]) + lane * EPL, score_bits);
     // k rounds: the warp's largest key, from the lowest lane that holds it
     sort_descending<EPL>(key);
     uint32_t my_key = 0u;
@@ -287,8 +328,14 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scores_kernel(RsArgs a) {
   }
 }
 
-// Blocks on an SM at most; a long batch's warps then take several tokens each.
-constexpr int kRsBlocks = 8;
+template <int EPL, bool BF16>
+cudaError_t launch(const RsArgs& a, int blocks, cudaStream_t s) {
+  if (a.sigmoid)
+    return a.bias ? launch_pdl(route_scores_kernel<EPL, BF16, true, true>, blocks, kRsWarps * 32, 0, s, a)
+                  : launch_pdl(route_scores_kernel<EPL, BF16, true, false>, blocks, kRsWarps * 32, 0, s, a);
+  return a.bias ? launch_pdl(route_scores_kernel<EPL, BF16, false, true>, blocks, kRsWarps * 32, 0, s, a)
+                : launch_pdl(route_scores_kernel<EPL, BF16, false, false>, blocks, kRsWarps * 32, 0, s, a);
+}
 
 template <int EPL>
 cudaError_t launch(RsArgs a, bool bf16, int num_sms, cudaStream_t s) {
@@ -298,8 +345,7 @@ cudaError_t launch(RsArgs a, bool bf16, int num_sms, cudaStream_t s) {
   a.vectors = a.E == 32 * EPL && row_bytes % 4 == 0 && base % align == 0 && a.stride * (bf16 ? 2 : 4) % align == 0;
   const int blocks = std::min(ceil_div(a.T, kRsWarps), num_sms * kRsBlocks);
   count_launches(1);
-  return bf16 ? launch_pdl(route_scores_kernel<EPL, true>, blocks, kRsWarps * 32, 0, s, a)
-              : launch_pdl(route_scores_kernel<EPL, false>, blocks, kRsWarps * 32, 0, s, a);
+  return bf16 ? launch<EPL, true>(a, blocks, s) : launch<EPL, false>(a, blocks, s);
 }
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
