@@ -11,7 +11,8 @@
 //  - each lane sorts its keys once (19 compare-exchanges of eight keys, each a
 //    minimum and a maximum; no index travels with them);
 //  - a round of the top-k is one warp maximum of the lanes' heads and one
-//    ballot; the lowest lane that holds it gives its head up;
+//    ballot; the lowest lane that holds it goes on to its next key, which waits
+//    in shared memory (moving a list up in registers took a third of a round);
 //  - which expert a key belongs to is looked up at the end, for the chosen ones
 //    alone, by the lane of their slot.
 #include <cmath>
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(
   // per warp: a token's keys (first the values that rank groups) and scores
   __shared__ __align__(16) uint32_t s_key[kRsWarps][32 * EPL];
   __shared__ __align__(16) float s_score[kRsWarps][32 * EPL];
+  __shared__ uint32_t s_sorted[kRsWarps][EPL + 1][32];   // each lane's keys in order, 0 behind the last
   pdl_enter();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = gridDim.x * kRsWarps;
   int t = blockIdx.x * kRsWarps + warp;
@@ -175,6 +177,7 @@ __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(
   const int lpg = gs / EPL;
   const bool by_lanes = gs == lpg * EPL && (lpg & (lpg - 1)) == 0;
   const int my_group = lane * EPL / gs;   // by_lanes
+  s_sorted[warp][EPL][lane] = 0u;
 
   while (true) {
     float L[EPL], s[EPL], c[EPL];
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(
 #pragma unroll
     for (int i = 0; i < EPL; ++i) c[i] = !BIAS ? L[i] : L[i] > kMasked ? __fadd_rn(s[i], bias[i]) : kMasked;
     // groups
-    uint32_t keep = 0xffffffffu;   // by_lanes: of this lane; else a bit a group
+    uint32_t keep = 0xffffffffu;   // by_lanes: all or nothing of this lane; else a bit for each of its experts
     if (a.tg < a.G) {
       // what ranks the groups: the values, or without a bias the scores where two are added
       float v[EPL];
@@ -263,31 +266,38 @@ __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(
           better += (u > value || (u == value && g < lane)) ? 1 : 0;
         }
         const unsigned bits = __ballot_sync(0xffffffffu, lane < a.G && better < a.tg);
-        keep = 0u;   // a bit for each of this lane's experts
+        keep = 0u;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) keep |= ((bits >> ((lane * EPL + i) / gs)) & 1u) << i;
         __syncwarp();
       }
     }
+    // keys; lanes behind the last expert hold masked ones, which no slot reaches
     uint32_t key[EPL], score_bits[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      key[i] = (lane * EPL + i < a.E && ((keep >> i) & 1u)) ? value_key(c[i]) : 0u;
+      key[i] = value_key(c[i]) & keep;
       score_bits[i] = __float_as_uint(s[i]);
+    }
+    if (!by_lanes && a.tg < a.G) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) key[i] = (keep >> i) & 1u ? value_key(c[i]) : 0u;
     }
     put(s_key[warp] + lane * EPL, key);
     put(reinterpret_cast<uint32_t*>(s_score[warp]) + lane * EPL, score_bits);
     // k rounds: the warp's largest key, from the lowest lane that holds it
     sort_descending<EPL>(key);
-    uint32_t my_key = 0u;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) s_sorted[warp][i][lane] = key[i];
+    uint32_t head = key[0], my_key = 0u;
+    const uint32_t* rest = &s_sorted[warp][1][lane];
     int my_src = 0;
     for (int j = 0; j < a.k; ++j) {
-      const uint32_t wk = __reduce_max_sync(0xffffffffu, key[0]);
-      const int src = __ffs(__ballot_sync(0xffffffffu, key[0] == wk)) - 1;
+      const uint32_t wk = __reduce_max_sync(0xffffffffu, head);
+      const int src = __ffs(__ballot_sync(0xffffffffu, head == wk)) - 1;
       if (lane == src) {
-#pragma unroll
-        for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
-        key[EPL - 1] = 0u;
+        head = *rest;
+        rest += 32;
       }
       if (lane == j) {
         my_key = wk;
