@@ -83,6 +83,26 @@ class MoELayer:
             return y, ids, w, offs
         return y
 
+    def forward_routed(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
+                       y: Optional[torch.Tensor] = None, stream=None):
+        """The experts, routed and shared, on a choice made elsewhere (moe_route_scores): permutation, expert FFN and
+        combine.  topk_ids [T, k] int32, topk_w [T, k] float32."""
+        T = x.shape[0]
+        cfg = self.config(T)
+        ws = self.workspace(T)
+        if y is None:
+            y = self.empty_y(T)
+        if T == 0:
+            return y
+        n, dt = T * self.k, torch.bfloat16 if self.flags & abi.MOE_FLAG_BF16_EXPERT_OUT else torch.float32
+        ints = torch.empty(self.E + 1 + 2 * n, dtype=torch.int32, device=self.device)
+        offsets, sorted_pair, row_of = ints.split([self.E + 1, n, n])
+        outs = torch.empty((n + T, self.d), dtype=dt, device=self.device)
+        abi.moe_permute(cfg, topk_ids, offsets, sorted_pair, row_of, ws, stream)
+        abi.moe_expert_ffn(cfg, x, topk_w, offsets, sorted_pair, self.weights, outs[:n], outs[n:], ws, stream)
+        abi.moe_combine(cfg, outs[:n], row_of, outs[n:], y, stream)
+        return y
+
     def capture(self, x: torch.Tensor, y: Optional[torch.Tensor] = None, warmup: int = 2):
         """Record one layer pass over the device buffers x -> y as a CUDA graph.
 
