@@ -787,8 +787,9 @@ bool attention_config_ok(const moe_paged_attention_config_t* c, const moe_kv_cac
   if (!c || !kv_cache_shape_ok(cache)) return false;
   if (c->T < 0 || c->T > (1 << 28) || c->batch < 1 || c->batch > kMaxBatch || c->max_q_len < 0) return false;
   if (c->n_q_heads < 1 || c->n_q_heads % cache->n_kv_heads != 0 || c->n_q_heads / cache->n_kv_heads > 256) return false;
-  // row counts are 32-bit
-  if (static_cast<int64_t>(c->T) * (c->n_q_heads / cache->n_kv_heads) > (int64_t(1) << 30)) return false;
+  // row and item counts are 32-bit
+  const int64_t rows = static_cast<int64_t>(c->T) * (c->n_q_heads / cache->n_kv_heads);
+  if (rows > (int64_t(1) << 30) || (rows / kTcItemRows + c->batch) * cache->n_kv_heads > (int64_t(1) << 30)) return false;
   if (c->window < 0 || c->window > (1 << 30) || c->n_sink < 0 || c->n_sink > (1 << 30)) return false;
   if (!(c->sm_scale > 0.f) || !std::isfinite(c->sm_scale)) return false;
   const int64_t width = static_cast<int64_t>(c->n_q_heads) * cache->head_dim;

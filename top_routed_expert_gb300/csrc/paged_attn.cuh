@@ -20,7 +20,8 @@ struct PaArgs {
   const int32_t* kv_len;
   float* part;          // workspace: partial sums,
   JoinTile* joins;      // the row tile that each CTA leaves to others to finish,
-  int2* tc_list;        // and the row blocks for paged_attn_tc.cu: [0].x of them, (request, block) from [1] on
+  int2* tc_list;        // and the row blocks for paged_attn_tc.cu: [0] how many and how many
+                        // items were taken, then (request, block)
   moe_kv_cache_t c;
   unsigned* status;
   int64_t qs, os;

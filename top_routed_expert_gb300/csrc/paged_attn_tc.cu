@@ -100,20 +100,26 @@ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The upper half of desc_sw128's descriptors; the lower half holds the address.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// ACC 0: D = A B, 1: D += A B, 2: by `accumulate`.
+template <int ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(ACC == 2 ? accumulate : static_cast<uint32_t>(ACC)), "n"(kDescHigh)
       : "memory");
 }
 
 // A from tensor memory: row i in lane i, two f16 of consecutive K in a column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+template <int ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(ACC == 2 ? accumulate : static_cast<uint32_t>(ACC)), "n"(kDescHigh)
       : "memory");
 }
 
@@ -638,24 +644,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
     regs_down<kIssueRegs>();
     if (warp == 17) {
       // -------------------------------------------------------- planning
-      // Takes this CTA's items from the list (the longest come first; the CTAs
-      // take them forth and back), announces them, and looks up their steps:
-      // four at a time, a lane for each 16-token group: page id, place in the
-      // cache, scales.
+      // Takes items from the list as they come (the longest first; which CTA
+      // works on one does not matter to its results), announces them, and looks
+      // up their steps: four at a time, a lane for each 16-token group: page id,
+      // place in the cache, scales.
       constexpr int kNotSeen = INT_MIN;
       const int ps = a.c.page_size, ps_log = 31 - __clz(ps), grp = lane & 7;
-      const int64_t total = static_cast<int64_t>(a.tc_list[0].x) * a.c.n_kv_heads;
+      const int total = a.tc_list[0].x * a.c.n_kv_heads;
       bool ok = true;
       int g = 0;
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
-        const int64_t at = static_cast<int64_t>(k) * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        // [0].y counts the items handed out
+        int at = lane == 0 ? atomicAdd(&a.tc_list[0].y, 1) : 0;
+        at = __shfl_sync(0xffffffffu, at, 0);
         Item it = {};
         if (at < total) {
           const int2 e = a.tc_list[1 + at / a.c.n_kv_heads];
           const Request rq = load_request(a.cu, a.kv_len, e.x, a.T);
           it.b = e.x;
-          it.kvh = static_cast<int>(at % a.c.n_kv_heads);
+          it.kvh = at % a.c.n_kv_heads;
           it.token0 = rq.row0;
           it.n = rq.n;
           it.end = rq.end;
@@ -704,30 +712,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       // descriptors of the first tile and stage; the others lie a multiple of
       // the operand's size (in 16-byte units) behind
-      const uint64_t dq = desc_sw128(s_q), dk = desc_sw128(s_k), dv = desc_sw128(s_v);
+      auto low = [](uint32_t saddr) { return static_cast<uint32_t>(desc_sw128(saddr)); };
+      const uint32_t dq = low(s_q), dk = low(s_k), dv = low(s_v);
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_phase(bar, parity, abort)) != 0;
       };
       auto scores = [&](int tile, int st) {   // st: step & 1
-        const uint64_t da = dq + tile * (L::kQ >> 4), db = dk + st * (L::kK >> 4);
+        const uint32_t da = dq + tile * (L::kQ >> 4), db = dk + st * (L::kK >> 4);
         const uint32_t d = tm + L::kS + tile * kTok;
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const int o = (i >> 2) * (kRowTile * 128 >> 4) + 2 * (i & 3);   // 128-byte column block, 32-byte step
-            mma_ss(d, da + o, db + o, is, i != 0);
+            if (i == 0) mma_ss<0>(d, da + o, db + o, is, 0);
+            else mma_ss<1>(d, da + o, db + o, is, 1);
           }
           mma_commit(smem_u32(&c->s_full[tile][st]));
         }
         __syncwarp();
       };
       auto output = [&](int tile, int st, bool first) {
-        const uint64_t db = dv + st * (L::kK >> 4);
+        const uint32_t db = dv + st * (L::kK >> 4);
         const uint32_t d = tm + L::kO + tile * D, p = tm + L::kS + tile * kTok;
         if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < kTok / 16; ++i)
-            mma_ts(d, p + i * 8, db + (i >> 2) * (D * 128 >> 4) + 2 * (i & 3), io, !first || i != 0);
+          for (int i = 0; i < kTok / 16; ++i) {
+            const int o = (i >> 2) * (D * 128 >> 4) + 2 * (i & 3);
+            if (i == 0) mma_ts<2>(d, p, db + o, io, !first);
+            else mma_ts<1>(d, p + i * 8, db + o, io, 1);
+          }
         }
         __syncwarp();
       };
