@@ -144,8 +144,8 @@ __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* sc
   int* bins = reinterpret_cast<int*>(scratch);            // [256]
   int* s_max = bins + 256;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ int s_warp[kWarps];
-  for (int i = threadIdx.x; i < 256; i += kWarps * 32) bins[i] = 0;
+  __shared__ int s_warp[32];
+  for (int i = threadIdx.x; i < 256; i += blockDim.x) bins[i] = 0;
   if (threadIdx.x == 0) *s_max = 0;
   __syncthreads();
   auto blocks_of = [&](const Request& r) { return r.n * a.group > a.tc_rows ? ceil_div(r.n * a.group, kTcItemRows) : 0; };
@@ -154,11 +154,12 @@ __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* sc
     return span_for(a, r.start + row0 / a.group, r.start + row1 / a.group, kTcStep).units;
   };
   int base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
+  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
     int n = 0;
     if (b < a.B) {
       const Request r = load_request(a.cu, a.kv_len, b, a.T);
+      if (!r.ok || r.end > a.c.max_pages * a.c.page_size) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
       n = blocks_of(r);
       if (n > 0) atomicMax(s_max, length(r, n - 1));
     }
@@ -170,7 +171,7 @@ __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* sc
     if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
     int all = 0, below = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) {
       all += s_warp[w];
       below += w < warp ? s_warp[w] : 0;
     }
@@ -191,7 +192,7 @@ __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* sc
     return 255 - static_cast<int>(min(static_cast<int64_t>(255), units * 256 / widest));
   };
   int2 e;
-  for (int i = threadIdx.x; i < total; i += kWarps * 32) atomicAdd(&bins[look(i, e)], 1);
+  for (int i = threadIdx.x; i < total; i += blockDim.x) atomicAdd(&bins[look(i, e)], 1);
   __syncthreads();
   if (warp == 0) {   // exclusive prefix over the classes
     int sum = 0, mine[8];
@@ -208,12 +209,19 @@ __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* sc
     for (int i = 0; i < 8; ++i) bins[lane * 8 + i] = before + mine[i];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < total; i += kWarps * 32) {
+  for (int i = threadIdx.x; i < total; i += blockDim.x) {
     const int at = atomicAdd(&bins[look(i, e)], 1);
     a.tc_list[1 + at] = e;
   }
   if (threadIdx.x == 0) a.tc_list[0] = make_int2(total, 0);
   __syncthreads();
+}
+
+// The list alone, for a batch that has no small requests.
+__global__ void __launch_bounds__(512) list_kernel(PaArgs a) {
+  extern __shared__ __align__(128) char smem[];
+  pdl_enter();
+  list_tc_items(a, reinterpret_cast<int*>(smem + 2048), smem);
 }
 
 template <int D, int NB>
@@ -758,6 +766,14 @@ constexpr int kTcRows = 64;
 cudaError_t launch_paged_attn(PaArgs a, int max_q_len, int num_sms, cudaStream_t s) {
   const int64_t most = static_cast<int64_t>(max_q_len > 0 ? std::min(max_q_len, a.T) : a.T) * a.group;
   const bool tc = most > kTcRows && paged_attn_tc_supported(a.c.head_dim);
+  // As many rows as if every request had max_q_len of them: they all do (or the
+  // hint is wrong, and the tcgen05 kernel takes small ones too).
+  if (tc && static_cast<int64_t>(max_q_len) * a.B == a.T) {
+    a.tc_rows = 0;
+    count_launches(1);
+    const cudaError_t err = launch_pdl(list_kernel, 1, 512, 2048 + sizeof(int) * (a.B + 1), s, a);
+    return err == cudaSuccess ? launch_paged_attn_tc(a, num_sms, s) : err;
+  }
   a.tc_rows = tc ? kTcRows : INT_MAX;
   cudaError_t err;
   switch (a.c.head_dim) {
