@@ -122,7 +122,8 @@ typedef struct {
   int64_t out_stride;
 } moe_paged_attention_config_t;
 
-/* Workspace bytes of moe_paged_attention; 0 for an invalid configuration. */
+/* Workspace bytes of moe_paged_attention for this configuration (max_q_len = 0
+ * needs the most); 0 for an invalid one. */
 size_t moe_paged_attention_ws_bytes(const moe_paged_attention_config_t* cfg, const moe_kv_cache_t* cache);
 
 /*

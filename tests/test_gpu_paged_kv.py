@@ -365,6 +365,109 @@ def test_attention_same_bits_every_time():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+# Enough rows for the tensor-memory kernel, and contexts long enough that it cuts
+# row blocks along the cached tokens; the third mixes both kernels, the fourth and
+# fifth have equal prompts.
+MANY = [
+    ([64, 130], [900, 130], dict(Hq=16, Hkv=2)),
+    ([300], [1500], dict(Hq=7, Hkv=1, D=64, page=64)),
+    ([1, 100, 0, 3], [700, 2100, 40, 5], dict(Hq=32, Hkv=4, page=32, order="nhd")),
+    ([128, 128], [128, 1000], dict(Hq=8, Hkv=8)),
+    ([65] * 4, [65, 770, 769, 66], dict(Hq=8, Hkv=8, D=64, page=128)),
+]
+
+
+@pytest.mark.parametrize("new,total,kw", MANY)
+@pytest.mark.parametrize("hint", [False, True])
+def test_attention_many_rows(new, total, kw, hint):
+    bt = Batch(new, total, seed=sum(total), **kw)
+    check_attention(bt, max_q_len=max(new) if hint else 0)
+
+
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (1, 1), (130, 4), (800, 0), (900, 300), (10 ** 6, 3)])
+@pytest.mark.parametrize("new,total,kw", MANY[:3])
+def test_attention_many_rows_window(new, total, kw, window, n_sink):
+    bt = Batch(new, total, seed=window + n_sink, **kw)
+    check_attention(bt, window, n_sink, max_q_len=max(new))
+
+
+def test_attention_many_rows_evicted_pages():
+    bt = Batch([100, 64, 150], [1900, 300, 1260], Hq=8, Hkv=1, seed=21)
+    window, n_sink = 900, 4
+    ref = do.paged_attention(bt.oracle_cache(), values64(bt.q), bt.cu, bt.kv_len, bt.D ** -0.5, window, n_sink)
+    for b in range(bt.B):
+        first = bt.total[b] - bt.new[b]
+        for pg in range(1, (first - window + 1) // bt.page):
+            bt.codes["k"][bt.table[b, pg]] = 0x7F
+            bt.codes["v"][bt.table[b, pg]] = 0xFF
+            bt.scales["k"][bt.table[b, pg]] = math.nan
+            bt.table[b, pg] = -1
+    out, lse, st = run_attention(bt, window, n_sink, max_q_len=150)
+    assert st == 0
+    assert np.max(np.abs(values64(out) - ref[0])) <= 2.0 ** -8 * np.max(np.abs(ref[0])) + 2.0 ** -10 * 32
+    assert np.max(np.abs(values64(lse) - ref[1])) <= 2e-5 * (1 + np.max(np.abs(ref[1])))
+
+
+def test_attention_many_rows_that_see_nothing():
+    bt = Batch([50, 100, 60, 300], [50, 100, 60, 1300], Hq=8, Hkv=1, seed=22)
+    bt.kv_len[:] = [20, 0, -7, 1100]
+    for hint in (0, 300):
+        out, lse = check_attention(bt, max_q_len=hint)
+        assert np.all(values64(out)[:30] == 0.0) and np.all(values64(lse)[50:210] == -math.inf)
+
+
+def test_attention_many_rows_nan_query_stays_in_its_row():
+    bt = Batch([260], [1150], Hq=8, Hkv=2, seed=23)
+    clean_o, clean_l, _ = run_attention(bt)
+    bt.q[1, 3, 5], bt.q[0, 6, 0], bt.q[259, 0, 127] = math.nan, math.inf, -math.inf
+    out, lse, _ = run_attention(bt)
+    bad = np.zeros((bt.T, 8), dtype=bool)
+    bad[1, 3] = bad[0, 6] = bad[259, 0] = True
+    assert np.all(np.isnan(values64(out)[bad])) and np.all(np.isnan(values64(lse)[bad]))
+    assert np.array_equal(values64(out)[~bad], values64(clean_o)[~bad])
+    assert np.array_equal(values64(lse)[~bad], values64(clean_l)[~bad])
+
+
+def test_attention_many_rows_extreme_scales_and_scores():
+    bt = Batch([256], [1140], Hq=8, Hkv=2, seed=24)
+    n = bt.scales["v"].shape[0]
+    bt.scales["v"] = 2.0 ** np.linspace(-40, 0, n * 2).round().reshape(n, 2)
+    check_attention(bt)
+    bt.q.mul_(200.0)
+    out, lse, st = run_attention(bt)
+    ref_o, ref_l = do.paged_attention(bt.oracle_cache(), values64(bt.q), bt.cu, bt.kv_len, bt.D ** -0.5)
+    assert np.max(np.abs(values64(lse) - ref_l)) <= 2e-5 * (1 + np.max(np.abs(ref_l)))
+
+
+def test_attention_many_rows_page_out_of_the_cache():
+    bt = Batch([100, 160], [1000, 900], Hq=8, Hkv=2, seed=25)
+    full = Batch([100, 160], [1000, 900], Hq=8, Hkv=2, seed=25)
+    bt.table[0, 2] = bt.n_pages
+    out, lse, st = run_attention(bt)
+    assert st == 6
+    ref_o, _ = do.paged_attention(full.oracle_cache(), values64(full.q), full.cu, full.kv_len, full.D ** -0.5)
+    assert np.max(np.abs(values64(out)[100:] - ref_o[100:])) <= 2.0 ** -8 * np.max(np.abs(ref_o)) + 2.0 ** -10 * 32
+
+
+def test_attention_many_rows_same_bits_strided_other_stream():
+    bt = Batch([1, 256, 3, 90], [1700, 1333, 260, 900], Hq=8, Hkv=2, seed=26)
+    ref, ref_l, st = run_attention(bt, max_q_len=256)
+    assert st == 0
+    for _ in range(3):
+        out, lse, _ = run_attention(bt, max_q_len=256)
+        assert torch.equal(out, ref) and torch.equal(lse, ref_l)
+    out, _, _ = run_attention(bt, max_q_len=256, lse=False)
+    assert torch.equal(out, ref)
+    wide = torch.zeros(bt.T, bt.Hq + 3, bt.D, dtype=torch.bfloat16, device="cuda")
+    wide[:, :bt.Hq] = bt.q.cuda()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        out, lse, st = run_attention(bt, max_q_len=256, stream=s, q=wide[:, :bt.Hq])
+    s.synchronize()
+    assert st == 0 and torch.equal(out, ref) and torch.equal(lse, ref_l)
+
+
 def test_append_then_attend_in_a_graph():
     """Both calls captured on a side stream and replayed on new inputs."""
     bt = Batch([1, 1, 1], [20, 1, 50], Hq=8, Hkv=2, seed=18)

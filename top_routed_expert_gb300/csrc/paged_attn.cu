@@ -42,7 +42,7 @@
 namespace moe {
 
 bool paged_attn_tc_supported(int D);
-cudaError_t launch_paged_attn_tc(const PaArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_paged_attn_tc(const PaArgs& a, cudaStream_t s);
 
 namespace {
 
@@ -138,15 +138,23 @@ template <int D> __device__ __forceinline__ uint32_t chunk_at(int row, int chunk
 
 // Lists the row blocks of the requests that go to paged_attn_tc.cu, the longest
 // first (a counting sort by 256 classes of length; the order inside a class
-// does not matter to the results).  One block; `first`: B + 1 ints, `scratch`:
-// the block's other shared memory.
+// does not matter to the results).  Where that is allowed, a block longer than
+// 1.5 times a CTA's share of the work is cut along the cached tokens into parts
+// of at least 3/4 of that share.  One thread block; `first`: B + 1 ints, `scratch`: the
+// block's other shared memory.
 __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* scratch) {
   int* bins = reinterpret_cast<int*>(scratch);            // [256]
   int* s_max = bins + 256;
+  unsigned long long* s_sum = reinterpret_cast<unsigned long long*>(bins + 258);
+  TcList* s_list = reinterpret_cast<TcList*>(bins + 260);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ int s_warp[32];
   for (int i = threadIdx.x; i < 256; i += blockDim.x) bins[i] = 0;
-  if (threadIdx.x == 0) *s_max = 0;
+  if (threadIdx.x == 0) {
+    *s_max = 0;
+    *s_sum = 0;
+    *s_list = TcList{};
+  }
   __syncthreads();
   auto blocks_of = [&](const Request& r) { return r.n * a.group > a.tc_rows ? ceil_div(r.n * a.group, kTcItemRows) : 0; };
   auto length = [&](const Request& r, int blk) {
@@ -181,18 +189,36 @@ __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* sc
   }
   const int total = base;
   const int64_t widest = *s_max + 1;
-  auto look = [&](int i, int2& e) {   // the i-th block and its class
+  auto look = [&](int i, int& b, int& blk) {   // the i-th block; its length
     int lo = 0, hi = a.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (first[mid] <= i) lo = mid; else hi = mid - 1;
     }
-    e = make_int2(lo, i - first[lo]);
-    const int units = length(load_request(a.cu, a.kv_len, lo, a.T), e.y);
-    return 255 - static_cast<int>(min(static_cast<int64_t>(255), units * 256 / widest));
+    b = lo;
+    blk = i - first[lo];
+    return length(load_request(a.cu, a.kv_len, b, a.T), blk);
   };
-  int2 e;
-  for (int i = threadIdx.x; i < total; i += blockDim.x) atomicAdd(&bins[look(i, e)], 1);
+  int b, blk;
+  int64_t share = INT_MAX;   // steps of a part
+  if (a.tc_split) {
+    unsigned long long sum = 0;
+    for (int i = threadIdx.x; i < total; i += blockDim.x) sum += look(i, b, blk);
+    atomicAdd(s_sum, sum);
+    __syncthreads();
+    share = max(int64_t(4), static_cast<int64_t>(*s_sum * a.c.n_kv_heads + a.tc_ctas - 1) / a.tc_ctas);
+  }
+  // rounded down: with equal blocks, the parts then are no more than the CTAs
+  auto parts_of = [&](int units) {
+    return 2 * int64_t(units) <= 3 * share ? 1 : max(2, static_cast<int>(units / share));
+  };
+  auto class_of = [&](int units, int parts) {
+    return 255 - static_cast<int>(min(static_cast<int64_t>(255), static_cast<int64_t>(units / parts) * 256 / widest));
+  };
+  for (int i = threadIdx.x; i < total; i += blockDim.x) {
+    const int units = look(i, b, blk), parts = parts_of(units);
+    atomicAdd(&bins[class_of(units, parts)], parts);
+  }
   __syncthreads();
   if (warp == 0) {   // exclusive prefix over the classes
     int sum = 0, mine[8];
@@ -210,10 +236,18 @@ __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* sc
   }
   __syncthreads();
   for (int i = threadIdx.x; i < total; i += blockDim.x) {
-    const int at = atomicAdd(&bins[look(i, e)], 1);
-    a.tc_list[1 + at] = e;
+    const int units = look(i, b, blk), parts = parts_of(units);
+    const int at = atomicAdd(&bins[class_of(units, parts)], parts);
+    atomicAdd(&s_list->entries, parts);
+    int slot = -1;
+    if (parts > 1) {
+      slot = atomicAdd(&s_list->slots, parts);
+      a.tc_joins[atomicAdd(&s_list->joins, 1)] = TcJoin{b, blk, parts, slot};
+    }
+    for (int k = 0; k < parts; ++k) a.tc_entries[at + k] = TcEntry{b, blk, k, parts, slot};
   }
-  if (threadIdx.x == 0) a.tc_list[0] = make_int2(total, 0);
+  __syncthreads();
+  if (threadIdx.x == 0) *a.tc = *s_list;
   __syncthreads();
 }
 
@@ -580,7 +614,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB>::kCtas) paged_attn_k
 // their references and sums, one part a lane.
 constexpr int kJoinWarps = 32;
 // The workspace is sized for kMaxSms SMs, so that its size needs no device.
-constexpr int kMaxSms = 160, kMaxCtas = kMaxSms * 5;
+constexpr int kMaxCtas = kMaxSms * 5;
 
 template <int D, int NB>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join(PaArgs a, int n_ctas) {
@@ -760,42 +794,75 @@ size_t paged_attn_part_bytes(int D) {
   }
 }
 
-// Requests with more rows than this go to the tcgen05 kernel.
-constexpr int kTcRows = 64;
+// Which kernels a call takes, from what the host knows.
+struct Path {
+  bool tc;      // the tcgen05 kernel, for requests with more than kTcRows rows
+  bool alone;   // ... and it alone
+  bool split;   // ... which may cut row blocks along the cached tokens
+};
 
-cudaError_t launch_paged_attn(PaArgs a, int max_q_len, int num_sms, cudaStream_t s) {
+// Measured with 4 key heads of 8 query heads of 128 (us, few-row kernel /
+// tcgen05 kernel): contexts of 1792 to 3584, 64 requests of 32 rows 94 / 115,
+// of 64 rows 167 / 113, of 128 rows 318 / 113; 8 requests of 64 rows (2048 rows
+// of all key heads) 31 / 37, of 128 rows 49 / 38, of 512 rows 162 / 61; one
+// request of 256 rows (1024 of all) 25 / about 34, of 512 rows 37 / 34, of 1024
+// rows 61 / 35; contexts of 32768, 4 requests of 128 rows 170 / 81.
+constexpr int kTcRows = 48;
+constexpr int64_t kTcWork = 2048;   // rows of all key heads
+
+Path path_of(const PaArgs& a, int max_q_len) {
   const int64_t most = static_cast<int64_t>(max_q_len > 0 ? std::min(max_q_len, a.T) : a.T) * a.group;
-  const bool tc = most > kTcRows && paged_attn_tc_supported(a.c.head_dim);
+  Path p;
+  p.tc = most > kTcRows && static_cast<int64_t>(a.T) * a.group * a.c.n_kv_heads >= kTcWork &&
+         paged_attn_tc_supported(a.c.head_dim);
   // As many rows as if every request had max_q_len of them: they all do (or the
   // hint is wrong, and the tcgen05 kernel takes small ones too).
-  if (tc && static_cast<int64_t>(max_q_len) * a.B == a.T) {
-    a.tc_rows = 0;
-    count_launches(1);
-    const cudaError_t err = launch_pdl(list_kernel, 1, 512, 2048 + sizeof(int) * (a.B + 1), s, a);
-    return err == cudaSuccess ? launch_paged_attn_tc(a, num_sms, s) : err;
-  }
-  a.tc_rows = tc ? kTcRows : INT_MAX;
+  p.alone = p.tc && static_cast<int64_t>(max_q_len) * a.B == a.T;
+  p.split = p.tc && tc_places(a) * a.c.n_kv_heads <= 4 * kMaxSms;
+  return p;
+}
+
+cudaError_t launch_paged_attn(PaArgs a, int max_q_len, int num_sms, cudaStream_t s) {
+  const Path path = path_of(a, max_q_len);
+  const int64_t most = static_cast<int64_t>(max_q_len > 0 ? std::min(max_q_len, a.T) : a.T) * a.group;
+  a.tc_rows = path.alone ? 0 : path.tc ? kTcRows : INT_MAX;
+  a.tc_ctas = std::min(num_sms, kMaxSms);
+  a.tc_split = path.split;
   cudaError_t err;
-  switch (a.c.head_dim) {
-    case 64: err = launch<64>(a, std::min<int64_t>(most, a.tc_rows), num_sms, s); break;
-    case 128: err = launch<128>(a, std::min<int64_t>(most, a.tc_rows), num_sms, s); break;
-    default: err = launch<256>(a, most, num_sms, s); break;
+  if (path.alone) {
+    count_launches(1);
+    err = launch_pdl(list_kernel, 1, 512, 2048 + sizeof(int) * (a.B + 1), s, a);
+  } else {
+    switch (a.c.head_dim) {
+      case 64: err = launch<64>(a, std::min<int64_t>(most, a.tc_rows), num_sms, s); break;
+      case 128: err = launch<128>(a, std::min<int64_t>(most, a.tc_rows), num_sms, s); break;
+      default: err = launch<256>(a, most, num_sms, s); break;
+    }
   }
-  return err == cudaSuccess && tc ? launch_paged_attn_tc(a, num_sms, s) : err;
+  return err == cudaSuccess && path.tc ? launch_paged_attn_tc(a, s) : err;
 }
 
 namespace {
 
-// Workspace: partial sums, the row tiles to join, the list of row blocks.
+// Workspace: partial sums and the row tiles to join, then what the tcgen05
+// kernel needs where a call can take it.
 struct Workspace {
-  size_t joins, tc_list, total;
+  size_t joins, tc, tc_entries, tc_joins, tc_part, total;
 };
 
-Workspace plan_workspace(const PaArgs& a, int D) {
+Workspace plan_workspace(const PaArgs& a, int max_q_len) {
+  const int D = a.c.head_dim;
+  const Path path = path_of(a, max_q_len);
   Workspace w;
-  w.joins = align_up(paged_attn_part_bytes(D), 256);
-  w.tc_list = w.joins + align_up(kMaxCtas * sizeof(JoinTile), 256);
-  w.total = w.tc_list + align_up((tc_places(a) + 1) * sizeof(int2), 256);
+  size_t at = 0;
+  auto take = [&](size_t bytes) { const size_t from = at; at += align_up(bytes, 256); return from; };
+  take(path.alone ? 0 : paged_attn_part_bytes(D));
+  w.joins = take(kMaxCtas * sizeof(JoinTile));
+  w.tc = take(sizeof(TcList));
+  w.tc_entries = take(path.tc ? (tc_places(a) + kTcSlots) * sizeof(TcEntry) : 0);
+  w.tc_joins = take(path.split ? kTcSlots * sizeof(TcJoin) : 0);
+  w.tc_part = take(path.split ? static_cast<size_t>(kTcSlots) * kTcItemRows * (D + 2) * sizeof(float) : 0);
+  w.total = at;
   return w;
 }
 
@@ -821,8 +888,9 @@ extern "C" size_t moe_paged_attention_ws_bytes(const moe_paged_attention_config_
   PaArgs a;
   a.T = cfg->T;
   a.B = cfg->batch;
+  a.c = *cache;
   a.group = cfg->n_q_heads / cache->n_kv_heads;
-  return plan_workspace(a, cache->head_dim).total;
+  return plan_workspace(a, cfg->max_q_len).total;
 }
 
 extern "C" moe_status_t moe_paged_attention(const moe_paged_attention_config_t* cfg, const moe_kv_cache_t* cache,
@@ -857,9 +925,13 @@ extern "C" moe_status_t moe_paged_attention(const moe_paged_attention_config_t* 
   a.window = cfg->window;
   a.n_sink = cfg->n_sink;
   a.sm_scale = cfg->sm_scale;
-  const Workspace w = plan_workspace(a, cache->head_dim);
-  a.part = static_cast<float*>(ws);
-  a.joins = reinterpret_cast<JoinTile*>(static_cast<char*>(ws) + w.joins);
-  a.tc_list = reinterpret_cast<int2*>(static_cast<char*>(ws) + w.tc_list);
+  const Workspace w = plan_workspace(a, cfg->max_q_len);
+  char* base = static_cast<char*>(ws);
+  a.part = reinterpret_cast<float*>(base);
+  a.joins = reinterpret_cast<JoinTile*>(base + w.joins);
+  a.tc = reinterpret_cast<TcList*>(base + w.tc);
+  a.tc_entries = reinterpret_cast<TcEntry*>(base + w.tc_entries);
+  a.tc_joins = reinterpret_cast<TcJoin*>(base + w.tc_joins);
+  a.tc_part = reinterpret_cast<float*>(base + w.tc_part);
   return launch_paged_attn(a, cfg->max_q_len, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

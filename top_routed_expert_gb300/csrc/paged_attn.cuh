@@ -12,6 +12,19 @@ struct JoinTile {
   int rows, token0, row0, kvh, slot, last;
 };
 
+// The row blocks of paged_attn_tc.cu: part `part` of `parts` of block `blk` of
+// request `b`; the parts of a cut block, for key head h, leave their sums in
+// slots (slot + part) n_kv_heads + h.
+struct TcList {
+  int entries, taken, joins, slots;
+};
+struct TcEntry {
+  int b, blk, part, parts, slot;
+};
+struct TcJoin {
+  int b, blk, parts, slot;
+};
+
 struct PaArgs {
   const uint16_t* q;
   uint16_t* out;
@@ -20,18 +33,26 @@ struct PaArgs {
   const int32_t* kv_len;
   float* part;          // workspace: partial sums,
   JoinTile* joins;      // the row tile that each CTA leaves to others to finish,
-  int2* tc_list;        // and the row blocks for paged_attn_tc.cu: [0] how many and how many
-                        // items were taken, then (request, block)
+  TcList* tc;           // and for paged_attn_tc.cu the list of its row blocks
+  TcEntry* tc_entries;
+  TcJoin* tc_joins;     // ... those cut along the cached tokens,
+  float* tc_part;       // and their partial sums: rows of D outputs, then (reference, sum) pairs
   moe_kv_cache_t c;
   unsigned* status;
   int64_t qs, os;
   int T, B, group, window, n_sink;
   int tc_rows;          // requests with more rows (tokens x heads of the group) go to paged_attn_tc.cu
+  int tc_ctas;          // its CTAs
+  bool tc_split;        // whether row blocks may be cut
   float sm_scale;
 };
 
 constexpr int kTcItemRows = 256;   // rows of an item of paged_attn_tc.cu
 constexpr int kTcStep = 128;       // cached tokens of its steps
+
+// The most CTAs, and the most slots of cut row blocks: a part is at least 3/4 of
+// 1/tc_ctas of the work, so that all parts are at most 4/3 of the CTAs.
+constexpr int kMaxSms = 160, kTcSlots = kMaxSms * 4 / 3 + 1;
 
 // The most row blocks that the requests can have, for one key head.
 inline int64_t tc_places(const PaArgs& a) { return static_cast<int64_t>(a.T) * a.group / kTcItemRows + a.B; }

@@ -58,10 +58,11 @@ constexpr float kMostSum = 32768.0f;     // sum of 16 weights that moves the max
 constexpr long long kWaitCycles = 3000000000ll;
 constexpr uint64_t kDrainNs = 200000000ull;
 
-// A row block's work: up to 256 rows of one request and key head; rows = 0:
-// there is no more.
+// A row block's work, or a part of it: up to 256 rows of one request and key
+// head, over `steps` steps from step u0 on; rows = 0: there is no more.
 struct Item {
   int b, kvh, token0, n, end, row0, rows;   // token0, n, end: the request's rows and length
+  int u0, steps, slot;                      // slot: where a part leaves its sums; -1: the whole block
   __device__ __forceinline__ Span span(const PaArgs& a) const {
     const int start = end - n;
     return span_for(a, start + row0 / a.group, start + (row0 + rows - 1) / a.group, kTok);
@@ -78,7 +79,7 @@ struct Ctrl {
   uint64_t q_full, k_full[2], v_full[2], s_full[2][2], p_full[2], o_full[2], plan_full[kSlots], plan_free[kSlots],
       item_full[kItems], drain;
   // of a step's eight 16-token groups: key scale, log2 of the value scale, 1 /
-  // value scale; byte offset in the cache, -1: none
+  // value scale, first token (an integer's bits); byte offset in the cache, -1: none
   float4 scale[kSlots][kGroups];
   int64_t place[kSlots][kGroups];
   Item item[kItems];
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       const Item& it = c->item[k % kItems];
       if (it.rows == 0) break;
       const Span sp = it.span(a);
-      const int steps = sp.units, start = it.end - it.n;
+      const int steps = it.steps, start = it.end - it.n;
       // this thread's row, and the first and last position of the warp's live rows
       const int w0 = it.row0 + tile * kRowTile + (warp & 3) * 32, r = w0 + lane;
       const int w1 = min(w0 + 31, it.row0 + it.rows - 1);
@@ -401,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const int j0 = sp.block_of(j) * kTok;
         const float4* sc = c->scale[slot];
+        const int j0 = __float_as_int(sc[0].w);
         if (!sp.all_see(j0, j0 + kTok - 1, pos_min, pos_max)) {
           // scores that the row does not see become -infinity, in place: what
           // follows needs no mask
@@ -495,16 +496,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       ok = __all_sync(0xffffffffu, wait_phase(&c->o_full[tile], k & 1, abort));
       if (!ok) break;
       tc_fence_after();
-      const bool empty = l == 0.f;   // nothing visible (a NaN sum is not)
-      const float f = empty ? 0.f : 1.0f / l;
+      const bool cut = it.slot >= 0;
+      const float f = cut ? 1.0f : l == 0.f ? 0.f : 1.0f / l;   // 0: nothing visible (a NaN sum is not)
       const int head = it.kvh * a.group + r % a.group, token = it.token0 + r / a.group;
       uint16_t* dst = a.out + static_cast<int64_t>(token) * a.os + static_cast<int64_t>(head) * D;
+      float* part = a.tc_part + static_cast<int64_t>(it.slot) * (kTcItemRows * (D + 2));
+      const int row = tile * kRowTile + (threadIdx.x & 127);
 #pragma unroll 1
       for (int i = 0; i < D; i += 32) {
         float v[32];
         tmem_ld32_issue(t_o + i, v);
         tmem_ld32_wait(v);
-        if (live) {
+        if (live && cut) {
+#pragma unroll
+          for (int q = 0; q < 32; q += 4)
+            *reinterpret_cast<float4*>(part + row * D + i + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+        } else if (live) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t w[4];
@@ -517,7 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
           }
         }
       }
-      if (live && a.lse) store_lse(a, token, head, m, l);
+      if (live && cut) *reinterpret_cast<float2*>(part + kTcItemRows * D + 2 * row) = make_float2(m, l);
+      else if (live && a.lse) store_lse(a, token, head, m, l);
       tc_fence_before();
       rf = rf_next;
     }
@@ -538,14 +546,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         const Item& it = c->item[k % kItems];
         if (it.rows == 0) return false;
         sp = it.span(a);
-        steps = sp.units;
+        steps = it.steps;
         head_at = it.kvh * a.c.head_stride;
         j = 0;
       }
-      j0 = sp.block_of(j) * kTok;
+      if (!wait_phase(&c->plan_full[g % kSlots], (g / kSlots) & 1, abort)) return false;
+      j0 = __float_as_int(c->scale[g % kSlots][0].w);
       // every token of the step is seen by some row
       all = j0 + kTok <= sp.end && (j0 >= sp.lo || j0 + kTok <= sp.n_sink);
-      return wait_phase(&c->plan_full[g % kSlots], (g / kSlots) & 1, abort);
+      return true;
     };
     if (warp < 12) {
       // keys: token (+ i KSTEP) and 16-byte chunk; eight neighbouring lanes have
@@ -650,25 +659,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
       // place in the cache, scales.
       constexpr int kNotSeen = INT_MIN;
       const int ps = a.c.page_size, ps_log = 31 - __clz(ps), grp = lane & 7;
-      const int total = a.tc_list[0].x * a.c.n_kv_heads;
+      const int total = a.tc->entries * a.c.n_kv_heads;
       bool ok = true;
       int g = 0;
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
-        // [0].y counts the items handed out
-        int at = lane == 0 ? atomicAdd(&a.tc_list[0].y, 1) : 0;
+        int at = lane == 0 ? atomicAdd(&a.tc->taken, 1) : 0;
         at = __shfl_sync(0xffffffffu, at, 0);
         Item it = {};
         if (at < total) {
-          const int2 e = a.tc_list[1 + at / a.c.n_kv_heads];
-          const Request rq = load_request(a.cu, a.kv_len, e.x, a.T);
-          it.b = e.x;
+          const TcEntry e = a.tc_entries[at / a.c.n_kv_heads];
+          const Request rq = load_request(a.cu, a.kv_len, e.b, a.T);
+          it.b = e.b;
           it.kvh = at % a.c.n_kv_heads;
           it.token0 = rq.row0;
           it.n = rq.n;
           it.end = rq.end;
-          it.row0 = e.y * kTcItemRows;
+          it.row0 = e.blk * kTcItemRows;
           it.rows = min(kTcItemRows, rq.n * a.group - it.row0);
+          const int64_t units = it.span(a).units;
+          it.u0 = static_cast<int>(units * e.part / e.parts);
+          it.steps = static_cast<int>(units * (e.part + 1) / e.parts) - it.u0;
+          it.slot = e.parts > 1 ? (e.slot + e.part) * a.c.n_kv_heads + it.kvh : -1;
         }
         if (lane == 0) {
           c->item[k % kItems] = it;
@@ -678,10 +690,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         const Span sp = it.span(a);
         const int32_t* table = a.c.page_table + static_cast<int64_t>(it.b) * a.c.max_pages;
 #pragma unroll 1
-        for (int jb = 0; ok && jb < sp.units; jb += 4) {
+        for (int jb = 0; ok && jb < it.steps; jb += 4) {
           const int j = jb + (lane >> 3), s = g + j, slot = s % kSlots;
-          const bool mine = j < sp.units;
-          const int x = mine ? sp.block_of(j) * kTok + grp * 16 : 0;
+          const bool mine = j < it.steps;
+          const int x = mine ? sp.block_of(it.u0 + j) * kTok + grp * 16 : 0;
           const int gp = mine && sp.any_seen(x, x + 15) ? __ldg(table + (x >> ps_log)) : kNotSeen;
           const bool have = static_cast<unsigned>(gp) < static_cast<unsigned>(a.c.n_pages);
           if (!have && gp != kNotSeen) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
@@ -696,12 +708,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
           if (mine && ok) {
             // a group without a page masks itself
             c->place[slot][grp] = have ? gp * a.c.page_stride + (x & (ps - 1)) * a.c.token_stride : -1;
-            c->scale[slot][grp] =
-                have ? make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
+            c->scale[slot][grp] = have ? make_float4(ks, __log2f(vs), __frcp_rn(vs), __int_as_float(x))
+                                       : make_float4(1.f, -INFINITY, 0.f, __int_as_float(x));
             mbar_arrive(smem_u32(&c->plan_full[slot]));
           }
         }
-        g += sp.units;
+        g += it.steps;
       }
     }
     // ---------------------------------------------------------- MMA issue
@@ -755,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
         if (!(ok = __all_sync(0xffffffffu, next_item(k)))) break;
         const Item& it = c->item[k % kItems];
         if (it.rows == 0) break;
-        const int steps = it.span(a).units;
+        const int steps = it.steps;
         if (!(ok = wait(&c->q_full, k & 1) && wait(&c->k_full[g & 1], (g >> 1) & 1))) break;
         tc_fence_after();
         scores(0, g & 1);
@@ -795,22 +807,77 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
   if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
+// Joins the parts of cut row blocks, a warp for each row, in the parts' order.
 template <int D>
-cudaError_t launch(const PaArgs& a, int num_sms, cudaStream_t s) {
-  const cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(paged_attn_tc_kernel<D>), Tc<D>::kSmem);
+__global__ void __launch_bounds__(256) paged_attn_tc_join(PaArgs a) {
+  constexpr int VEC = D / 64;   // pairs of columns of a lane
+  pdl_enter();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t groups = static_cast<int64_t>(a.tc->joins) * a.c.n_kv_heads * (kTcItemRows / 8);
+  for (int64_t x = blockIdx.x; x < groups; x += gridDim.x) {
+    const int row = static_cast<int>(x % (kTcItemRows / 8)) * 8 + warp;
+    const int kvh = static_cast<int>(x / (kTcItemRows / 8) % a.c.n_kv_heads);
+    const TcJoin jn = a.tc_joins[x / (kTcItemRows / 8) / a.c.n_kv_heads];
+    const Request rq = load_request(a.cu, a.kv_len, jn.b, a.T);
+    const int r = jn.blk * kTcItemRows + row;
+    if (r >= rq.n * a.group) continue;
+    auto part_of = [&](int k) {
+      return a.tc_part + (static_cast<int64_t>(jn.slot + k) * a.c.n_kv_heads + kvh) * (kTcItemRows * (D + 2));
+    };
+    float m = -INFINITY, sum = 0.f;
+    float2 acc[VEC] = {};
+    for (int k0 = 0; k0 < jn.parts; k0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (k0 + lane < jn.parts) ml = *reinterpret_cast<const float2*>(part_of(k0 + lane) + kTcItemRows * D + 2 * row);
+      float to = fmaxf(m, ml.x);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
+      const float old = ex2_from(m, to), w = ex2_from(ml.x, to);
+      m = to;
+      float l = ml.y * w;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+      sum = sum * old + l;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = make_float2(acc[e].x * old, acc[e].y * old);
+#pragma unroll 4
+      for (int k = k0; k < min(jn.parts, k0 + 32); ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k - k0);
+        const float2* p = reinterpret_cast<const float2*>(part_of(k) + row * D) + lane;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float2 v = p[e * 32];
+          acc[e].x += v.x * wk;
+          acc[e].y += v.y * wk;
+        }
+      }
+    }
+    const int token = rq.row0 + r / a.group, head = kvh * a.group + r % a.group;
+    const float f = sum == 0.f ? 0.f : 1.0f / sum;   // nothing visible (a NaN sum is not)
+    __nv_bfloat162* out =
+        reinterpret_cast<__nv_bfloat162*>(a.out + static_cast<int64_t>(token) * a.os + static_cast<int64_t>(head) * D);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e * 32 + lane] = __floats2bfloat162_rn(acc[e].x * f, acc[e].y * f);
+    if (a.lse && lane == 0) store_lse(a, token, head, m, sum);
+  }
+}
+
+template <int D>
+cudaError_t launch(const PaArgs& a, cudaStream_t s) {
+  cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(paged_attn_tc_kernel<D>), Tc<D>::kSmem);
   if (err != cudaSuccess) return err;
-  const int64_t items = tc_places(a) * a.c.n_kv_heads;
-  count_launches(1);
-  return launch_pdl(paged_attn_tc_kernel<D>, static_cast<unsigned>(std::min<int64_t>(num_sms, items)), kThreads,
-                    Tc<D>::kSmem, s, a);
+  count_launches(a.tc_split ? 2 : 1);
+  err = launch_pdl(paged_attn_tc_kernel<D>, a.tc_ctas, kThreads, Tc<D>::kSmem, s, a);
+  if (err != cudaSuccess || !a.tc_split) return err;
+  return launch_pdl(paged_attn_tc_join<D>, 4 * a.tc_ctas, 256, 0, s, a);
 }
 
 }  // namespace
 
 bool paged_attn_tc_supported(int D) { return D == 64 || D == 128; }
 
-cudaError_t launch_paged_attn_tc(const PaArgs& a, int num_sms, cudaStream_t s) {
-  return a.c.head_dim == 64 ? launch<64>(a, num_sms, s) : launch<128>(a, num_sms, s);
+cudaError_t launch_paged_attn_tc(const PaArgs& a, cudaStream_t s) {
+  return a.c.head_dim == 64 ? launch<64>(a, s) : launch<128>(a, s);
 }
 
 }  // namespace moe
