@@ -449,6 +449,21 @@ def test_attention_many_rows_page_out_of_the_cache():
     assert np.max(np.abs(values64(out)[100:] - ref_o[100:])) <= 2.0 ** -8 * np.max(np.abs(ref_o)) + 2.0 ** -10 * 32
 
 
+def test_attention_offsets_that_name_rows_again():
+    """Offsets out of order are reported; requests that overlap make no more work than the rows have."""
+    bt = Batch([300], [1100], Hq=8, Hkv=1, seed=27)
+    ref, _, _ = run_attention(bt)
+    bt.B = 101
+    bt.cu = np.array([0, 300] * 51, dtype=np.int32)
+    bt.kv_len = np.full(101, 1100, dtype=np.int32)
+    bt.table = np.repeat(bt.table, 101, 0)
+    out, _, st = run_attention(bt)
+    assert st == 6
+    # every request that names a row has the same result for it, within twice the bound above (|v| <= 448 / 32)
+    got, ref = values64(out), values64(ref)
+    assert np.all(np.abs(got - ref) <= 2.0 ** -7 * np.abs(ref) + 2.0 ** -9 * 14)
+
+
 def test_attention_many_rows_same_bits_strided_other_stream():
     bt = Batch([1, 256, 3, 90], [1700, 1333, 260, 900], Hq=8, Hkv=2, seed=26)
     ref, ref_l, st = run_attention(bt, max_q_len=256)

@@ -161,7 +161,7 @@ __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* sc
     const int row0 = blk * kTcItemRows, row1 = min(row0 + kTcItemRows, r.n * a.group) - 1;
     return span_for(a, r.start + row0 / a.group, r.start + row1 / a.group, kTcStep).units;
   };
-  int base = 0;
+  int64_t base = 0;
   for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
     int n = 0;
@@ -183,11 +183,12 @@ __device__ __noinline__ void list_tc_items(const PaArgs& a, int* first, char* sc
       all += s_warp[w];
       below += w < warp ? s_warp[w] : 0;
     }
-    if (b < a.B) first[b] = base + below + sum - n;
+    if (b < a.B) first[b] = static_cast<int>(min(base + below + sum - n, static_cast<int64_t>(INT_MAX)));
     base += all;
     __syncthreads();
   }
-  const int total = base;
+  // offsets out of order can name rows twice; the list has room for them once
+  const int total = static_cast<int>(min(base, tc_places(a)));
   const int64_t widest = *s_max + 1;
   auto look = [&](int i, int& b, int& blk) {   // the i-th block; its length
     int lo = 0, hi = a.B - 1;

@@ -55,7 +55,7 @@ constexpr int kTcStep = 128;       // cached tokens of its steps
 constexpr int kMaxSms = 160, kTcSlots = kMaxSms * 4 / 3 + 1;
 
 // The most row blocks that the requests can have, for one key head.
-inline int64_t tc_places(const PaArgs& a) { return static_cast<int64_t>(a.T) * a.group / kTcItemRows + a.B; }
+__host__ __device__ inline int64_t tc_places(const PaArgs& a) { return static_cast<int64_t>(a.T) * a.group / kTcItemRows + a.B; }
 
 // Cached tokens that the new tokens of a request can see, in blocks of `unit`
 // tokens: the blocks with the first visible positions of a window's sinks,
