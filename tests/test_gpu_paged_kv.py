@@ -366,14 +366,15 @@ def test_attention_same_bits_every_time():
 
 
 # Enough rows for the tensor-memory kernel, and contexts long enough that it cuts
-# row blocks along the cached tokens; the third mixes both kernels, the fourth and
-# fifth have equal prompts.
+# row blocks along the cached tokens; the third and the last mix both kernels, the
+# fourth and fifth have equal prompts.
 MANY = [
     ([64, 130], [900, 130], dict(Hq=16, Hkv=2)),
     ([300], [1500], dict(Hq=7, Hkv=1, D=64, page=64)),
     ([1, 100, 0, 3], [700, 2100, 40, 5], dict(Hq=32, Hkv=4, page=32, order="nhd")),
     ([128, 128], [128, 1000], dict(Hq=8, Hkv=8)),
     ([65] * 4, [65, 770, 769, 66], dict(Hq=8, Hkv=8, D=64, page=128)),
+    ([1] * 6 + [100] + [1] * 6, [1700] * 6 + [400] + [1700] * 6, dict(Hq=32, Hkv=8, D=64, page=64)),
 ]
 
 
