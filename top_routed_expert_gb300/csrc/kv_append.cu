@@ -91,9 +91,23 @@ struct Raw {
   uint2 a, b;
 };
 
-// (Plain loads: the queries may be turned in place.)
+// (Plain loads: the queries may be turned in place.  The interleaved layout's
+// eight elements are one piece.)
+template <bool HALF>
 __device__ __forceinline__ Raw load_raw(const uint16_t* row, const Place& p) {
-  return Raw{*reinterpret_cast<const uint2*>(row + p.oa), *reinterpret_cast<const uint2*>(row + p.ob)};
+  if (HALF) return Raw{*reinterpret_cast<const uint2*>(row + p.oa), *reinterpret_cast<const uint2*>(row + p.ob)};
+  const uint4 w = *reinterpret_cast<const uint4*>(row + p.oa);
+  return Raw{make_uint2(w.x, w.y), make_uint2(w.z, w.w)};
+}
+template <bool HALF>
+__device__ __forceinline__ void store_row(uint16_t* row, const Place& p, const float (&x)[8]) {
+  const uint2 a = pack4(x), b = pack4(x + 4);
+  if (HALF) {
+    *reinterpret_cast<uint2*>(row + p.oa) = a;
+    *reinterpret_cast<uint2*>(row + p.ob) = b;
+  } else {
+    *reinterpret_cast<uint4*>(row + p.oa) = make_uint4(a.x, a.y, b.x, b.y);
+  }
 }
 
 // (cos, sin) of the thread's four pairs: frequencies oa..oa+3 of the half
@@ -167,9 +181,10 @@ __device__ __forceinline__ int table_row(const KaArgs& a, int t, int pos) {
 
 // The new codes of a thread's eight elements, or the old ones rounded to a scale
 // that has grown.
+template <bool HALF>
 __device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, const float (&x)[8], float inv) {
   const uint32_t lo = codes4(x, inv), hi = codes4(x + 4, inv);
-  if (p.ob == p.oa + 4) {
+  if (!HALF || p.ob == p.oa + 4) {
     *reinterpret_cast<uint2*>(row + p.oa) = make_uint2(lo, hi);
   } else {
     *reinterpret_cast<uint32_t*>(row + p.oa) = lo;
@@ -219,7 +234,7 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
   if (page < a.c.max_pages) pid = a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page];
   const int lr = threadIdx.x % TPR, grp = threadIdx.x / TPR, rows = blockDim.x / TPR;
   const bool norm = a.gamma_k;
-  const Place p = place_of<HALF>(lr, a.rot), pv = place_of<HALF>(lr, 0);
+  const Place p = place_of<HALF>(lr, a.rot), pv = place_of<false>(lr, 0);
   const int t0 = r.row0 - r.start;         // row of position 0
   Gamma gamma = {};
   if (norm) gamma = load_gamma(a.gamma_k, p);
@@ -234,7 +249,7 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
     rk[i] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
     rv[i] = make_uint4(0, 0, 0, 0);
     if (take[i]) {
-      rk[i] = load_raw(a.k + (t0 + j) * a.ks + static_cast<int64_t>(head) * D, p);
+      rk[i] = load_raw<HALF>(a.k + (t0 + j) * a.ks + static_cast<int64_t>(head) * D, p);
       rv[i] = *reinterpret_cast<const uint4*>(a.v + (t0 + j) * a.vs + static_cast<int64_t>(head) * D + pv.oa);
     }
   }
@@ -313,11 +328,11 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
     uint8_t* kc = static_cast<uint8_t*>(a.c.k) + row;
     uint8_t* vc = static_cast<uint8_t*>(a.c.v) + row;
     if (take[i]) {
-      store_codes(kc, p, x[i], inv_k);
+      store_codes<HALF>(kc, p, x[i], inv_k);
       float y[8];
       unpack4(make_uint2(rv[i].x, rv[i].y), y);
       unpack4(make_uint2(rv[i].z, rv[i].w), y + 4);
-      store_codes(vc, pv, y, inv_v);
+      store_codes<false>(vc, pv, y, inv_v);
     } else if (had && j < r.start) {
       if (sk > old_k) rescale_codes(kc, p, old_k * inv_k);
       if (sv > old_v) rescale_codes(vc, pv, old_v * inv_v);
@@ -340,7 +355,7 @@ __device__ __forceinline__ void query_block(const KaArgs& a, int t) {
       for (int i = 0; i < HEADS; ++i) {
         const int h = h0 + i * groups + grp;
         raw[n][i] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
-        if (h < a.Hq && t + n < a.T) raw[n][i] = load_raw(a.q + (t + n) * a.qs + h * D, p);
+        if (h < a.Hq && t + n < a.T) raw[n][i] = load_raw<HALF>(a.q + (t + n) * a.qs + h * D, p);
       }
   };
   load(0);
@@ -377,8 +392,7 @@ __device__ __forceinline__ void query_block(const KaArgs& a, int t) {
         norm_rotate<TPR, HALF>(x, norm, gamma, p, cs[n], a.eps);
         if (h < a.Hq && live[n]) {
           uint16_t* dst = a.q_out + (t + n) * a.qos + h * D;
-          *reinterpret_cast<uint2*>(dst + p.oa) = pack4(x);
-          *reinterpret_cast<uint2*>(dst + p.ob) = pack4(x + 4);
+          store_row<HALF>(dst, p, x);
         }
       }
   }
