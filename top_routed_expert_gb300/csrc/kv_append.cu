@@ -2,10 +2,22 @@
 // norm, rotation, page scale and E4M3 codes in one launch.
 //
 // Two kinds of blocks.  A cache block owns one page of one request for one
-// head, keys and values: all new tokens of the page pass through its
-// registers, so the page's scales are one block reduction and every code is
-// written once.  A query block owns a token, or a few where a token has few
-// heads, and turns all query heads.
+// head or several, keys and values: a head's new tokens of the page all pass
+// through its registers, so the page's scales are one block reduction and every
+// code is written once.  A query block owns a token, or a few where a token has
+// few heads, and turns all query heads.
+//
+// With y = norm(x) rotated and s the smallest power of two that holds the page's
+// largest |y| in E4M3's 448, a code is y / s rounded once; everything before it
+// is fp32.  A page that already holds tokens keeps the larger of its scales, and
+// its old codes are halved as often as that grew.
+//
+// Bound by memory, and by how many bytes the look-ups before them let be on
+// their way: q is read and written once (bf16), k and v are read, their codes
+// written.  Measured: 32 x 256 tokens of 32 + 4 heads of 128, norm and rotation,
+// 164 MB in 32.4 us = 5.1 TB/s; ragged prompts up to 1999 tokens of 16 + 16 heads
+// of 64, 238 MB in 54 us = 4.4 TB/s; 64 single tokens 4.1 us, a launch and four
+// dependent loads.
 //
 // Which pages a ragged batch touches is known on the device only.  A request
 // of n new tokens touches at most n/page + 2 pages, so request b's blocks
@@ -18,6 +30,7 @@ namespace {
 
 constexpr float kMinScale = 9.094947017729282e-13f;   // 2^-40
 constexpr int kQueryThreads = 128;
+constexpr int kMaxHeads = 8;   // of a cache block
 
 struct KaArgs {
   const uint16_t* q;
@@ -33,7 +46,8 @@ struct KaArgs {
   moe_kv_cache_t c;
   unsigned* status;
   int64_t qs, ks, vs, qos;
-  int T, B, Hq, rot, n_pos, items;   // items: page blocks per head
+  int T, B, Hq, rot, n_pos, items;   // items: pages that the requests can touch
+  int heads, head_blocks;            // heads of a cache block; its blocks for a page
   float eps;
   bool half;
 };
@@ -212,12 +226,27 @@ __device__ __forceinline__ float largest(const float (&x)[8], bool& bad) {
   return top;
 }
 
-// One page, one head.  PASSES rows per thread group; the block covers the
-// page's slots in PASSES rounds of blockDim / TPR rows.
-template <int D, int PASSES, bool HALF>
-__device__ __forceinline__ void append_block(const KaArgs& a, int item, int head) {
-  constexpr int TPR = D / 8;
-  __shared__ float s_amax[2][32];
+// Heads that a cache block has under way at a time: two where they fit.
+__host__ __device__ constexpr int append_stages(int passes, int threads) { return passes * threads <= 512 ? 2 : 1; }
+constexpr size_t append_smem(int passes, int threads) {
+  return static_cast<size_t>(append_stages(passes, threads)) * passes * threads * 2 * sizeof(uint4);
+}
+
+__device__ __forceinline__ void copy_async(void* to, const void* from, int bytes) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+  if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
+}
+
+// One page, heads [head0, head1).  PASSES rows per thread group; the block
+// covers the page's slots in PASSES rounds of blockDim / TPR rows.  A thread
+// fetches its own elements of the next head (asynchronously, so they cost no
+// registers and no barrier) while it works on this one.
+template <int D, int PASSES, bool HALF, int THREADS>
+__device__ __forceinline__ void append_block(const KaArgs& a, int item, int head0, int head1) {
+  constexpr int TPR = D / 8, STAGES = append_stages(PASSES, THREADS);
+  __shared__ float s_amax[2][2][32];
+  extern __shared__ __align__(16) uint4 s_rows[];   // [STAGES][PASSES][key, value][THREADS]
   const int ps = a.c.page_size, ps_log = 31 - __clz(ps);
   const int b = warp_find_request(a.cu, a.B, item, 1, ps, 2);
   const Request r = load_request(a.cu, a.kv_len, b, a.T);
@@ -230,112 +259,141 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
   const int page = (r.start >> ps_log) + at;
   const int base = page << ps_log;
   if (at < 0 || base >= r.end) return;   // one block too many, or before the first request
-  int pid = -1;
-  if (page < a.c.max_pages) pid = a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page];
   const int lr = threadIdx.x % TPR, grp = threadIdx.x / TPR, rows = blockDim.x / TPR;
   const bool norm = a.gamma_k;
   const Place p = place_of<HALF>(lr, a.rot), pv = place_of<false>(lr, 0);
   const int t0 = r.row0 - r.start;         // row of position 0
-  Gamma gamma = {};
-  if (norm) gamma = load_gamma(a.gamma_k, p);
-  Raw rk[PASSES];
-  uint4 rv[PASSES];
-  float2 cs[PASSES][4];
-  bool take[PASSES], outside = false;
+  bool take[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int j = base + i * rows + grp;
     take[i] = j >= r.start && j < r.end && j < base + ps;
-    rk[i] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
-    rv[i] = make_uint4(0, 0, 0, 0);
-    if (take[i]) {
-      rk[i] = load_raw<HALF>(a.k + (t0 + j) * a.ks + static_cast<int64_t>(head) * D, p);
-      rv[i] = *reinterpret_cast<const uint4*>(a.v + (t0 + j) * a.vs + static_cast<int64_t>(head) * D + pv.oa);
-    }
   }
+  auto slot = [&](int head, int i, int kv) {
+    return s_rows + (((head - head0) % STAGES * PASSES + i) * 2 + kv) * THREADS + threadIdx.x;
+  };
+  auto fetch = [&](int head) {
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      if (!take[i]) continue;
+      const int64_t row = t0 + base + i * rows + grp;
+      const uint16_t* k = a.k + row * a.ks + static_cast<int64_t>(head) * D;
+      uint4* to = slot(head, i, 0);
+      if (HALF) {
+        copy_async(to, k + p.oa, 8);
+        copy_async(reinterpret_cast<uint2*>(to) + 1, k + p.ob, 8);
+      } else {
+        copy_async(to, k + p.oa, 16);
+      }
+      copy_async(slot(head, i, 1), a.v + row * a.vs + static_cast<int64_t>(head) * D + pv.oa, 16);
+    }
+  };
+  int next = head0;   // the next head to fetch
+  auto fetch_next = [&] {
+    if (next < head1) fetch(next);
+    ++next;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch_next();
+  if (STAGES > 1) fetch_next();
+  int pid = -1;
+  if (page < a.c.max_pages) pid = a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page];
+  Gamma gamma = {};
+  if (norm) gamma = load_gamma(a.gamma_k, p);
+  float2 cs[PASSES][4];
+  bool outside = false;
   if (a.rot > 0) {
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int j = base + i * rows + grp;
       if (!take[i]) continue;
       const int f = table_row(a, t0 + j, j);
-      if (f < 0) {
-        outside = true;
-        take[i] = false;
-        rv[i] = make_uint4(0, 0, 0, 0);
-      } else if (p.rotates) {
-        load_cs<HALF>(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), p, cs[i]);
-      }
+      if (f < 0) outside = true;
+      if (f < 0) take[i] = false;   // what is on its way goes unread
+      else if (p.rotates) load_cs<HALF>(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), p, cs[i]);
     }
   }
+  if (outside && lr == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
   if (pid < 0 || pid >= a.c.n_pages) {
     if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
-  const int64_t scale_at = static_cast<int64_t>(pid) * a.c.n_kv_heads + head;
   const bool had = r.start > base;
-  const float old_k = had ? a.c.k_scale[scale_at] : 0.f, old_v = had ? a.c.v_scale[scale_at] : 0.f;
-  float x[PASSES][8], top_k = 0.f;
-  uint32_t bits_v = 0;   // the largest size among the values as bf16 bits
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    unpack4(rk[i].a, x[i]);
-    unpack4(rk[i].b, x[i] + 4);
-    norm_rotate<TPR, HALF>(x[i], norm, gamma, p, cs[i], a.eps);
-    if (take[i]) top_k = fmaxf(top_k, largest(x[i], bad));
-    const uint32_t w = __vmaxu2(__vmaxu2(rv[i].x & 0x7fff7fffu, rv[i].y & 0x7fff7fffu),
-                                __vmaxu2(rv[i].z & 0x7fff7fffu, rv[i].w & 0x7fff7fffu));
-    bits_v = __vmaxu2(bits_v, w);
-  }
-  bits_v = max(bits_v & 0xffffu, bits_v >> 16);
-  float top_v = __uint_as_float(bits_v << 16);
-  if (bits_v >= 0x7f80u) {   // an infinity or a NaN among them
-    top_v = 0.f;
+#pragma unroll 1
+  for (int head = head0; head < head1; ++head) {
+    const int64_t scale_at = static_cast<int64_t>(pid) * a.c.n_kv_heads + head;
+    const float old_k = had ? a.c.k_scale[scale_at] : 0.f, old_v = had ? a.c.v_scale[scale_at] : 0.f;
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+    float x[PASSES][8], top_k = 0.f;
+    uint4 rv[PASSES];
+    uint32_t bits_v = 0;   // the largest size among the values as bf16 bits
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-      float y[8];
-      unpack4(make_uint2(rv[i].x, rv[i].y), y);
-      unpack4(make_uint2(rv[i].z, rv[i].w), y + 4);
-      top_v = fmaxf(top_v, largest(y, bad));
+      const uint4 zero = make_uint4(0, 0, 0, 0), rk = take[i] ? *slot(head, i, 0) : zero;
+      rv[i] = take[i] ? *slot(head, i, 1) : zero;
+      unpack4(make_uint2(rk.x, rk.y), x[i]);
+      unpack4(make_uint2(rk.z, rk.w), x[i] + 4);
     }
-  }
-  if (bad) set_status(a.status, MOE_ERR_DEVICE_NONFINITE);
-  if (outside && lr == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-  // sizes order like their bits
-  top_k = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_k)));
-  top_v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_v)));
-  if ((threadIdx.x & 31) == 0) {
-    s_amax[0][threadIdx.x >> 5] = top_k;
-    s_amax[1][threadIdx.x >> 5] = top_v;
-  }
-  __syncthreads();   // also: every thread has read the old scales
-  for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) {
-    top_k = fmaxf(top_k, s_amax[0][w]);
-    top_v = fmaxf(top_v, s_amax[1][w]);
-  }
-  const float sk = fmaxf(scale_for(top_k), old_k), sv = fmaxf(scale_for(top_v), old_v);
-  if (threadIdx.x == 0) {
-    a.c.k_scale[scale_at] = sk;
-    a.c.v_scale[scale_at] = sv;
-  }
-  const float inv_k = 1.0f / sk, inv_v = 1.0f / sv;
-  const int64_t page_at = pid * a.c.page_stride + head * a.c.head_stride;
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int j = base + i * rows + grp;
-    const int64_t row = page_at + (j - base) * a.c.token_stride;
-    uint8_t* kc = static_cast<uint8_t*>(a.c.k) + row;
-    uint8_t* vc = static_cast<uint8_t*>(a.c.v) + row;
-    if (take[i]) {
-      store_codes<HALF>(kc, p, x[i], inv_k);
-      float y[8];
-      unpack4(make_uint2(rv[i].x, rv[i].y), y);
-      unpack4(make_uint2(rv[i].z, rv[i].w), y + 4);
-      store_codes<false>(vc, pv, y, inv_v);
-    } else if (had && j < r.start) {
-      if (sk > old_k) rescale_codes(kc, p, old_k * inv_k);
-      if (sv > old_v) rescale_codes(vc, pv, old_v * inv_v);
+    for (int i = 0; i < PASSES; ++i) {
+      norm_rotate<TPR, HALF>(x[i], norm, gamma, p, cs[i], a.eps);
+      if (take[i]) top_k = fmaxf(top_k, largest(x[i], bad));
+      const uint32_t w = __vmaxu2(__vmaxu2(rv[i].x & 0x7fff7fffu, rv[i].y & 0x7fff7fffu),
+                                  __vmaxu2(rv[i].z & 0x7fff7fffu, rv[i].w & 0x7fff7fffu));
+      bits_v = __vmaxu2(bits_v, w);
+    }
+    bits_v = max(bits_v & 0xffffu, bits_v >> 16);
+    float top_v = __uint_as_float(bits_v << 16);
+    if (bits_v >= 0x7f80u) {   // an infinity or a NaN among them
+      top_v = 0.f;
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        float y[8];
+        unpack4(make_uint2(rv[i].x, rv[i].y), y);
+        unpack4(make_uint2(rv[i].z, rv[i].w), y + 4);
+        top_v = fmaxf(top_v, largest(y, bad));
+      }
+    }
+    if (bad) set_status(a.status, MOE_ERR_DEVICE_NONFINITE);
+    // sizes order like their bits
+    top_k = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_k)));
+    top_v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_v)));
+    float(&amax)[2][32] = s_amax[head & 1];   // in turn: one barrier for a head
+    if ((threadIdx.x & 31) == 0) {
+      amax[0][threadIdx.x >> 5] = top_k;
+      amax[1][threadIdx.x >> 5] = top_v;
+    }
+    __syncthreads();   // also: every thread has read the old scales
+    fetch_next();      // over what was read above
+    for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) {
+      top_k = fmaxf(top_k, amax[0][w]);
+      top_v = fmaxf(top_v, amax[1][w]);
+    }
+    const float sk = fmaxf(scale_for(top_k), old_k), sv = fmaxf(scale_for(top_v), old_v);
+    if (threadIdx.x == 0) {
+      a.c.k_scale[scale_at] = sk;
+      a.c.v_scale[scale_at] = sv;
+    }
+    const float inv_k = 1.0f / sk, inv_v = 1.0f / sv;
+    const int64_t page_at = pid * a.c.page_stride + head * a.c.head_stride;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int j = base + i * rows + grp;
+      const int64_t row = page_at + (j - base) * a.c.token_stride;
+      uint8_t* kc = static_cast<uint8_t*>(a.c.k) + row;
+      uint8_t* vc = static_cast<uint8_t*>(a.c.v) + row;
+      if (take[i]) {
+        store_codes<HALF>(kc, p, x[i], inv_k);
+        float y[8];
+        unpack4(make_uint2(rv[i].x, rv[i].y), y);
+        unpack4(make_uint2(rv[i].z, rv[i].w), y + 4);
+        store_codes<false>(vc, pv, y, inv_v);
+      } else if (had && j < r.start) {
+        if (sk > old_k) rescale_codes(kc, p, old_k * inv_k);
+        if (sv > old_v) rescale_codes(vc, pv, old_v * inv_v);
+      }
     }
   }
 }
@@ -404,22 +462,22 @@ template <int D> __host__ __device__ __forceinline__ int query_tokens(int Hq, in
   return Hq <= groups ? 4 : Hq <= 2 * groups ? 2 : 1;
 }
 
-// Blocks [0, Hkv items): cache blocks; the rest: query blocks.
 // Blocks on an SM that the registers are cut for: more of them hide more of the
-// look-ups' latency (prefill of 32 x 256 tokens, two rows a thread: 37.4 us with
-// the compiler's choice of 5, 32.6 us with 7; ragged prompts with four rows a
-// thread: 67.6 and 58.7 us).
+// look-ups' latency (before a block took several heads: prefill of 32 x 256
+// tokens, two rows a thread, 37.4 us with the compiler's choice of 5, 32.6 us
+// with 7; ragged prompts, four rows a thread, 67.6 and 58.7 us).
 template <int PASSES, int THREADS> constexpr int blocks_on_sm() {
   return THREADS == 128 ? (PASSES < 4 ? 7 : 6) : THREADS == 256 ? 3 : 1;
 }
 
+// Blocks [0, head_blocks items): cache blocks; the rest: query blocks.
 template <int D, int PASSES, bool HALF, int THREADS>
 __global__ void __launch_bounds__(THREADS, blocks_on_sm<PASSES, THREADS>()) kv_append_kernel(KaArgs a) {
   pdl_enter();
-  const int n_cache = a.c.n_kv_heads * a.items, i = blockIdx.x;
+  const int n_cache = a.head_blocks * a.items, i = blockIdx.x;
   if (i < n_cache) {
-    const int item = i / a.c.n_kv_heads;
-    append_block<D, PASSES, HALF>(a, item, i - item * a.c.n_kv_heads);
+    const int item = i / a.head_blocks, head0 = (i - item * a.head_blocks) * a.heads;
+    append_block<D, PASSES, HALF, THREADS>(a, item, head0, min(head0 + a.heads, a.c.n_kv_heads));
     return;
   }
   const int q = i - n_cache;
@@ -431,25 +489,37 @@ __global__ void __launch_bounds__(THREADS, blocks_on_sm<PASSES, THREADS>()) kv_a
 }
 
 template <int D, int PASSES, int THREADS>
-cudaError_t launch(const KaArgs& a, int threads, cudaStream_t s) {
-  int64_t blocks = int64_t(a.c.n_kv_heads) * a.items;
+cudaError_t launch(KaArgs a, int threads, int sms, cudaStream_t s) {
+  // A block takes several heads of a page where there are more pages and heads
+  // than blocks at a time: look-ups and angles then serve them all, and the next
+  // head's rows come while one is worked on (16 heads, 64 tokens a page: 68 us
+  // with a head a block, 57 with four, 54 with six; fewer blocks than fit at
+  // once would leave SMs idle).
+  const int64_t at_once = static_cast<int64_t>(sms) * blocks_on_sm<PASSES, THREADS>();
+  const int64_t pages = a.T / a.c.page_size + std::min<int64_t>(a.B, a.T);
+  a.heads = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxHeads, pages * a.c.n_kv_heads / at_once)));
+  a.head_blocks = ceil_div(a.c.n_kv_heads, a.heads);
+  int64_t blocks = static_cast<int64_t>(a.head_blocks) * a.items;
   if (a.q) blocks += ceil_div(a.T, query_tokens<D>(a.Hq, threads));
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  count_launches(1);
   const unsigned n = static_cast<unsigned>(blocks);
-  return a.half ? launch_pdl(kv_append_kernel<D, PASSES, true, THREADS>, n, threads, 0, s, a)
-                : launch_pdl(kv_append_kernel<D, PASSES, false, THREADS>, n, threads, 0, s, a);
+  const auto kernel = a.half ? kv_append_kernel<D, PASSES, true, THREADS> : kv_append_kernel<D, PASSES, false, THREADS>;
+  constexpr size_t smem = append_smem(PASSES, THREADS);
+  const cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  count_launches(1);
+  return launch_pdl(kernel, n, threads, smem, s, a);
 }
 
 template <int D>
-cudaError_t launch_d(const KaArgs& a, cudaStream_t s) {
+cudaError_t launch_d(const KaArgs& a, int sms, cudaStream_t s) {
   // rows of eight elements a thread, at most four a thread
   const int work = a.c.page_size * (D / 8), threads = std::max(kQueryThreads, work / 4);
-  if (work <= kQueryThreads) return launch<D, 1, kQueryThreads>(a, kQueryThreads, s);
-  if (work <= 2 * kQueryThreads) return launch<D, 2, kQueryThreads>(a, kQueryThreads, s);
-  if (threads <= kQueryThreads) return launch<D, 4, kQueryThreads>(a, threads, s);
-  if (threads <= 256) return launch<D, 4, 256>(a, threads, s);
-  return launch<D, 4, D == 256 ? 1024 : 512>(a, threads, s);
+  if (work <= kQueryThreads) return launch<D, 1, kQueryThreads>(a, kQueryThreads, sms, s);
+  if (work <= 2 * kQueryThreads) return launch<D, 2, kQueryThreads>(a, kQueryThreads, sms, s);
+  if (threads <= kQueryThreads) return launch<D, 4, kQueryThreads>(a, threads, sms, s);
+  if (threads <= 256) return launch<D, 4, 256>(a, threads, sms, s);
+  return launch<D, 4, D == 256 ? 1024 : 512>(a, threads, sms, s);
 }
 
 bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
@@ -517,9 +587,9 @@ extern "C" moe_status_t moe_kv_append(const moe_kv_append_config_t* cfg, const m
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err;
   switch (D) {
-    case 64: err = launch_d<64>(a, s); break;
-    case 128: err = launch_d<128>(a, s); break;
-    default: err = launch_d<256>(a, s); break;
+    case 64: err = launch_d<64>(a, sms, s); break;
+    case 128: err = launch_d<128>(a, sms, s); break;
+    default: err = launch_d<256>(a, sms, s); break;
   }
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -29,6 +29,16 @@
 // sums to over 2^15: until then they fit f16 (65504), and the quotient is the
 // same.  So the scores are read once, no maximum is taken in the ordinary step,
 // and the accumulator is almost never rescaled.
+//
+// Few items would leave SMs idle, so long ones are cut along the tokens
+// (paged_attn.cu) and paged_attn_tc_join adds the parts up in order.
+//
+// Measured: 32 x 256 tokens of 4 x 8 heads of 128 behind up to 3328 others, 241
+// GFLOP in 263 us = 915 TFLOP/s; the tensor pipe is active 41 % of the time.  A
+// step of 128 tokens takes about 2 us.  Its 32 MMAs of 128 x 128 x 16 take about
+// 104 cycles each where one of 128 x 256 x 16 takes 135 (the accumulators of both
+// tiles and a second score buffer leave no room for wider ones), which makes 1.75
+// us; the rest is the hand-over between scores, weights and products.
 #include <climits>
 
 #include "paged_attn.cuh"

@@ -15,6 +15,16 @@
 //    in shared memory (moving a list up in registers took a third of a round);
 //  - which expert a key belongs to is looked up at the end, for the chosen ones
 //    alone, by the lane of their slot.
+//
+// score s = sigmoid(L) or softmax(L); choice c = s + bias (without a bias the
+// order of L is that of s, and c = L); a group's value is the sum of its `rank`
+// largest c; k experts of the best groups by c, ties to the lowest; weights
+// scale s / sum of the chosen s.
+//
+// Measured: 65519 tokens of 256 experts (8 groups, bias, sigmoid, bf16, k = 8)
+// 53 us, 730 warp instructions a token at 73 % of the issue slots, 0.7 TB/s; one
+// token of 128 experts 3.0 us, a launch.  A token for half a warp would halve the
+// rounds' cost but double the sort's and leaves the scores' as it is.
 #include <cmath>
 
 #include "common.cuh"
