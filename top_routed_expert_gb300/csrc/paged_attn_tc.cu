@@ -34,11 +34,13 @@
 // (paged_attn.cu) and paged_attn_tc_join adds the parts up in order.
 //
 // Measured: 32 x 256 tokens of 4 x 8 heads of 128 behind up to 3328 others, 241
-// GFLOP in 263 us = 915 TFLOP/s; the tensor pipe is active 41 % of the time.  A
-// step of 128 tokens takes about 2 us.  Its 32 MMAs of 128 x 128 x 16 take about
-// 104 cycles each where one of 128 x 256 x 16 takes 135 (the accumulators of both
-// tiles and a second score buffer leave no room for wider ones), which makes 1.75
-// us; the rest is the hand-over between scores, weights and products.
+// GFLOP in 262 us = 919 TFLOP/s, the tensor pipe active 41 % of the time; one
+// prompt of 8192, 550 GFLOP in 477 us = 1153 TFLOP/s.  A step of 128 tokens takes
+// about 2.2 us.  Its 32 MMAs of 128 x 128 x 16 take about 104 cycles each, 1.75 us
+// (one of 128 x 256 x 16 takes 135, but two tiles' scores and outputs fill the
+// tensor memory); the rest is the hand-over between scores, weights and products.
+// An item's start and end (its q, the first reference, its output) cost two to
+// three steps more, which is what the short prompts lose.
 #include <climits>
 
 #include "paged_attn.cuh"
