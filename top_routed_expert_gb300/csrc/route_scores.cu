@@ -39,10 +39,10 @@ namespace {
 constexpr int kRsWarps = 4;
 constexpr float kMasked = -INFINITY;
 
-// Order-preserving key of a value that is finite or -infinity (-0 folded onto
-// +0).  -infinity maps to 0x007fffff, so 0 is free to mark "not available".
+// Order-preserving key of a value that is finite or -infinity, and not -0.
+// -infinity maps to 0x007fffff, so 0 is free to mark "not available".
 __device__ __forceinline__ uint32_t value_key(float v) {
-  const uint32_t u = __float_as_uint(v + 0.0f);
+  const uint32_t u = __float_as_uint(v);
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 constexpr uint32_t kMaskedKey = 0x007fffffu;
@@ -95,6 +95,23 @@ __device__ __forceinline__ void put(uint32_t* to, const uint32_t (&v)[N]) {
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) to[i] = v[i];
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void get(const uint32_t* from, uint32_t (&v)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(from + i);
+      v[i] = x.x;
+      v[i + 1] = x.y;
+      v[i + 2] = x.z;
+      v[i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = from[i];
   }
 }
 
@@ -165,7 +182,8 @@ __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(
   // per warp: a token's keys (first the values that rank groups) and scores
   __shared__ __align__(16) uint32_t s_key[kRsWarps][32 * EPL];
   __shared__ __align__(16) float s_score[kRsWarps][32 * EPL];
-  __shared__ uint32_t s_sorted[kRsWarps][EPL + 1][32];   // each lane's keys in order, 0 behind the last
+  constexpr int kList = EPL % 4 == 0 ? 12 : EPL + 1;   // words of a lane's list: 16-byte stores without conflicts
+  __shared__ __align__(16) uint32_t s_sorted[kRsWarps][32 * kList];   // each lane's keys in order, 0 behind the last
   pdl_enter();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = gridDim.x * kRsWarps;
   int t = blockIdx.x * kRsWarps + warp;
@@ -186,8 +204,9 @@ __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(
   // groups that are a power of two of whole lanes are ranked by shuffles
   const int lpg = gs / EPL;
   const bool by_lanes = gs == lpg * EPL && (lpg & (lpg - 1)) == 0;
-  const int my_group = lane * EPL / gs;   // by_lanes
-  s_sorted[warp][EPL][lane] = 0u;
+  const int lpg_log = by_lanes ? 31 - __clz(lpg) : 0, my_group = lane >> lpg_log;
+  uint32_t* list = s_sorted[warp] + lane * kList;
+  list[EPL] = 0u;
 
   while (true) {
     float L[EPL], s[EPL], c[EPL];
@@ -245,23 +264,29 @@ __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(
 #pragma unroll
     for (int i = 0; i < EPL; ++i) c[i] = !BIAS ? L[i] : L[i] > kMasked ? __fadd_rn(s[i], bias[i]) : kMasked;
     // groups
-    uint32_t keep = 0xffffffffu;   // by_lanes: all or nothing of this lane; else a bit for each of its experts
+    bool kept = true;              // by_lanes: this lane's group
+    uint32_t keep = 0xffffffffu;   // else a bit for each of the lane's experts
     if (a.tg < a.G) {
       // what ranks the groups: the values, or without a bias the scores where two are added
       float v[EPL];
 #pragma unroll
       for (int i = 0; i < EPL; ++i) v[i] = !BIAS && a.rank == 2 ? numer[i] : c[i];
-      int better = 0;
       if (by_lanes) {
         Top2 two = top2_of<EPL>(v);
         for (int off = 1; off < lpg; off <<= 1)
           two = merge(two, Top2{__shfl_xor_sync(0xffffffffu, two.first, off), __shfl_xor_sync(0xffffffffu, two.second, off)});
         const float value = (a.rank == 2 && gs > 1) ? two.first + two.second : two.first;
-        for (int g = 0; g < a.G; ++g) {
-          const float u = __shfl_sync(0xffffffffu, value, g * lpg);
-          better += (u > value || (u == value && g < my_group)) ? 1 : 0;
+        // the best group that is left, the lowest among equals, tg times
+        uint32_t left = my_group < a.G ? value_key(value + 0.0f) : 0u;
+        kept = false;
+        for (int j = 0; j < a.tg; ++j) {
+          const uint32_t best = __reduce_max_sync(0xffffffffu, left);
+          const int src = __ffs(__ballot_sync(0xffffffffu, left == best)) - 1;
+          if (my_group == src >> lpg_log) {
+            kept = true;
+            left = 0u;
+          }
         }
-        keep = better < a.tg ? 0xffffffffu : 0u;
       } else {
         float* val = s_score[warp];
 #pragma unroll
@@ -271,6 +296,7 @@ __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(
         if (lane < a.G)
           for (int i = 0; i < gs; ++i) two = merge(two, Top2{val[lane * gs + i], kMasked});
         const float value = (a.rank == 2 && gs > 1) ? two.first + two.second : two.first;
+        int better = 0;
         for (int g = 0; g < a.G; ++g) {
           const float u = __shfl_sync(0xffffffffu, value, g);
           better += (u > value || (u == value && g < lane)) ? 1 : 0;
@@ -286,29 +312,25 @@ __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(
     uint32_t key[EPL], score_bits[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      key[i] = value_key(c[i]) & keep;
+      key[i] = value_key(BIAS ? c[i] : c[i] + 0.0f);   // s + bias is never -0
       score_bits[i] = __float_as_uint(s[i]);
     }
     if (!by_lanes && a.tg < a.G) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) key[i] = (keep >> i) & 1u ? value_key(c[i]) : 0u;
+      for (int i = 0; i < EPL; ++i) key[i] = (keep >> i) & 1u ? key[i] : 0u;
     }
     put(s_key[warp] + lane * EPL, key);
     put(reinterpret_cast<uint32_t*>(s_score[warp]) + lane * EPL, score_bits);
     // k rounds: the warp's largest key, from the lowest lane that holds it
     sort_descending<EPL>(key);
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) s_sorted[warp][i][lane] = key[i];
-    uint32_t head = key[0], my_key = 0u;
-    const uint32_t* rest = &s_sorted[warp][1][lane];
+    put(list, key);
+    uint32_t head = kept ? key[0] : 0u, my_key = 0u;
+    const uint32_t* rest = list;
     int my_src = 0;
     for (int j = 0; j < a.k; ++j) {
       const uint32_t wk = __reduce_max_sync(0xffffffffu, head);
       const int src = __ffs(__ballot_sync(0xffffffffu, head == wk)) - 1;
-      if (lane == src) {
-        head = *rest;
-        rest += 32;
-      }
+      if (lane == src) head = *++rest;
       if (lane == j) {
         my_key = wk;
         my_src = src;
@@ -320,18 +342,13 @@ __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(
     const int before_src = __shfl_up_sync(0xffffffffu, my_src, 1);
     const unsigned starts = __ballot_sync(0xffffffffu, lane == 0 || before_key != my_key || before_src != my_src);
     int nth = lane - (31 - __clz(starts & (0xffffffffu >> (31 - lane))));
-    int my_e = my_src * EPL;
     __syncwarp();
-    bool found = false;
+    get(s_key[warp] + my_src * EPL, key);
+    uint32_t hits = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const bool hit = !found && s_key[warp][my_src * EPL + i] == my_key;
-      if (hit && nth == 0) {
-        my_e = my_src * EPL + i;
-        found = true;
-      }
-      if (hit) --nth;
-    }
+    for (int i = 0; i < EPL; ++i) hits |= key[i] == my_key ? 1u << i : 0u;
+    for (nth = lane < a.k ? nth : 0; nth > 0; --nth) hits &= hits - 1;
+    const int my_e = my_src * EPL + __ffs(hits) - 1;
     float my_s = lane < a.k && my_key > kMaskedKey ? s_score[warp][my_e] : 0.f;
     float sum = my_s;
 #pragma unroll
