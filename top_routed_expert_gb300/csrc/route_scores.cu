@@ -22,9 +22,10 @@
 // scale s / sum of the chosen s.
 //
 // Measured: 65519 tokens of 256 experts (8 groups, bias, sigmoid, bf16, k = 8)
-// 53 us, 730 warp instructions a token at 73 % of the issue slots, 0.7 TB/s; one
-// token of 128 experts 3.0 us, a launch.  A token for half a warp would halve the
-// rounds' cost but double the sort's and leaves the scores' as it is.
+// 49.5 us, about 670 warp instructions a token at three quarters of the issue
+// slots, 0.76 TB/s; one token of 128 experts 3.0 us, a launch.  A token for half
+// a warp would halve the rounds' cost but double the sort's and leaves the
+// scores' as it is.
 #include <cmath>
 
 #include "common.cuh"
@@ -173,9 +174,9 @@ __device__ __forceinline__ RawLogits<EPL, BF16> load_logits(const RsArgs& a, int
   return r;
 }
 
-// Blocks on an SM (64 registers a thread); a long batch's warps take several
-// tokens each.
-constexpr int kRsBlocks = 8;
+// Blocks on an SM (48 registers a thread); a long batch's warps take several
+// tokens each (65519 tokens of 256 experts: 50.4 us with 8 blocks, 49.5 with 10).
+constexpr int kRsBlocks = 10;
 
 template <int EPL, bool BF16, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRsWarps * 32, kRsBlocks) route_scores_kernel(RsArgs a) {
