@@ -122,8 +122,9 @@ typedef struct {
   int64_t out_stride;
 } moe_paged_attention_config_t;
 
-/* Workspace bytes of moe_paged_attention for this configuration (max_q_len = 0
- * needs the most); 0 for an invalid one. */
+/* Workspace bytes of moe_paged_attention; 0 for an invalid configuration.  They
+ * never shrink when T, batch or max_q_len grow (0 counts as T), so a workspace
+ * for the largest call serves the smaller ones too. */
 size_t moe_paged_attention_ws_bytes(const moe_paged_attention_config_t* cfg, const moe_kv_cache_t* cache);
 
 /*

@@ -150,6 +150,18 @@ def test_attention_refuses_pointers_and_workspaces(lib):
     assert attend(lib, cfg=attention_cfg(T=0), q=None, out=None, ws=None, n=0) == 0
 
 
+def test_attention_workspace_of_the_largest_call_serves_all(lib):
+    def need(T, batch, hint):
+        return lib.moe_paged_attention_ws_bytes(attention_cfg(T=T, batch=batch, max_q_len=hint), cache(n_kv_heads=2))
+
+    for batch in (1, 3, 200):
+        sizes = [need(T, batch, 0) for T in (1, 7, 64, 300, 1024, 5000, 40000)]
+        assert sizes[0] > 0 and sizes == sorted(sizes)
+        for T in (7, 300, 40000):
+            by_hint = [need(T, batch, h) for h in sorted((1, 6, 7, 100, T // 3, T)) + [0]]
+            assert by_hint == sorted(by_hint)
+
+
 def test_binding_checks_tensors():
     codes = torch.zeros(3, 2, 16, 64, dtype=torch.uint8)
     sc, table = torch.ones(3, 2), torch.zeros(1, 2, dtype=torch.int32)

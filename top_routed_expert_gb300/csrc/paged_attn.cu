@@ -861,7 +861,8 @@ cudaError_t launch_paged_attn(PaArgs a, int max_q_len, int num_sms, cudaStream_t
 namespace {
 
 // Workspace: partial sums and the row tiles to join, then what the tcgen05
-// kernel needs where a call can take it.
+// kernel needs where a call can take it (cut blocks or not, alone or not, so
+// that a smaller call never needs more).
 struct Workspace {
   size_t joins, tc, tc_entries, tc_joins, tc_part, total;
 };
@@ -872,12 +873,12 @@ Workspace plan_workspace(const PaArgs& a, int max_q_len) {
   Workspace w;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t from = at; at += align_up(bytes, 256); return from; };
-  take(path.alone ? 0 : paged_attn_part_bytes(D));
+  take(paged_attn_part_bytes(D));
   w.joins = take(kMaxCtas * sizeof(JoinTile));
   w.tc = take(sizeof(TcList));
   w.tc_entries = take(path.tc ? (tc_places(a) + kTcSlots) * sizeof(TcEntry) : 0);
-  w.tc_joins = take(path.split ? kTcSlots * sizeof(TcJoin) : 0);
-  w.tc_part = take(path.split ? static_cast<size_t>(kTcSlots) * kTcItemRows * (D + 2) * sizeof(float) : 0);
+  w.tc_joins = take(path.tc ? kTcSlots * sizeof(TcJoin) : 0);
+  w.tc_part = take(path.tc ? static_cast<size_t>(kTcSlots) * kTcItemRows * (D + 2) * sizeof(float) : 0);
   w.total = at;
   return w;
 }
