@@ -365,9 +365,11 @@ def test_attention_same_bits_every_time():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-# Enough rows for the tensor-memory kernel, and contexts long enough that it cuts
+# Enough rows, and a page table wide enough, for the tensor-memory kernel, and
+# contexts long enough that it cuts
 # row blocks along the cached tokens; the third and the last mix both kernels, the
 # fourth and fifth have equal prompts.
+WIDE = dict(extra_width=1024)
 MANY = [
     ([64, 130], [900, 130], dict(Hq=16, Hkv=2)),
     ([300], [1500], dict(Hq=7, Hkv=1, D=64, page=64)),
@@ -381,19 +383,19 @@ MANY = [
 @pytest.mark.parametrize("new,total,kw", MANY)
 @pytest.mark.parametrize("hint", [False, True])
 def test_attention_many_rows(new, total, kw, hint):
-    bt = Batch(new, total, seed=sum(total), **kw)
+    bt = Batch(new, total, seed=sum(total), **WIDE, **kw)
     check_attention(bt, max_q_len=max(new) if hint else 0)
 
 
 @pytest.mark.parametrize("window,n_sink", [(1, 0), (1, 1), (130, 4), (800, 0), (900, 300), (10 ** 6, 3)])
 @pytest.mark.parametrize("new,total,kw", MANY[:3])
 def test_attention_many_rows_window(new, total, kw, window, n_sink):
-    bt = Batch(new, total, seed=window + n_sink, **kw)
+    bt = Batch(new, total, seed=window + n_sink, **WIDE, **kw)
     check_attention(bt, window, n_sink, max_q_len=max(new))
 
 
 def test_attention_many_rows_evicted_pages():
-    bt = Batch([100, 64, 150], [1900, 300, 1260], Hq=8, Hkv=1, seed=21)
+    bt = Batch([100, 64, 150], [1900, 300, 1260], Hq=8, Hkv=1, seed=21, **WIDE)
     window, n_sink = 900, 4
     ref = do.paged_attention(bt.oracle_cache(), values64(bt.q), bt.cu, bt.kv_len, bt.D ** -0.5, window, n_sink)
     for b in range(bt.B):
@@ -410,7 +412,7 @@ def test_attention_many_rows_evicted_pages():
 
 
 def test_attention_many_rows_that_see_nothing():
-    bt = Batch([50, 100, 60, 300], [50, 100, 60, 1300], Hq=8, Hkv=1, seed=22)
+    bt = Batch([50, 100, 60, 300], [50, 100, 60, 1300], Hq=8, Hkv=1, seed=22, **WIDE)
     bt.kv_len[:] = [20, 0, -7, 1100]
     for hint in (0, 300):
         out, lse = check_attention(bt, max_q_len=hint)
@@ -418,7 +420,7 @@ def test_attention_many_rows_that_see_nothing():
 
 
 def test_attention_many_rows_nan_query_stays_in_its_row():
-    bt = Batch([260], [1150], Hq=8, Hkv=2, seed=23)
+    bt = Batch([260], [1150], Hq=8, Hkv=2, seed=23, **WIDE)
     clean_o, clean_l, _ = run_attention(bt)
     bt.q[1, 3, 5], bt.q[0, 6, 0], bt.q[259, 0, 127] = math.nan, math.inf, -math.inf
     out, lse, _ = run_attention(bt)
@@ -430,7 +432,7 @@ def test_attention_many_rows_nan_query_stays_in_its_row():
 
 
 def test_attention_many_rows_extreme_scales_and_scores():
-    bt = Batch([256], [1140], Hq=8, Hkv=2, seed=24)
+    bt = Batch([256], [1140], Hq=8, Hkv=2, seed=24, **WIDE)
     n = bt.scales["v"].shape[0]
     bt.scales["v"] = 2.0 ** np.linspace(-40, 0, n * 2).round().reshape(n, 2)
     check_attention(bt)
@@ -441,8 +443,8 @@ def test_attention_many_rows_extreme_scales_and_scores():
 
 
 def test_attention_many_rows_page_out_of_the_cache():
-    bt = Batch([100, 160], [1000, 900], Hq=8, Hkv=2, seed=25)
-    full = Batch([100, 160], [1000, 900], Hq=8, Hkv=2, seed=25)
+    bt = Batch([100, 160], [1000, 900], Hq=8, Hkv=2, seed=25, **WIDE)
+    full = Batch([100, 160], [1000, 900], Hq=8, Hkv=2, seed=25, **WIDE)
     bt.table[0, 2] = bt.n_pages
     out, lse, st = run_attention(bt)
     assert st == 6
@@ -452,7 +454,7 @@ def test_attention_many_rows_page_out_of_the_cache():
 
 def test_attention_offsets_that_name_rows_again():
     """Offsets out of order are reported; requests that overlap make no more work than the rows have."""
-    bt = Batch([300], [1100], Hq=8, Hkv=1, seed=27)
+    bt = Batch([300], [1100], Hq=8, Hkv=1, seed=27, **WIDE)
     ref, _, _ = run_attention(bt)
     bt.B = 101
     bt.cu = np.array([0, 300] * 51, dtype=np.int32)
@@ -466,7 +468,7 @@ def test_attention_offsets_that_name_rows_again():
 
 
 def test_attention_many_rows_same_bits_strided_other_stream():
-    bt = Batch([1, 256, 3, 90], [1700, 1333, 260, 900], Hq=8, Hkv=2, seed=26)
+    bt = Batch([1, 256, 3, 90], [1700, 1333, 260, 900], Hq=8, Hkv=2, seed=26, **WIDE)
     ref, ref_l, st = run_attention(bt, max_q_len=256)
     assert st == 0
     for _ in range(3):
