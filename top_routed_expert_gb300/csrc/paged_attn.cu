@@ -819,24 +819,26 @@ struct Path {
 
 // The few-row kernel reads a request's tokens once for every 16 rows, the tcgen05
 // kernel once for 256, but takes longer to start and to join: with heads of 128
-// about 13 us + 3.1 us for a million (row, token) pairs against 29 us + 0.6 us.
+// about 13 us + 3.1 us for a million pairs of a row and a token (a row tile's
+// start counting as kTileCost units of tokens) against 29 us + 0.6 us.
 // Measured (us, few-row / tcgen05): one request of 1024 rows (of all key heads)
 // at 3584 tokens 25 / 33, at 8192 40 / 37, at 16384 65 / 44, at 65536 221 / 67; of
 // 512 rows at 8192 27 / 34, at 65536 118 / 63; of 256 rows at 65536 66 / 63; 2048 rows
 // of 1 / 8 requests at 3584 37 / 34 and 31 / 37; 64 requests of 32 rows each (8192)
-// at 1792 to 3584 94 / 115, of 64 rows 167 / 113.  The host does not know the
-// lengths: the page table's width stands for them, up to kTcTokens, since a wide
-// table may be a short one's.
+// at 1792 to 3584 94 / 115, of 64 rows 167 / 113; 125 prompts of up to 26 tokens, 8
+// x 7 heads, at 40 to 49 tokens 112 / 69.  The host does not know the lengths:
+// the page table's width stands for them, up to kTcTokens, since a wide table may
+// be a short one's.
 constexpr int kTcRows = 48;                  // of a request and key head
 constexpr int kTcTokens = 16384;
-constexpr int64_t kTcWork = int64_t(6) << 20;   // (row, token) pairs
+constexpr int64_t kTcWork = int64_t(6) << 20;   // pairs
 
 Path path_of(const PaArgs& a, int max_q_len) {
   const int64_t most = static_cast<int64_t>(max_q_len > 0 ? std::min(max_q_len, a.T) : a.T) * a.group;
   Path p;
   const int64_t rows = static_cast<int64_t>(a.T) * a.group * a.c.n_kv_heads;
   const int64_t tokens = std::min<int64_t>(static_cast<int64_t>(a.c.max_pages) * a.c.page_size, kTcTokens);
-  p.tc = most > kTcRows && rows * tokens >= kTcWork && paged_attn_tc_supported(a.c.head_dim);
+  p.tc = most > kTcRows && rows * (tokens + kTileCost * kUnit) >= kTcWork && paged_attn_tc_supported(a.c.head_dim);
   // As many rows as if every request had max_q_len of them: they all do (or the
   // hint is wrong, and the tcgen05 kernel takes small ones too).
   p.alone = p.tc && static_cast<int64_t>(max_q_len) * a.B == a.T;
