@@ -22,7 +22,7 @@
 // scale s / sum of the chosen s.
 //
 // Measured: 65519 tokens of 256 experts (8 groups, bias, sigmoid, bf16, k = 8)
-// 49.5 us, about 670 warp instructions a token at three quarters of the issue
+// 49.5 us, 675 warp instructions a token at three quarters of the issue
 // slots, 0.76 TB/s; one token of 128 experts 3.0 us, a launch.  A token for half
 // a warp would halve the rounds' cost but double the sort's and leaves the
 // scores' as it is.
