@@ -1,0 +1,60 @@
+"""Host-side checks of the decoder layer (no GPU needed): the library's calls
+are replaced by the fp64 oracles, so what the layer passes to them shows."""
+import numpy as np
+import pytest
+import torch
+
+import moe_synth
+import oracle
+from oracle import decode_oracle as do
+from top_routed_expert_gb300 import abi
+from top_routed_expert_gb300.decoder import DecoderLayer, PagedKVCache
+from top_routed_expert_gb300.layer import MoELayer
+
+D, HQ, HKV, DM, E, K = 64, 4, 2, 128, 32, 4
+
+
+def make(skew=False, **kw):
+    inp = moe_synth.make_custom(T=8, d=DM, E=E, k=K, f=64, fs=64, x_dtype="bf16", w_dtype="e4m3", seed=1, skew=skew)
+    cache = PagedKVCache(12, 16, HKV, D, 2, 5, device="cpu")
+    g = torch.Generator().manual_seed(2)
+    w_qkv = (torch.randn((HQ + 2 * HKV) * D, DM, generator=g) / DM ** 0.5).to(torch.bfloat16)
+    w_o = (torch.randn(DM, HQ * D, generator=g) / (HQ * D) ** 0.5).to(torch.bfloat16)
+    one = torch.ones(DM)
+    layer = DecoderLayer(MoELayer(inp, device="cpu"), cache, w_qkv, w_o, one, one, torch.zeros(80, D // 2, 2), HQ, **kw)
+    return layer, inp
+
+
+@pytest.fixture
+def scores_by_oracle(monkeypatch):
+    def call(cfg, logits, bias, ids, w, stream=None):
+        a, b, _ = do.route_scores(logits.double().numpy(), None if bias is None else bias.numpy(), cfg.top_k, cfg.n_groups,
+                                  cfg.top_groups, cfg.group_rank, "sigmoid" if cfg.score else "softmax",
+                                  bool(cfg.renormalise), cfg.scale)
+        ids.copy_(torch.from_numpy(a)), w.copy_(torch.from_numpy(b))
+    monkeypatch.setattr(abi, "moe_route_scores", call)
+
+
+def test_choice_of_a_biased_router_is_the_moe_layers(scores_by_oracle):
+    """A MoELayer's bias belongs to its logits: it moves the choice and the gates."""
+    layer, inp = make(skew=True)
+    assert inp.bias is not None
+    h = torch.randn(50, DM, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    ids, w = layer.choose(h)
+    L, want, gates = oracle.route(h.double().numpy(), inp.w_router, inp.bias, K)
+    clear = ~np.logical_or(*oracle.near_ties(L, K))   # fp32 logits are about 1e-6 off
+    assert clear.sum() > 40 and np.array_equal(ids.numpy()[clear], want[clear])
+    assert np.max(np.abs(w.double().numpy() - gates)[clear]) <= 1e-4
+
+
+def test_choice_bias_moves_the_choice_alone(scores_by_oracle):
+    b = torch.linspace(-0.3, 0.3, E)
+    layer, inp = make(skew=True, choice_bias=b, route=dict(score=abi.MOE_SCORE_SIGMOID, n_groups=4, top_groups=2))
+    h = torch.randn(50, DM, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    ids, w = layer.choose(h)
+    L = h.double().numpy() @ inp.w_router.astype(np.float64).T + inp.bias
+    want, gates, c = do.route_scores(L, b.numpy(), K, 4, 2, 1, "sigmoid")
+    sorted_c = np.sort(c, axis=1)
+    clear = np.min(np.diff(sorted_c, axis=1), axis=1) > 1e-5   # groups are ranked by the same values
+    assert clear.sum() > 30 and np.array_equal(ids.numpy()[clear], want[clear])
+    assert np.max(np.abs(w.double().numpy() - gates)[clear]) <= 1e-4

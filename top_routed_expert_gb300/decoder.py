@@ -78,19 +78,21 @@ class DecoderLayer:
     w_qkv [(Hq + 2 Hkv) D, d], w_o [d, Hq D] bf16; norm_attn, norm_moe [d];
     gamma_q, gamma_k [D] float32 or None (no QK norm); cos_sin
     [n_pos, rot/2, 2] float32; moe: a MoELayer over bf16 x (its router weights
-    give the logits, its bias moves the choice); route: further keyword
+    and its bias give the logits, as in MoELayer.forward); choice_bias [E]
+    float32 or None: added to the scores for the choice alone, the weights stay
+    those of the scores (the bias of moe_route_scores); route: further keyword
     arguments of abi.make_route_scores_config.
     """
 
     def __init__(self, moe: MoELayer, cache: PagedKVCache, w_qkv, w_o, norm_attn, norm_moe, cos_sin, n_q_heads: int,
                  gamma_q=None, gamma_k=None, rope_layout=abi.MOE_ROPE_HALF, window=0, n_sink=0, eps=1e-6,
-                 route: Optional[dict] = None):
+                 route: Optional[dict] = None, choice_bias: Optional[torch.Tensor] = None):
         self.moe, self.cache, self.w_qkv, self.w_o = moe, cache, w_qkv, w_o
         self.norm_attn, self.norm_moe, self.cos_sin = norm_attn, norm_moe, cos_sin
         self.gamma_q, self.gamma_k = gamma_q, gamma_k
         self.Hq, self.Hkv, self.D = n_q_heads, cache.k.shape[1], cache.k.shape[3]
         self.rope_layout, self.window, self.n_sink, self.eps = rope_layout, window, n_sink, eps
-        self.route = dict(route or {})
+        self.route, self.choice_bias = dict(route or {}), choice_bias
         self._ws = None
 
     def attention(self, h: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor, max_q_len: int) -> torch.Tensor:
@@ -115,10 +117,12 @@ class DecoderLayer:
     def choose(self, h: torch.Tensor):
         """(ids, weights) [T, k] of the experts for the states h [T, d]."""
         logits = h.float() @ self.moe.w_router.T
+        if self.moe.bias is not None:
+            logits += self.moe.bias
         T, k = h.shape[0], self.moe.k
         ids = torch.empty((T, k), dtype=torch.int32, device=h.device)
         w = torch.empty((T, k), dtype=torch.float32, device=h.device)
-        abi.moe_route_scores(abi.make_route_scores_config(T, self.moe.E, k, **self.route), logits, self.moe.bias, ids, w)
+        abi.moe_route_scores(abi.make_route_scores_config(T, self.moe.E, k, **self.route), logits, self.choice_bias, ids, w)
         return ids, w
 
     def forward(self, x: torch.Tensor, new: List[int]) -> torch.Tensor:
