@@ -29,7 +29,7 @@ typedef struct {
   void* k;                   /* E4M3 codes of the keys, page 0                    */
   void* v;                   /* E4M3 codes of the values, same strides            */
   float* k_scale;            /* [n_pages][n_kv_heads], 2^-100 to 2^100            */
-  float* v_scale;            /* [n_pages][n_kv_heads], likewise, and those of     */
+  float* v_scale;            /* [n_pages][n_kv_heads], 2^-80 to 2^80, those of    */
                              /*   one request and head within 2^80 of each other  */
   const int32_t* page_table; /* [batch][max_pages]                                */
   int32_t n_pages;           /* pages in the cache, >= 1                          */
@@ -145,11 +145,14 @@ size_t moe_paged_attention_ws_bytes(const moe_paged_attention_config_t* cfg, con
  * The products take the codes exactly (E4M3 fits f16) and q scaled by a power
  * of two per head to f16, which is exact but for elements 2^-28 below the
  * head's largest; scores, maxima, sums and outputs are accumulated in fp32;
- * the weights exp(z_j - max) are rounded to f16 (11 bits) for the product
- * with V.  Results do not depend on scheduling: the same call gives the same
- * bits.  A NaN or infinite q makes its own head's row NaN.  A NaN code in a
- * position that a request's new tokens can see makes NaN of the rows that see
- * it and may make NaN of other rows of the same request and key head.
+ * the weights w_j, the softmax times the page's value scale, are rounded to f16
+ * for the product with V: to 11 bits down to 2^-22 of the row's largest, smaller
+ * ones by up to 2^-33 of it, which can move an output by up to
+ * 448 (tokens) 2^-33 max_j w_j.  Results do not depend on scheduling: the same
+ * call gives the same bits.  A NaN or infinite q makes its own head's row NaN.
+ * A NaN code in a position that a request's new tokens can see makes NaN of the
+ * rows that see it and may make NaN of other rows of the same request and key
+ * head.
  * A page outside the cache or a position past the page table records
  * MOE_ERR_DEVICE_BOUNDS and is treated as not visible; a request whose
  * offsets decrease or leave [0, T] records it too and its rows stay

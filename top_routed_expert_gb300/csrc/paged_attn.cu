@@ -30,15 +30,16 @@
 // Sums and references are kept per warp and joined at the end.  Page scales: a
 // key's scale multiplies its score; a value's scale goes into the exponent of
 // its weight, and the weights' sum takes it out again.  A row's weights are
-// relative to the maximum of the first tile that it sees something in; that
-// reference moves only when weights grow over 2^15 (f16 holds 65504), so the
+// relative to 2^-8 of the maximum of the first tile that it sees something in
+// (kRefBelow); that reference moves only when weights outgrow f16 (65504), so the
 // ordinary tile takes no maximum and rescales nothing.
 //
 // What each row computes, with p its position and w the window:
 //   z_j = sm_scale q . (k_scale_j k_j),  j <= p and (j > p - w or j < n_sink)
 //   out = sum 2^(z_j log2 e - m) v_scale_j v_j / sum 2^(z_j log2 e - m)
-// The weights are rounded to f16 (2^-11, under the output's bf16 rounding, 2^-9);
-// scores, sums, references and outputs are fp32.
+// The weights are rounded to f16 for the second product (2^-11, under the
+// output's bf16 rounding, 2^-9; weights under 2^-22 of the largest by up to 2^-33 of
+// it); scores, sums, references and outputs are fp32.
 //
 // Measured (key heads x query heads of a group x D): 12 requests at 49157 to 65536
 // tokens, 4 x 8 x 128, 705 MB in 115.5 us = 6.1 TB/s, bound by memory; 64 at 17
@@ -65,7 +66,6 @@ constexpr int kUnit = 64;        // tokens of a unit
 // warps), in units.
 constexpr int kTileCost = 4;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMostSum = 32768.0f;   // sum of a lane's two weights that moves the reference: f16 holds 65504
 
 // D: elements of a head, NB: blocks of eight rows in a row tile.
 template <int D, int NB> struct Shape {
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB>::kCtas) paged_attn_k
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
               if (of_row) {
-                const float to = fmaxf(m[n][h], top), f = m[n][h] == -INFINITY ? 0.f : ex2(m[n][h] - to);
+                const float to = fmaxf(m[n][h], top - kRefBelow), f = m[n][h] == -INFINITY ? 0.f : ex2(m[n][h] - to);
                 m[n][h] = to;
                 l[n][h] *= f;
 #pragma unroll

@@ -158,6 +158,17 @@ __device__ __forceinline__ int64_t piece_of(int64_t total, int ctas) {
 // 2^(m - top) for the join of partial maxima; m = -infinity: an empty part.
 __device__ __forceinline__ float ex2_from(float m, float top) { return m == -INFINITY ? 0.f : exp2f(m - top); }
 
+// A row's reference lies kRefBelow (base 2) under the maximum that it is taken
+// from.  Weights are f16, 11 bits from 2^-14 on and steps of 2^-24 below, so one
+// keeps its 11 bits down to 2^-22 of the row's largest and is off by up to 2^-33 of
+// it below that; with the maximum itself as reference these would be 2^-14 and
+// 2^-25, and the losses of 65536 tokens 2^-9.  A reference moves when weights (16 of
+// a group, or a lane's two) sum to over kMostSum, so that none is over f16's 65504.
+// A move costs a step most of its time again, which is why it is 8: 32 x 256
+// tokens take 264 us with 0, 266 with 8, 273 with 9, 297 with 10; ragged prompts
+// 174, 179, 188, 196.
+constexpr float kRefBelow = 8.0f, kMostSum = 65504.0f;
+
 // A key scale times a row's factor, kept above 0: a masked score is -infinity
 // and has to stay so (a product that small leaves no score to speak of).
 __device__ __forceinline__ float score_factor(float k_scale, float rf) { return fmaxf(k_scale * rf, 1e-37f); }

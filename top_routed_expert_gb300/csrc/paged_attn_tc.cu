@@ -24,11 +24,11 @@
 // exponent (its logarithm), so that P V needs no scaling and the sum of the
 // weights is the group sums divided by the same scale.
 //
-// A row's weights are taken relative to the maximum of the first step that it
-// sees something in, and that reference moves only when a group of 16 weights
-// sums to over 2^15: until then they fit f16 (65504), and the quotient is the
-// same.  So the scores are read once, no maximum is taken in the ordinary step,
-// and the accumulator is almost never rescaled.
+// A row's weights are taken relative to 2^-8 of the maximum of the first step that
+// it sees something in (kRefBelow), and that reference moves only when a group of
+// 16 weights sums to over 65504: until then they fit f16, and the quotient is the
+// same.  So the scores are read once, no maximum is taken in the ordinary
+// step, and the accumulator is almost never rescaled.
 //
 // Few items would leave SMs idle, so long ones are cut along the tokens
 // (paged_attn.cu) and paged_attn_tc_join adds the parts up in order.
@@ -66,7 +66,6 @@ constexpr int kConvThreads = 128;
 constexpr int kSlots = 8;              // steps that are planned ahead, at most
 constexpr int kItems = 16;             // items that are announced ahead; more than kSlots, as an item has a step or more
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMostSum = 32768.0f;     // sum of 16 weights that moves the maximum: none is over f16's 65504
 constexpr long long kWaitCycles = 3000000000ll;
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -459,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
                 top = fmaxf(top, fmaf(u, score_factor(s.x, rf), s.y));
               }
             }
-            const float to = move ? fmaxf(m, top) : m, f = m == -INFINITY ? 0.f : ex2(m - to);
+            const float to = move ? fmaxf(m, top - kRefBelow) : m, f = m == -INFINITY ? 0.f : ex2(m - to);
             m = to;
             l *= f;
             if (j > 0) {
