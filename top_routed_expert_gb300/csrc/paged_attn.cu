@@ -346,11 +346,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB>::kCtas) paged_attn_k
     const int64_t v_minus_k = static_cast<const uint8_t*>(a.c.v) - static_cast<const uint8_t*>(a.c.k);
     const int32_t* table = a.c.page_table + static_cast<int64_t>(b) * a.c.max_pages;
     auto tile_base = [&](int u) { return sp.block_of(u) * kUnit + warp * 16; };
-    // Page ids are asked for a tile ahead of the copies and looked at there.
+    // Page ids are asked for a tile ahead of the copies and looked at there (any
+    // negative id as -1: the table may hold kNothing's value).
     constexpr int kNothing = INT_MIN;
     auto page_id = [&](int u) -> int {
       const int j = tile_base(u);
-      return u < u1 && sp.any_seen(j, j + 15) ? __ldg(table + (j >> ps_log)) : kNothing;
+      return u < u1 && sp.any_seen(j, j + 15) ? max(__ldg(table + (j >> ps_log)), -1) : kNothing;
     };
     auto issue = [&](int u, int pid, int stage) {
       if (pid == kNothing) return;

@@ -705,7 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(PaArgs a) {
           const int j = jb + (lane >> 3), s = g + j, slot = s % kSlots;
           const bool mine = j < it.steps;
           const int x = mine ? sp.block_of(it.u0 + j) * kTok + grp * 16 : 0;
-          const int gp = mine && sp.any_seen(x, x + 15) ? __ldg(table + (x >> ps_log)) : kNotSeen;
+          // any negative id as -1: the table may hold kNotSeen's value
+          const int gp = mine && sp.any_seen(x, x + 15) ? max(__ldg(table + (x >> ps_log)), -1) : kNotSeen;
           const bool have = static_cast<unsigned>(gp) < static_cast<unsigned>(a.c.n_pages);
           if (!have && gp != kNotSeen) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
           float ks = 0.f, vs = 1.f;
