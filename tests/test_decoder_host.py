@@ -1,5 +1,7 @@
 """Host-side checks of the decoder layer (no GPU needed): the library's calls
 are replaced by the fp64 oracles, so what the layer passes to them shows."""
+import inspect
+
 import numpy as np
 import pytest
 import torch
@@ -58,3 +60,36 @@ def test_choice_bias_moves_the_choice_alone(scores_by_oracle):
     clear = np.min(np.diff(sorted_c, axis=1), axis=1) > 1e-5   # groups are ranked by the same values
     assert clear.sum() > 30 and np.array_equal(ids.numpy()[clear], want[clear])
     assert np.max(np.abs(w.double().numpy() - gates)[clear]) <= 1e-4
+
+
+@pytest.mark.parametrize("stream", [None, "side"])
+def test_routed_experts_allocate_on_the_stream_that_they_use(monkeypatch, stream):
+    """What forward_routed drops at its end must belong to the stream whose kernels still use it."""
+    current, seen = [None], []
+
+    class use:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            current.append(self.s)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    empty = torch.empty
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: seen.append(("alloc", current[-1])) or empty(*a, **kw))
+    monkeypatch.setattr(abi, "moe_workspace_bytes", lambda cfg: 64)
+    for name in ("moe_permute", "moe_expert_ffn", "moe_combine"):
+        takes = len(inspect.signature(getattr(abi, name)).parameters)   # the last is the stream
+
+        def call(*a, name=name, takes=takes, stream=None):
+            seen.append((name, a[takes - 1] if len(a) == takes else stream or current[-1]))
+        monkeypatch.setattr(abi, name, call)
+    layer, _ = make()
+    seen.clear()
+    ids, w = torch.zeros(8, K, dtype=torch.int32), torch.zeros(8, K)
+    layer.moe.forward_routed(torch.zeros(8, DM, dtype=torch.bfloat16), ids, w, stream=stream)
+    assert {what for what, _ in seen} == {"alloc", "moe_permute", "moe_expert_ffn", "moe_combine"}
+    assert {s for _, s in seen} == {stream}

@@ -86,7 +86,11 @@ class MoELayer:
     def forward_routed(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
                        y: Optional[torch.Tensor] = None, stream=None):
         """The experts, routed and shared, on a choice made elsewhere (moe_route_scores): permutation, expert FFN and
-        combine.  topk_ids [T, k] int32, topk_w [T, k] float32."""
+        combine.  topk_ids [T, k] int32, topk_w [T, k] float32.  With `stream` it is as if the call were made under
+        torch.cuda.stream(stream): what it allocates, y among it, belongs to that stream."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward_routed(x, topk_ids, topk_w, y)
         T = x.shape[0]
         cfg = self.config(T)
         ws = self.workspace(T)
@@ -98,9 +102,9 @@ class MoELayer:
         ints = torch.empty(self.E + 1 + 2 * n, dtype=torch.int32, device=self.device)
         offsets, sorted_pair, row_of = ints.split([self.E + 1, n, n])
         outs = torch.empty((n + T, self.d), dtype=dt, device=self.device)
-        abi.moe_permute(cfg, topk_ids, offsets, sorted_pair, row_of, ws, stream)
-        abi.moe_expert_ffn(cfg, x, topk_w, offsets, sorted_pair, self.weights, outs[:n], outs[n:], ws, stream)
-        abi.moe_combine(cfg, outs[:n], row_of, outs[n:], y, stream)
+        abi.moe_permute(cfg, topk_ids, offsets, sorted_pair, row_of, ws)
+        abi.moe_expert_ffn(cfg, x, topk_w, offsets, sorted_pair, self.weights, outs[:n], outs[n:], ws)
+        abi.moe_combine(cfg, outs[:n], row_of, outs[n:], y)
         return y
 
     def capture(self, x: torch.Tensor, y: Optional[torch.Tensor] = None, warmup: int = 2):
