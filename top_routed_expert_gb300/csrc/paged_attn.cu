@@ -346,15 +346,16 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB>::kCtas) paged_attn_k
     const int64_t v_minus_k = static_cast<const uint8_t*>(a.c.v) - static_cast<const uint8_t*>(a.c.k);
     const int32_t* table = a.c.page_table + static_cast<int64_t>(b) * a.c.max_pages;
     auto tile_base = [&](int u) { return sp.block_of(u) * kUnit + warp * 16; };
-    // Page ids are asked for a tile ahead of the copies and looked at there (any
-    // negative id as -1: the table may hold kNothing's value).
+    // Page ids are asked for a tile ahead of the copies and looked at there.  A
+    // table may hold kNothing's value too: then the tile decides.
     constexpr int kNothing = INT_MIN;
-    auto page_id = [&](int u) -> int {
+    auto needed = [&](int u) {
       const int j = tile_base(u);
-      return u < u1 && sp.any_seen(j, j + 15) ? max(__ldg(table + (j >> ps_log)), -1) : kNothing;
+      return u < u1 && sp.any_seen(j, j + 15);
     };
+    auto page_id = [&](int u) -> int { return needed(u) ? __ldg(table + (tile_base(u) >> ps_log)) : kNothing; };
     auto issue = [&](int u, int pid, int stage) {
-      if (pid == kNothing) return;
+      if (pid == kNothing && !needed(u)) return;
       const int j0 = tile_base(u);
       float* sc = s_scale[warp][stage];
       const bool ok = static_cast<unsigned>(pid) < static_cast<unsigned>(a.c.n_pages);
