@@ -71,6 +71,7 @@ class moe_kv_cache_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table")]
     _fields_ += [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim", "max_pages")]
     _fields_ += [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")]
+    device = None   # of make_kv_cache's tensors
 
 
 class moe_kv_append_config_t(ctypes.Structure):
@@ -226,15 +227,20 @@ def _need(cond: bool, what: str):
         raise ValueError(what)
 
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+# The calling thread's current CUDA device, the one that the library launches
+# on, and the address of its current stream.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+# The calls below are a few microseconds long: what they look at is written out
+# in them.
+_ELSEWHERE = "every tensor has to be on the current CUDA device"
 
 
-def _raw_stream(t: torch.Tensor, stream):
-    """Address of the stream, or of the current stream of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _stream_of(stream, device: int) -> int:
+    """Address of a stream that was given."""
+    _need(stream.device_index == device, "the stream has to be one of the current CUDA device")
+    return stream.cuda_stream
 
 
 def make_route_scores_config(T, n_experts, top_k, n_groups=1, top_groups=1, group_rank=1, score=MOE_SCORE_SOFTMAX,
@@ -246,8 +252,14 @@ def make_route_scores_config(T, n_experts, top_k, n_groups=1, top_groups=1, grou
 
 def moe_route_scores(cfg, logits, bias, topk_ids, topk_w, stream=None):
     """Experts and weights from given logits (include/route_scores.h)."""
-    _check(load().moe_route_scores(cfg, logits.data_ptr(), _addr(bias), topk_ids.data_ptr(), topk_w.data_ptr(),
-                                   _raw_stream(logits, stream)), "moe_route_scores")
+    dev = _current_device()
+    if not (dev == logits.get_device() == topk_ids.get_device() == topk_w.get_device()
+            and (bias is None or bias.get_device() == dev)):
+        raise ValueError(_ELSEWHERE)
+    code = load().moe_route_scores(cfg, logits.data_ptr(), None if bias is None else bias.data_ptr(), topk_ids.data_ptr(),
+                                   topk_w.data_ptr(), _current_stream(dev) if stream is None else _stream_of(stream, dev))
+    if code:
+        raise MoEError(code, "moe_route_scores")
 
 
 def make_kv_cache(k, v, k_scale, v_scale, page_table) -> moe_kv_cache_t:
@@ -267,6 +279,8 @@ def make_kv_cache(k, v, k_scale, v_scale, page_table) -> moe_kv_cache_t:
     c = moe_kv_cache_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
                        n_pages, page, heads, D, page_table.shape[1], *strides)
     c.tensors = (k, v, k_scale, v_scale, page_table)
+    c.device = k.get_device()
+    _need(all(t.get_device() == c.device for t in c.tensors), "the cache's tensors: one device")
     return c
 
 
@@ -290,9 +304,21 @@ def make_kv_append_config(q, k, v, q_out, batch, rot_dim=0, n_pos=0, rope_layout
 
 def moe_kv_append(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream=None):
     """Norm, rotation and append to the paged cache (include/paged_kv.h)."""
-    _check(load().moe_kv_append(cfg, cache, _addr(q), k.data_ptr(), v.data_ptr(), _addr(gamma_q), _addr(gamma_k),
-                                _addr(cos_sin), _addr(positions), cu.data_ptr(), kv_len.data_ptr(), _addr(q_out),
-                                _raw_stream(k, stream)), "moe_kv_append")
+    dev = _current_device()
+    if not (dev == k.get_device() == v.get_device() == cu.get_device() == kv_len.get_device()
+            and (q is None or q.get_device() == q_out.get_device() == dev)
+            and (gamma_q is None or gamma_q.get_device() == dev) and (gamma_k is None or gamma_k.get_device() == dev)
+            and (cos_sin is None or cos_sin.get_device() == dev) and (positions is None or positions.get_device() == dev)
+            and (cache.device is None or cache.device == dev)):
+        raise ValueError(_ELSEWHERE)
+    code = load().moe_kv_append(
+        cfg, cache, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        None if gamma_q is None else gamma_q.data_ptr(), None if gamma_k is None else gamma_k.data_ptr(),
+        None if cos_sin is None else cos_sin.data_ptr(), None if positions is None else positions.data_ptr(),
+        cu.data_ptr(), kv_len.data_ptr(), None if q is None else q_out.data_ptr(),
+        _current_stream(dev) if stream is None else _stream_of(stream, dev))
+    if code:
+        raise MoEError(code, "moe_kv_append")
 
 
 def make_paged_attention_config(q, out, batch, max_q_len=0, window=0, n_sink=0,
@@ -310,9 +336,17 @@ def moe_paged_attention_ws_bytes(cfg, cache) -> int:
 
 def moe_paged_attention(cfg, cache, q, cu, kv_len, out, lse=None, ws=None, stream=None):
     """Attention of the new tokens over the paged cache (include/paged_kv.h)."""
-    _check(load().moe_paged_attention(cfg, cache, q.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(),
-                                      _addr(lse), _addr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                                      _raw_stream(q, stream)), "moe_paged_attention")
+    dev = _current_device()
+    if not (dev == q.get_device() == cu.get_device() == kv_len.get_device() == out.get_device()
+            and (lse is None or lse.get_device() == dev) and (ws is None or ws.get_device() == dev)
+            and (cache.device is None or cache.device == dev)):
+        raise ValueError(_ELSEWHERE)
+    code = load().moe_paged_attention(
+        cfg, cache, q.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
+        _current_stream(dev) if stream is None else _stream_of(stream, dev))
+    if code:
+        raise MoEError(code, "moe_paged_attention")
 
 
 def moe_launch_count() -> int:
