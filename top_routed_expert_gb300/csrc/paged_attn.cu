@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB>::kCtas) paged_attn_k
     const int32_t* table = a.c.page_table + static_cast<int64_t>(b) * a.c.max_pages;
     auto tile_base = [&](int u) { return sp.block_of(u) * kUnit + warp * 16; };
     // Page ids are asked for a tile ahead of the copies and looked at there.  A
-    // table may hold kNothing's value too: then the tile decides.
+    // table may hold kNothing's value too: then the tile tells which it is.
     constexpr int kNothing = INT_MIN;
     auto needed = [&](int u) {
       const int j = tile_base(u);
@@ -355,9 +355,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB>::kCtas) paged_attn_k
     };
     auto page_id = [&](int u) -> int { return needed(u) ? __ldg(table + (tile_base(u) >> ps_log)) : kNothing; };
     auto issue = [&](int u, int pid, int stage) {
-      if (pid == kNothing && !needed(u)) return;
-      const int j0 = tile_base(u);
       float* sc = s_scale[warp][stage];
+      if (pid == kNothing) {
+        if (lane == 0 && needed(u)) {
+          sc[2] = 0.f;
+          set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+        }
+        return;
+      }
+      const int j0 = tile_base(u);
       const bool ok = static_cast<unsigned>(pid) < static_cast<unsigned>(a.c.n_pages);
       if (lane == 0) sc[2] = ok ? 1.f : 0.f;
       if (!ok) {
