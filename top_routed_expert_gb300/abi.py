@@ -71,18 +71,23 @@ class moe_kv_cache_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table")]
     _fields_ += [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim", "max_pages")]
     _fields_ += [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")]
-    device = None   # of make_kv_cache's tensors
+    # of make_kv_cache's tensors: device, rows of the page table, (n_kv_heads, head_dim)
+    device, batch, heads = None, 1 << 30, None
 
 
 class moe_kv_append_config_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "batch", "n_q_heads", "rot_dim", "rope_layout", "n_pos")]
     _fields_ += [("eps", ctypes.c_float)]
     _fields_ += [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")]
+    # of make_kv_append_config's tensors: bytes of a row of q and of k, (n_kv_heads, head_dim)
+    q_row, k_row, heads = 0, 0, None
 
 
 class moe_paged_attention_config_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "batch", "n_q_heads", "max_q_len", "window", "n_sink")]
     _fields_ += [("sm_scale", ctypes.c_float), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+    # of make_paged_attention_config's tensors: bytes of a row of q, head_dim
+    q_row, head_dim = 0, None
 
 
 class moe_weights_t(ctypes.Structure):
@@ -232,8 +237,11 @@ def _need(cond: bool, what: str):
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
-# The calls below are a few microseconds long: what they look at is written out
-# in them.
+# The calls below are a few microseconds long and so is what they cost here: each
+# looks at types, sizes and devices alone, written out in it.  Rows' layouts are
+# looked at by the make_ functions, which leave what no field of the C structures
+# says beside those (a structure made by hand lacks that part of the checks).
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 _ELSEWHERE = "every tensor has to be on the current CUDA device"
 
 
@@ -241,6 +249,9 @@ def _stream_of(stream, device: int) -> int:
     """Address of a stream that was given."""
     _need(stream.device_index == device, "the stream has to be one of the current CUDA device")
     return stream.cuda_stream
+
+
+_RAGGED = "cu: int32 [batch + 1], kv_len: int32 [batch], batch: at most the rows of the page table"
 
 
 def make_route_scores_config(T, n_experts, top_k, n_groups=1, top_groups=1, group_rank=1, score=MOE_SCORE_SOFTMAX,
@@ -256,6 +267,16 @@ def moe_route_scores(cfg, logits, bias, topk_ids, topk_w, stream=None):
     if not (dev == logits.get_device() == topk_ids.get_device() == topk_w.get_device()
             and (bias is None or bias.get_device() == dev)):
         raise ValueError(_ELSEWHERE)
+    T, E = cfg.T, cfg.n_experts
+    if not (topk_ids.dtype is _I32 and topk_w.dtype is _F32 and topk_ids.numel() >= T * cfg.top_k <= topk_w.numel()
+            and logits.dtype is (_BF16 if cfg.logit_dtype == MOE_BF16 else _F32)
+            and (bias is None or bias.dtype is _F32 and bias.numel() >= E)):
+        raise ValueError("logits: of the configuration's type, bias: float32 [E], topk_ids: int32 [T, k], topk_w: "
+                         "float32 [T, k]")
+    if logits.numel() < (T - 1) * cfg.logit_stride + E:   # a view, or too short
+        _need(T < 1 or (logits.dim() == 2 and logits.shape[0] >= T and logits.shape[1] >= E
+                        and logits.stride(0) == cfg.logit_stride),
+              "logits: rows of E elements with the configuration's distance between them")
     code = load().moe_route_scores(cfg, logits.data_ptr(), None if bias is None else bias.data_ptr(), topk_ids.data_ptr(),
                                    topk_w.data_ptr(), _current_stream(dev) if stream is None else _stream_of(stream, dev))
     if code:
@@ -263,11 +284,13 @@ def moe_route_scores(cfg, logits, bias, topk_ids, topk_w, stream=None):
 
 
 def make_kv_cache(k, v, k_scale, v_scale, page_table) -> moe_kv_cache_t:
-    """A paged cache from its tensors: k, v [n_pages, n_kv_heads, page_size, D] of torch.float8_e4m3fn (or uint8
-    codes) in any stride order with contiguous D, the scales [n_pages, n_kv_heads] float32, page_table
+    """A paged cache from its tensors: k, v [n_pages, n_kv_heads, page_size, D] of torch.float8_e4m3fn (or their
+    bytes) in any stride order with contiguous D, the scales [n_pages, n_kv_heads] float32, page_table
     [batch, max_pages] int32.  The tensors stay alive with the returned object."""
     _need(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride(), "k and v: one 4-d shape, the same strides")
-    _need(k.element_size() == 1 and v.element_size() == 1 and k.stride(3) == 1, "k and v: 8-bit codes, contiguous heads")
+    codes = (torch.float8_e4m3fn, torch.uint8, torch.int8)
+    _need(k.dtype in codes and v.dtype in codes and k.stride(3) == 1,
+          "k and v: E4M3 codes (torch.float8_e4m3fn, or bytes), contiguous heads")
     n_pages, heads, page, D = k.shape
     for s in (k_scale, v_scale):
         _need(s.shape == (n_pages, heads) and s.dtype == torch.float32 and s.is_contiguous(),
@@ -279,7 +302,7 @@ def make_kv_cache(k, v, k_scale, v_scale, page_table) -> moe_kv_cache_t:
     c = moe_kv_cache_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
                        n_pages, page, heads, D, page_table.shape[1], *strides)
     c.tensors = (k, v, k_scale, v_scale, page_table)
-    c.device = k.get_device()
+    c.device, c.batch, c.heads = k.get_device(), page_table.shape[0], (heads, D)
     _need(all(t.get_device() == c.device for t in c.tensors), "the cache's tensors: one device")
     return c
 
@@ -297,9 +320,13 @@ def make_kv_append_config(q, k, v, q_out, batch, rot_dim=0, n_pos=0, rope_layout
     """Sizes and strides of an append from its tensors (q and q_out may be None)."""
     _need(k.shape == v.shape and (q is None or (q.shape[0] == k.shape[0] and q.shape == q_out.shape)),
           "q, k, v and q_out: the same rows")
-    return moe_kv_append_config_t(k.shape[0], batch, 0 if q is None else q.shape[1], rot_dim, rope_layout, n_pos, eps,
-                                  0 if q is None else _row_stride(q), _row_stride(k), _row_stride(v),
-                                  0 if q is None else _row_stride(q_out))
+    _need(q is None or q.shape[2] == k.shape[2], "q and k: one head size")
+    c = moe_kv_append_config_t(k.shape[0], batch, 0 if q is None else q.shape[1], rot_dim, rope_layout, n_pos, eps,
+                               0 if q is None else _row_stride(q), _row_stride(k), _row_stride(v),
+                               0 if q is None else _row_stride(q_out))
+    c.heads = heads, D = tuple(k.shape[1:])
+    c.q_row, c.k_row = 2 * c.n_q_heads * D, 2 * heads * D
+    return c
 
 
 def moe_kv_append(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream=None):
@@ -311,6 +338,18 @@ def moe_kv_append(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu,
             and (cos_sin is None or cos_sin.get_device() == dev) and (positions is None or positions.get_device() == dev)
             and (cache.device is None or cache.device == dev)):
         raise ValueError(_ELSEWHERE)
+    B = cfg.batch
+    if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
+        raise ValueError(_RAGGED)
+    T = cfg.T
+    if not (k.nbytes >= T * cfg.k_row <= v.nbytes and (cfg.heads == cache.heads or cfg.heads is None or cache.heads is None)
+            and (q is None or q.nbytes >= T * cfg.q_row <= q_out.nbytes)):
+        raise ValueError("q, k, v and q_out: rows of the configuration's shape and the cache's heads")
+    if not ((gamma_k is None or gamma_k.dtype is _F32 and gamma_k.numel() >= cache.head_dim)
+            and (gamma_q is None or gamma_q.dtype is _F32 and gamma_q.numel() >= cache.head_dim)
+            and (cos_sin is None or cos_sin.dtype is _F32 and cos_sin.numel() >= cfg.n_pos * cfg.rot_dim)
+            and (positions is None or positions.dtype is _I32 and positions.numel() >= T)):
+        raise ValueError("gamma_q, gamma_k: float32 [D], cos_sin: float32 [n_pos, rot_dim / 2, 2], positions: int32 [T]")
     code = load().moe_kv_append(
         cfg, cache, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
         None if gamma_q is None else gamma_q.data_ptr(), None if gamma_k is None else gamma_k.data_ptr(),
@@ -325,9 +364,10 @@ def make_paged_attention_config(q, out, batch, max_q_len=0, window=0, n_sink=0,
                                 sm_scale=None) -> moe_paged_attention_config_t:
     """Sizes and strides of an attention call from its tensors; sm_scale defaults to 1/sqrt(D)."""
     _need(q.shape == out.shape, "q and out: the same shape")
-    return moe_paged_attention_config_t(q.shape[0], batch, q.shape[1], max_q_len, window, n_sink,
-                                        q.shape[2] ** -0.5 if sm_scale is None else sm_scale, _row_stride(q),
-                                        _row_stride(out))
+    c = moe_paged_attention_config_t(q.shape[0], batch, q.shape[1], max_q_len, window, n_sink,
+                                     q.shape[2] ** -0.5 if sm_scale is None else sm_scale, _row_stride(q), _row_stride(out))
+    c.q_row, c.head_dim = 2 * q.shape[1] * q.shape[2], q.shape[2]
+    return c
 
 
 def moe_paged_attention_ws_bytes(cfg, cache) -> int:
@@ -341,6 +381,14 @@ def moe_paged_attention(cfg, cache, q, cu, kv_len, out, lse=None, ws=None, strea
             and (lse is None or lse.get_device() == dev) and (ws is None or ws.get_device() == dev)
             and (cache.device is None or cache.device == dev)):
         raise ValueError(_ELSEWHERE)
+    B = cfg.batch
+    if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
+        raise ValueError(_RAGGED)
+    T = cfg.T
+    if not (q.nbytes >= T * cfg.q_row <= out.nbytes and (cfg.head_dim is None or cfg.head_dim == cache.head_dim)
+            and (lse is None or lse.dtype is _F32 and lse.numel() >= T * cfg.n_q_heads)):
+        raise ValueError("q and out: rows of the configuration's shape and the cache's head size, lse: float32 "
+                         "[T, n_q_heads]")
     code = load().moe_paged_attention(
         cfg, cache, q.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
