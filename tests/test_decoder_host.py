@@ -93,3 +93,52 @@ def test_routed_experts_allocate_on_the_stream_that_they_use(monkeypatch, stream
     layer.moe.forward_routed(torch.zeros(8, DM, dtype=torch.bfloat16), ids, w, stream=stream)
     assert {what for what, _ in seen} == {"alloc", "moe_permute", "moe_expert_ffn", "moe_combine"}
     assert {s for _, s in seen} == {stream}
+
+
+def test_a_step_that_raises_can_be_made_again(monkeypatch):
+    """The cache's lengths stay those of the tokens that were computed, whichever part of the step fails."""
+    layer, _ = make()
+    steps, fail = [], []
+
+    def attention(h, cu, kv_len, max_q_len):
+        steps.append((cu.tolist(), kv_len.tolist(), max_q_len))
+        if fail == ["attention"]:
+            raise abi.MoEError(4, "moe_paged_attention")
+        return torch.zeros(h.shape[0], HQ, D, dtype=torch.bfloat16)
+
+    def choose(h):
+        if fail == ["choose"]:
+            raise MemoryError
+        return None, None
+    monkeypatch.setattr(layer, "attention", attention)
+    monkeypatch.setattr(layer, "choose", choose)
+    monkeypatch.setattr(layer.moe, "forward_routed", lambda h, ids, w: torch.zeros(h.shape[0], DM))
+    cache, x = layer.cache, torch.zeros(21, DM, dtype=torch.bfloat16)
+    layer.forward(x[:18], [17, 1])
+    assert cache.length == [17, 1]
+    for what, error in (("attention", abi.MoEError), ("choose", MemoryError)):
+        fail[:] = [what]
+        with pytest.raises(error):
+            layer.forward(x, [20, 1])
+        assert cache.length == [17, 1]
+        assert sorted(cache.free + cache.pages[0] + cache.pages[1]) == list(range(12))
+    fail[:] = []
+    layer.forward(x, [20, 1])
+    assert cache.length == [37, 2] and steps[-1] == steps[1] == ([0, 20, 21], [37, 2], 20)
+    assert [len(p) for p in cache.pages] == [3, 1]
+    assert cache.table[0, :3].tolist() == cache.pages[0] and cache.table[0, 3:].eq(-1).all()
+
+
+def test_room_that_cannot_be_made_changes_nothing():
+    layer, _ = make()
+    cache = layer.cache
+    cache.extend([30, 5])
+    before = cache.length[:], [p[:] for p in cache.pages], cache.free[:], cache.table.clone()
+    for new, error in (([60, 0], ValueError), ([-1, 0], ValueError), ([1], ValueError)):
+        with pytest.raises(error):
+            cache.extend(new)
+    cache.free, spare = [], cache.free
+    with pytest.raises(RuntimeError):
+        cache.extend([10, 0])
+    cache.free = spare
+    assert (cache.length, cache.pages, cache.free) == before[:3] and torch.equal(cache.table, before[3])

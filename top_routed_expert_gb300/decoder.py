@@ -47,16 +47,23 @@ class PagedKVCache:
             raise RuntimeError(f"{sum(need)} pages wanted, {len(self.free)} free")
         for b, n in enumerate(need):
             if n:
-                first = len(self.pages[b])
-                self.pages[b] += [self.free.pop() for _ in range(n)]
-                self.table[b, first:first + n] = torch.tensor(self.pages[b][first:], dtype=torch.int32)
-            self.length[b] += new[b]
+                first, got = len(self.pages[b]), self.free[:-n - 1:-1]
+                self.table[b, first:first + n] = torch.tensor(got, dtype=torch.int32)
+                self.pages[b] += got
+                del self.free[-n:]
         cu = [0]
         for n in new:
             cu.append(cu[-1] + n)
+        length = [have + n for have, n in zip(self.length, new)]
         dev = self.table.device
-        return (torch.tensor(cu, dtype=torch.int32, device=dev),
-                torch.tensor(self.length, dtype=torch.int32, device=dev))
+        arrays = (torch.tensor(cu, dtype=torch.int32, device=dev), torch.tensor(length, dtype=torch.int32, device=dev))
+        self.length[:] = length
+        return arrays
+
+    def retract(self, new: List[int]):
+        """Takes back the last extend(new), whose tokens were not computed.  The pages stay with their requests, which
+        will need them again."""
+        self.length[:] = [have - n for have, n in zip(self.length, new)]
 
     def release(self, b: int):
         """Gives request b's pages back."""
@@ -127,13 +134,18 @@ class DecoderLayer:
 
     def forward(self, x: torch.Tensor, new: List[int]) -> torch.Tensor:
         """x [T, d] bf16, the states of new[b] more tokens of each request one after the other; the layer's output for
-        them."""
+        them.  Pages are handed out on the host, so it runs eagerly; a call that raises leaves the cache's lengths as
+        they were, and can be made again."""
         if x.shape[0] != sum(new):
             raise ValueError("as many rows as new tokens")
         cu, kv_len = self.cache.extend(new)
         if x.shape[0] == 0:
             return x
-        a = self.attention(rms_norm(x, self.norm_attn, self.eps), cu, kv_len, max(new))
-        x = x + a.flatten(1) @ self.w_o.T
-        h = rms_norm(x, self.norm_moe, self.eps)
-        return (x.float() + self.moe.forward_routed(h, *self.choose(h)).float()).to(torch.bfloat16)
+        try:
+            a = self.attention(rms_norm(x, self.norm_attn, self.eps), cu, kv_len, max(new))
+            x = x + a.flatten(1) @ self.w_o.T
+            h = rms_norm(x, self.norm_moe, self.eps)
+            return (x.float() + self.moe.forward_routed(h, *self.choose(h)).float()).to(torch.bfloat16)
+        except BaseException:
+            self.cache.retract(new)
+            raise
