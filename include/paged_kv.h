@@ -94,9 +94,11 @@ typedef struct {
  * k, v, q, q_out, gamma, cos_sin and the cache's k and v are 16-byte aligned.
  * A table row outside [0, n_pos), a page outside the cache, a position past
  * the page table, offsets that decrease or leave [0, T], and kv_len[b] < n_b
- * record MOE_ERR_DEVICE_BOUNDS; the tokens concerned are not written (a
- * request whose offsets or length are wrong: none of its tokens; after
- * offsets that decrease, other requests' tokens may stay unwritten too).
+ * record MOE_ERR_DEVICE_BOUNDS; the tokens concerned are not written: by a bad
+ * page or position past the page table their keys and values (q_out is), by a
+ * bad table row that token's q_out as well, by wrong offsets or a wrong length
+ * nothing of the request (after offsets that decrease, other requests' tokens
+ * may stay unwritten too).
  * Rows of no request (before cu[0], from cu[batch] on) are left alone.
  * Requests of one call must not share a page that either writes.
  */
