@@ -16,8 +16,8 @@
 // their way: q is read and written once (bf16), k and v are read, their codes
 // written.  Measured: 32 x 256 tokens of 32 + 4 heads of 128, norm and rotation,
 // 164 MB in 32.4 us = 5.1 TB/s; ragged prompts up to 1999 tokens of 16 + 16 heads
-// of 64, 238 MB in 54 us = 4.4 TB/s; 64 single tokens 4.1 us, a launch and four
-// dependent loads.
+// of 64, 238 MB in 54 us = 4.4 TB/s; 64 single tokens 4.0 us in a graph, a launch and
+// four dependent loads.
 //
 // Which pages a ragged batch touches is known on the device only.  A request
 // of n new tokens touches at most n/page + 2 pages, so request b's blocks
@@ -465,7 +465,10 @@ template <int D> __host__ __device__ __forceinline__ int query_tokens(int Hq, in
 // Blocks on an SM that the registers are cut for: more of them hide more of the
 // look-ups' latency (before a block took several heads: prefill of 32 x 256
 // tokens, two rows a thread, 37.4 us with the compiler's choice of 5, 32.6 us
-// with 7; ragged prompts, four rows a thread, 67.6 and 58.7 us).
+// with 7; ragged prompts, four rows a thread, 67.6 and 58.7 us).  With four rows a
+// thread that costs spills: 96 to 104 bytes of 80 registers (their angles, 32 of
+// them, are held over all heads), 328 to 368 of 64 where D = 256 and pages of 128
+// tokens need 1024 threads.
 template <int PASSES, int THREADS> constexpr int blocks_on_sm() {
   return THREADS == 128 ? (PASSES < 4 ? 7 : 6) : THREADS == 256 ? 3 : 1;
 }

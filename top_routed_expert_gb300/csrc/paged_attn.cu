@@ -42,11 +42,14 @@
 // it); scores, sums, references and outputs are fp32.
 //
 // Measured (key heads x query heads of a group x D): 12 requests at 49157 to 65536
-// tokens, 4 x 8 x 128, 705 MB in 115.5 us = 6.1 TB/s, bound by memory; 64 at 17
-// to 3712, 123 MB in 33 us = 3.7 TB/s, of which the join and the two launches
+// tokens, 4 x 8 x 128, 705 MB in 114 us = 6.2 TB/s, bound by memory; 64 at 17
+// to 3712, 123 MB in 32.4 us = 3.8 TB/s, of which the join and the two launches
 // are 7; one at 3585 13 us, two launches and eight dependent loads; 48 drafts of
-// up to 4 tokens in a window of 1024, 8 x 4 x 64, 49 MB in 28.4 us, bound by the
-// issue of instructions (conversion and weights) and the row tiles' starts.
+// up to 4 tokens in a window of 1024, 8 x 4 x 64, 49 MB in 29 us, bound by the
+// issue of instructions (conversion and weights) and the row tiles' starts; 64 at
+// 3584, 4 x 8 x 256, 470 MB in 93 us = 5.0 TB/s.
+// Registers spilled (bytes stored, D / blocks of rows): 64/1 60, 64/2 48, 128/2 92,
+// 256/1 76, outside the loop over the units; 128/1 none.
 #include <climits>
 
 #include "paged_kv.cuh"
@@ -825,8 +828,8 @@ struct Path {
   bool split;   // ... which may cut row blocks along the cached tokens
 };
 
-// The few-row kernel reads a request's tokens once for every 16 rows, the tcgen05
-// kernel once for 256, but takes longer to start and to join: with heads of 128
+// The few-row kernel reads a request's tokens once for every 16 rows (8 where D =
+// 256), the tcgen05 kernel once for 256, but takes longer to start and to join: with heads of 128
 // about 13 us + 3.1 us for a million pairs of a row and a token (a row tile's
 // start counting as kTileCost units of tokens) against 29 us + 0.6 us.
 // Measured (us, few-row / tcgen05): one request of 1024 rows (of all key heads)
@@ -834,9 +837,32 @@ struct Path {
 // 512 rows at 8192 27 / 34, at 65536 118 / 63; of 256 rows at 65536 66 / 63; 2048 rows
 // of 1 / 8 requests at 3584 37 / 34 and 31 / 37; 64 requests of 32 rows each (8192)
 // at 1792 to 3584 94 / 115, of 64 rows 167 / 113; 125 prompts of up to 26 tokens, 8
-// x 7 heads, at 40 to 49 tokens 112 / 69.  The host does not know the lengths:
-// the page table's width stands for them, up to kTcTokens, since a wide table may
-// be a short one's.
+// x 7 heads, at 40 to 49 tokens 112 / 69.  These are with page tables as wide as
+// the longest request.
+//
+// The host does not know the lengths: the page table's width stands for them, up
+// to kTcTokens, since a wide table may be a short one's.  With a table of 131072
+// tokens (us, few-row / tcgen05; *: the rule takes the slower), 4 x 8 heads: 32 new
+// tokens at 512 18 / 34*, at 2048 25 / 38*, at 4096 31 / 41*; 64 new tokens at 512
+// 23 / 34*, at 4096 45 / 40; 16 at 4096 25 / 38*; 4 x 32 at 1024 33 / 40*; and where
+// the table is as long as it is wide: 8 new tokens at 131072 122* / 100, 10 150* / 100,
+// 12 172 / 100, 16 224 / 101.  A lower limit would trade the first against these.
+//
+// Cutting row blocks along the tokens adds a launch for their join and pays where
+// one block is longer than a CTA's share of the work.  Measured (us, not cut / cut;
+// 4 x 8 x 128; places: row blocks and requests, times key heads):
+//   512 new tokens at 4096 (68 places) 81 / 69, 1024 (132) 82 / 87, 2048 (260) 119 /
+//   126; 512 at 32768 beside 8 x 256 at 512 (356) 520 / 308; 256 at 65536 beside 16 x
+//   256 at 512 (612) 978 / 314, at 16384 266 / 153, at 8192 147 / 122; equal requests
+//   8 x 512 at 3584 (544) 242 / 251, 16 x 256 (576) 254 / 263;
+//   above the limit: 18 x 256 at 256 to 3584 (648) 159 / 169, 32 x 256 (1152) 266 / 280,
+//   but 256 at 16384 beside 24 x 256 (900) 271 / 179, at 65536 beside 40 (1476) 1000 /
+//   426.
+// A call that gains nothing loses up to 10 us, one long request among short ones
+// gains several times that; more places make the second rarer, so that cutting is
+// allowed up to 4 kMaxSms of them.  The device then cuts what is longer than 1.5
+// shares (2 instead of 1.5: the same times to 1 us, with 8 x 512 at 3584, 4 x 1024 at
+// 32768, 2 x 2048 at 4096 to 65536, 3 x 512 at 2048 to 16384).
 constexpr int kTcRows = 48;                  // of a request and key head
 constexpr int kTcTokens = 16384;
 constexpr int64_t kTcWork = int64_t(6) << 20;   // pairs

@@ -34,13 +34,16 @@
 // (paged_attn.cu) and paged_attn_tc_join adds the parts up in order.
 //
 // Measured: 32 x 256 tokens of 4 x 8 heads of 128 behind up to 3328 others, 241
-// GFLOP in 262 us = 919 TFLOP/s, the tensor pipe active 41 % of the time; one
-// prompt of 8192, 550 GFLOP in 477 us = 1153 TFLOP/s.  A step of 128 tokens takes
+// GFLOP in 266 us = 906 TFLOP/s, the tensor pipe active 41 % of the time; one
+// prompt of 8192, 550 GFLOP in 478 us = 1151 TFLOP/s.  A step of 128 tokens takes
 // about 2.2 us.  Its 32 MMAs of 128 x 128 x 16 take about 104 cycles each, 1.75 us
 // (one of 128 x 256 x 16 takes 135, but two tiles' scores and outputs fill the
 // tensor memory); the rest is the hand-over between scores, weights and products.
-// An item's start and end (its q, the first reference, its output) cost two to
-// three steps more, which is what the short prompts lose.
+// What holds an MMA to 104 cycles is not known: shared memory is at 51 % of its
+// rate (30 % operands of the MMAs, 21 % the other warps), so not its bandwidth
+// alone.  An item's start and end (its q, the first reference, its output) cost
+// two to three steps more, which is what the short prompts lose.  Of 128 registers
+// the softmax warps spill 88 bytes (D = 64: 40).
 #include <climits>
 
 #include "paged_attn.cuh"

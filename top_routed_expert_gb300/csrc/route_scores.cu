@@ -23,7 +23,7 @@
 //
 // Measured: 65519 tokens of 256 experts (8 groups, bias, sigmoid, bf16, k = 8)
 // 49.5 us, 675 warp instructions a token at three quarters of the issue
-// slots, 0.76 TB/s; one token of 128 experts 3.0 us, a launch.  A token for half
+// slots, 0.76 TB/s; one token of 128 experts 1.7 us in a graph, a launch.  A token for half
 // a warp would halve the rounds' cost but double the sort's and leaves the
 // scores' as it is.
 #include <cmath>
@@ -175,7 +175,9 @@ __device__ __forceinline__ RawLogits<EPL, BF16> load_logits(const RsArgs& a, int
 }
 
 // Blocks on an SM (48 registers a thread); a long batch's warps take several
-// tokens each (65519 tokens of 256 experts: 50.4 us with 8 blocks, 49.5 with 10).
+// tokens each (65519 tokens of 256 experts, 8 groups, 8 / 10 blocks: sigmoid 49.4 to
+// 50.6 / 48.2 to 50.1 us, softmax 57.0 to 58.9 / 57.0 to 58.6; softmax without a bias
+// spills 12 to 16 bytes with ten, f32 57.0 / 58.0, bf16 57.6 / 57.0).
 constexpr int kRsBlocks = 10;
 
 template <int EPL, bool BF16, bool SIGMOID, bool BIAS>
