@@ -1,6 +1,6 @@
 """GPU parity of moe_paged_attention (include/paged_kv.h) on long contexts in
 which a few tokens take almost all of the softmax but have no value, so that
-the output is what the many small weights leave.  Judged relative to the row's
+the output is what the many small weights leave.  Compared relative to the row's
 own exact output.
 
 All values are positive, so relative errors of the weights carry over to the

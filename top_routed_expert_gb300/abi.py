@@ -233,9 +233,9 @@ def _need(cond: bool, what: str):
 
 
 # The calling thread's current CUDA device, the one that the library launches
-# on, and the address of its current stream.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# on, and the address of its current stream (a torch without CUDA has neither).
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 # The calls below are a few microseconds long and so is what they cost here: each
 # looks at types, sizes and devices alone, written out in it.  Rows' layouts are
