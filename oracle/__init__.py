@@ -12,3 +12,4 @@ from .moe_oracle import (E2M1_TABLE, E4M3_TABLE, decode_bf16, decode_e2m1_packed
                          encode_e2m1, nvfp4_row_scale, nvfp4_block_scale, quantize_nvfp4_act_rows)
 from . import qk_rope_oracle  # noqa: F401,E402
 from . import decode_oracle  # noqa: F401,E402
+from . import block_oracle  # noqa: F401,E402

@@ -40,7 +40,8 @@ MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 0, 1
 EXPORTS = ("moe_abi_version", "moe_status_str", "moe_workspace_bytes", "moe_route", "moe_permute",
            "moe_permute_noalloc", "moe_expert_ffn", "moe_combine", "moe_layer_forward", "moe_launch_count",
            "moe_get_device_status", "moe_qk_norm_rope", "moe_route_scores", "moe_kv_append",
-           "moe_paged_attention", "moe_paged_attention_ws_bytes")
+           "moe_paged_attention", "moe_paged_attention_ws_bytes", "moe_blockkv_append", "moe_blockkv_attention",
+           "moe_blockkv_attention_ws_bytes", "moe_blockkv_read", "moe_add_rms_norm")
 
 
 class MoEError(RuntimeError):
@@ -90,6 +91,29 @@ class moe_paged_attention_config_t(ctypes.Structure):
     q_row, head_dim = 0, None
 
 
+class moe_blockkv_cache_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table")]
+    _fields_ += [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim", "max_pages")]
+    _fields_ += [(n, ctypes.c_float) for n in ("k_gscale", "v_gscale")]
+    _fields_ += [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride", "scale_page_stride",
+                                               "scale_head_stride", "scale_token_stride")]
+    # of make_blockkv_cache's tensors: device, rows of the page table, (n_kv_heads, head_dim)
+    device, batch, heads = None, 1 << 30, None
+
+
+class moe_blockkv_read_config_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "batch", "out_dtype")]
+    _fields_ += [(n, ctypes.c_int64) for n in ("k_stride", "v_stride")]
+    # of make_blockkv_read_config's tensors: (n_kv_heads, head_dim), type, bytes of a row
+    heads, dtype, row = None, None, 0
+
+
+class moe_add_norm_config_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "x_dtype", "res_dtype", "out_dtype", "group")]
+    _fields_ += [("eps", ctypes.c_float)]
+    _fields_ += [(n, ctypes.c_int64) for n in ("x_stride", "res_stride", "sum_stride", "out_stride")]
+
+
 class moe_weights_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "w13", "w13_scale", "w13_gscale", "w2", "w2_scale", "w2_gscale",
@@ -129,6 +153,13 @@ def load(path: str = LIB) -> ctypes.CDLL:
                                 + [vp] * 6 + [sz, vp]),
         "moe_paged_attention_ws_bytes": (sz, [ctypes.POINTER(moe_paged_attention_config_t),
                                               ctypes.POINTER(moe_kv_cache_t)]),
+        "moe_blockkv_append": (i32, [ctypes.POINTER(moe_kv_append_config_t), ctypes.POINTER(moe_blockkv_cache_t)] + [vp] * 11),
+        "moe_blockkv_attention": (i32, [ctypes.POINTER(moe_paged_attention_config_t), ctypes.POINTER(moe_blockkv_cache_t)]
+                                  + [vp] * 6 + [sz, vp]),
+        "moe_blockkv_attention_ws_bytes": (sz, [ctypes.POINTER(moe_paged_attention_config_t),
+                                                ctypes.POINTER(moe_blockkv_cache_t)]),
+        "moe_blockkv_read": (i32, [ctypes.POINTER(moe_blockkv_read_config_t), ctypes.POINTER(moe_blockkv_cache_t)] + [vp] * 5),
+        "moe_add_rms_norm": (i32, [ctypes.POINTER(moe_add_norm_config_t)] + [vp] * 8),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -307,11 +338,11 @@ def make_kv_cache(k, v, k_scale, v_scale, page_table) -> moe_kv_cache_t:
     return c
 
 
-def _row_stride(t: torch.Tensor) -> int:
+def _row_stride(t: torch.Tensor, dtype=torch.bfloat16) -> int:
     """Row stride of [T, heads, D] with contiguous heads."""
     _need(t.dim() == 3 and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2]),
           "rows of [T, heads, D] with contiguous heads")
-    _need(t.dtype == torch.bfloat16, "bf16 rows")
+    _need(t.dtype == dtype, f"{'bf16' if dtype == torch.bfloat16 else dtype} rows")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
 
 
@@ -329,8 +360,7 @@ def make_kv_append_config(q, k, v, q_out, batch, rot_dim=0, n_pos=0, rope_layout
     return c
 
 
-def moe_kv_append(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream=None):
-    """Norm, rotation and append to the paged cache (include/paged_kv.h)."""
+def _append(call, where, cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream):
     dev = _current_device()
     if not (dev == k.get_device() == v.get_device() == cu.get_device() == kv_len.get_device()
             and (q is None or q.get_device() == q_out.get_device() == dev)
@@ -350,14 +380,20 @@ def moe_kv_append(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu,
             and (cos_sin is None or cos_sin.dtype is _F32 and cos_sin.numel() >= cfg.n_pos * cfg.rot_dim)
             and (positions is None or positions.dtype is _I32 and positions.numel() >= T)):
         raise ValueError("gamma_q, gamma_k: float32 [D], cos_sin: float32 [n_pos, rot_dim / 2, 2], positions: int32 [T]")
-    code = load().moe_kv_append(
+    code = call(
         cfg, cache, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
         None if gamma_q is None else gamma_q.data_ptr(), None if gamma_k is None else gamma_k.data_ptr(),
         None if cos_sin is None else cos_sin.data_ptr(), None if positions is None else positions.data_ptr(),
         cu.data_ptr(), kv_len.data_ptr(), None if q is None else q_out.data_ptr(),
         _current_stream(dev) if stream is None else _stream_of(stream, dev))
     if code:
-        raise MoEError(code, "moe_kv_append")
+        raise MoEError(code, where)
+
+
+def moe_kv_append(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream=None):
+    """Norm, rotation and append to the paged cache (include/paged_kv.h)."""
+    _append(load().moe_kv_append, "moe_kv_append", cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len,
+            q_out, stream)
 
 
 def make_paged_attention_config(q, out, batch, max_q_len=0, window=0, n_sink=0,
@@ -374,8 +410,7 @@ def moe_paged_attention_ws_bytes(cfg, cache) -> int:
     return load().moe_paged_attention_ws_bytes(cfg, cache)
 
 
-def moe_paged_attention(cfg, cache, q, cu, kv_len, out, lse=None, ws=None, stream=None):
-    """Attention of the new tokens over the paged cache (include/paged_kv.h)."""
+def _attention(call, where, cfg, cache, q, cu, kv_len, out, lse, ws, stream):
     dev = _current_device()
     if not (dev == q.get_device() == cu.get_device() == kv_len.get_device() == out.get_device()
             and (lse is None or lse.get_device() == dev) and (ws is None or ws.get_device() == dev)
@@ -389,12 +424,143 @@ def moe_paged_attention(cfg, cache, q, cu, kv_len, out, lse=None, ws=None, strea
             and (lse is None or lse.dtype is _F32 and lse.numel() >= T * cfg.n_q_heads)):
         raise ValueError("q and out: rows of the configuration's shape and the cache's head size, lse: float32 "
                          "[T, n_q_heads]")
-    code = load().moe_paged_attention(
+    code = call(
         cfg, cache, q.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
         _current_stream(dev) if stream is None else _stream_of(stream, dev))
     if code:
-        raise MoEError(code, "moe_paged_attention")
+        raise MoEError(code, where)
+
+
+def moe_paged_attention(cfg, cache, q, cu, kv_len, out, lse=None, ws=None, stream=None):
+    """Attention of the new tokens over the paged cache (include/paged_kv.h)."""
+    _attention(load().moe_paged_attention, "moe_paged_attention", cfg, cache, q, cu, kv_len, out, lse, ws, stream)
+
+
+def make_blockkv_cache(k, v, k_scale, v_scale, page_table, k_gscale=1.0, v_gscale=1.0) -> moe_blockkv_cache_t:
+    """A paged cache in 4 bits from its tensors: k, v [n_pages, n_kv_heads, page_size, D / 2] bytes of two E2M1 codes
+    each, the scales [n_pages, n_kv_heads, page_size, D / 16] of torch.float8_e4m3fn (or their bytes), both in any
+    stride order with a contiguous last dimension; page_table [batch, max_pages] int32; the factors powers of two.
+    The tensors stay alive with the returned object."""
+    _need(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride(), "k and v: one 4-d shape, the same strides")
+    _need(k_scale.dim() == 4 and k_scale.shape == v_scale.shape and k_scale.stride() == v_scale.stride(),
+          "scales: one 4-d shape, the same strides")
+    n_pages, heads, page, D = *k.shape[:3], 2 * k.shape[3]
+    _need(k_scale.shape == (n_pages, heads, page, D // 16) and D % 16 == 0, "scales: [n_pages, n_kv_heads, page_size, D / 16]")
+    byte = (torch.uint8, torch.int8)
+    _need(all(t.dtype in byte and t.stride(3) == 1 for t in (k, v)), "k and v: bytes of two codes, contiguous heads")
+    _need(all(t.dtype in (torch.float8_e4m3fn, *byte) and t.stride(3) == 1 for t in (k_scale, v_scale)),
+          "scales: E4M3 codes (torch.float8_e4m3fn, or bytes), contiguous heads")
+    _need(page_table.dim() == 2 and page_table.dtype == torch.int32 and page_table.is_contiguous(),
+          "page_table: contiguous int32 [batch, max_pages]")
+    # a dimension of size 1 may carry any stride: give it one that the library takes
+    strides = [st if n > 1 else D // 2 for n, st in zip(k.shape[:3], k.stride()[:3])]
+    strides += [st if n > 1 else D // 16 for n, st in zip(k_scale.shape[:3], k_scale.stride()[:3])]
+    c = moe_blockkv_cache_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
+                            n_pages, page, heads, D, page_table.shape[1], k_gscale, v_gscale, *strides)
+    c.tensors = (k, v, k_scale, v_scale, page_table)
+    c.device, c.batch, c.heads = k.get_device(), page_table.shape[0], (heads, D)
+    _need(all(t.get_device() == c.device for t in c.tensors), "the cache's tensors: one device")
+    return c
+
+
+def moe_blockkv_append(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream=None):
+    """Norm, rotation and append to the paged cache in 4 bits (include/block_kv.h)."""
+    _append(load().moe_blockkv_append, "moe_blockkv_append", cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu,
+            kv_len, q_out, stream)
+
+
+def moe_blockkv_attention_ws_bytes(cfg, cache) -> int:
+    return load().moe_blockkv_attention_ws_bytes(cfg, cache)
+
+
+def moe_blockkv_attention(cfg, cache, q, cu, kv_len, out, lse=None, ws=None, stream=None):
+    """Attention of the new tokens over the paged cache in 4 bits (include/block_kv.h)."""
+    _attention(load().moe_blockkv_attention, "moe_blockkv_attention", cfg, cache, q, cu, kv_len, out, lse, ws, stream)
+
+
+def _float_type(t: torch.Tensor) -> int:
+    _need(t.dtype is _BF16 or t.dtype is _F32, "bf16 or float32")
+    return MOE_BF16 if t.dtype is _BF16 else MOE_F32
+
+
+def make_blockkv_read_config(k_out, v_out, batch) -> moe_blockkv_read_config_t:
+    """Sizes, type and strides of a read from its outputs [T, n_kv_heads, D], bf16 or float32 (one may be None)."""
+    like = k_out if k_out is not None else v_out
+    _need(like is not None and all(t is None or (t.shape == like.shape and t.dtype == like.dtype) for t in (k_out, v_out)),
+          "k_out and v_out: one shape and type")
+    rows = [0 if t is None else _row_stride(t, like.dtype) for t in (k_out, v_out)]
+    c = moe_blockkv_read_config_t(like.shape[0], batch, _float_type(like), *rows)
+    c.heads, c.dtype = tuple(like.shape[1:]), like.dtype
+    c.row = like.shape[1] * like.shape[2] * like.element_size()
+    return c
+
+
+def moe_blockkv_read(cfg, cache, cu, kv_len, k_out, v_out, stream=None):
+    """Rows of the paged cache in 4 bits as bf16 or float32 (include/block_kv.h)."""
+    dev = _current_device()
+    if not (dev == cu.get_device() == kv_len.get_device() and (k_out is None or k_out.get_device() == dev)
+            and (v_out is None or v_out.get_device() == dev) and (cache.device is None or cache.device == dev)):
+        raise ValueError(_ELSEWHERE)
+    B = cfg.batch
+    if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
+        raise ValueError(_RAGGED)
+    if not ((cfg.heads == cache.heads or cfg.heads is None or cache.heads is None)
+            and all(t is None or t.nbytes >= cfg.T * cfg.row and (cfg.dtype is None or t.dtype is cfg.dtype)
+                    for t in (k_out, v_out))):
+        raise ValueError("k_out and v_out: rows of the configuration's shape and type and the cache's heads")
+    code = load().moe_blockkv_read(cfg, cache, cu.data_ptr(), kv_len.data_ptr(), None if k_out is None else k_out.data_ptr(),
+                                   None if v_out is None else v_out.data_ptr(),
+                                   _current_stream(dev) if stream is None else _stream_of(stream, dev))
+    if code:
+        raise MoEError(code, "moe_blockkv_read")
+
+
+def make_add_rms_norm_config(x, residual=None, out=None, out8=None, sum=None, group=0, eps=1e-6) -> moe_add_norm_config_t:
+    """Sizes, types and strides of an addition and norm from its tensors [T, d]."""
+    _need(x.dim() == 2 and all(t is None or t.shape == x.shape for t in (residual, out, out8, sum)), "one shape [T, d]")
+    _need(all(t is None or t.stride(1) == 1 for t in (x, residual, out, out8, sum)), "contiguous rows")
+    _need(sum is None or (residual is not None and sum.dtype == residual.dtype), "sum: of the residual's type")
+    codes = (torch.float8_e4m3fn, torch.uint8, torch.int8)
+    _need(out8 is None or (out8.dtype in codes and out8.is_contiguous()),
+          "out8: contiguous E4M3 codes (torch.float8_e4m3fn, or bytes)")
+    T, d = x.shape
+    stride = lambda t: d if t is None or T <= 1 else t.stride(0)
+    c = moe_add_norm_config_t(T, d, _float_type(x), MOE_BF16 if residual is None else _float_type(residual),
+                              MOE_BF16 if out is None else _float_type(out), group, eps, stride(x), stride(residual),
+                              stride(sum), stride(out))
+    # the types that the call's tensors have to have
+    c.types = tuple(None if t is None else t.dtype for t in (x, residual, out, sum))
+    return c
+
+
+def moe_add_rms_norm(cfg, x, residual, gamma, out=None, out8=None, out8_scale=None, sum=None, stream=None):
+    """Residual's addition and RMS norm, with an E4M3 copy (include/add_rms_norm.h)."""
+    dev = _current_device()
+    T, d, types = cfg.T, cfg.d, getattr(cfg, "types", (None,) * 4)
+    strides = cfg.x_stride, cfg.res_stride, cfg.out_stride, cfg.sum_stride
+    for t, dtype, stride in zip((x, residual, out, sum), types, strides):
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise ValueError(_ELSEWHERE)
+        if not ((dtype is None or t.dtype is dtype) and t.dim() == 2 and t.shape[0] >= T and t.shape[1] >= d
+                and (T <= 1 or t.stride(0) == stride) and t.stride(1) == 1):
+            raise ValueError("x, residual, out and sum: [T, d] of the configuration's types and strides")
+    if gamma.get_device() != dev or (out8 is not None and not out8.get_device() == dev == out8_scale.get_device()):
+        raise ValueError(_ELSEWHERE)
+    if not (gamma.dtype is _F32 and gamma.numel() >= d and gamma.is_contiguous()):
+        raise ValueError("gamma: float32 [d]")
+    if out8 is not None and not (out8.nbytes >= T * d and out8.is_contiguous() and out8_scale.dtype is _F32 and out8_scale.is_contiguous()
+                                 and out8_scale.numel() >= T * (d // cfg.group if cfg.group > 0 else 1)):
+        raise ValueError("out8: contiguous [T, d], out8_scale: contiguous float32 [T, d / group]")
+    code = load().moe_add_rms_norm(cfg, x.data_ptr(), None if residual is None else residual.data_ptr(), gamma.data_ptr(),
+                                   None if out is None else out.data_ptr(), None if out8 is None else out8.data_ptr(),
+                                   None if out8_scale is None else out8_scale.data_ptr(),
+                                   None if sum is None else sum.data_ptr(),
+                                   _current_stream(dev) if stream is None else _stream_of(stream, dev))
+    if code:
+        raise MoEError(code, "moe_add_rms_norm")
 
 
 def moe_launch_count() -> int:

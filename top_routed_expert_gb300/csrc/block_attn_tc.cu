@@ -1,0 +1,10 @@
+// Attention over the paged 4-bit cache: the tcgen05 kernel.
+#include "paged_attn_tc.cuh"
+
+namespace moe {
+
+cudaError_t launch_paged_attn_tc(const BlockPaArgs& a, cudaStream_t s) {
+  return a.c.head_dim == 64 ? launch_tc<64>(a, s) : launch_tc<128>(a, s);
+}
+
+}  // namespace moe

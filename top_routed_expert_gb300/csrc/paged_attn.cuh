@@ -26,6 +26,7 @@ struct TcJoin {
 };
 
 struct PaArgs {
+  static constexpr bool kBlocks = false;   // a scale for a page and head (paged_kv.h)
   const uint16_t* q;
   uint16_t* out;
   float* lse;
@@ -46,6 +47,21 @@ struct PaArgs {
   bool tc_split;        // whether row blocks may be cut
   float sm_scale;
 };
+
+// A cache in 4 bits (block_kv.h): c holds its codes, page table and sizes.
+struct BlockPaArgs : PaArgs {
+  static constexpr bool kBlocks = true;    // ... for a token, head and 16 elements
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  int64_t scale_page, scale_head, scale_token;   // strides of the scales
+  float kg, vg;                                  // factors of keys and values
+};
+
+// What a row's outputs are multiplied by: 1 / sum, and the values' factor.
+template <class Args> __device__ __forceinline__ float out_factor(const Args& a, float sum) {
+  if constexpr (Args::kBlocks) return sum == 0.f ? 0.f : a.vg / sum;   // 0: nothing visible (a NaN sum is not)
+  else return sum == 0.f ? 0.f : 1.0f / sum;
+}
 
 constexpr int kTcItemRows = 256;   // rows of an item of paged_attn_tc.cu
 constexpr int kTcStep = 128;       // cached tokens of its steps
@@ -173,6 +189,29 @@ constexpr float kRefBelow = 8.0f, kMostSum = 65504.0f;
 // and has to stay so (a product that small leaves no score to speak of).
 __device__ __forceinline__ float score_factor(float k_scale, float rf) { return fmaxf(k_scale * rf, 1e-37f); }
 
+// The two codes of each of a word's four bytes -> two f16 (the low four bits in the low half).
+__device__ __forceinline__ void f16x2_of_e2m1(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+// Codes of elements 0, 2, 4, 6 (even) and 1, 3, 5, 7 (odd) of two tokens, a token's code in each half of a byte.
+__device__ __forceinline__ uint32_t even_codes(uint32_t a, uint32_t b) { return (a & 0x0f0f0f0fu) | (b << 4 & 0xf0f0f0f0u); }
+__device__ __forceinline__ uint32_t odd_codes(uint32_t a, uint32_t b) { return (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u); }
+// Two E4M3 scales (the low 16 bits) -> two f16, exact.
+__device__ __forceinline__ uint32_t f16x2_of_scales(uint32_t two) {
+  uint32_t r;
+  asm("{\n .reg .b16 t, u;\n mov.b32 {t, u}, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(r) : "r"(two));
+  return r;
+}
+// A code times its scale: six significant bits, 2^-10 to 2688, exact in f16.
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
 // Factor that brings a head's largest |q| into [2^14, 2^15), a power of two;
 // NaN when the head holds a non-finite element (its row becomes NaN).
 __device__ __forceinline__ float q_factor(float amax, bool finite) {
@@ -190,10 +229,10 @@ __device__ __forceinline__ void store_lse(const PaArgs& a, int row, int head, fl
 
 // Four columns of a finished row: outputs `acc` and the weights' sum, both
 // relative to 2^m.
-__device__ __forceinline__ void store_row4(const PaArgs& a, int row, int head, int D, int d, const float4& acc, float m,
+template <class Args>
+__device__ __forceinline__ void store_row4(const Args& a, int row, int head, int D, int d, const float4& acc, float m,
                                            float sum) {
-  const bool empty = sum == 0.f;   // nothing visible (a NaN sum is not)
-  const float f = empty ? 0.f : 1.0f / sum;
+  const float f = out_factor(a, sum);
   const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * f, acc.y * f), y = __floats2bfloat162_rn(acc.z * f, acc.w * f);
   *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(row) * a.os + static_cast<int64_t>(head) * D + d) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
