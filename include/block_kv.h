@@ -42,10 +42,12 @@ typedef struct {
   float v_gscale;             /*   2^-60 to 2^60                                    */
   int64_t page_stride;        /* bytes of codes between pages, heads and tokens:     */
   int64_t head_stride;        /*   positive multiples of 16, at least D / 2, in any  */
-  int64_t token_stride;       /*   order; a token's D / 2 bytes are contiguous       */
+  int64_t token_stride;       /*   order; a token's D / 2 bytes are contiguous;      */
+                              /*   n_pages page_stride below 2^36 (64 GB)            */
   int64_t scale_page_stride;  /* bytes of scales between pages, heads and tokens:    */
   int64_t scale_head_stride;  /*   positive multiples of D / 16, in any order; a     */
-  int64_t scale_token_stride; /*   token's D / 16 bytes are contiguous               */
+  int64_t scale_token_stride; /*   token's D / 16 bytes are contiguous; n_pages      */
+                              /*   scale_page_stride below 2^32 D / 16               */
 } moe_blockkv_cache_t;
 
 /*

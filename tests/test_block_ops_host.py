@@ -37,7 +37,7 @@ BAD_CACHES = [
     dict(head_stride=-1024), dict(token_stride=48), dict(token_stride=72), dict(scale_page_stride=0),
     dict(scale_head_stride=-128), dict(scale_token_stride=4), dict(scale_token_stride=12), dict(k_gscale=0.0),
     dict(k_gscale=3.0), dict(k_gscale=-1.0), dict(v_gscale=math.nan), dict(v_gscale=math.inf), dict(v_gscale=2.0 ** 61),
-    dict(k_gscale=2.0 ** -61),
+    dict(k_gscale=2.0 ** -61), dict(n_pages=1 << 20, page_stride=1 << 16), dict(n_pages=1 << 20, scale_page_stride=1 << 15),
 ]
 BAD_POINTERS = [dict(k=None), dict(v=None), dict(k_scale=None), dict(v_scale=None), dict(page_table=None), dict(k=0x10008),
                 dict(v=0x10008), dict(k_scale=0x10004), dict(v_scale=ODD), dict(page_table=ODD)]

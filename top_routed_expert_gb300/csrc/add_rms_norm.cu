@@ -2,9 +2,11 @@
 // moe_add_rms_norm), with an E4M3 copy and its scales where that is asked for.
 //
 // Bound by memory: every input is read once and every output written once.  A
-// block owns a row and keeps it in registers between the sum of squares and the
-// outputs, eight consecutive elements a thread and pass, so that every access is
-// 16 bytes (fp32: 32) beside its neighbours'.  A group's largest size is taken
+// block works on one row after the other: it keeps gamma in registers, and the
+// next row's elements are on their way while a row's squares are summed and its
+// outputs leave.  A thread has eight consecutive elements a pass, 16 bytes (fp32:
+// 32) beside its neighbours', reads and writes no others (so outputs may lie over
+// inputs), and one barrier a row joins the sums.  A group's largest size is taken
 // by the 2 to 32 lanes that hold the group, a row's by the block.
 #include "common.cuh"
 #include "../../include/add_rms_norm.h"
@@ -26,32 +28,48 @@ struct NormArgs {
   float* scale8;
   void* sum;
   int64_t xs, rs, ss, os;
-  int d, group;
+  int T, d, group;
   float eps;
-  bool x_f32, res_f32, out_f32;
+  bool x_f32, out_f32;
 };
 
-__device__ __forceinline__ void load8(const void* base, bool f32, int64_t at, float (&x)[8]) {
-  if (f32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+// Eight elements as they lie in memory.
+template <bool F32> struct Raw8 {
+  uint4 w[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load8(const void* base, int64_t at) {
+  Raw8<F32> r;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + at * (F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(v[i] << 16);
-      x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) r.w[i] = p[i];
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack8(const Raw8<F32>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    const uint32_t v[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (F32) {
+        x[4 * i + e] = __uint_as_float(v[e]);
+      } else {
+        x[2 * e] = __uint_as_float(v[e] << 16);
+        x[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+      }
     }
   }
 }
-
-// Rounds to the stored type and stores; x is left as what was stored.
-__device__ __forceinline__ void round8(bool f32, float (&x)[8]) {
-  if (f32) return;
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  uint32_t v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(__float2bfloat16_rn(x[i]));
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    v[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 __device__ __forceinline__ void store8(void* base, bool f32, int64_t at, const float (&x)[8]) {
   if (f32) {
@@ -59,107 +77,132 @@ __device__ __forceinline__ void store8(void* base, bool f32, int64_t at, const f
     p[0] = make_float4(x[0], x[1], x[2], x[3]);
     p[1] = make_float4(x[4], x[5], x[6], x[7]);
   } else {
-    uint32_t v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      v[i] = *reinterpret_cast<const uint32_t*>(&y);
-    }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = pack8(x);
   }
 }
+// Eight elements times `inv` as E4M3 codes.
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
+  uint32_t c[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; e += 2)
+    c[e / 4] |= static_cast<uint32_t>(
+                    __nv_cvt_float2_to_fp8x2(make_float2(x[e] * inv, x[e + 1] * inv), __NV_SATFINITE, __NV_E4M3))
+                << (8 * (e % 4));
+  return make_uint2(c[0], c[1]);
+}
 
-// PASSES: pieces of eight elements of a thread.
-template <int THREADS, int PASSES>
-__global__ void __launch_bounds__(THREADS) add_rms_norm_kernel(NormArgs a) {
+// Blocks on an SM that the registers are cut for.
+template <int THREADS, int PASSES> constexpr int blocks_on_sm() { return (PASSES < 4 ? 1024 : 512) / THREADS; }
+
+// PASSES: pieces of eight elements of a thread.  RES: residual 0 none, 1 bf16, 2 fp32.
+template <int THREADS, int PASSES, bool XF32, int RES>
+__global__ void __launch_bounds__(THREADS, blocks_on_sm<THREADS, PASSES>()) add_rms_norm_kernel(NormArgs a) {
   constexpr int WARPS = THREADS / 32;
-  __shared__ float s_sum[WARPS], s_top[WARPS];
+  __shared__ float s_sum[2][WARPS], s_top[2][WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pieces = a.d / 8;
-  const int64_t row = blockIdx.x;
-  float gamma[PASSES][8], h[PASSES][8];
+  auto live = [&](int i) { return static_cast<int>(threadIdx.x) + i * THREADS < pieces; };
+  auto at = [&](int i) { return (static_cast<int>(threadIdx.x) + i * THREADS) * 8; };
   pdl_enter();
-  float sum = 0.f;
+  float gamma[PASSES][8];
+  Raw8<XF32> x[PASSES];
+  Raw8<RES == 2> r[PASSES];
+  auto load = [&](int64_t row) {
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int p = threadIdx.x + i * THREADS;
-    if (p >= pieces) continue;
-    load8(a.x, a.x_f32, row * a.xs + p * 8, h[i]);
-    float r[8];
-    if (a.res) load8(a.res, a.res_f32, row * a.rs + p * 8, r);
-    load8(a.gamma, true, p * 8, gamma[i]);
-    if (a.res) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] += r[e];
-      round8(a.res_f32, h[i]);
+    for (int i = 0; i < PASSES; ++i) {
+      if (!live(i)) continue;
+      x[i] = load8<XF32>(a.x, row * a.xs + at(i));
+      if (RES) r[i] = load8<RES == 2>(a.res, row * a.rs + at(i));
     }
+  };
+  load(blockIdx.x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(h[i][e], h[i][e], sum);
-  }
+  for (int i = 0; i < PASSES; ++i)
+    if (live(i)) unpack8<true>(load8<true>(a.gamma, at(i)), gamma[i]);
+  int odd = 0;   // in turn: one barrier a row
+#pragma unroll 1
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, odd ^= 1) {
+    float h[PASSES][8], sum = 0.f;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();   // also: the whole row has been read, outputs may lie over it
-  sum = 0.f;
+    for (int i = 0; i < PASSES; ++i) {
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) sum += s_sum[w];
-  const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.d) + a.eps);
-  float top = 0.f;
+      for (int e = 0; e < 8; ++e) h[i][e] = 0.f;
+      if (!live(i)) continue;
+      unpack8<XF32>(x[i], h[i]);
+      if (RES) {
+        float y[8];
+        unpack8<RES == 2>(r[i], y);
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int p = threadIdx.x + i * THREADS;
-    const bool live = p < pieces;
-    if (live && a.sum) store8(a.sum, a.res_f32, row * a.ss + p * 8, h[i]);
-    float t = 0.f;
+        for (int e = 0; e < 8; ++e) h[i][e] += y[e];
+        if (RES == 1) {   // the norm is that of the rounded sum
+          Raw8<false> rounded;
+          rounded.w[0] = pack8(h[i]);
+          if (a.sum) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.sum) + row * a.ss + at(i)) = rounded.w[0];
+          unpack8<false>(rounded, h[i]);
+        } else if (a.sum) {
+          store8(a.sum, true, row * a.ss + at(i), h[i]);
+        }
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      h[i][e] = live ? h[i][e] * rstd * gamma[i][e] : 0.f;
-      t = fmaxf(t, fabsf(h[i][e]));   // a NaN is left out
+      for (int e = 0; e < 8; ++e) sum = fmaf(h[i][e], h[i][e], sum);
     }
-    if (live && a.out) store8(a.out, a.out_f32, row * a.os + p * 8, h[i]);
-    if (!a.out8) continue;
-    if (a.group == 0) {
-      top = fmaxf(top, t);
-      continue;
+    if (row + gridDim.x < a.T) load(row + gridDim.x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) s_sum[odd][warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) sum += s_sum[odd][w];
+    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.d) + a.eps);
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      float t = 0.f;
+      if (live(i)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[i][e] = h[i][e] * rstd * gamma[i][e];
+          t = fmaxf(t, fabsf(h[i][e]));   // a NaN is left out
+        }
+        if (a.out) store8(a.out, a.out_f32, row * a.os + at(i), h[i]);
+      }
+      if (!a.out8) continue;
+      if (a.group == 0) {
+        top = fmaxf(top, t);
+        continue;
+      }
+      for (int off = 1; off < a.group / 8; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+      if (!live(i)) continue;
+      const float s = fmaxf(t / 448.f, kMinScale);
+      if (at(i) % a.group == 0) a.scale8[row * (a.d / a.group) + at(i) / a.group] = s;
+      *reinterpret_cast<uint2*>(a.out8 + row * a.d + at(i)) = codes8(h[i], 1.0f / s);
     }
-    for (int off = 1; off < a.group / 8; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
-    const float s = fmaxf(t / 448.f, kMinScale), inv = 1.0f / s;
-    if (!live) continue;
-    if (p * 8 % a.group == 0) a.scale8[row * (a.d / a.group) + p * 8 / a.group] = s;
-    uint32_t c[2] = {0, 0};
+    if (!a.out8 || a.group != 0) continue;
 #pragma unroll
-    for (int e = 0; e < 8; e += 2)
-      c[e / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(h[i][e] * inv, h[i][e + 1] * inv),
-                                                                 __NV_SATFINITE, __NV_E4M3))
-                  << (8 * (e % 4));
-    *reinterpret_cast<uint2*>(a.out8 + row * a.d + p * 8) = make_uint2(c[0], c[1]);
-  }
-  if (!a.out8 || a.group != 0) return;
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (lane == 0) s_top[odd][warp] = top;
+    __syncthreads();
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_top[odd][w]);
+    const float s = fmaxf(top / 448.f, kMinScale), inv = 1.0f / s;
+    if (threadIdx.x == 0) a.scale8[row] = s;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_top[w]);
-  const float s = fmaxf(top / 448.f, kMinScale), inv = 1.0f / s;
-  if (threadIdx.x == 0) a.scale8[row] = s;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int p = threadIdx.x + i * THREADS;
-    if (p >= pieces) continue;
-    uint32_t c[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; e += 2)
-      c[e / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(h[i][e] * inv, h[i][e + 1] * inv),
-                                                                 __NV_SATFINITE, __NV_E4M3))
-                  << (8 * (e % 4));
-    *reinterpret_cast<uint2*>(a.out8 + row * a.d + p * 8) = make_uint2(c[0], c[1]);
+    for (int i = 0; i < PASSES; ++i)
+      if (live(i)) *reinterpret_cast<uint2*>(a.out8 + row * a.d + at(i)) = codes8(h[i], inv);
   }
 }
 
 template <int THREADS, int PASSES>
-cudaError_t launch(const NormArgs& a, int T, cudaStream_t s) {
+cudaError_t launch(const NormArgs& a, int res, int sms, cudaStream_t s) {
   count_launches(1);
-  return launch_pdl(add_rms_norm_kernel<THREADS, PASSES>, T, THREADS, 0, s, a);
+  const int blocks = std::min(a.T, sms * blocks_on_sm<THREADS, PASSES>());
+  auto go = [&](auto kernel) { return launch_pdl(kernel, blocks, THREADS, 0, s, a); };
+  if (a.x_f32) {
+    if (res == 0) return go(add_rms_norm_kernel<THREADS, PASSES, true, 0>);
+    return res == 1 ? go(add_rms_norm_kernel<THREADS, PASSES, true, 1>) : go(add_rms_norm_kernel<THREADS, PASSES, true, 2>);
+  }
+  if (res == 0) return go(add_rms_norm_kernel<THREADS, PASSES, false, 0>);
+  return res == 1 ? go(add_rms_norm_kernel<THREADS, PASSES, false, 1>) : go(add_rms_norm_kernel<THREADS, PASSES, false, 2>);
 }
 
 bool al(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -206,19 +249,19 @@ extern "C" moe_status_t moe_add_rms_norm(const moe_add_norm_config_t* cfg, const
   a.rs = cfg->res_stride;
   a.ss = cfg->sum_stride;
   a.os = cfg->out_stride;
+  a.T = cfg->T;
   a.d = cfg->d;
   a.group = cfg->group;
   a.eps = cfg->eps;
   a.x_f32 = cfg->x_dtype == MOE_F32;
-  a.res_f32 = residual && cfg->res_dtype == MOE_F32;
   a.out_f32 = cfg->out_dtype == MOE_F32;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int pieces = cfg->d / 8;
+  const int pieces = cfg->d / 8, res = !residual ? 0 : cfg->res_dtype == MOE_F32 ? 2 : 1;
   cudaError_t err;
-  if (pieces <= 128) err = launch<128, 1>(a, cfg->T, s);
-  else if (pieces <= 256) err = launch<256, 1>(a, cfg->T, s);
-  else if (pieces <= 512) err = launch<512, 1>(a, cfg->T, s);
-  else if (pieces <= 1024) err = launch<512, 2>(a, cfg->T, s);
-  else err = launch<512, 4>(a, cfg->T, s);
+  if (pieces <= 128) err = launch<128, 1>(a, res, sms, s);
+  else if (pieces <= 256) err = launch<128, 2>(a, res, sms, s);
+  else if (pieces <= 512) err = launch<256, 2>(a, res, sms, s);
+  else if (pieces <= 1024) err = launch<512, 2>(a, res, sms, s);
+  else err = launch<512, 4>(a, res, sms, s);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -25,11 +25,12 @@ namespace {
 
 constexpr int kSlots = 16;       // of a cache block
 constexpr int kThreads = kQueryThreads;
-constexpr int kRowsAtOnce = 2;   // that a thread has under way
+constexpr int kHeads = 4;        // of a token, that a thread has under way
 
 struct BaArgs : RowArgs {
   moe_blockkv_cache_t c;
   int items, parts;   // groups of slots that the requests can touch; blocks for one
+  int chunks;         // kHeads heads of a token
 };
 
 // The row's sum of squares, in the header's order: the thread's two fours, then a
@@ -94,11 +95,12 @@ __device__ __forceinline__ uint32_t codes_of(const float* x, float sg) {
   return r;
 }
 
-// Share `part` of the rows of 16 slots.
+// Share `part` of the rows of 16 slots: for keys, then for values, every token and
+// kHeads of its heads at a time.
 template <int D, bool HALF>
 __device__ __forceinline__ void append_slots(const BaArgs& a, int item, int part) {
-  constexpr int TPR = D / 8, GROUPS = kThreads / TPR, U = kRowsAtOnce;
-  __shared__ float4 s_top[U][GROUPS][D / 16];   // sizes of a row's fours
+  constexpr int TPR = D / 8, GROUPS = kThreads / TPR, U = kHeads;
+  __shared__ float4 s_top[2][GROUPS][D / 16];   // sizes of a row's fours, in turn
   const int ps = a.c.page_size, ps_log = 31 - __clz(ps), Hkv = a.c.n_kv_heads;
   const int b = warp_find_request(a.cu, a.B, item, 1, kSlots, 2);
   const Request r = load_request(a.cu, a.kv_len, b, a.T);
@@ -111,106 +113,99 @@ __device__ __forceinline__ void append_slots(const BaArgs& a, int item, int part
   const int base = (r.start / kSlots + at) * kSlots;
   if (at < 0 || base >= r.end) return;   // one block too many, or before the first request
   const int first = max(base, r.start), tokens = min(base + kSlots, r.end) - first;
+  const int n = tokens * a.chunks;       // of keys; as many of values behind them
+  if (part * GROUPS >= 2 * n) return;
   const int page = base >> ps_log;
   int pid = -1;
   if (page < a.c.max_pages) pid = a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page];
-  if (pid < 0 || pid >= a.c.n_pages) {
-    if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-    return;
-  }
   const int lr = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const Place pk = place_of<HALF>(lr, a.rot), pv = place_of<false>(lr, 0);
   const bool norm = a.gamma_k;
   Gamma gamma = {};
   if (norm) gamma = load_gamma(a.gamma_k, pk);
-  const float inv_6k = 1.f / (6.f * a.c.k_gscale), inv_6v = 1.f / (6.f * a.c.v_gscale);
-  const int rows = tokens * Hkv;   // of keys; as many of values behind them
+  int buffer = 0;
 #pragma unroll 1
-  for (int row0 = part * U * GROUPS; row0 < 2 * rows; row0 += a.parts * U * GROUPS) {
+  for (int i0 = part * GROUPS; i0 < 2 * n; i0 += a.parts * GROUPS) {
+    const int i = i0 + grp;
+    const bool key = i < n;
+    bool live = i < 2 * n;
+    const int j = key ? i : i - n, token = live ? j / a.chunks : 0, h0 = live ? (j - token * a.chunks) * U : 0;
+    const int64_t row = r.row0 + (first - r.start) + token;
+    const Place p = key ? pk : pv;
     Raw raw[U];
-    float2 cs[U][4];
-    int token[U], head[U];
-    bool key[U], live[U];
+    const uint16_t* from = key ? a.k + row * a.ks : a.v + row * a.vs;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = row0 + u * GROUPS + grp;
-      live[u] = i < 2 * rows;
-      key[u] = i < rows;
-      const int j = key[u] ? i : i - rows;
-      token[u] = live[u] ? j / Hkv : 0;
-      head[u] = live[u] ? j - token[u] * Hkv : 0;
-      const int64_t row = r.row0 + (first - r.start) + token[u];
       raw[u] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
-      if (live[u] && key[u]) raw[u] = load_raw<HALF>(a.k + row * a.ks + static_cast<int64_t>(head[u]) * D, pk);
-      else if (live[u]) raw[u] = load_raw<false>(a.v + row * a.vs + static_cast<int64_t>(head[u]) * D, pv);
+      if (live && h0 + u < Hkv) raw[u] = load_raw<HALF>(from + static_cast<int64_t>(h0 + u) * D, p);
     }
-    if (a.rot > 0) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (!live[u]) continue;
-        const int f = table_row(a, r.row0 + (first - r.start) + token[u], first + token[u]);
-        live[u] = f >= 0;
-        if (f < 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-        else if (key[u] && pk.rotates) load_cs<HALF>(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), pk, cs[u]);
-      }
+    float2 cs[4];
+    if (a.rot > 0 && live) {
+      const int f = table_row(a, static_cast<int>(row), first + token);
+      live = f >= 0;
+      if (f < 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      else if (key && p.rotates) load_cs<HALF>(a.cos_sin + static_cast<int64_t>(f) * (a.rot / 2), p, cs);
     }
-    if (HALF) __syncwarp();   // the sizes of the round before have been read
-    float x[U][8], top[U][2];
+    if (pid < 0 || pid >= a.c.n_pages) {
+      if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      return;
+    }
+    const float g = key ? a.c.k_gscale : a.c.v_gscale, inv_6g = 1.f / (6.f * g);
+    const int64_t slot = (first + token) & (ps - 1);
+    uint8_t* codes = static_cast<uint8_t*>(key ? a.c.k : a.c.v) + pid * a.c.page_stride + h0 * a.c.head_stride +
+                     slot * a.c.token_stride;
+    uint8_t* scales = static_cast<uint8_t*>(key ? a.c.k_scale : a.c.v_scale) + pid * a.c.scale_page_stride +
+                      h0 * a.c.scale_head_stride + slot * a.c.scale_token_stride;
     bool bad = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      unpack4(raw[u].a, x[u]);
-      unpack4(raw[u].b, x[u] + 4);
+      float x[8], top[2];
+      unpack4(raw[u].a, x);
+      unpack4(raw[u].b, x + 4);
       if (norm) {
-        const float mean = __fmul_rn(sum_of_squares<TPR>(x[u]), 1.0f / D);
+        const float mean = __fmul_rn(sum_of_squares<TPR>(x), 1.0f / D);
         const float rstd = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, a.eps)));
-        if (key[u])
+        if (key)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[u][e] = __fmul_rn(__fmul_rn(x[u][e], rstd), gamma.g[e]);
+          for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], rstd), gamma.g[e]);
       }
-      if (live[u] && key[u] && pk.rotates) rotate<HALF>(x[u], cs[u]);
+      const bool stored = live && h0 + u < Hkv;
+      if (live && key && p.rotates) rotate<HALF>(x, cs);
       bool not_finite = false;
-      top[u][0] = largest4(x[u], not_finite);
-      top[u][1] = largest4(x[u] + 4, not_finite);
-      bad |= not_finite && live[u];
+      top[0] = largest4(x, not_finite);
+      top[1] = largest4(x + 4, not_finite);
+      bad |= not_finite && stored;
       if (HALF) {
-        float* fours = reinterpret_cast<float*>(s_top[u][grp]);
-        const Place p = key[u] ? pk : pv;
-        fours[p.oa / 4] = top[u][0];
-        fours[p.ob / 4] = top[u][1];
+        float* fours = reinterpret_cast<float*>(s_top[buffer][grp]);
+        fours[p.oa / 4] = top[0];
+        fours[p.ob / 4] = top[1];
+        __syncwarp();   // (what the other buffer held has been read)
+        if (stored) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int o = h ? p.ob : p.oa;
+            const float4 t = s_top[buffer][grp][o / 16];
+            float sg;
+            const uint32_t sc = scale_code(max_or_nan(max_or_nan(t.x, t.y), max_or_nan(t.z, t.w)), g, inv_6g, sg);
+            *reinterpret_cast<uint16_t*>(codes + o / 2) = static_cast<uint16_t>(codes_of(x + 4 * h, sg));
+            if (o % 16 == 0) scales[o / 16] = static_cast<uint8_t>(sc);
+          }
+        }
+        buffer ^= 1;
       } else {
-        top[u][0] = max_or_nan(top[u][0], top[u][1]);
-        top[u][0] = max_or_nan(top[u][0], __shfl_xor_sync(0xffffffffu, top[u][0], 1));
+        top[0] = max_or_nan(top[0], top[1]);
+        top[0] = max_or_nan(top[0], __shfl_xor_sync(0xffffffffu, top[0], 1));
+        if (stored) {
+          float sg;
+          const uint32_t sc = scale_code(top[0], g, inv_6g, sg);
+          *reinterpret_cast<uint32_t*>(codes + lr * 4) = codes_of(x, sg) | codes_of(x + 4, sg) << 16;
+          if (lr % 2 == 0) scales[lr / 2] = static_cast<uint8_t>(sc);
+        }
       }
+      codes += a.c.head_stride;
+      scales += a.c.scale_head_stride;
     }
     if (bad) set_status(a.status, MOE_ERR_DEVICE_NONFINITE);
-    if (HALF) __syncwarp();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!live[u]) continue;
-      const float g = key[u] ? a.c.k_gscale : a.c.v_gscale, inv_6g = key[u] ? inv_6k : inv_6v;
-      const int64_t slot = (first + token[u]) & (ps - 1);
-      uint8_t* codes = static_cast<uint8_t*>(key[u] ? a.c.k : a.c.v) + pid * a.c.page_stride + head[u] * a.c.head_stride +
-                       slot * a.c.token_stride;
-      uint8_t* scales = static_cast<uint8_t*>(key[u] ? a.c.k_scale : a.c.v_scale) + pid * a.c.scale_page_stride +
-                        head[u] * a.c.scale_head_stride + slot * a.c.scale_token_stride;
-      float sg;
-      if (HALF) {
-        const Place p = key[u] ? pk : pv;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int o = h ? p.ob : p.oa;
-          const float4 t = s_top[u][grp][o / 16];
-          const uint32_t sc = scale_code(max_or_nan(max_or_nan(t.x, t.y), max_or_nan(t.z, t.w)), g, inv_6g, sg);
-          *reinterpret_cast<uint16_t*>(codes + o / 2) = static_cast<uint16_t>(codes_of(x[u] + 4 * h, sg));
-          if (o % 16 == 0) scales[o / 16] = static_cast<uint8_t>(sc);
-        }
-      } else {
-        const uint32_t sc = scale_code(top[u][0], g, inv_6g, sg);
-        *reinterpret_cast<uint32_t*>(codes + lr * 4) = codes_of(x[u], sg) | codes_of(x[u] + 4, sg) << 16;
-        if (lr % 2 == 0) scales[lr / 2] = static_cast<uint8_t>(sc);
-      }
-    }
   }
 }
 
@@ -233,11 +228,10 @@ __global__ void __launch_bounds__(kThreads, 7) blockkv_append_kernel(BaArgs a) {
 }
 
 template <int D>
-cudaError_t launch(BaArgs a, int sms, cudaStream_t s) {
-  // Few groups of slots are shared by several blocks, down to one round of rows each.
-  const int64_t groups = a.T / kSlots + std::min(a.B, a.T);
-  const int64_t rounds = ceil_div(2 * std::min(a.T, kSlots) * a.c.n_kv_heads, kRowsAtOnce * (kThreads / (D / 8)));
-  a.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rounds, 4 * sms / groups)));
+cudaError_t launch(BaArgs a, cudaStream_t s) {
+  // a round of rows for each block
+  a.chunks = ceil_div(a.c.n_kv_heads, kHeads);
+  a.parts = ceil_div(2 * kSlots * a.chunks, kThreads / (D / 8));
   int64_t blocks = static_cast<int64_t>(a.parts) * a.items;
   if (a.q) blocks += ceil_div(a.T, query_tokens<D>(a.Hq, kThreads));
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
@@ -271,9 +265,9 @@ extern "C" moe_status_t moe_blockkv_append(const moe_kv_append_config_t* cfg, co
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err;
   switch (D) {
-    case 64: err = launch<64>(a, sms, s); break;
-    case 128: err = launch<128>(a, sms, s); break;
-    default: err = launch<256>(a, sms, s); break;
+    case 64: err = launch<64>(a, s); break;
+    case 128: err = launch<128>(a, s); break;
+    default: err = launch<256>(a, s); break;
   }
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -26,6 +26,9 @@ inline bool blockkv_shape_ok(const moe_blockkv_cache_t* c) {
   const int64_t row = c->head_dim / 16, b[3] = {c->scale_page_stride, c->scale_head_stride, c->scale_token_stride};
   for (int64_t v : b)
     if (v < row || v % row != 0) return false;
+  // offsets of pages are counted in 32 bits, in units of 16 bytes and of a row of scales
+  const int64_t most = (int64_t(1) << 32) - 1, pages = c->n_pages;
+  if (c->page_stride / 16 > most / pages || c->scale_page_stride / row > most / pages) return false;
   return gscale_ok(c->k_gscale) && gscale_ok(c->v_gscale);
 }
 

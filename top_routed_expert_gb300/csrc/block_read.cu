@@ -2,17 +2,18 @@
 // moe_blockkv_read).
 //
 // A block owns 16 slots of a page, keys and values of all heads: one look-up of
-// request and page, then a thread takes eight codes (four bytes) and their
-// scale at a time and writes eight elements, so that neighbouring threads write
-// neighbouring 16 bytes.  Bound by memory: 0.56 bytes read and 2 (or 4) written
-// an element.  Request b's blocks start at cu[b]/16 + 2b, as in kv_append.cu.
+// request and page, then a thread takes the codes of 16 elements (eight bytes)
+// and their scale at a time and writes 32 bytes (fp32: 64), so that neighbouring
+// threads write beside each other; what it reads of keys and values is on its way
+// together.  Bound by memory: 0.56 bytes read and 2 (or 4) written an element.
+// Request b's blocks start at cu[b]/16 + 2b, as in kv_append.cu.
 #include "block_kv.cuh"
 #include "paged_attn.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kSlots = 16, kThreads = 256, kAtOnce = 4;
+constexpr int kSlots = 16, kThreads = 256, kAtOnce = 4;   // blocks of elements that a thread has under way
 
 struct BrArgs {
   moe_blockkv_cache_t c;
@@ -22,14 +23,31 @@ struct BrArgs {
   void* v_out;
   unsigned* status;
   int64_t ks, vs;
+  uint32_t per_row;   // 2^32 / blocks of a token's keys, rounded up
   int T, B;
 };
 
 __device__ __forceinline__ float2 halves(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
-template <int D, bool F32>
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// 32 bytes: in one access where the rows are aligned to that.
+template <bool WIDE> __device__ __forceinline__ void put(void* p, const uint32_t (&v)[8]) {
+  if (WIDE) {
+    store32(p, v);
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+template <int D, bool F32, bool WIDE>
 __global__ void __launch_bounds__(kThreads) blockkv_read_kernel(BrArgs a) {
-  constexpr int WORDS = D / 8;   // of a row
+  constexpr int BLOCKS = D / 16;   // of a row
   pdl_enter();
   const int item = blockIdx.x, ps = a.c.page_size, ps_log = 31 - __clz(ps);
   const int b = warp_find_request(a.cu, a.B, item, 1, kSlots, 2);
@@ -50,63 +68,85 @@ __global__ void __launch_bounds__(kThreads) blockkv_read_kernel(BrArgs a) {
     if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     return;
   }
-  const int cols = a.c.n_kv_heads * WORDS, n = tokens * cols;   // words of keys; as many of values
+  const int cols = a.c.n_kv_heads * BLOCKS, n = tokens * cols;   // blocks of keys; as many of values
   const int64_t row0 = r.row0 + (first - r.start), slot0 = first & (ps - 1);
-  auto copy = [&](const void* codes_at, const void* scales_at, float g, void* out, int64_t stride) {
-    const uint8_t* codes = static_cast<const uint8_t*>(codes_at) + pid * a.c.page_stride + slot0 * a.c.token_stride;
-    const uint8_t* scales =
-        static_cast<const uint8_t*>(scales_at) + pid * a.c.scale_page_stride + slot0 * a.c.scale_token_stride;
+  const int64_t codes0 = pid * a.c.page_stride + slot0 * a.c.token_stride;
+  const int64_t scales0 = pid * a.c.scale_page_stride + slot0 * a.c.scale_token_stride;
+  const int lo = a.k_out ? 0 : n, hi = a.v_out ? 2 * n : n;
 #pragma unroll 1
-    for (int i0 = threadIdx.x; i0 < n; i0 += kAtOnce * kThreads) {
-      uint32_t w[kAtOnce], sc[kAtOnce];
-      int64_t to[kAtOnce];
+  for (int i0 = lo + threadIdx.x; i0 < hi; i0 += kAtOnce * kThreads) {
+    uint2 w[kAtOnce];
+    uint32_t sc[kAtOnce];
+    int64_t to[kAtOnce];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int i = i0 + u * kThreads;
-        to[u] = -1;
-        if (i >= n) continue;
-        const int token = i / cols, col = i - token * cols, head = col / WORDS, word = col % WORDS;
-        w[u] = __ldg(reinterpret_cast<const uint32_t*>(codes + token * a.c.token_stride + head * a.c.head_stride + word * 4));
-        sc[u] = __ldg(scales + token * a.c.scale_token_stride + head * a.c.scale_head_stride + word / 2);
-        to[u] = (row0 + token) * stride + static_cast<int64_t>(col) * 8;
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kThreads;
+      to[u] = -1;
+      if (i >= hi) continue;
+      const bool value = i >= n;
+      const int j = value ? i - n : i;
+      const int token = __umulhi(j, a.per_row), col = j - token * cols, head = col / BLOCKS, block = col % BLOCKS;
+      const uint8_t* codes = static_cast<const uint8_t*>(value ? a.c.v : a.c.k) + codes0;
+      const uint8_t* scales = static_cast<const uint8_t*>(value ? a.c.v_scale : a.c.k_scale) + scales0;
+      w[u] = __ldg(reinterpret_cast<const uint2*>(codes + token * a.c.token_stride + head * a.c.head_stride + block * 8));
+      sc[u] = __ldg(scales + token * a.c.scale_token_stride + head * a.c.scale_head_stride + block);
+      to[u] = (row0 + token) * (value ? a.vs : a.ks) + static_cast<int64_t>(col) * 16;
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (to[u] < 0) continue;
+      const bool value = i0 + u * kThreads >= n;
+      void* out = value ? a.v_out : a.k_out;
+      const float f = e4m3_to_float(static_cast<uint8_t>(sc[u])) * (value ? a.c.v_gscale : a.c.k_gscale);
+      uint32_t x[8];
+      {
+        uint32_t y[4];
+        f16x2_of_e2m1(w[u].x, y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = y[e];
+        f16x2_of_e2m1(w[u].y, y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 + e] = y[e];
       }
+      if (F32) {
+        float* dst = static_cast<float*>(out) + to[u];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        if (to[u] < 0) continue;
-        uint32_t x[4];
-        f16x2_of_e2m1(w[u], x);
-        const float f = e4m3_to_float(static_cast<uint8_t>(sc[u])) * g;
-        float2 y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 h = halves(x[e]);
-          y[e] = make_float2(h.x * f, h.y * f);
-        }
-        if (F32) {
-          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + to[u]);
-          dst[0] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
-          dst[1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
-        } else {
-          uint32_t p[4];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 z = __floats2bfloat162_rn(y[e].x, y[e].y);
-            p[e] = *reinterpret_cast<const uint32_t*>(&z);
+            const float2 y = halves(x[4 * h + e]);
+            p[2 * e] = __float_as_uint(y.x * f);
+            p[2 * e + 1] = __float_as_uint(y.y * f);
           }
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to[u]) = make_uint4(p[0], p[1], p[2], p[3]);
+          put<WIDE>(dst + 8 * h, p);
         }
+      } else {
+        uint32_t p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 y = halves(x[e]);
+          const __nv_bfloat162 z = __floats2bfloat162_rn(y.x * f, y.y * f);
+          p[e] = *reinterpret_cast<const uint32_t*>(&z);
+        }
+        put<WIDE>(static_cast<uint16_t*>(out) + to[u], p);
       }
     }
-  };
-  if (a.k_out) copy(a.c.k, a.c.k_scale, a.c.k_gscale, a.k_out, a.ks);
-  if (a.v_out) copy(a.c.v, a.c.v_scale, a.c.v_gscale, a.v_out, a.vs);
+  }
 }
 
 template <int D>
-cudaError_t launch(const BrArgs& a, bool f32, cudaStream_t s) {
+cudaError_t launch(BrArgs a, bool f32, cudaStream_t s) {
+  const uint32_t cols = a.c.n_kv_heads * (D / 16);
+  a.per_row = static_cast<uint32_t>(((uint64_t(1) << 32) + cols - 1) / cols);   // exact below 16 cols
+  // 32-byte accesses need rows at 32 bytes
+  const int per32 = f32 ? 8 : 16;
+  const bool wide = (!a.k_out || (aligned_to(a.k_out, 32) && a.ks % per32 == 0)) &&
+                    (!a.v_out || (aligned_to(a.v_out, 32) && a.vs % per32 == 0));
   count_launches(1);
-  return launch_pdl(f32 ? blockkv_read_kernel<D, true> : blockkv_read_kernel<D, false>, a.T / kSlots + 2 * a.B, kThreads, 0,
-                    s, a);
+  auto go = [&](auto kernel) { return launch_pdl(kernel, a.T / kSlots + 2 * a.B, kThreads, 0, s, a); };
+  if (f32) return wide ? go(blockkv_read_kernel<D, true, true>) : go(blockkv_read_kernel<D, true, false>);
+  return wide ? go(blockkv_read_kernel<D, false, true>) : go(blockkv_read_kernel<D, false, false>);
 }
 
 }  // namespace

@@ -53,6 +53,7 @@ struct BlockPaArgs : PaArgs {
   static constexpr bool kBlocks = true;    // ... for a token, head and 16 elements
   const uint8_t* k_scales;
   const uint8_t* v_scales;
+  uint32_t page16, page_s;   // page strides in units of 16 bytes, and of D / 16
   int64_t scale_page, scale_head, scale_token;   // strides of the scales
   float kg, vg;                                  // factors of keys and values
 };
@@ -209,6 +210,17 @@ __device__ __forceinline__ uint32_t f16x2_of_scales(uint32_t two) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+// One half of two in both places (the multiplication takes it from where it is).
+__device__ __forceinline__ uint32_t low_twice(uint32_t x) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n mov.b32 %0, {l, l};\n}\n" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t high_twice(uint32_t x) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n mov.b32 %0, {h, h};\n}\n" : "=r"(r) : "r"(x));
   return r;
 }
 

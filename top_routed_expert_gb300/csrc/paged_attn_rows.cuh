@@ -1,7 +1,7 @@
-// Attention over the paged caches of 8 bits (include/paged_kv.h,
-// moe_paged_attention) and of 4 (include/block_kv.h, moe_blockkv_attention) for
-// few query rows per request and key head: the single-token form, small drafts,
-// and every shape that paged_attn_tc.cuh does not take.
+// What the attention kernels for few query rows share, over the paged caches of
+// 8 bits (paged_attn.cu) and of 4 (block_attn.cu): the cut of the work into
+// pieces, the list of the row blocks that go to paged_attn_tc.cuh, the join of
+// partial sums, the choice of kernels and the call.
 //
 // The rows of one (request, key head) are its new tokens times the query
 // heads of the group, row r = token r / group, head r % group; 8 or 16 rows make
@@ -11,45 +11,6 @@
 // of mixed lengths keeps every SM busy to the end.  A piece may end inside a
 // row tile; then all its CTAs leave partial sums and paged_attn_join adds them
 // in order (a fixed order: the same bits every time).
-//
-// A CTA has four warps; in a unit each has 16 tokens of its own, fetched by
-// cp.async into a ring that only this warp uses (no block barrier in the
-// loop).  Both products run on the tensor cores as m16n8k16 with f16 operands
-// and the rows as N, so that the eight heads of a group fill it:
-//   S^T = K Q^T (M = 16 tokens),  O^T = V^T P^T (M = 16 elements of the head)
-// The codes are the A operands, converted exactly to f16 in registers, straight
-// from the stored rows:
-//  - the order of the head's elements inside the first product's K is free if q
-//    uses the same: a lane takes 16 consecutive codes of a key and calls them
-//    its elements of four K steps;
-//  - so is the order of the elements in the second product's M: a lane takes 16
-//    consecutive codes of four tokens, and one byte permutation pairs two
-//    tokens' codes for the conversion;
-//  - the weights become the second product's B operand by a transposition of
-//    8x8 blocks between the lanes.
-// Sums and references are kept per warp and joined at the end.  Page scales: a
-// key's scale multiplies its score; a value's scale goes into the exponent of
-// its weight, and the weights' sum takes it out again.  A row's weights are
-// relative to 2^-8 of the maximum of the first tile that it sees something in
-// (kRefBelow); that reference moves only when weights outgrow f16 (65504), so the
-// ordinary tile takes no maximum and rescales nothing.
-//
-// What each row computes, with p its position and w the window:
-//   z_j = sm_scale q . (k_scale_j k_j),  j <= p and (j > p - w or j < n_sink)
-//   out = sum 2^(z_j log2 e - m) v_scale_j v_j / sum 2^(z_j log2 e - m)
-// The weights are rounded to f16 for the second product (2^-11, under the
-// output's bf16 rounding, 2^-9; weights under 2^-22 of the largest by up to 2^-33 of
-// it); scores, sums, references and outputs are fp32.
-//
-// Measured (key heads x query heads of a group x D): 12 requests at 49157 to 65536
-// tokens, 4 x 8 x 128, 705 MB in 114 us = 6.2 TB/s, bound by memory; 64 at 17
-// to 3712, 123 MB in 32.4 us = 3.8 TB/s, of which the join and the two launches
-// are 7; one at 3585 13 us, two launches and eight dependent loads; 48 drafts of
-// up to 4 tokens in a window of 1024, 8 x 4 x 64, 49 MB in 29 us, bound by the
-// issue of instructions (conversion and weights) and the row tiles' starts; 64 at
-// 3584, 4 x 8 x 256, 470 MB in 93 us = 5.0 TB/s.
-// Registers spilled (bytes stored, D / blocks of rows): 64/1 60, 64/2 48, 128/2 92,
-// 256/1 76, outside the loop over the units; 128/1 none.
 #pragma once
 
 #include <climits>
@@ -67,22 +28,22 @@ cudaError_t launch_paged_attn_tc(const BlockPaArgs& a, cudaStream_t s);
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kUnit = 64;        // tokens of a unit
-// What a row tile costs beside its units (finding it, q, the join of the
-// warps), in units.
-constexpr int kTileCost = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// D: elements of a head, NB: blocks of eight rows in a row tile.
+// D: elements of a head, NB: blocks of eight rows in a row tile.  A stage of a
+// warp's ring holds one tile of 16 tokens, with codes of four bits (BLOCKS) two.
 template <int D, int NB, bool BLOCKS> struct Shape {
   static constexpr int kRows = 8 * NB;
+  static constexpr int kUnit = BLOCKS ? 128 : 64;         // tokens of a unit, in equal parts for the four warps
+  // What a row tile costs beside its units (finding it, q, the join of the
+  // warps), in units.
+  static constexpr int kTileCost = BLOCKS ? 3 : 4;
   static constexpr int kTile = BLOCKS ? 8 * D : 16 * D;   // bytes of 16 tokens' keys (or values)
-  static constexpr int kScales = BLOCKS ? D : 0;          // ... and of their scales
-  static constexpr int kStage = 2 * (kTile + kScales);    // keys, values, keys' scales, values' scales
+  static constexpr int kStage = BLOCKS ? 4 * kTile + 4 * D : 2 * kTile;
   // CTAs on an SM, by registers (O takes D NB / 4 of a thread's, q D NB / 8),
   // and the stages of the ring that fit then
   static constexpr int kCtas = D * NB == 64 ? 5 : D * NB == 128 ? 4 : D * NB == 256 ? 3 : 2;
-  static constexpr int kStages = BLOCKS ? (D == 256 ? 3 : 4) : D == 256 ? 2 : D * NB == 128 && D == 128 ? 3 : 4;
+  static constexpr int kStages = BLOCKS ? 2 : D == 256 ? 2 : D * NB == 128 && D == 128 ? 3 : 4;
   static constexpr int kRing = kStages * kStage;        // per warp
   static constexpr int kPart = kRows * D + 2 * kRows;   // floats of a partial: outputs, references, sums
   static_assert(kRing >= kRows * D * 4, "a warp's outputs are joined in its ring");
@@ -128,17 +89,6 @@ template <int N> __device__ __forceinline__ void cp_or_zero(uint32_t dst, const 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Two E4M3 codes (the low 16 bits) -> two f16, exact.
-__device__ __forceinline__ uint32_t f16x2_of(uint32_t two) {
-  uint32_t r;
-  asm("{\n .reg .b16 t, u;\n mov.b32 {t, u}, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(r) : "r"(two));
-  return r;
-}
-__device__ __forceinline__ uint32_t f16x2_of_hi(uint32_t two) {
-  uint32_t r;
-  asm("{\n .reg .b16 t, u;\n mov.b32 {t, u}, %1;\n cvt.rn.f16x2.e4m3x2 %0, u;\n}\n" : "=r"(r) : "r"(two));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -161,26 +111,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-// Where a 16-byte chunk of token `row` lies in a tile: no bank conflicts for
-// the copies (whole rows), the key reads (two neighbouring rows, 64 bytes of
-// each) and the value reads (four rows two apart, one or two chunks of each).
-// With codes of four bits a row is half as long, key reads take 32 bytes of four
-// neighbouring rows at a time and value reads 32 (D = 64: eight rows, 32-bit
-// words) of rows 0, 2, 4, 6 or 1, 3, 5, 7: bits 0 + 2 and 1 of the row's number
-// tell the rows of either apart.
-template <int D, bool BLOCKS> __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
-  if (BLOCKS) {
-    if (D == 64) return (row ^ (row >> 2 & 1)) * 32 + (chunk << 4);
-    if (D == 128) return (row ^ (row >> 2 & 1)) * 64 + ((chunk ^ (row & 2)) << 4);
-    return row * 128 + ((chunk ^ (((row ^ row >> 2) & 1) << 2) ^ (row & 2)) << 4);
-  }
-  if (D == 64) {
-    const int slot = (row & ~1) | ((row ^ (row >> 1)) & 1);
-    return slot * 64 + ((chunk ^ (((row >> 2) & 1) << 1)) << 4);
-  }
-  return row * D + ((chunk ^ (((row >> 1) & 3) << 1) ^ ((row & 1) << 2)) << 4);
 }
 
 // Lists the row blocks of the requests that go to paged_attn_tc.cuh, the longest
@@ -304,436 +234,6 @@ __global__ void __launch_bounds__(512) list_kernel(PaArgs a) {
   extern __shared__ __align__(128) char smem[];
   pdl_enter();
   list_tc_items(a, reinterpret_cast<int*>(smem + 2048), smem);
-}
-
-template <int D, int NB, class Args>
-__global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, Args::kBlocks>::kCtas) paged_attn_kernel(Args a) {
-  constexpr bool BLOCKS = Args::kBlocks;
-  using S = Shape<D, NB, BLOCKS>;
-  constexpr int KC = D / 64;      // 64-element chunks of a head
-  constexpr int MT = D / 16;      // 16-element tiles of the output
-  constexpr int kStages = S::kStages, kRows = S::kRows;
-  extern __shared__ __align__(128) char smem[];
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-  __shared__ float s_scale[kWarps][kStages][4];
-  int64_t* s_start = reinterpret_cast<int64_t*>(smem + kWarps * S::kRing);
-  pdl_enter();
-  // the last CTA has the least to do here, often nothing
-  if (a.tc_rows < INT_MAX && blockIdx.x == gridDim.x - 1) list_tc_items(a, reinterpret_cast<int*>(s_start), smem);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  build_unit_table<kRows, kUnit, kTileCost>(a, s_start, blockIdx.x == 0 ? a.status : nullptr);
-  const int64_t total = s_start[a.B];
-  const int64_t piece = piece_of(total, gridDim.x);
-  const int64_t first = piece * blockIdx.x, last = min(total, first + piece);
-  const uint32_t ring = ptx::smem_u32(smem) + warp * S::kRing;
-  const int ps = a.c.page_size, ps_log = 31 - __clz(ps);
-  const int64_t ts = a.c.token_stride;
-  // this lane's 16-byte chunks of a tile: token (+ RSTEP each) and chunk
-  constexpr int CPR = BLOCKS ? D / 32 : D / 16, RSTEP = 32 / CPR, COPIES = 16 / RSTEP;
-  const int crow = lane / CPR, cchunk = lane % CPR;
-  const int64_t lane_off = crow * ts + cchunk * 16;
-  JoinTile cut = {};   // the row tile that this CTA begins and others go on with
-
-  int b = -1;
-  Request rq = {};
-  for (int64_t at = first; at < last;) {
-    // the row tile at `at`, and the piece of it that is this CTA's
-    const int b_now = find_entry(s_start, a.B, at);
-    if (b_now != b) {
-      b = b_now;
-      rq = load_request(a.cu, a.kv_len, b, a.T);
-    }
-    const Span sp = span_of(a, rq, kUnit);
-    const int64_t in_b = at - s_start[b];
-    const int width = sp.units + kTileCost;
-    int tile;   // (key head, row tile)
-    if (in_b <= 0x7fffffff) tile = static_cast<int>(in_b) / width;
-    else tile = static_cast<int>(in_b / width);
-    const int v0 = static_cast<int>(in_b - static_cast<int64_t>(tile) * width);
-    const int v1 = static_cast<int>(min(static_cast<int64_t>(width), v0 + (last - at)));
-    const int u0 = max(v0 - kTileCost, 0), u1 = v1 - kTileCost;
-    const int64_t tile_end = at + (width - v0);
-    const int slot = at == first ? 0 : 1;
-    at += v1 - v0;
-    if (u1 <= u0) continue;   // the next CTA begins it
-    const int rts = ceil_div(rq.n * a.group, kRows);
-    const int kvh = tile / rts, row0 = (tile - kvh * rts) * kRows;
-    const int rows = min(kRows, rq.n * a.group - row0);
-    const bool whole = u0 == 0 && u1 == sp.units;
-    if (u0 == 0 && !whole) cut = JoinTile{rows, rq.row0, row0, kvh, slot, static_cast<int>((tile_end - 1) / piece)};
-
-    // q of this lane's row g of each block, on its way while the rest starts
-    uint4 raw[NB][KC][2];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int r = row0 + 8 * n + g;
-      const bool live = 8 * n + g < rows;
-      const uint16_t* src = a.q + static_cast<int64_t>(rq.row0 + (live ? r / a.group : 0)) * a.qs +
-                            static_cast<int64_t>(kvh * a.group + (live ? r % a.group : 0)) * D + t * 16;
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          raw[n][c][i] = live ? __ldg(reinterpret_cast<const uint4*>(src + c * 64 + i * 8)) : make_uint4(0, 0, 0, 0);
-    }
-
-    const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + kvh * a.c.head_stride;
-    const int64_t v_minus_k = static_cast<const uint8_t*>(a.c.v) - static_cast<const uint8_t*>(a.c.k);
-    const int32_t* table = a.c.page_table + static_cast<int64_t>(b) * a.c.max_pages;
-    auto tile_base = [&](int u) { return sp.block_of(u) * kUnit + warp * 16; };
-    // Page ids are asked for a tile ahead of the copies and looked at there.  A
-    // table may hold kNothing's value too: then the tile tells which it is.
-    constexpr int kNothing = INT_MIN;
-    auto needed = [&](int u) {
-      const int j = tile_base(u);
-      return u < u1 && sp.any_seen(j, j + 15);
-    };
-    auto page_id = [&](int u) -> int { return needed(u) ? __ldg(table + (tile_base(u) >> ps_log)) : kNothing; };
-    auto issue = [&](int u, int pid, int stage) {
-      float* sc = s_scale[warp][stage];
-      if (pid == kNothing) {
-        if (lane == 0 && needed(u)) {
-          sc[2] = 0.f;
-          set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-        }
-        return;
-      }
-      const int j0 = tile_base(u);
-      const bool ok = static_cast<unsigned>(pid) < static_cast<unsigned>(a.c.n_pages);
-      if (lane == 0) sc[2] = ok ? 1.f : 0.f;
-      if (!ok) {
-        if (lane == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-        return;
-      }
-      if (!BLOCKS && lane < 2)
-        cp4(ptx::smem_u32(sc + lane), (lane ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(pid) * a.c.n_kv_heads + kvh);
-      const uint8_t* src = kbase + (pid * a.c.page_stride + (j0 & (ps - 1)) * ts + lane_off);
-      const uint32_t kd = ring + stage * S::kStage, vd = kd + S::kTile;
-      if constexpr (BLOCKS) {   // a token's scales: the keys' in lanes 0 to 15, the values' in 16 to 31
-        const int token = j0 + (lane & 15);
-        const int64_t off = kvh * a.scale_head + pid * a.scale_page + (token & (ps - 1)) * a.scale_token;
-        const uint8_t* from = lane < 16 ? a.k_scales : a.v_scales;
-        const bool seen = sp.seen(token);
-        cp_or_zero<D / 16>(kd + 2 * S::kTile + lane * (D / 16), seen ? from + off : from, seen);
-      }
-      if (sp.all_seen(j0, j0 + 15)) {
-#pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-          const uint32_t d = chunk_at<D, BLOCKS>(i * RSTEP + crow, cchunk);
-          cp16(kd + d, src);
-          cp16(vd + d, src + v_minus_k);
-          src += RSTEP * ts;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-          const uint32_t d = chunk_at<D, BLOCKS>(i * RSTEP + crow, cchunk);
-          const bool seen = sp.seen(j0 + i * RSTEP + crow);
-          cp16_or_zero(kd + d, seen ? src : kbase, seen);
-          cp16_or_zero(vd + d, seen ? src + v_minus_k : kbase, seen);
-          src += RSTEP * ts;
-        }
-      }
-    };
-
-    int pid = page_id(u0);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      const int next = page_id(u0 + i + 1);
-      issue(u0 + i, pid, i);
-      cp_commit();
-      pid = next;
-    }
-
-    // q as f16, each head scaled by a power of two; the lane's score columns are
-    // rows 2t and 2t+1 of each block
-    uint32_t qf[NB][KC][4][2];
-    float rf[NB][2], m[NB][2], l[NB][2];
-    int pos[NB][2];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      uint32_t top = 0;   // the largest size as bits: a NaN's are above infinity's
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 w = raw[n][c][i];
-          top = __vmaxu2(top, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
-          top = __vmaxu2(top, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-        }
-      top = max(top & 0xffffu, top >> 16);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float f = q_factor(__uint_as_float(top << 16), top < 0x7f80u);
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t w[4] = {raw[n][c][i].x, raw[n][c][i].y, raw[n][c][i].z, raw[n][c][i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            qf[n][c][2 * i + (e >> 1)][e & 1] =
-                pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
-        }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 8 * n + 2 * t + h;
-        rf[n][h] = a.sm_scale * kLog2e / __shfl_sync(0xffffffffu, f, (2 * t + h) * 4);
-        if constexpr (BLOCKS) rf[n][h] *= a.kg;
-        pos[n][h] = r < rows ? rq.start + (row0 + r) / a.group : -1;
-        // a row that sees nothing at all needs no reference
-        m[n][h] = pos[n][h] >= 0 ? -INFINITY : 0.f;
-        l[n][h] = 0.f;
-      }
-    }
-    const int pos_min = rq.start + row0 / a.group, pos_max = rq.start + (row0 + rows - 1) / a.group;
-
-    float o[NB][MT][4];
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
-
-#pragma unroll 1
-    for (int u = u0, stage = 0; u < u1; ++u, stage = stage + 1 == kStages ? 0 : stage + 1) {
-      cp_wait<kStages - 2>();
-      __syncwarp();
-      const int j0 = tile_base(u);
-      const float* sc = s_scale[warp][stage];
-      if (sp.any_seen(j0, j0 + 15) && sc[2] != 0.f) {
-        const uint32_t kd = ring + stage * S::kStage, vd = kd + S::kTile;
-        // scores: tokens g and g+8 (e >> 1) by rows 2t and 2t+1 (e & 1)
-        float s[NB][4] = {};
-        if constexpr (BLOCKS) {
-          // a lane's 16 codes of a key have one scale
-          const uint32_t ksc = vd + S::kTile + g * (D / 16) + t;
-#pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const int ch = 2 * c + (t >> 1), in = (t & 1) * 8;
-            const uint2 klo = lds64(kd + chunk_at<D, true>(g, ch) + in), khi = lds64(kd + chunk_at<D, true>(g + 8, ch) + in);
-            const uint32_t both = f16x2_of_scales(lds8(ksc + 4 * c) | lds8(ksc + D / 2 + 4 * c) << 8);
-            const uint32_t slo = __byte_perm(both, both, 0x1010), shi = __byte_perm(both, both, 0x3232);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              uint32_t lo[4], hi[4];
-              f16x2_of_e2m1(w ? klo.y : klo.x, lo);
-              f16x2_of_e2m1(w ? khi.y : khi.x, hi);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t ka[4] = {mul_f16x2(lo[2 * e], slo), mul_f16x2(hi[2 * e], shi), mul_f16x2(lo[2 * e + 1], slo),
-                                        mul_f16x2(hi[2 * e + 1], shi)};
-#pragma unroll
-                for (int n = 0; n < NB; ++n) mma16816(s[n], ka, qf[n][c][2 * w + e][0], qf[n][c][2 * w + e][1]);
-              }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const uint4 klo = lds128(kd + chunk_at<D, false>(g, 4 * c + t)), khi = lds128(kd + chunk_at<D, false>(g + 8, 4 * c + t));
-            const uint32_t lo[4] = {klo.x, klo.y, klo.z, klo.w}, hi[4] = {khi.x, khi.y, khi.z, khi.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t ka[4] = {f16x2_of(lo[e]), f16x2_of(hi[e]), f16x2_of_hi(lo[e]), f16x2_of_hi(hi[e])};
-#pragma unroll
-              for (int n = 0; n < NB; ++n) mma16816(s[n], ka, qf[n][c][e][0], qf[n][c][e][1]);
-            }
-          }
-        }
-        // (a block's scales are in its values already)
-        const float ks = BLOCKS ? 1.f : sc[0], lvs = BLOCKS ? 0.f : __log2f(sc[1]), ivs = BLOCKS ? 1.f : __frcp_rn(sc[1]);
-        if (!sp.all_see(j0, j0 + 15, pos_min, pos_max)) {
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!sp.sees(pos[n][e & 1], j0 + g + 8 * (e >> 1))) s[n][e] = -INFINITY;
-        }
-        // weights relative to the reference so far
-        float w[NB][4];
-        bool move = false;
-        auto weigh = [&](int n, int h) {
-          const float f = score_factor(ks, rf[n][h]), shift = lvs - (m[n][h] == -INFINITY ? 0.f : m[n][h]);
-          w[n][h] = ex2(fmaf(s[n][h], f, shift));
-          w[n][2 + h] = ex2(fmaf(s[n][2 + h], f, shift));
-          return m[n][h] == -INFINITY || w[n][h] + w[n][2 + h] > kMostSum;
-        };
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) move |= weigh(n, h);
-        if (__any_sync(0xffffffffu, move)) {
-          // rows whose weights are too large for f16, or that have no reference
-          // yet, take their maximum
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const unsigned of_row = __ballot_sync(0xffffffffu, weigh(n, h)) & (0x11111111u << t);
-              float top = fmaf(fmaxf(s[n][h], s[n][2 + h]), score_factor(ks, rf[n][h]), lvs);
-#pragma unroll
-              for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-              if (of_row) {
-                const float to = fmaxf(m[n][h], top - kRefBelow), f = m[n][h] == -INFINITY ? 0.f : ex2(m[n][h] - to);
-                m[n][h] = to;
-                l[n][h] *= f;
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                  o[n][i][h] *= f;
-                  o[n][i][2 + h] *= f;
-                }
-                weigh(n, h);
-              }
-            }
-        }
-        uint32_t p[NB][2];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) l[n][h] = fmaf(w[n][h] + w[n][2 + h], ivs, l[n][h]);
-          p[n][0] = transpose8x8(pack_f16(w[n][0], w[n][1]));
-          p[n][1] = transpose8x8(pack_f16(w[n][2], w[n][3]));
-        }
-        if constexpr (BLOCKS) {
-          // values: the lane's run of codes, 16 (D = 64: 8) of one block, of tokens
-          // 2t, 2t+1 | 2t+8, 2t+9
-          constexpr int RW = D >= 128 ? 2 : 1;   // words of the run
-          const uint32_t vsc = vd + S::kTile + D + (D >= 128 ? g : g >> 1);
-#pragma unroll
-          for (int c = 0; c < (D + 127) / 128; ++c) {
-            uint32_t vw[4][RW], scale[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-              if constexpr (D == 64) {
-                vw[i][0] = lds32(vd + chunk_at<D, true>(row, g >> 2) + (g & 3) * 4);
-              } else {
-                const uint2 x = lds64(vd + chunk_at<D, true>(row, 4 * c + (g >> 1)) + (g & 1) * 8);
-                vw[i][0] = x.x;
-                vw[i][RW - 1] = x.y;
-              }
-              scale[i] = lds8(vsc + row * (D / 16) + 8 * c);
-            }
-            const uint32_t sa = f16x2_of_scales(scale[0] | scale[1] << 8), sb = f16x2_of_scales(scale[2] | scale[3] << 8);
-#pragma unroll
-            for (int w = 0; w < RW; ++w) {
-              uint32_t ae[4], ao[4], be[4], bo[4];   // elements 0, 2, 4, 6 and 1, 3, 5, 7 of tokens 2t, 2t+1 and 2t+8, 2t+9
-              f16x2_of_e2m1(even_codes(vw[0][w], vw[1][w]), ae);
-              f16x2_of_e2m1(odd_codes(vw[0][w], vw[1][w]), ao);
-              f16x2_of_e2m1(even_codes(vw[2][w], vw[3][w]), be);
-              f16x2_of_e2m1(odd_codes(vw[2][w], vw[3][w]), bo);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t va[4] = {mul_f16x2(ae[e], sa), mul_f16x2(ao[e], sa), mul_f16x2(be[e], sb), mul_f16x2(bo[e], sb)};
-#pragma unroll
-                for (int n = 0; n < NB; ++n) mma16816(o[n][c * 8 + 4 * w + e], va, p[n][0], p[n][1]);
-              }
-            }
-          }
-        } else {
-          // values: words of tokens 2t, 2t+1 | 2t+8, 2t+9
-          constexpr int VW = D >= 128 ? 4 : 2;     // words of a lane's run of codes
-#pragma unroll
-          for (int c = 0; c < (D + 127) / 128; ++c) {
-            uint32_t vw[4][VW];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-              if (D == 64) {
-                const uint2 x = lds64(vd + chunk_at<D, false>(row, g >> 1) + (g & 1) * 8);
-                vw[i][0] = x.x;
-                vw[i][1] = x.y;
-              } else {
-                const uint4 x = lds128(vd + chunk_at<D, false>(row, 8 * c + g));
-                vw[i][0] = x.x;
-                vw[i][1] = x.y;
-                vw[i][VW - 2] = x.z;
-                vw[i][VW - 1] = x.w;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < VW; ++i) {
-              const uint32_t a01 = __byte_perm(vw[0][i], vw[1][i], 0x5140), a23 = __byte_perm(vw[0][i], vw[1][i], 0x7362);
-              const uint32_t b01 = __byte_perm(vw[2][i], vw[3][i], 0x5140), b23 = __byte_perm(vw[2][i], vw[3][i], 0x7362);
-              const uint32_t lo[4] = {f16x2_of(a01), f16x2_of_hi(a01), f16x2_of(b01), f16x2_of_hi(b01)};
-              const uint32_t hi[4] = {f16x2_of(a23), f16x2_of_hi(a23), f16x2_of(b23), f16x2_of_hi(b23)};
-#pragma unroll
-              for (int n = 0; n < NB; ++n) {
-                mma16816(o[n][c * 8 + 2 * i], lo, p[n][0], p[n][1]);
-                mma16816(o[n][c * 8 + 2 * i + 1], hi, p[n][0], p[n][1]);
-              }
-            }
-          }
-        }
-      }
-      __syncwarp();
-      const int next = page_id(u + kStages);
-      issue(u + kStages - 1, pid, stage == 0 ? kStages - 1 : stage - 1);
-      cp_commit();
-      pid = next;
-    }
-    cp_wait<0>();
-    __syncthreads();   // every warp is done with its ring
-
-    // join the four warps' sums
-    float* mine = reinterpret_cast<float*>(smem) + warp * (S::kRing / 4);
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 8 * n + 2 * t + h;
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], off);
-        if (g == 0) {
-          s_m[warp][r] = m[n][h];
-          s_l[warp][r] = l[n][h];
-        }
-        // the lane's columns: tiles 2i and 2i+1 of a 128-element chunk have
-        // elements 4i, 4i+1 and 4i+2, 4i+3 of its run of codes
-        constexpr int RUN = D >= 128 ? 16 : 8;
-#pragma unroll
-        for (int i = 0; i < MT / 2; ++i) {
-          const int col = D == 64 ? RUN * g + 4 * i : i / 4 * 128 + RUN * g + i % 4 * 4;
-          *reinterpret_cast<float4*>(mine + r * D + (col ^ ((r & 7) << 2))) =
-              make_float4(o[n][2 * i][h], o[n][2 * i][2 + h], o[n][2 * i + 1][h], o[n][2 * i + 1][2 + h]);
-        }
-      }
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4;
-      float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2_from(s_m[w][r], mm);
-        sum += s_l[w][r] * f;
-        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + w * (S::kRing / 4) + r * D +
-                                                          (d ^ ((r & 7) << 2)));
-        acc.x += x.x * f;
-        acc.y += x.y * f;
-        acc.z += x.z * f;
-        acc.w += x.w * f;
-      }
-      if (whole) {
-        const int tok = (row0 + r) / a.group, head = kvh * a.group + (row0 + r) % a.group;
-        store_row4(a, rq.row0 + tok, head, D, d, acc, mm, sum);
-      } else {
-        float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::kPart;
-        *reinterpret_cast<float4*>(part + r * D + d) = acc;
-        if (d == 0) {
-          part[kRows * D + r] = mm;
-          part[kRows * D + kRows + r] = sum;
-        }
-      }
-    }
-    __syncthreads();   // the ring is free again
-  }
-  if (threadIdx.x == 0) a.joins[blockIdx.x] = cut;
 }
 
 // Joins the partial sums of the row tiles that more than one CTA worked on.  The
@@ -889,11 +389,12 @@ template <int D, int NB, bool BLOCKS> int ctas_for(int num_sms) {
   return std::min(num_sms, kMaxSms) * Shape<D, NB, BLOCKS>::kCtas;
 }
 
-template <int D, int NB, class Args>
+// Kernels: a type whose of<D, NB>() is the few-row kernel.
+template <int D, int NB, class Kernels, class Args>
 cudaError_t launch(const Args& a, int num_sms, cudaStream_t s) {
   using S = Shape<D, NB, Args::kBlocks>;
   const size_t smem = kWarps * S::kRing + sizeof(int64_t) * (a.B + 1);
-  const auto kernel = paged_attn_kernel<D, NB, Args>;
+  const auto kernel = Kernels::template of<D, NB>();
   cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   const int ctas = ctas_for<D, NB, Args::kBlocks>(num_sms);
@@ -908,10 +409,10 @@ cudaError_t launch(const Args& a, int num_sms, cudaStream_t s) {
 // warps (eight rows, tiles of eight / sixteen: 64 requests at 17 to 3712 tokens
 // 33 / 41 us, 12 at about 57000 115 / 150 us).  With more rows, tiles of sixteen
 // convert the codes half as often (64 requests of 32 rows at 3584 117 / 92 us).
-template <int D, class Args>
+template <int D, class Kernels, class Args>
 cudaError_t launch(const Args& a, int64_t most_rows, int num_sms, cudaStream_t s) {
-  if (D == 256 || most_rows <= 8) return launch<D, 1>(a, num_sms, s);
-  return launch<D == 256 ? 128 : D, 2>(a, num_sms, s);
+  if (D == 256 || most_rows <= 8) return launch<D, 1, Kernels>(a, num_sms, s);
+  return launch<D == 256 ? 128 : D, 2, Kernels>(a, num_sms, s);
 }
 
 template <int D, int NB, bool BLOCKS> size_t part_bytes() {
@@ -936,7 +437,7 @@ struct Path {
 // The few-row kernel reads a request's tokens once for every 16 rows (8 where D =
 // 256), the tcgen05 kernel once for 256, but takes longer to start and to join: with heads of 128
 // about 13 us + 3.1 us for a million pairs of a row and a token (a row tile's
-// start counting as kTileCost units of tokens) against 29 us + 0.6 us.
+// start counting as kTileTokens tokens) against 29 us + 0.6 us.
 // Measured (us, few-row / tcgen05): one request of 1024 rows (of all key heads)
 // at 3584 tokens 25 / 33, at 8192 40 / 37, at 16384 65 / 44, at 65536 221 / 67; of
 // 512 rows at 8192 27 / 34, at 65536 118 / 63; of 256 rows at 65536 66 / 63; 2048 rows
@@ -968,6 +469,7 @@ struct Path {
 // allowed up to 4 kMaxSms of them.  The device then cuts what is longer than 1.5
 // shares (2 instead of 1.5: the same times to 1 us, with 8 x 512 at 3584, 4 x 1024 at
 // 32768, 2 x 2048 at 4096 to 65536, 3 x 512 at 2048 to 16384).
+constexpr int kTileTokens = 256;
 constexpr int kTcRows = 48;                  // of a request and key head
 constexpr int kTcTokens = 16384;
 constexpr int64_t kTcWork = int64_t(6) << 20;   // pairs
@@ -977,7 +479,7 @@ Path path_of(const PaArgs& a, int max_q_len) {
   Path p;
   const int64_t rows = static_cast<int64_t>(a.T) * a.group * a.c.n_kv_heads;
   const int64_t tokens = std::min<int64_t>(static_cast<int64_t>(a.c.max_pages) * a.c.page_size, kTcTokens);
-  p.tc = most > kTcRows && rows * (tokens + kTileCost * kUnit) >= kTcWork && paged_attn_tc_supported(a.c.head_dim);
+  p.tc = most > kTcRows && rows * (tokens + kTileTokens) >= kTcWork && paged_attn_tc_supported(a.c.head_dim);
   // As many rows as if every request had max_q_len of them: they all do (or the
   // hint is wrong, and the tcgen05 kernel takes small ones too).
   p.alone = p.tc && static_cast<int64_t>(max_q_len) * a.B == a.T;
@@ -985,7 +487,7 @@ Path path_of(const PaArgs& a, int max_q_len) {
   return p;
 }
 
-template <class Args>
+template <class Kernels, class Args>
 cudaError_t launch_paged_attn(Args a, int max_q_len, int num_sms, cudaStream_t s) {
   const Path path = path_of(a, max_q_len);
   const int64_t most = static_cast<int64_t>(max_q_len > 0 ? std::min(max_q_len, a.T) : a.T) * a.group;
@@ -998,9 +500,9 @@ cudaError_t launch_paged_attn(Args a, int max_q_len, int num_sms, cudaStream_t s
     err = launch_pdl(list_kernel, 1, 512, 2048 + sizeof(int) * (a.B + 1), s, static_cast<const PaArgs&>(a));
   } else {
     switch (a.c.head_dim) {
-      case 64: err = launch<64, Args>(a, std::min<int64_t>(most, a.tc_rows), num_sms, s); break;
-      case 128: err = launch<128, Args>(a, std::min<int64_t>(most, a.tc_rows), num_sms, s); break;
-      default: err = launch<256, Args>(a, most, num_sms, s); break;
+      case 64: err = launch<64, Kernels>(a, std::min<int64_t>(most, a.tc_rows), num_sms, s); break;
+      case 128: err = launch<128, Kernels>(a, std::min<int64_t>(most, a.tc_rows), num_sms, s); break;
+      default: err = launch<256, Kernels>(a, most, num_sms, s); break;
     }
   }
   return err == cudaSuccess && path.tc ? launch_paged_attn_tc(a, s) : err;
@@ -1053,7 +555,7 @@ size_t attention_ws_bytes(Args a, const moe_paged_attention_config_t* cfg) {
 
 // The call, the configuration and the cache's pointers having been looked at;
 // `a` comes with the cache.
-template <class Args>
+template <class Kernels, class Args>
 moe_status_t attention_call(Args a, const moe_paged_attention_config_t* cfg, const void* q, const int32_t* cu,
                             const int32_t* kv_len, void* out, float* lse, void* ws, size_t ws_bytes, moe_stream_t stream) {
   if (!q || !cu || !kv_len || !out) return MOE_ERR_INVALID_ARG;
@@ -1088,7 +590,7 @@ moe_status_t attention_call(Args a, const moe_paged_attention_config_t* cfg, con
   a.tc_entries = reinterpret_cast<TcEntry*>(base + w.tc_entries);
   a.tc_joins = reinterpret_cast<TcJoin*>(base + w.tc_joins);
   a.tc_part = reinterpret_cast<float*>(base + w.tc_part);
-  return launch_paged_attn(a, cfg->max_q_len, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_paged_attn<Kernels>(a, cfg->max_q_len, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace

@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
             const uint32_t w[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t f = e < 2 ? __byte_perm(both, both, 0x1010) : __byte_perm(both, both, 0x3232);
+              const uint32_t f = e < 2 ? low_twice(both) : high_twice(both);
               uint32_t x[4];
               f16x2_of_e2m1(w[e], x);
               sts128(base + sw128(row, (kc & 1) * 4 + e), mul_f16x2(x[0], f), mul_f16x2(x[1], f), mul_f16x2(x[2], f),
