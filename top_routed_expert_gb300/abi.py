@@ -112,6 +112,8 @@ class moe_add_norm_config_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "x_dtype", "res_dtype", "out_dtype", "group")]
     _fields_ += [("eps", ctypes.c_float)]
     _fields_ += [(n, ctypes.c_int64) for n in ("x_stride", "res_stride", "sum_stride", "out_stride")]
+    # of make_add_rms_norm_config's tensors: type and strides of x, residual, out and sum
+    rows = None
 
 
 class moe_weights_t(ctypes.Structure):
@@ -360,40 +362,44 @@ def make_kv_append_config(q, k, v, q_out, batch, rot_dim=0, n_pos=0, rope_layout
     return c
 
 
-def _append(call, where, cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream):
-    dev = _current_device()
-    if not (dev == k.get_device() == v.get_device() == cu.get_device() == kv_len.get_device()
-            and (q is None or q.get_device() == q_out.get_device() == dev)
-            and (gamma_q is None or gamma_q.get_device() == dev) and (gamma_k is None or gamma_k.get_device() == dev)
-            and (cos_sin is None or cos_sin.get_device() == dev) and (positions is None or positions.get_device() == dev)
-            and (cache.device is None or cache.device == dev)):
-        raise ValueError(_ELSEWHERE)
-    B = cfg.batch
-    if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
-        raise ValueError(_RAGGED)
-    T = cfg.T
-    if not (k.nbytes >= T * cfg.k_row <= v.nbytes and (cfg.heads == cache.heads or cfg.heads is None or cache.heads is None)
-            and (q is None or q.nbytes >= T * cfg.q_row <= q_out.nbytes)):
-        raise ValueError("q, k, v and q_out: rows of the configuration's shape and the cache's heads")
-    if not ((gamma_k is None or gamma_k.dtype is _F32 and gamma_k.numel() >= cache.head_dim)
-            and (gamma_q is None or gamma_q.dtype is _F32 and gamma_q.numel() >= cache.head_dim)
-            and (cos_sin is None or cos_sin.dtype is _F32 and cos_sin.numel() >= cfg.n_pos * cfg.rot_dim)
-            and (positions is None or positions.dtype is _I32 and positions.numel() >= T)):
-        raise ValueError("gamma_q, gamma_k: float32 [D], cos_sin: float32 [n_pos, rot_dim / 2, 2], positions: int32 [T]")
-    code = call(
-        cfg, cache, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        None if gamma_q is None else gamma_q.data_ptr(), None if gamma_k is None else gamma_k.data_ptr(),
-        None if cos_sin is None else cos_sin.data_ptr(), None if positions is None else positions.data_ptr(),
-        cu.data_ptr(), kv_len.data_ptr(), None if q is None else q_out.data_ptr(),
-        _current_stream(dev) if stream is None else _stream_of(stream, dev))
-    if code:
-        raise MoEError(code, where)
+def _appending(where: str, doc: str):
+    """An append's call, to either cache."""
+    def call(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream=None):
+        dev = _current_device()
+        if not (dev == k.get_device() == v.get_device() == cu.get_device() == kv_len.get_device()
+                and (q is None or q.get_device() == q_out.get_device() == dev)
+                and (gamma_q is None or gamma_q.get_device() == dev) and (gamma_k is None or gamma_k.get_device() == dev)
+                and (cos_sin is None or cos_sin.get_device() == dev) and (positions is None or positions.get_device() == dev)
+                and (cache.device is None or cache.device == dev)):
+            raise ValueError(_ELSEWHERE)
+        B = cfg.batch
+        if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
+            raise ValueError(_RAGGED)
+        T = cfg.T
+        if not (k.nbytes >= T * cfg.k_row <= v.nbytes and (cfg.heads == cache.heads or cfg.heads is None or cache.heads is None)
+                and (q is None or q.nbytes >= T * cfg.q_row <= q_out.nbytes)):
+            raise ValueError("q, k, v and q_out: rows of the configuration's shape and the cache's heads")
+        if not ((gamma_k is None or gamma_k.dtype is _F32 and gamma_k.numel() >= cache.head_dim)
+                and (gamma_q is None or gamma_q.dtype is _F32 and gamma_q.numel() >= cache.head_dim)
+                and (cos_sin is None or cos_sin.dtype is _F32 and cos_sin.numel() >= cfg.n_pos * cfg.rot_dim)
+                and (positions is None or positions.dtype is _I32 and positions.numel() >= T)):
+            raise ValueError("gamma_q, gamma_k: float32 [D], cos_sin: float32 [n_pos, rot_dim / 2, 2], positions: int32 [T]")
+        code = getattr(load(), where)(
+            cfg, cache, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            None if gamma_q is None else gamma_q.data_ptr(), None if gamma_k is None else gamma_k.data_ptr(),
+            None if cos_sin is None else cos_sin.data_ptr(), None if positions is None else positions.data_ptr(),
+            cu.data_ptr(), kv_len.data_ptr(), None if q is None else q_out.data_ptr(),
+            _current_stream(dev) if stream is None else _stream_of(stream, dev))
+        if code:
+            raise MoEError(code, where)
+    call.__name__ = call.__qualname__ = where
+    call.__doc__ = doc
+    return call
 
 
-def moe_kv_append(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream=None):
-    """Norm, rotation and append to the paged cache (include/paged_kv.h)."""
-    _append(load().moe_kv_append, "moe_kv_append", cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len,
-            q_out, stream)
+moe_kv_append = _appending("moe_kv_append", "Norm, rotation and append to the paged cache (include/paged_kv.h).")
+moe_blockkv_append = _appending("moe_blockkv_append",
+                                "Norm, rotation and append to the paged cache in 4 bits (include/block_kv.h).")
 
 
 def make_paged_attention_config(q, out, batch, max_q_len=0, window=0, n_sink=0,
@@ -410,31 +416,37 @@ def moe_paged_attention_ws_bytes(cfg, cache) -> int:
     return load().moe_paged_attention_ws_bytes(cfg, cache)
 
 
-def _attention(call, where, cfg, cache, q, cu, kv_len, out, lse, ws, stream):
-    dev = _current_device()
-    if not (dev == q.get_device() == cu.get_device() == kv_len.get_device() == out.get_device()
-            and (lse is None or lse.get_device() == dev) and (ws is None or ws.get_device() == dev)
-            and (cache.device is None or cache.device == dev)):
-        raise ValueError(_ELSEWHERE)
-    B = cfg.batch
-    if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
-        raise ValueError(_RAGGED)
-    T = cfg.T
-    if not (q.nbytes >= T * cfg.q_row <= out.nbytes and (cfg.head_dim is None or cfg.head_dim == cache.head_dim)
-            and (lse is None or lse.dtype is _F32 and lse.numel() >= T * cfg.n_q_heads)):
-        raise ValueError("q and out: rows of the configuration's shape and the cache's head size, lse: float32 "
-                         "[T, n_q_heads]")
-    code = call(
-        cfg, cache, q.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
-        _current_stream(dev) if stream is None else _stream_of(stream, dev))
-    if code:
-        raise MoEError(code, where)
+def _attending(where: str, doc: str):
+    """An attention's call, over either cache."""
+    def call(cfg, cache, q, cu, kv_len, out, lse=None, ws=None, stream=None):
+        dev = _current_device()
+        if not (dev == q.get_device() == cu.get_device() == kv_len.get_device() == out.get_device()
+                and (lse is None or lse.get_device() == dev) and (ws is None or ws.get_device() == dev)
+                and (cache.device is None or cache.device == dev)):
+            raise ValueError(_ELSEWHERE)
+        B = cfg.batch
+        if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
+            raise ValueError(_RAGGED)
+        T = cfg.T
+        if not (q.nbytes >= T * cfg.q_row <= out.nbytes and (cfg.head_dim is None or cfg.head_dim == cache.head_dim)
+                and (lse is None or lse.dtype is _F32 and lse.numel() >= T * cfg.n_q_heads)):
+            raise ValueError("q and out: rows of the configuration's shape and the cache's head size, lse: float32 "
+                             "[T, n_q_heads]")
+        code = getattr(load(), where)(
+            cfg, cache, q.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
+            _current_stream(dev) if stream is None else _stream_of(stream, dev))
+        if code:
+            raise MoEError(code, where)
+    call.__name__ = call.__qualname__ = where
+    call.__doc__ = doc
+    return call
 
 
-def moe_paged_attention(cfg, cache, q, cu, kv_len, out, lse=None, ws=None, stream=None):
-    """Attention of the new tokens over the paged cache (include/paged_kv.h)."""
-    _attention(load().moe_paged_attention, "moe_paged_attention", cfg, cache, q, cu, kv_len, out, lse, ws, stream)
+moe_paged_attention = _attending("moe_paged_attention",
+                                 "Attention of the new tokens over the paged cache (include/paged_kv.h).")
+moe_blockkv_attention = _attending("moe_blockkv_attention",
+                                   "Attention of the new tokens over the paged cache in 4 bits (include/block_kv.h).")
 
 
 def make_blockkv_cache(k, v, k_scale, v_scale, page_table, k_gscale=1.0, v_gscale=1.0) -> moe_blockkv_cache_t:
@@ -464,19 +476,8 @@ def make_blockkv_cache(k, v, k_scale, v_scale, page_table, k_gscale=1.0, v_gscal
     return c
 
 
-def moe_blockkv_append(cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu, kv_len, q_out, stream=None):
-    """Norm, rotation and append to the paged cache in 4 bits (include/block_kv.h)."""
-    _append(load().moe_blockkv_append, "moe_blockkv_append", cfg, cache, q, k, v, gamma_q, gamma_k, cos_sin, positions, cu,
-            kv_len, q_out, stream)
-
-
 def moe_blockkv_attention_ws_bytes(cfg, cache) -> int:
     return load().moe_blockkv_attention_ws_bytes(cfg, cache)
-
-
-def moe_blockkv_attention(cfg, cache, q, cu, kv_len, out, lse=None, ws=None, stream=None):
-    """Attention of the new tokens over the paged cache in 4 bits (include/block_kv.h)."""
-    _attention(load().moe_blockkv_attention, "moe_blockkv_attention", cfg, cache, q, cu, kv_len, out, lse, ws, stream)
 
 
 def _float_type(t: torch.Tensor) -> int:
@@ -529,35 +530,40 @@ def make_add_rms_norm_config(x, residual=None, out=None, out8=None, sum=None, gr
     c = moe_add_norm_config_t(T, d, _float_type(x), MOE_BF16 if residual is None else _float_type(residual),
                               MOE_BF16 if out is None else _float_type(out), group, eps, stride(x), stride(residual),
                               stride(sum), stride(out))
-    # the types that the call's tensors have to have
-    c.types = tuple(None if t is None else t.dtype for t in (x, residual, out, sum))
+    c.rows = tuple((None if t is None else t.dtype, (stride(t), 1)) for t in (x, residual, out, sum))
     return c
+
+
+def _one_row(t: torch.Tensor, T: int) -> bool:
+    """A single row, which may carry any distance to a next one."""
+    return T <= 1 and t.dim() == 2 and t.stride(1) == 1
 
 
 def moe_add_rms_norm(cfg, x, residual, gamma, out=None, out8=None, out8_scale=None, sum=None, stream=None):
     """Residual's addition and RMS norm, with an E4M3 copy (include/add_rms_norm.h)."""
     dev = _current_device()
-    T, d, types = cfg.T, cfg.d, getattr(cfg, "types", (None,) * 4)
-    strides = cfg.x_stride, cfg.res_stride, cfg.out_stride, cfg.sum_stride
-    for t, dtype, stride in zip((x, residual, out, sum), types, strides):
-        if t is None:
-            continue
-        if t.get_device() != dev:
-            raise ValueError(_ELSEWHERE)
-        if not ((dtype is None or t.dtype is dtype) and t.dim() == 2 and t.shape[0] >= T and t.shape[1] >= d
-                and (T <= 1 or t.stride(0) == stride) and t.stride(1) == 1):
-            raise ValueError("x, residual, out and sum: [T, d] of the configuration's types and strides")
-    if gamma.get_device() != dev or (out8 is not None and not out8.get_device() == dev == out8_scale.get_device()):
+    if not (dev == x.get_device() == gamma.get_device() and (residual is None or residual.get_device() == dev)
+            and (out is None or out.get_device() == dev) and (sum is None or sum.get_device() == dev)
+            and (out8 is None or out8.get_device() == out8_scale.get_device() == dev)):
         raise ValueError(_ELSEWHERE)
+    T, d = cfg.T, cfg.d
+    n = T * d
+    if cfg.rows is not None:
+        (xt, xs), (rt, rs), (ot, os), (st, ss) = cfg.rows
+        if not (x.dtype is xt and x.numel() >= n and (x.stride() == xs or _one_row(x, T))
+                and (residual is None or residual.dtype is rt and residual.numel() >= n
+                     and (residual.stride() == rs or _one_row(residual, T)))
+                and (out is None or out.dtype is ot and out.numel() >= n and (out.stride() == os or _one_row(out, T)))
+                and (sum is None or sum.dtype is st and sum.numel() >= n and (sum.stride() == ss or _one_row(sum, T)))):
+            raise ValueError("x, residual, out and sum: [T, d] of the configuration's types and strides")
     if not (gamma.dtype is _F32 and gamma.numel() >= d and gamma.is_contiguous()):
         raise ValueError("gamma: float32 [d]")
-    if out8 is not None and not (out8.nbytes >= T * d and out8.is_contiguous() and out8_scale.dtype is _F32 and out8_scale.is_contiguous()
-                                 and out8_scale.numel() >= T * (d // cfg.group if cfg.group > 0 else 1)):
+    if not (out8 is None or out8.nbytes >= n and out8.is_contiguous() and out8_scale.dtype is _F32
+            and out8_scale.is_contiguous() and out8_scale.numel() * max(cfg.group, 1) >= (n if cfg.group > 0 else T)):
         raise ValueError("out8: contiguous [T, d], out8_scale: contiguous float32 [T, d / group]")
     code = load().moe_add_rms_norm(cfg, x.data_ptr(), None if residual is None else residual.data_ptr(), gamma.data_ptr(),
                                    None if out is None else out.data_ptr(), None if out8 is None else out8.data_ptr(),
-                                   None if out8_scale is None else out8_scale.data_ptr(),
-                                   None if sum is None else sum.data_ptr(),
+                                   None if out8 is None else out8_scale.data_ptr(), None if sum is None else sum.data_ptr(),
                                    _current_stream(dev) if stream is None else _stream_of(stream, dev))
     if code:
         raise MoEError(code, "moe_add_rms_norm")

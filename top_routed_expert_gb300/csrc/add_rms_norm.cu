@@ -259,8 +259,8 @@ extern "C" moe_status_t moe_add_rms_norm(const moe_add_norm_config_t* cfg, const
   const int pieces = cfg->d / 8, res = !residual ? 0 : cfg->res_dtype == MOE_F32 ? 2 : 1;
   cudaError_t err;
   if (pieces <= 128) err = launch<128, 1>(a, res, sms, s);
-  else if (pieces <= 256) err = launch<128, 2>(a, res, sms, s);
-  else if (pieces <= 512) err = launch<256, 2>(a, res, sms, s);
+  else if (pieces <= 256) err = launch<256, 1>(a, res, sms, s);
+  else if (pieces <= 512) err = launch<512, 1>(a, res, sms, s);
   else if (pieces <= 1024) err = launch<512, 2>(a, res, sms, s);
   else err = launch<512, 4>(a, res, sms, s);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
