@@ -9,9 +9,10 @@
 //               memory)
 //   P = 2^(S k_scale .. - m), f16, written over S in tensor memory
 //   O += P V    (A = P from tensor memory, B = V^T from shared memory)
-// Warps 0-3 and 4-7 are the softmax of tile 0 and 1 (one thread a row), warps
-// 8-11 convert keys and 12-15 values, warp 16 issues the MMAs, warp 17 looks up
-// pages and scales some steps ahead (18 and 19 only lend registers): while one
+// Warps 0-3 and 4-7 are the softmax of tile 0 and 1 (one thread a row), the next
+// four (codes of four bits: eight) convert keys, as many more values, the next one
+// issues the MMAs, the one behind it looks up pages and scales some steps ahead
+// (two more only lend registers): while one
 // tile's softmax runs, the tensor core works on the other's products.  The CTAs
 // are persistent, one on an SM, and take items from a list that
 // paged_attn_rows.cuh has sorted by length; steps of the next item start beside the last of this.
@@ -61,13 +62,22 @@ constexpr int kRowTile = 128;
 static_assert(kTcItemRows == 2 * kRowTile, "two row tiles");
 constexpr int kTok = kTcStep;            // tokens of a step
 constexpr int kGroups = kTok / 16;       // scale groups of a step
-constexpr int kThreads = 20 * 32;
-// Registers of a thread, by warpgroup: two of softmax, two of conversion, one
-// that plans and issues.  The launch has 96 for each of the 640 threads;
-// 256 x 128 + 256 x 72 + 128 x 80 are the same 61440.
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 128, kConvRegs = 72, kIssueRegs = 80;
-static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kIssueRegs <= 5 * kLaunchRegs, "setmaxnreg would wait forever");
-constexpr int kConvThreads = 128;
+// Warps by their work, and registers of a thread by warpgroup: two of softmax, one
+// (codes of four bits: two, as each code is multiplied by its scale besides) of
+// keys and of values, one that plans and issues.  What the warpgroups take may not
+// exceed what the launch has: setmaxnreg would wait forever.
+constexpr int kSoftmaxWarps = 8;
+template <bool BLOCKS> struct Split {
+  static constexpr int kConvWarps = BLOCKS ? 8 : 4;            // for keys, and for values
+  static constexpr int kConvThreads = kConvWarps * 32;
+  static constexpr int kIssueWarp = kSoftmaxWarps + 2 * kConvWarps;
+  static constexpr int kThreads = (kIssueWarp + 4) * 32;
+  static constexpr int kLaunchRegs = BLOCKS ? 72 : 96, kSoftmaxRegs = 128, kConvRegs = BLOCKS ? 48 : 72,
+                       kIssueRegs = BLOCKS ? 56 : 80;
+  static_assert(2 * kSoftmaxRegs + kConvWarps / 2 * kConvRegs + kIssueRegs <= kThreads / 128 * kLaunchRegs,
+                "setmaxnreg would wait forever");
+  static_assert(kThreads * kLaunchRegs <= 65536, "registers of an SM");
+};
 constexpr int kSlots = 8;              // steps that are planned ahead, at most
 constexpr int kItems = 16;             // items that are announced ahead; more than kSlots, as an item has a step or more
 constexpr float kLog2e = 1.4426950408889634f;
@@ -295,8 +305,10 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 template <int D, class Args>
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
+__global__ void __launch_bounds__(Split<Args::kBlocks>::kThreads, 1) paged_attn_tc_kernel(Args a) {
   constexpr bool BLOCKS = Args::kBlocks;
+  using W = Split<BLOCKS>;
+  constexpr int kConvThreads = W::kConvThreads, kIssueWarp = W::kIssueWarp;
   using L = Tc<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -324,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
     c->abort = 0;
     fence_barrier_init();
   }
-  if (warp == 16) {
+  if (warp == kIssueWarp) {
     tmem_alloc(smem_u32(&c->tmem_base), 512);
     tmem_relinquish();
   }
@@ -336,9 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
   // item k, once the planning warp has announced it
   auto next_item = [&](int k) { return wait_phase(&c->item_full[k % kItems], (k / kItems) & 1, abort); };
 
-  if (warp < 8) {
+  if (warp < kSoftmaxWarps) {
     // ---------------------------------------------------------- softmax
-    regs_up<kSoftmaxRegs>();
+    regs_up<W::kSoftmaxRegs>();
     const int tile = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + L::kS + tile * kTok, t_o = tmem + lanes + L::kO + tile * D;
@@ -548,10 +560,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
       tc_fence_before();
       rf = rf_next;
     }
-  } else if (warp < 16) {
+  } else if (warp < kIssueWarp) {
     // ---------------------------------------------------------- conversion
-    regs_down<kConvRegs>();
-    const int t = threadIdx.x & 127;
+    regs_down<W::kConvRegs>();
+    const int t = (threadIdx.x - kSoftmaxWarps * 32) % kConvThreads;
     const int64_t ts = a.c.token_stride;
     // walks the steps of all items; false: there are no more
     int k = -1, j = 0, g = -1, steps = 0, j0 = 0;
@@ -576,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
       all = j0 + kTok <= sp.end && (j0 >= sp.lo || j0 + kTok <= sp.n_sink);
       return true;
     };
-    if (warp < 12) {
+    if (warp < kSoftmaxWarps + W::kConvWarps) {
       if constexpr (BLOCKS) {
         // keys: token (+ i KSTEP) and 16-byte chunk, 32 codes of two blocks; eight
         // neighbouring lanes have two chunks of four rows, which the swizzle puts in
@@ -670,29 +682,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
       }
     } else {
       if constexpr (BLOCKS) {
-        // values: 8 tokens (an octet of the 64 that the warp's parity names) by 16
-        // elements, a block (D = 64: by 8, half of one); eight neighbouring lanes store
-        // their octets' pieces of one row to eight banks
-        constexpr int VE = D / 8;   // elements
-        const int vt = (warp & 1) * 64 + (lane & 7) * 8, vx = ((warp >> 1) & 1) * 4 + (lane >> 3);
+        // values: 8 tokens (an octet of the 64 that the warp's parity names) by VE
+        // elements of a block; eight neighbouring lanes store their octets' pieces
+        // of one row to eight banks
+        constexpr int VE = D * 16 / kConvThreads;   // 8 (D = 64: 4)
+        const int vt = (warp & 1) * 64 + (lane & 7) * 8, vx = (t >> 6) * 4 + (lane >> 3);
         const uint8_t* mine = static_cast<const uint8_t*>(a.c.v) + (vt & 15) * ts + vx * (VE / 2);
         const uint8_t* mine_s = a.v_scales + (vt & 15) * a.scale_token + vx * VE / 16;
-        uint32_t vw[8][VE / 8], vs[8];
+        uint32_t vw[8], vs[8];
         auto load = [&] {
           const int64_t off = c->place[g % kSlots][vt >> 4];
           const uint8_t *row = mine + head_at + off, *row_s = mine_s + scale_head_at + c->scale_place[g % kSlots][vt >> 4];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const bool there = off >= 0 && (all || sp.seen(j0 + vt + i));
-            vs[i] = vw[i][0] = vw[i][VE / 8 - 1] = 0u;
+            vs[i] = vw[i] = 0u;
             if (there) {
-              if constexpr (VE == 16) {
-                const uint2 x = __ldg(reinterpret_cast<const uint2*>(row));
-                vw[i][0] = x.x;
-                vw[i][VE / 8 - 1] = x.y;
-              } else {
-                vw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(row));
-              }
+              vw[i] = VE == 8 ? __ldg(reinterpret_cast<const uint32_t*>(row)) : __ldg(reinterpret_cast<const uint16_t*>(row));
               vs[i] = __ldg(row_s);
             }
             row += ts;
@@ -717,18 +723,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[i] = f16x2_of_scales(vs[2 * i] | vs[2 * i + 1] << 8);
 #pragma unroll
-          for (int w = 0; w < VE / 8; ++w)
+          for (int odd = 0; odd < 2; ++odd) {
+            uint32_t x[4][4];   // token pair, element
 #pragma unroll
-            for (int odd = 0; odd < 2; ++odd) {
-              uint32_t x[4][4];   // token pair, element
+            for (int i = 0; i < 4; ++i)
+              f16x2_of_e2m1(odd ? odd_codes(vw[2 * i], vw[2 * i + 1]) : even_codes(vw[2 * i], vw[2 * i + 1]), x[i]);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                f16x2_of_e2m1(odd ? odd_codes(vw[2 * i][w], vw[2 * i + 1][w]) : even_codes(vw[2 * i][w], vw[2 * i + 1][w]), x[i]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                sts128(base + sw128(vx * VE + 8 * w + 2 * e + odd, ch), mul_f16x2(x[0][e], f[0]), mul_f16x2(x[1][e], f[1]),
-                       mul_f16x2(x[2][e], f[2]), mul_f16x2(x[3][e], f[3]));
-            }
+            for (int e = 0; e < VE / 2; ++e)
+              sts128(base + sw128(vx * VE + 2 * e + odd, ch), mul_f16x2(x[0][e], f[0]), mul_f16x2(x[1][e], f[1]),
+                     mul_f16x2(x[2][e], f[2]), mul_f16x2(x[3][e], f[3]));
+          }
           fence_async();
           mbar_arrive(smem_u32(&c->v_full[st]));
           more = next_step();
@@ -791,8 +795,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
       }
     }
   } else {
-    regs_down<kIssueRegs>();
-    if (warp == 17) {
+    regs_down<W::kIssueRegs>();
+    if (warp == kIssueWarp + 1) {
       // -------------------------------------------------------- planning
       // Takes items from the list as they come (the longest first; which CTA
       // works on one does not matter to its results), announces them, and looks
@@ -862,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
     // ---------------------------------------------------------- MMA issue
     // The whole warp walks the loop, so that descriptors stay in uniform
     // registers (per-thread ones cost an MMA's time to move); one lane issues.
-    if (warp == 16) {
+    if (warp == kIssueWarp) {
       constexpr uint32_t is = idesc_f16(kRowTile, kTok), io = idesc_f16(kRowTile, D);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       // descriptors of the first tile and stage; the others lie a multiple of
@@ -947,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(Args a) {
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0 && c->abort) set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  if (warp == kIssueWarp) tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of cut row blocks, a warp for each row, in the parts' order.
@@ -1011,7 +1015,7 @@ cudaError_t launch_tc(const Args& a, cudaStream_t s) {
   cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(kernel), Tc<D>::kSmem);
   if (err != cudaSuccess) return err;
   count_launches(a.tc_split ? 2 : 1);
-  err = launch_pdl(kernel, a.tc_ctas, kThreads, Tc<D>::kSmem, s, a);
+  err = launch_pdl(kernel, a.tc_ctas, Split<Args::kBlocks>::kThreads, Tc<D>::kSmem, s, a);
   if (err != cudaSuccess || !a.tc_split) return err;
   return launch_pdl(paged_attn_tc_join<D, Args>, 4 * a.tc_ctas, 256, 0, s, a);
 }
