@@ -68,15 +68,17 @@ constexpr int kGroups = kTok / 16;       // scale groups of a step
 // exceed what the launch has: setmaxnreg would wait forever.
 constexpr int kSoftmaxWarps = 8;
 template <bool BLOCKS> struct Split {
-  static constexpr int kConvWarps = BLOCKS ? 8 : 4;            // for keys, and for values
-  static constexpr int kConvThreads = kConvWarps * 32;
-  static constexpr int kIssueWarp = kSoftmaxWarps + 2 * kConvWarps;
+  static constexpr int kKeyWarps = BLOCKS ? 8 : 4, kValueWarps = BLOCKS ? 8 : 4;   // that convert
+  static constexpr int kKeyThreads = kKeyWarps * 32, kValueThreads = kValueWarps * 32;
+  static constexpr int kIssueWarp = kSoftmaxWarps + kKeyWarps + kValueWarps;
   static constexpr int kThreads = (kIssueWarp + 4) * 32;
-  static constexpr int kLaunchRegs = BLOCKS ? 72 : 96, kSoftmaxRegs = 128, kConvRegs = BLOCKS ? 48 : 72,
-                       kIssueRegs = BLOCKS ? 56 : 80;
-  static_assert(2 * kSoftmaxRegs + kConvWarps / 2 * kConvRegs + kIssueRegs <= kThreads / 128 * kLaunchRegs,
+  static constexpr int kLaunchRegs = BLOCKS ? 72 : 96, kSoftmaxRegs = 128, kKeyRegs = BLOCKS ? 56 : 72,
+                       kValueRegs = BLOCKS ? 48 : 72, kIssueRegs = BLOCKS ? 40 : 80;
+  static_assert(2 * kSoftmaxRegs + kKeyWarps / 4 * kKeyRegs + kValueWarps / 4 * kValueRegs + kIssueRegs <=
+                    kThreads / 128 * kLaunchRegs,
                 "setmaxnreg would wait forever");
   static_assert(kThreads * kLaunchRegs <= 65536, "registers of an SM");
+  static_assert(kKeyWarps == kValueWarps && (BLOCKS || kKeyRegs == kValueRegs), "one numbering of the threads");
 };
 constexpr int kSlots = 8;              // steps that are planned ahead, at most
 constexpr int kItems = 16;             // items that are announced ahead; more than kSlots, as an item has a step or more
@@ -308,7 +310,7 @@ template <int D, class Args>
 __global__ void __launch_bounds__(Split<Args::kBlocks>::kThreads, 1) paged_attn_tc_kernel(Args a) {
   constexpr bool BLOCKS = Args::kBlocks;
   using W = Split<BLOCKS>;
-  constexpr int kConvThreads = W::kConvThreads, kIssueWarp = W::kIssueWarp;
+  constexpr int kKeyThreads = W::kKeyThreads, kValueThreads = W::kValueThreads, kIssueWarp = W::kIssueWarp;
   using L = Tc<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -320,8 +322,8 @@ __global__ void __launch_bounds__(Split<Args::kBlocks>::kThreads, 1) paged_attn_
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&c->q_full), 2 * kRowTile);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&c->k_full[i]), kConvThreads);
-      mbar_init(smem_u32(&c->v_full[i]), kConvThreads);
+      mbar_init(smem_u32(&c->k_full[i]), kKeyThreads);
+      mbar_init(smem_u32(&c->v_full[i]), kValueThreads);
       mbar_init(smem_u32(&c->s_full[i][0]), 1);
       mbar_init(smem_u32(&c->s_full[i][1]), 1);
       mbar_init(smem_u32(&c->p_full[i]), kRowTile);
@@ -562,8 +564,8 @@ __global__ void __launch_bounds__(Split<Args::kBlocks>::kThreads, 1) paged_attn_
     }
   } else if (warp < kIssueWarp) {
     // ---------------------------------------------------------- conversion
-    regs_down<W::kConvRegs>();
-    const int t = (threadIdx.x - kSoftmaxWarps * 32) % kConvThreads;
+    if (!BLOCKS) regs_down<W::kKeyRegs>();   // (the same for both)
+    const int t = BLOCKS ? (threadIdx.x - kSoftmaxWarps * 32) % kKeyThreads : threadIdx.x & 127;
     const int64_t ts = a.c.token_stride;
     // walks the steps of all items; false: there are no more
     int k = -1, j = 0, g = -1, steps = 0, j0 = 0;
@@ -588,12 +590,13 @@ __global__ void __launch_bounds__(Split<Args::kBlocks>::kThreads, 1) paged_attn_
       all = j0 + kTok <= sp.end && (j0 >= sp.lo || j0 + kTok <= sp.n_sink);
       return true;
     };
-    if (warp < kSoftmaxWarps + W::kConvWarps) {
+    if (warp < kSoftmaxWarps + W::kKeyWarps) {
+      if (BLOCKS) regs_down<W::kKeyRegs>();
       if constexpr (BLOCKS) {
         // keys: token (+ i KSTEP) and 16-byte chunk, 32 codes of two blocks; eight
         // neighbouring lanes have two chunks of four rows, which the swizzle puts in
         // eight banks
-        constexpr int CPT = D / 32, KN = kTok * CPT / kConvThreads, KSTEP = kConvThreads / CPT;
+        constexpr int CPT = D / 32, KN = kTok * CPT / kKeyThreads, KSTEP = kKeyThreads / CPT;
         const int kc = D == 128 ? (t & 1) | ((t >> 2) & 2) : t & 1;
         const int kr = D == 128 ? ((t >> 1) & 3) | (t >> 4 << 2) : t >> 1;
         const uint8_t* mine = static_cast<const uint8_t*>(a.c.k) + (kr & 15) * ts + kc * 16;
@@ -644,7 +647,7 @@ __global__ void __launch_bounds__(Split<Args::kBlocks>::kThreads, 1) paged_attn_
       } else {
         // keys: token (+ i KSTEP) and 16-byte chunk; eight neighbouring lanes have
         // four chunks of two rows, which the swizzle puts in eight banks
-        constexpr int CPT = D / 16, KN = kTok * CPT / kConvThreads, KSTEP = kConvThreads / CPT;
+        constexpr int CPT = D / 16, KN = kTok * CPT / kKeyThreads, KSTEP = kKeyThreads / CPT;
         const int kc = D == 128 ? (t & 3) | ((t >> 1) & 4) : t & 3;
         const int kr = D == 128 ? ((t >> 2) & 1) | (t >> 4 << 1) : t >> 2;
         const uint8_t* mine = static_cast<const uint8_t*>(a.c.k) + (kr & 15) * ts + kc * 16;
@@ -681,11 +684,12 @@ __global__ void __launch_bounds__(Split<Args::kBlocks>::kThreads, 1) paged_attn_
         }
       }
     } else {
+      if (BLOCKS) regs_down<W::kValueRegs>();
       if constexpr (BLOCKS) {
         // values: 8 tokens (an octet of the 64 that the warp's parity names) by VE
         // elements of a block; eight neighbouring lanes store their octets' pieces
         // of one row to eight banks
-        constexpr int VE = D * 16 / kConvThreads;   // 8 (D = 64: 4)
+        constexpr int VE = D * 16 / kValueThreads;   // 8 (D = 64: 4)
         const int vt = (warp & 1) * 64 + (lane & 7) * 8, vx = (t >> 6) * 4 + (lane >> 3);
         const uint8_t* mine = static_cast<const uint8_t*>(a.c.v) + (vt & 15) * ts + vx * (VE / 2);
         const uint8_t* mine_s = a.v_scales + (vt & 15) * a.scale_token + vx * VE / 16;
