@@ -37,12 +37,13 @@ template <int D, int NB, bool BLOCKS> struct Shape {
   static constexpr int kUnit = BLOCKS ? 128 : 64;         // tokens of a unit, in equal parts for the four warps
   // What a row tile costs beside its units (finding it, q, the join of the
   // warps), in units.
-  static constexpr int kTileCost = BLOCKS ? 3 : 4;
+  static constexpr int kTileCost = BLOCKS ? 4 : 4;
   static constexpr int kTile = BLOCKS ? 8 * D : 16 * D;   // bytes of 16 tokens' keys (or values)
   static constexpr int kStage = BLOCKS ? 4 * kTile + 4 * D : 2 * kTile;
   // CTAs on an SM, by registers (O takes D NB / 4 of a thread's, q D NB / 8),
   // and the stages of the ring that fit then
-  static constexpr int kCtas = D * NB == 64 ? 5 : D * NB == 128 ? 4 : D * NB == 256 ? 3 : 2;
+  static constexpr int kCtas = BLOCKS ? (D * NB == 64 ? 4 : D * NB == 128 ? 3 : 2)
+                                      : D * NB == 64 ? 5 : D * NB == 128 ? 4 : D * NB == 256 ? 3 : 2;
   static constexpr int kStages = BLOCKS ? 2 : D == 256 ? 2 : D * NB == 128 && D == 128 ? 3 : 4;
   static constexpr int kRing = kStages * kStage;        // per warp
   static constexpr int kPart = kRows * D + 2 * kRows;   // floats of a partial: outputs, references, sums
