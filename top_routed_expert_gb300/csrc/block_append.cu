@@ -106,27 +106,58 @@ __device__ __forceinline__ uint8_t scale_code(float s) {
   return static_cast<uint8_t>(__nv_cvt_float_to_fp8(s, __NV_SATFINITE, __NV_E4M3));
 }
 
-// Four codes, element 0 in the low four bits: x / sg to the nearest, ties to even.
-// The quotient is x inv (inv: 1 / sg to a unit of the last place) corrected by its
-// remainder, which is exact.  That decides every code as x / sg itself would: sg
-// has four significant bits and a border m between two codes three, so x (24
-// bits) either is m sg, and then the corrected quotient is m (it is off by 2^-45
-// before its rounding), or lies a unit of its last place away, and then x / sg is
-// over half a unit of m's from m.
-// fine: the four are finite and none is over 6 sg; x inv may overflow otherwise.
-__device__ __forceinline__ uint32_t codes_of(const float* x, float sg, float inv, bool fine) {
-  float q[4];
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// N quotients x / sg, near enough to give every code as the exact ones would.
+// They are x inv (inv: 1 / sg to a unit of the last place) corrected by their
+// remainders, which are exact: sg has four significant bits and a border m between
+// two codes three, so x (24 bits) either is m sg, and then the corrected quotient
+// is m (it is off by 2^-45 before its rounding), or lies a unit of its last place
+// away, and then x / sg is over half a unit of m's from m.
+// fine: x is finite and none is over 6 sg; x inv may overflow otherwise.
+template <int N>
+__device__ __forceinline__ void quotients(float (&q)[N], const float* x, float sg, float inv, bool fine) {
+  const uint64_t sg2 = pair(-sg, -sg), inv2 = pair(inv, inv);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = __fmul_rn(x[i], inv);
-  if (fine) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = __fmaf_rn(__fmaf_rn(-q[i], sg, x[i]), inv, q[i]);
+  for (int i = 0; i < N; i += 2) {
+    const uint64_t x2 = pair(x[i], x[i + 1]);
+    uint64_t q2 = mul2(x2, inv2);
+    if (fine) q2 = fma2(fma2(q2, sg2, x2), inv2, q2);
+    unpair(q2, q[i], q[i + 1]);
   }
+}
+
+// Codes of the nearest values, ties to even, element 0 in the low four bits.
+__device__ __forceinline__ uint32_t codes4(const float* q) {
   uint32_t r;
-  asm("{\n .reg .b8 a, b;\n .reg .b16 c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+  asm("{\n .reg .b8 a, b;\n .reg .b16 c;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
       " mov.b16 c, {a, b};\n cvt.u32.u16 %0, c;\n}\n"
       : "=r"(r)
       : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes8(const float* q) {
+  uint32_t r;
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(r)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
   return r;
 }
 
@@ -140,10 +171,9 @@ __device__ __forceinline__ float reciprocal(float x) {
 __device__ __forceinline__ void store_block(uint8_t* codes, uint8_t* scale, const float (&x)[16], float top, bool odd, float g,
                                             float inv_g) {
   const float s = block_scale(top * inv_g), sg = s * g, inv = reciprocal(sg);
-  const bool fine = !odd && top <= 6.f * sg;
-  const uint32_t lo = codes_of(x, sg, inv, fine) | codes_of(x + 4, sg, inv, fine) << 16;
-  const uint32_t hi = codes_of(x + 8, sg, inv, fine) | codes_of(x + 12, sg, inv, fine) << 16;
-  *reinterpret_cast<uint2*>(codes) = make_uint2(lo, hi);
+  float q[16];
+  quotients(q, x, sg, inv, !odd && top <= 6.f * sg);
+  *reinterpret_cast<uint2*>(codes) = make_uint2(codes8(q), codes8(q + 8));
   *scale = scale_code(s);
 }
 
@@ -374,8 +404,9 @@ __device__ __forceinline__ void append_keys_half(const BaArgs& a, const Slots& s
         const int o = h ? p.ob : p.oa;
         const float4 t = s_top[u & 1][grp][o / 16];
         const float sc = block_scale(max_or_nan(max_or_nan(t.x, t.y), max_or_nan(t.z, t.w)) * inv_g), sg = sc * g;
-        *reinterpret_cast<uint16_t*>(to.codes + o / 2) =
-            static_cast<uint16_t>(codes_of(x + 4 * h, sg, reciprocal(sg), !odd[h] && top[h] <= 6.f * sg));
+        float q[4];
+        quotients(q, x + 4 * h, sg, reciprocal(sg), !odd[h] && top[h] <= 6.f * sg);
+        *reinterpret_cast<uint16_t*>(to.codes + o / 2) = static_cast<uint16_t>(codes4(q));
         if (o % 16 == 0) to.scales[o / 16] = scale_code(sc);
       }
     }
