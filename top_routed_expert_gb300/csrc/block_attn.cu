@@ -479,8 +479,87 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
   if (threadIdx.x == 0) a.joins[blockIdx.x] = cut;
 }
 
+// Joins the partial sums of the row tiles that more than one CTA worked on: a block
+// for each CTA that may have begun one, a warp for a row, the parts in order.  Small
+// blocks find room as soon as the first CTAs of the kernel before are gone, and
+// nothing but the tile has to be looked up (a block on each SM, to which the rows
+// are dealt, took 4.5 us beside the kernel, these 3.2).  Several parts' columns are on
+// their way at once, to shared memory.
+template <int D, int NB> struct JoinShape {
+  static constexpr int kBatch = 16 / NB / (D == 256 ? 2 : 1);   // parts
+  static constexpr int kSmem = 8 * NB * kBatch * D * 4;
+};
+
+template <int D, int NB>
+__global__ void __launch_bounds__(8 * NB * 32) block_attn_join(BlockPaArgs a) {
+  using S = Shape<D, NB, true>;
+  constexpr int kRows = S::kRows, VEC = D / 64, BATCH = JoinShape<D, NB>::kBatch;   // VEC: pairs of columns of a lane
+  extern __shared__ __align__(128) char smem[];
+  pdl_enter();
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c0 = blockIdx.x;
+  const JoinTile tile = a.joins[c0];
+  if (r >= tile.rows) return;
+  float* mine = reinterpret_cast<float*>(smem) + r * (BATCH * D);
+  auto part_of = [&](int c) { return a.part + (static_cast<int64_t>(c) * 2 + (c == c0 ? tile.slot : 0)) * S::kPart; };
+  float m = -INFINITY, sum = 0.f;
+  float2 acc[VEC] = {};
+#pragma unroll 1
+  for (int c = c0; c <= tile.last; c += BATCH) {
+    const int n = min(BATCH, tile.last + 1 - c);
+    float pm = -INFINITY, pl = 0.f;
+    if (lane < n) {
+      const float* p = part_of(c + lane) + kRows * D + r;
+      pm = p[0];
+      pl = p[kRows];
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH * D / 128; ++i) {
+      const int x = i * 32 + lane, part = x / (D / 4), col = x % (D / 4) * 4;
+      if (part < n) cp16(ptx::smem_u32(mine + part * D + col), part_of(c + part) + r * D + col);
+    }
+    cp_commit();
+    float to = fmaxf(m, pm);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
+    const float old = ex2_from(m, to), w = ex2_from(pm, to);
+    m = to;
+    pl *= w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) pl += __shfl_xor_sync(0xffffffffu, pl, off);
+    sum = sum * old + pl;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = make_float2(acc[e].x * old, acc[e].y * old);
+    cp_wait<0>();
+    __syncwarp();
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float2 v = *reinterpret_cast<const float2*>(mine + i * D + (e * 32 + lane) * 2);
+        acc[e].x += v.x * wi;
+        acc[e].y += v.y * wi;
+      }
+    }
+    __syncwarp();   // the columns have been read
+  }
+  const int tok = (tile.row0 + r) / a.group, head = tile.kvh * a.group + (tile.row0 + r) % a.group;
+  const float f = out_factor(a, sum);
+  __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + static_cast<int64_t>(tile.token0 + tok) * a.os +
+                                                          static_cast<int64_t>(head) * D);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) out[e * 32 + lane] = __floats2bfloat162_rn(acc[e].x * f, acc[e].y * f);
+  if (a.lse && lane == 0) store_lse(a, tile.token0 + tok, head, m, sum);
+}
+
 struct Kernels {
   template <int D, int NB> static constexpr auto of() { return &block_attn_kernel<D, NB>; }
+  template <int D, int NB> static cudaError_t join(const BlockPaArgs& a, int ctas, cudaStream_t s) {
+    constexpr int smem = JoinShape<D, NB>::kSmem;
+    const cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(block_attn_join<D, NB>), smem);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(block_attn_join<D, NB>, ctas, 8 * NB * 32, smem, s, a);
+  }
 };
 
 bool config_ok(const moe_paged_attention_config_t* cfg, const moe_blockkv_cache_t* cache) {

@@ -428,8 +428,158 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, false>::kCtas) paged
   if (threadIdx.x == 0) a.joins[blockIdx.x] = cut;
 }
 
+// Joins the partial sums of the row tiles that more than one CTA worked on.  The
+// rows to join are dealt to all blocks (one on an SM) and their warps; where that
+// leaves warps over, several share a row's parts.  The kernel is a chain of
+// latencies, so what a row needs is under way at once: eight parts' columns, and
+// their references and sums, one part a lane.
+constexpr int kJoinWarps = 32;
+template <int D, int NB>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join(PaArgs a, int n_ctas) {
+  using S = Shape<D, NB, false>;
+  constexpr int kRows = S::kRows;
+  constexpr int VEC = D / 64;   // pairs of columns of a lane
+  __shared__ int s_first[kJoinWarps * 32];   // rows to join before CTA i's
+  __shared__ JoinTile s_tile[kMaxCtas];
+  __shared__ int s_warp[kJoinWarps];
+  __shared__ float2 s_acc[kJoinWarps][VEC][32];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  pdl_enter();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int rows = 0;
+  if (threadIdx.x < n_ctas) {
+    const JoinTile tile = a.joins[threadIdx.x];
+    rows = tile.rows;
+    s_tile[threadIdx.x] = tile;
+  }
+  int before = rows;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, off);
+    if (lane >= off) before += v;
+  }
+  if (lane == 31) s_warp[warp] = before;
+  __syncthreads();
+  int in_warps = s_warp[lane];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, in_warps, off);
+    if (lane >= off) in_warps += v;
+  }
+  const int total = __shfl_sync(0xffffffffu, in_warps, 31);
+  const int prior = __shfl_sync(0xffffffffu, in_warps, max(warp - 1, 0));
+  s_first[threadIdx.x] = before - rows + (warp > 0 ? prior : 0);
+  __syncthreads();
+  const int items = (total - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x;   // this block's rows
+  if (items <= 0) return;
+  int shares = 1;
+  while (shares * 2 * items <= kJoinWarps) shares *= 2;
+  const int share = warp % shares;
+#pragma unroll 1
+  for (int base = 0; base < items; base += kJoinWarps / shares) {
+    const int item = base + warp / shares;
+    const bool live = item < items;
+    // the CTA that began the row's tile: the last that has no more rows before it
+    const int at = blockIdx.x + (live ? item : 0) * gridDim.x;
+    int c0 = 0;
+#pragma unroll
+    for (int step = kJoinWarps * 16; step > 0; step >>= 1)
+      if (c0 + step < n_ctas && s_first[c0 + step] <= at) c0 += step;
+    const int r = at - s_first[c0];
+    const JoinTile tile = s_tile[c0];
+    auto part_of = [&](int c) { return a.part + (static_cast<int64_t>(c) * 2 + (c == c0 ? tile.slot : 0)) * S::kPart; };
+    float m = -INFINITY, sum = 0.f;
+    float2 acc[VEC] = {};
+    // this share's parts
+    constexpr int BATCH = D == 256 ? 4 : 8;
+#pragma unroll 1
+    for (int c = c0 + share; live && c <= tile.last; c += BATCH * shares) {
+      float2 v[BATCH][VEC];
+      float pm = -INFINITY, pl = 0.f;
+      if (lane < BATCH && c + lane * shares <= tile.last) {
+        const float* p = part_of(c + lane * shares) + kRows * D + r;
+        pm = p[0];
+        pl = p[kRows];
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const float2* p = reinterpret_cast<const float2*>(part_of(c + i * shares) + r * D) + lane;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[i][e] = c + i * shares <= tile.last ? p[e * 32] : make_float2(0.f, 0.f);
+      }
+      float to = fmaxf(m, pm);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
+      const float old = ex2_from(m, to), w = ex2_from(pm, to);
+      m = to;
+      pl *= w;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) pl += __shfl_xor_sync(0xffffffffu, pl, off);
+      sum = sum * old + pl;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = make_float2(acc[e].x * old, acc[e].y * old);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          acc[e].x += v[i][e].x * wi;
+          acc[e].y += v[i][e].y * wi;
+        }
+      }
+    }
+    if (shares > 1) {
+      if (lane == 0) {
+        s_m[warp] = m;
+        s_l[warp] = sum;
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s_acc[warp][e][lane] = acc[e];
+      __syncthreads();
+      if (share == 0) {
+        const float pm = lane < shares ? s_m[warp + lane] : -INFINITY;
+        float to = pm;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
+        const float w = ex2_from(pm, to);
+        m = to;
+        sum = lane < shares ? s_l[warp + lane] * w : 0.f;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < shares; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float2 v = s_acc[warp + i][e][lane];
+            acc[e].x += v.x * wi;
+            acc[e].y += v.y * wi;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (live && share == 0) {
+      const int tok = (tile.row0 + r) / a.group, head = tile.kvh * a.group + (tile.row0 + r) % a.group;
+      const float f = out_factor(a, sum);
+      __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + static_cast<int64_t>(tile.token0 + tok) * a.os +
+                                                              static_cast<int64_t>(head) * D);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) out[e * 32 + lane] = __floats2bfloat162_rn(acc[e].x * f, acc[e].y * f);
+      if (a.lse && lane == 0) store_lse(a, tile.token0 + tok, head, m, sum);
+    }
+  }
+}
+
 struct Kernels {
   template <int D, int NB> static constexpr auto of() { return &paged_attn_kernel<D, NB>; }
+  template <int D, int NB> static cudaError_t join(const PaArgs& a, int ctas, cudaStream_t s) {
+    constexpr int on_sm = Shape<D, NB, false>::kCtas;
+    static_assert(kMaxSms * on_sm <= kMaxCtas && kMaxCtas <= kJoinWarps * 32, "a thread of the join for each CTA");
+    return launch_pdl(paged_attn_join<D, NB>, ctas / on_sm, kJoinWarps * 32, 0, s, a, ctas);
+  }
 };
 
 bool config_ok(const moe_paged_attention_config_t* cfg, const moe_kv_cache_t* cache) {

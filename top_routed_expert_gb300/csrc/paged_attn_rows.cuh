@@ -237,160 +237,16 @@ __global__ void __launch_bounds__(512) list_kernel(PaArgs a) {
   list_tc_items(a, reinterpret_cast<int*>(smem + 2048), smem);
 }
 
-// Joins the partial sums of the row tiles that more than one CTA worked on.  The
-// rows to join are dealt to all blocks (one on an SM) and their warps; where that
-// leaves warps over, several share a row's parts.  The kernel is a chain of
-// latencies, so what a row needs is under way at once: eight parts' columns, and
-// their references and sums, one part a lane.
-constexpr int kJoinWarps = 32;
 // The workspace is sized for kMaxSms SMs, so that its size needs no device.
 constexpr int kMaxCtas = kMaxSms * 5;
-
-template <int D, int NB, class Args>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join(Args a, int n_ctas) {
-  using S = Shape<D, NB, Args::kBlocks>;
-  constexpr int kRows = S::kRows;
-  constexpr int VEC = D / 64;   // pairs of columns of a lane
-  __shared__ int s_first[kJoinWarps * 32];   // rows to join before CTA i's
-  __shared__ JoinTile s_tile[kMaxCtas];
-  __shared__ int s_warp[kJoinWarps];
-  __shared__ float2 s_acc[kJoinWarps][VEC][32];
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
-  pdl_enter();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int rows = 0;
-  if (threadIdx.x < n_ctas) {
-    const JoinTile tile = a.joins[threadIdx.x];
-    rows = tile.rows;
-    s_tile[threadIdx.x] = tile;
-  }
-  int before = rows;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, before, off);
-    if (lane >= off) before += v;
-  }
-  if (lane == 31) s_warp[warp] = before;
-  __syncthreads();
-  int in_warps = s_warp[lane];
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, in_warps, off);
-    if (lane >= off) in_warps += v;
-  }
-  const int total = __shfl_sync(0xffffffffu, in_warps, 31);
-  const int prior = __shfl_sync(0xffffffffu, in_warps, max(warp - 1, 0));
-  s_first[threadIdx.x] = before - rows + (warp > 0 ? prior : 0);
-  __syncthreads();
-  const int items = (total - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x;   // this block's rows
-  if (items <= 0) return;
-  int shares = 1;
-  while (shares * 2 * items <= kJoinWarps) shares *= 2;
-  const int share = warp % shares;
-#pragma unroll 1
-  for (int base = 0; base < items; base += kJoinWarps / shares) {
-    const int item = base + warp / shares;
-    const bool live = item < items;
-    // the CTA that began the row's tile: the last that has no more rows before it
-    const int at = blockIdx.x + (live ? item : 0) * gridDim.x;
-    int c0 = 0;
-#pragma unroll
-    for (int step = kJoinWarps * 16; step > 0; step >>= 1)
-      if (c0 + step < n_ctas && s_first[c0 + step] <= at) c0 += step;
-    const int r = at - s_first[c0];
-    const JoinTile tile = s_tile[c0];
-    auto part_of = [&](int c) { return a.part + (static_cast<int64_t>(c) * 2 + (c == c0 ? tile.slot : 0)) * S::kPart; };
-    float m = -INFINITY, sum = 0.f;
-    float2 acc[VEC] = {};
-    // this share's parts
-    constexpr int BATCH = D == 256 ? 4 : 8;
-#pragma unroll 1
-    for (int c = c0 + share; live && c <= tile.last; c += BATCH * shares) {
-      float2 v[BATCH][VEC];
-      float pm = -INFINITY, pl = 0.f;
-      if (lane < BATCH && c + lane * shares <= tile.last) {
-        const float* p = part_of(c + lane * shares) + kRows * D + r;
-        pm = p[0];
-        pl = p[kRows];
-      }
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const float2* p = reinterpret_cast<const float2*>(part_of(c + i * shares) + r * D) + lane;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] = c + i * shares <= tile.last ? p[e * 32] : make_float2(0.f, 0.f);
-      }
-      float to = fmaxf(m, pm);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
-      const float old = ex2_from(m, to), w = ex2_from(pm, to);
-      m = to;
-      pl *= w;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) pl += __shfl_xor_sync(0xffffffffu, pl, off);
-      sum = sum * old + pl;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] = make_float2(acc[e].x * old, acc[e].y * old);
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          acc[e].x += v[i][e].x * wi;
-          acc[e].y += v[i][e].y * wi;
-        }
-      }
-    }
-    if (shares > 1) {
-      if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = sum;
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s_acc[warp][e][lane] = acc[e];
-      __syncthreads();
-      if (share == 0) {
-        const float pm = lane < shares ? s_m[warp + lane] : -INFINITY;
-        float to = pm;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
-        const float w = ex2_from(pm, to);
-        m = to;
-        sum = lane < shares ? s_l[warp + lane] * w : 0.f;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] = make_float2(0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < shares; ++i) {
-          const float wi = __shfl_sync(0xffffffffu, w, i);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float2 v = s_acc[warp + i][e][lane];
-            acc[e].x += v.x * wi;
-            acc[e].y += v.y * wi;
-          }
-        }
-      }
-      __syncthreads();
-    }
-    if (live && share == 0) {
-      const int tok = (tile.row0 + r) / a.group, head = tile.kvh * a.group + (tile.row0 + r) % a.group;
-      const float f = out_factor(a, sum);
-      __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + static_cast<int64_t>(tile.token0 + tok) * a.os +
-                                                              static_cast<int64_t>(head) * D);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) out[e * 32 + lane] = __floats2bfloat162_rn(acc[e].x * f, acc[e].y * f);
-      if (a.lse && lane == 0) store_lse(a, tile.token0 + tok, head, m, sum);
-    }
-  }
-}
 
 // Persistent CTAs: what the SMs hold at once.
 template <int D, int NB, bool BLOCKS> int ctas_for(int num_sms) {
   return std::min(num_sms, kMaxSms) * Shape<D, NB, BLOCKS>::kCtas;
 }
 
-// Kernels: a type whose of<D, NB>() is the few-row kernel.
+// Kernels: a type whose of<D, NB>() is the few-row kernel, and whose join<D, NB>()
+// launches the join of what its CTAs leave.
 template <int D, int NB, class Kernels, class Args>
 cudaError_t launch(const Args& a, int num_sms, cudaStream_t s) {
   using S = Shape<D, NB, Args::kBlocks>;
@@ -402,8 +258,7 @@ cudaError_t launch(const Args& a, int num_sms, cudaStream_t s) {
   count_launches(2);
   err = launch_pdl(kernel, ctas, kWarps * 32, smem, s, a);
   if (err != cudaSuccess) return err;
-  static_assert(kMaxSms * S::kCtas <= kMaxCtas && kMaxCtas <= kJoinWarps * 32, "a thread of the join for each CTA");
-  return launch_pdl(paged_attn_join<D, NB, Args>, ctas / S::kCtas, kJoinWarps * 32, 0, s, a, ctas);
+  return Kernels::template join<D, NB>(a, ctas, s);
 }
 
 // Row tiles of eight where no request has more rows: half the registers, more
@@ -430,7 +285,7 @@ template <bool BLOCKS> size_t part_bytes_of(int D) {
 
 // Which kernels a call takes, from what the host knows.
 struct Path {
-  bool tc;      // the tcgen05 kernel, for requests with more than kTcRows rows
+  bool tc;      // the tcgen05 kernel, for requests with more than TcRule::kRows rows
   bool alone;   // ... and it alone
   bool split;   // ... which may cut row blocks along the cached tokens
 };
@@ -470,17 +325,26 @@ struct Path {
 // allowed up to 4 kMaxSms of them.  The device then cuts what is longer than 1.5
 // shares (2 instead of 1.5: the same times to 1 us, with 8 x 512 at 3584, 4 x 1024 at
 // 32768, 2 x 2048 at 4096 to 65536, 3 x 512 at 2048 to 16384).
+//
+// Over the cache in 4 bits the few-row kernel is faster by what it reads less.
+// Measured (us, few-row / tcgen05; 4 x 8 x 128): 32 new tokens at 3584 20.7 / 32.1, at
+// 8192 (8.2 million pairs) 30.7 / 36.3, at 16384 47.2 / 43.1, at 65536 147 / 72; 64 at 3584
+// (7.5) 29.4 / 33.0; 256 at 1024 (10) 38.5 / 34.8; 16 x 16 at 3584 79.8 / 61.5; 64
+// requests of 64 rows each at 3584 151 / 159, at 1024 66 / 61.
 constexpr int kTileTokens = 256;
-constexpr int kTcRows = 48;                  // of a request and key head
+template <bool BLOCKS> struct TcRule {
+  static constexpr int kRows = BLOCKS ? 64 : 48;                                 // of a request and key head
+  static constexpr int64_t kWork = BLOCKS ? int64_t(9) << 20 : int64_t(6) << 20;   // pairs
+};
 constexpr int kTcTokens = 16384;
-constexpr int64_t kTcWork = int64_t(6) << 20;   // pairs
 
+template <bool BLOCKS>
 Path path_of(const PaArgs& a, int max_q_len) {
   const int64_t most = static_cast<int64_t>(max_q_len > 0 ? std::min(max_q_len, a.T) : a.T) * a.group;
   Path p;
   const int64_t rows = static_cast<int64_t>(a.T) * a.group * a.c.n_kv_heads;
   const int64_t tokens = std::min<int64_t>(static_cast<int64_t>(a.c.max_pages) * a.c.page_size, kTcTokens);
-  p.tc = most > kTcRows && rows * (tokens + kTileTokens) >= kTcWork && paged_attn_tc_supported(a.c.head_dim);
+  p.tc = most > TcRule<BLOCKS>::kRows && rows * (tokens + kTileTokens) >= TcRule<BLOCKS>::kWork && paged_attn_tc_supported(a.c.head_dim);
   // As many rows as if every request had max_q_len of them: they all do (or the
   // hint is wrong, and the tcgen05 kernel takes small ones too).
   p.alone = p.tc && static_cast<int64_t>(max_q_len) * a.B == a.T;
@@ -490,9 +354,9 @@ Path path_of(const PaArgs& a, int max_q_len) {
 
 template <class Kernels, class Args>
 cudaError_t launch_paged_attn(Args a, int max_q_len, int num_sms, cudaStream_t s) {
-  const Path path = path_of(a, max_q_len);
+  const Path path = path_of<Args::kBlocks>(a, max_q_len);
   const int64_t most = static_cast<int64_t>(max_q_len > 0 ? std::min(max_q_len, a.T) : a.T) * a.group;
-  a.tc_rows = path.alone ? 0 : path.tc ? kTcRows : INT_MAX;
+  a.tc_rows = path.alone ? 0 : path.tc ? TcRule<Args::kBlocks>::kRows : INT_MAX;
   a.tc_ctas = std::min(num_sms, kMaxSms);
   a.tc_split = path.split;
   cudaError_t err;
@@ -519,7 +383,7 @@ struct Workspace {
 template <class Args>
 Workspace plan_workspace(const Args& a, int max_q_len) {
   const int D = a.c.head_dim;
-  const Path path = path_of(a, max_q_len);
+  const Path path = path_of<Args::kBlocks>(a, max_q_len);
   Workspace w;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t from = at; at += align_up(bytes, 256); return from; };
