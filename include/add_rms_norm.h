@@ -10,7 +10,8 @@
  * once to its type, and to `out8` as E4M3 codes with one scale for a row or
  * for every `group` elements:
  *   s = max(max |y| / 448, 2^-40) over the group,  code = e4m3(y / s)
- * (nearest, ties to even; y / s as y times the fp32 reciprocal of s).  A NaN or
+ * (nearest, ties to even; y / s as y times the reciprocal of s, which like s is
+ * exact to a few units of fp32's last place).  A NaN or
  * infinite element of h makes NaN of its row's norm: y is NaN, or 0 where
  * finite elements meet an infinite mean, as the formula has it.  NaN elements
  * become the NaN code and are left out of their group's maximum; other rows
