@@ -106,6 +106,21 @@ def test_append(new, total, kw, rot, layout, norm, joint):
     check_append(bt, run_append(bt, rot, layout, norm, joint=joint), layout)
 
 
+@pytest.mark.parametrize("new,total,kw,rot,layout,norm", [
+    ([270, 1], [285, 40], dict(Hq=5, Hkv=5, D=64), 24, "half", True),
+    ([270, 1], [285, 40], dict(Hq=1, Hkv=6, D=64, page=32, order="nhd"), 40, "interleaved", True),
+    ([1, 300], [17, 300], dict(Hq=2, Hkv=3, D=128, page=64), 128, "half", False),
+    ([1, 300], [17, 300], dict(Hq=2, Hkv=1, D=128), 128, "interleaved", False),
+    ([260], [263], dict(Hq=1, Hkv=2, D=256, page=128), 192, "half", True),
+    ([260], [263], dict(Hq=1, Hkv=2, D=256), 72, "interleaved", True),
+    ([1] * 257, [1 + 5 * i % 61 for i in range(257)], dict(Hq=2, Hkv=2, D=64), 64, "half", True),
+])
+def test_append_many_tokens(new, total, kw, rot, layout, norm):
+    """Over 256 tokens a thread works on four heads at a time."""
+    bt = BlockBatch(new, total, seed=rot, **kw)
+    check_append(bt, run_append(bt, rot, layout, norm, joint=rot % 3 == 0), layout)
+
+
 def test_append_without_queries_and_with_positions():
     bt = BlockBatch([9, 4], [30, 4], seed=3)
     pos = np.array([3, 1, 4, 1, 5, 9, 2, 6, 5, 0, 33, 8, 7], dtype=np.int32)
@@ -482,6 +497,34 @@ def test_attention_pages_out_of_the_cache(new, total, pages, kw, bad):
         for b, (o, l, vmax) in enumerate(ref):
             at = slice(bt.cu[b], bt.cu[b + 1])
             compare(values64(out)[at], values64(lse)[at], o, l, vmax)
+
+
+@pytest.mark.parametrize("bad", [None, -1, -2 ** 31])
+@pytest.mark.parametrize("n,D,Hq", [(2, 64, 4), (2, 128, 4), (2, 256, 4), (5, 128, 3), (3, 64, 5)])
+def test_attention_many_requests(n, D, Hq, bad):
+    """Pieces of several units and of several requests, most units without masks; pages missing among them."""
+    lengths = [1500, 1499, 1281, 1280, 1279, 700, 129, 128, 40, n, 1]
+    one = BlockBatch([n], [1500], Hq=Hq, Hkv=1, D=D, seed=32)
+    pages = [] if bad is None else [0, 20, 41, 42, 43, 44, 93]
+    hidden = {j for p in pages for j in range(16 * p, 16 * p + 16)}
+    ref = []
+    for length in lengths:
+        one.kv_len[0] = length
+        ref.append(hide(one, 0, hidden) if pages else
+                   (*do.paged_attention(one.oracle_cache(), values64(one.q), one.cu, one.kv_len, D ** -0.5), one.vmax()))
+    if pages:
+        one.table[0, pages] = bad
+    bt, B = one, 60 * len(lengths)
+    bt.B, bt.T, bt.q = B, n * B, one.q.repeat(B, 1, 1)
+    bt.cu = np.arange(0, n * B + 1, n).astype(np.int32)
+    bt.kv_len = np.array(lengths * 60, dtype=np.int32)
+    bt.table = np.repeat(one.table, B, 0)
+    out, lse, st = run_attention(bt, max_q_len=n)
+    assert st == (BOUNDS if pages else 0)
+    out, lse = values64(out).reshape(60, len(lengths), n, Hq, D), values64(lse).reshape(60, len(lengths), n, Hq)
+    for i, (o, l, vmax) in enumerate(ref):
+        for k in range(60):
+            compare(out[k, i], lse[k, i], o, l, vmax)
 
 
 def test_attention_offsets_out_of_order():

@@ -5,7 +5,9 @@
 // request and page, then a thread takes the codes of 16 elements (eight bytes)
 // and their scale at a time and writes 32 bytes (fp32: 64), so that neighbouring
 // threads write beside each other; what it reads of keys and values is on its way
-// together.  Bound by memory: 0.56 bytes read and 2 (or 4) written an element.
+// together.  Bound by memory: 0.56 bytes read and 2 (or 4) written an element; 64
+// requests of up to 3712 tokens, 4 heads of 128, 312 MB in 49.5 us = 6.3 TB/s (16 bytes an
+// access, keys before values: 72 us).
 // Request b's blocks start at cu[b]/16 + 2b, as in kv_append.cu.
 #include "block_kv.cuh"
 #include "paged_attn.cuh"

@@ -42,7 +42,7 @@
 // issue of instructions (conversion and weights) and the row tiles' starts; 64 at
 // 3584, 4 x 8 x 256, 470 MB in 93 us = 5.0 TB/s.
 // Registers spilled (bytes stored, D / blocks of rows): 64/1 60, 64/2 48, 128/2 92,
-// 256/1 76, outside the loop over the units; 128/1 none.
+// 128/1 24, 256/1 76, outside the loop over the units.
 #include "paged_attn_rows.cuh"
 
 namespace moe {

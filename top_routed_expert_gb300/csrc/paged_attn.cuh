@@ -12,7 +12,7 @@ struct JoinTile {
   int rows, token0, row0, kvh, slot, last;
 };
 
-// The row blocks of paged_attn_tc.cu: part `part` of `parts` of block `blk` of
+// The row blocks of paged_attn_tc.cuh: part `part` of `parts` of block `blk` of
 // request `b`; the parts of a cut block, for key head h, leave their sums in
 // slots (slot + part) n_kv_heads + h.
 struct TcList {
@@ -34,7 +34,7 @@ struct PaArgs {
   const int32_t* kv_len;
   float* part;          // workspace: partial sums,
   JoinTile* joins;      // the row tile that each CTA leaves to others to finish,
-  TcList* tc;           // and for paged_attn_tc.cu the list of its row blocks
+  TcList* tc;           // and for paged_attn_tc.cuh the list of its row blocks
   TcEntry* tc_entries;
   TcJoin* tc_joins;     // ... those cut along the cached tokens,
   float* tc_part;       // and their partial sums: rows of D outputs, then (reference, sum) pairs
@@ -42,7 +42,7 @@ struct PaArgs {
   unsigned* status;
   int64_t qs, os;
   int T, B, group, window, n_sink;
-  int tc_rows;          // requests with more rows (tokens x heads of the group) go to paged_attn_tc.cu
+  int tc_rows;          // requests with more rows (tokens x heads of the group) go to paged_attn_tc.cuh
   int tc_ctas;          // its CTAs
   bool tc_split;        // whether row blocks may be cut
   float sm_scale;
@@ -64,7 +64,7 @@ template <class Args> __device__ __forceinline__ float out_factor(const Args& a,
   else return sum == 0.f ? 0.f : 1.0f / sum;
 }
 
-constexpr int kTcItemRows = 256;   // rows of an item of paged_attn_tc.cu
+constexpr int kTcItemRows = 256;   // rows of an item of paged_attn_tc.cuh
 constexpr int kTcStep = 128;       // cached tokens of its steps
 
 // The most CTAs, and the most slots of cut row blocks: a part is at least 3/4 of

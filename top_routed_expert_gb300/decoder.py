@@ -89,7 +89,7 @@ class PagedBlockKVCache(PagedKVCache):
     """The same in 4 bits: E2M1 codes with an E4M3 scale for every 16 elements
     of a token's head (include/block_kv.h), 9/16 of the memory.  k_gscale and
     v_gscale, powers of two, are the unit that the scales count in: a block
-    whose largest element lies outside 3/256 .. 2688 times that loses precision."""
+    whose largest element lies outside 3/32 .. 2688 times that loses precision."""
 
     def __init__(self, *args, k_gscale: float = 1.0, v_gscale: float = 1.0, **kw):
         self.gscales = k_gscale, v_gscale
