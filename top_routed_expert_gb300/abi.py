@@ -506,9 +506,10 @@ def moe_blockkv_read(cfg, cache, cu, kv_len, k_out, v_out, stream=None):
     B = cfg.batch
     if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
         raise ValueError(_RAGGED)
+    n, dtype = cfg.T * cfg.row, cfg.dtype
     if not ((cfg.heads == cache.heads or cfg.heads is None or cache.heads is None)
-            and all(t is None or t.nbytes >= cfg.T * cfg.row and (cfg.dtype is None or t.dtype is cfg.dtype)
-                    for t in (k_out, v_out))):
+            and (k_out is None or k_out.nbytes >= n and (k_out.dtype is dtype or dtype is None))
+            and (v_out is None or v_out.nbytes >= n and (v_out.dtype is dtype or dtype is None))):
         raise ValueError("k_out and v_out: rows of the configuration's shape and type and the cache's heads")
     code = load().moe_blockkv_read(cfg, cache, cu.data_ptr(), kv_len.data_ptr(), None if k_out is None else k_out.data_ptr(),
                                    None if v_out is None else v_out.data_ptr(),
