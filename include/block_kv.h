@@ -2,7 +2,7 @@
  * block_kv.h -- C ABI of a paged key/value cache in 4 bits, the attention that
  * reads it and the way back (libmoe_gb300.so; status codes, element types and
  * stream type from moe_gb300.h, append and attention configurations from
- * paged_kv.h).
+ * paged_kv.h; the calls of this header take up to 2^20 requests).
  *
  * The cache holds, for every token and key head, D values as E2M1 codes with
  * one E4M3 scale for every 16 consecutive elements and a factor g for the
@@ -106,7 +106,7 @@ moe_status_t moe_blockkv_attention(const moe_paged_attention_config_t* cfg, cons
 
 typedef struct {
   int32_t T;            /* rows of k_out and v_out, >= 0 (0 is a no-op)              */
-  int32_t batch;        /* requests, 1..4096                                        */
+  int32_t batch;        /* requests, 1..2^20                                        */
   int32_t out_dtype;    /* MOE_BF16 or MOE_F32                                      */
   int64_t k_stride;     /* elements between rows of k_out and of v_out (multiples of */
   int64_t v_stride;     /*   8; heads of a row are contiguous)                      */

@@ -70,7 +70,7 @@ def test_caches_refused(lib, bad):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(T=-1), dict(batch=0), dict(batch=4097), dict(n_q_heads=0), dict(rot_dim=12), dict(rot_dim=136), dict(rope_layout=2),
+    dict(T=-1), dict(batch=0), dict(batch=2 ** 20 + 1), dict(n_q_heads=0), dict(rot_dim=12), dict(rot_dim=136), dict(rope_layout=2),
     dict(n_pos=0), dict(eps=0.0), dict(eps=math.nan), dict(q_stride=4088), dict(k_stride=504), dict(v_stride=513),
     dict(q_out_stride=0),
 ])
@@ -91,7 +91,7 @@ def test_append_refuses_pointers(lib):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(T=-1), dict(batch=0), dict(n_q_heads=30), dict(n_q_heads=1028), dict(max_q_len=-1), dict(window=-1),
+    dict(T=-1), dict(batch=0), dict(batch=2 ** 20 + 1), dict(n_q_heads=30), dict(n_q_heads=1028), dict(max_q_len=-1), dict(window=-1),
     dict(n_sink=-1), dict(sm_scale=0.0), dict(sm_scale=math.inf), dict(q_stride=4088), dict(out_stride=4097),
     dict(T=1 << 28, n_q_heads=32),
 ])
@@ -128,7 +128,7 @@ def test_workspace_never_shrinks(lib, head_dim):
         last = size(T=T, batch=64, max_q_len=0)
 
 
-@pytest.mark.parametrize("bad", [dict(T=-1), dict(batch=0), dict(batch=4097), dict(out_dtype=abi.MOE_E4M3), dict(k_stride=504),
+@pytest.mark.parametrize("bad", [dict(T=-1), dict(batch=0), dict(batch=2 ** 20 + 1), dict(out_dtype=abi.MOE_E4M3), dict(k_stride=504),
                                  dict(v_stride=504), dict(k_stride=516)])
 def test_read_refuses(lib, bad):
     assert read(lib, cfg=read_cfg(**bad)) == 1

@@ -527,6 +527,48 @@ def test_attention_many_requests(n, D, Hq, bad):
             compare(out[k, i], lse[k, i], o, l, vmax)
 
 
+def repeated(bt, times):
+    """The batch `times` over, each with pages of its own."""
+    n = bt.n_pages
+    bt.table = np.concatenate([np.where(bt.table < 0, -1, bt.table + i * n) for i in range(times)]).astype(np.int32)
+    bt.cu = np.concatenate([[0]] + [bt.cu[1:] + i * bt.T for i in range(times)]).astype(np.int32)
+    bt.new, bt.total, bt.kv_len = bt.new * times, bt.total * times, np.tile(bt.kv_len, times)
+    for of in (bt.codes, bt.scales):
+        for name in "kv":
+            of[name] = np.tile(of[name], (times, 1, 1, 1))
+    bt.q, bt.k, bt.v = (x.repeat(times, 1, 1) for x in (bt.q, bt.k, bt.v))
+    bt.B, bt.T, bt.n_pages = bt.B * times, bt.T * times, n * times
+
+
+@pytest.mark.parametrize("new,total,kw,hint", [
+    ([1, 2, 0, 1, 1], [40, 16, 9, 130, 1], dict(D=64, Hq=2, Hkv=1), 2),
+    ([1, 2, 0, 1, 1], [40, 16, 9, 130, 1], dict(D=128, Hq=2, Hkv=1), 0),
+    ([17, 18, 1, 16], [34, 18, 200, 133], dict(D=64, Hq=4, Hkv=1), 18),
+    ([17, 17, 17], [34, 17, 140], dict(D=128, Hq=4, Hkv=1), 17),
+])
+def test_more_requests_than_a_launch_takes(new, total, kw, hint):
+    """Slices of 4096 requests, the last one short: of few rows, mixed, and of equal prompts."""
+    times = 8200 // len(new)
+    bt = BlockBatch(new, total, seed=33, **kw)
+    ref_o, ref_l = do.paged_attention(bt.oracle_cache(), values64(bt.q), bt.cu, bt.kv_len, bt.D ** -0.5)
+    base = run_append(bt, bt.D), run_read(bt, torch.float32)[0]
+    n_pages, vmax = bt.n_pages, bt.vmax()
+    repeated(bt, times)
+    assert bt.B > 2 * 4096
+    out, lse, st = run_attention(bt, max_q_len=hint)
+    assert st == 0
+    compare(values64(out).reshape(times, *ref_o.shape), values64(lse).reshape(times, *ref_l.shape), ref_o[None].repeat(times, 0),
+            ref_l[None].repeat(times, 0), vmax)
+    got = run_append(bt, bt.D), run_read(bt, torch.float32)[0]
+    assert got[0]["st"] == 0
+    assert torch.equal(got[0]["q_out"], base[0]["q_out"].repeat(times, 1, 1))
+    for a, b in zip(got[1], base[1]):
+        assert torch.equal(a, b.repeat(times, 1, 1))
+    for i in range(4):
+        a, b = host(got[0]["cache"][i]), host(base[0]["cache"][i])
+        assert np.array_equal(a.reshape(times, *b.shape), b[None].repeat(times, 0))
+
+
 def test_attention_offsets_out_of_order():
     bt = BlockBatch([1, 2], [100, 60], seed=15)
     bt.cu[1] = 9                                          # past T

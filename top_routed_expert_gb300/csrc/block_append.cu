@@ -481,7 +481,7 @@ extern "C" moe_status_t moe_blockkv_append(const moe_kv_append_config_t* cfg, co
   using namespace moe;
   if (!cfg || !blockkv_shape_ok(cache)) return MOE_ERR_INVALID_ARG;
   const int D = cache->head_dim;
-  if (!append_config_ok(cfg, cache->n_kv_heads, D, q, gamma_q, q_out)) return MOE_ERR_INVALID_ARG;
+  if (!append_config_ok(cfg, kMaxBlockBatch, cache->n_kv_heads, D, q, gamma_q, q_out)) return MOE_ERR_INVALID_ARG;
   if (cfg->T == 0) return MOE_OK;
   if (!blockkv_pointers_ok(cache) || !append_pointers_ok(cfg, k, v, gamma_k, cos_sin, positions, cu, kv_len))
     return MOE_ERR_INVALID_ARG;

@@ -573,7 +573,7 @@ struct Kernels {
 };
 
 bool config_ok(const moe_paged_attention_config_t* cfg, const moe_blockkv_cache_t* cache) {
-  return cfg && blockkv_shape_ok(cache) && attention_config_ok(cfg, cache->n_kv_heads, cache->head_dim);
+  return cfg && blockkv_shape_ok(cache) && attention_config_ok(cfg, kMaxBlockBatch, cache->n_kv_heads, cache->head_dim);
 }
 
 BlockPaArgs args_of(const moe_blockkv_cache_t* cache) {

@@ -6,6 +6,8 @@
 
 namespace moe {
 
+constexpr int kMaxBlockBatch = 1 << 20;
+
 // A power of two from 2^-60 to 2^60.
 inline bool gscale_ok(float g) {
   int e;

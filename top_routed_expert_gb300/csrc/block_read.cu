@@ -159,7 +159,7 @@ extern "C" moe_status_t moe_blockkv_read(const moe_blockkv_read_config_t* cfg, c
                                          moe_stream_t stream) {
   using namespace moe;
   if (!cfg || !blockkv_shape_ok(cache)) return MOE_ERR_INVALID_ARG;
-  if (cfg->T < 0 || cfg->T > (1 << 28) || cfg->batch < 1 || cfg->batch > kMaxBatch) return MOE_ERR_INVALID_ARG;
+  if (cfg->T < 0 || cfg->T > (1 << 28) || cfg->batch < 1 || cfg->batch > kMaxBlockBatch) return MOE_ERR_INVALID_ARG;
   if (cfg->out_dtype != MOE_BF16 && cfg->out_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
   const int64_t width = static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim;
   if (k_out && (cfg->k_stride < width || cfg->k_stride % 8 != 0 || !aligned_to(k_out, 16))) return MOE_ERR_INVALID_ARG;

@@ -317,7 +317,7 @@ extern "C" moe_status_t moe_kv_append(const moe_kv_append_config_t* cfg, const m
   using namespace moe;
   if (!cfg || !kv_cache_shape_ok(cache)) return MOE_ERR_INVALID_ARG;
   const int D = cache->head_dim;
-  if (!append_config_ok(cfg, cache->n_kv_heads, D, q, gamma_q, q_out)) return MOE_ERR_INVALID_ARG;
+  if (!append_config_ok(cfg, kMaxBatch, cache->n_kv_heads, D, q, gamma_q, q_out)) return MOE_ERR_INVALID_ARG;
   if (cfg->T == 0) return MOE_OK;
   if (!kv_cache_pointers_ok(cache) || !append_pointers_ok(cfg, k, v, gamma_k, cos_sin, positions, cu, kv_len))
     return MOE_ERR_INVALID_ARG;

@@ -232,10 +232,10 @@ template <int D> __host__ __device__ __forceinline__ int query_tokens(int Hq, in
 
 // What a call has to fulfil before anything is launched: the configuration and
 // q's arguments, then (T > 0) the pointers.
-inline bool append_config_ok(const moe_kv_append_config_t* cfg, int heads, int D, const void* q, const float* gamma_q,
-                             const void* q_out) {
+inline bool append_config_ok(const moe_kv_append_config_t* cfg, int max_batch, int heads, int D, const void* q,
+                             const float* gamma_q, const void* q_out) {
   auto stride_ok = [](int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; };
-  if (cfg->T < 0 || cfg->T > (1 << 28) || cfg->batch < 1 || cfg->batch > kMaxBatch) return false;
+  if (cfg->T < 0 || cfg->T > (1 << 28) || cfg->batch < 1 || cfg->batch > max_batch) return false;
   if (cfg->rot_dim < 0 || cfg->rot_dim > D || cfg->rot_dim % 8 != 0) return false;
   if (cfg->rope_layout != MOE_ROPE_HALF && cfg->rope_layout != MOE_ROPE_INTERLEAVED) return false;
   if (cfg->rot_dim > 0 && cfg->n_pos < 1) return false;

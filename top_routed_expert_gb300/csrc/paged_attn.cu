@@ -583,7 +583,7 @@ struct Kernels {
 };
 
 bool config_ok(const moe_paged_attention_config_t* cfg, const moe_kv_cache_t* cache) {
-  return cfg && kv_cache_shape_ok(cache) && attention_config_ok(cfg, cache->n_kv_heads, cache->head_dim);
+  return cfg && kv_cache_shape_ok(cache) && attention_config_ok(cfg, kMaxBatch, cache->n_kv_heads, cache->head_dim);
 }
 
 }  // namespace

@@ -71,8 +71,10 @@ constexpr int kTcStep = 128;       // cached tokens of its steps
 // 1/tc_ctas of the work, so that all parts are at most 4/3 of the CTAs.
 constexpr int kMaxSms = 160, kTcSlots = kMaxSms * 4 / 3 + 1;
 
-// The most row blocks that the requests can have, for one key head.
-__host__ __device__ inline int64_t tc_places(const PaArgs& a) { return static_cast<int64_t>(a.T) * a.group / kTcItemRows + a.B; }
+// The most row blocks that the requests of a launch can have, for one key head.
+__host__ __device__ inline int64_t tc_places(const PaArgs& a) {
+  return static_cast<int64_t>(a.T) * a.group / kTcItemRows + (a.B < kMaxBatch ? a.B : kMaxBatch);
+}
 
 // Cached tokens that the new tokens of a request can see, in blocks of `unit`
 // tokens: the blocks with the first visible positions of a window's sinks,

@@ -352,13 +352,10 @@ Path path_of(const PaArgs& a, int max_q_len) {
   return p;
 }
 
+// At most kMaxBatch requests: the tables of the requests are in shared memory.
 template <class Kernels, class Args>
-cudaError_t launch_paged_attn(Args a, int max_q_len, int num_sms, cudaStream_t s) {
-  const Path path = path_of<Args::kBlocks>(a, max_q_len);
+cudaError_t launch_requests(const Args& a, const Path& path, int max_q_len, int num_sms, cudaStream_t s) {
   const int64_t most = static_cast<int64_t>(max_q_len > 0 ? std::min(max_q_len, a.T) : a.T) * a.group;
-  a.tc_rows = path.alone ? 0 : path.tc ? TcRule<Args::kBlocks>::kRows : INT_MAX;
-  a.tc_ctas = std::min(num_sms, kMaxSms);
-  a.tc_split = path.split;
   cudaError_t err;
   if (path.alone) {
     count_launches(1);
@@ -373,9 +370,28 @@ cudaError_t launch_paged_attn(Args a, int max_q_len, int num_sms, cudaStream_t s
   return err == cudaSuccess && path.tc ? launch_paged_attn_tc(a, s) : err;
 }
 
+// Larger batches in slices of kMaxBatch requests, one after the other (the rows
+// of a request are where cu says, so that only the requests' arrays move on).
+template <class Kernels, class Args>
+cudaError_t launch_paged_attn(Args a, int max_q_len, int num_sms, cudaStream_t s) {
+  const Path path = path_of<Args::kBlocks>(a, max_q_len);
+  a.tc_rows = path.alone ? 0 : path.tc ? TcRule<Args::kBlocks>::kRows : INT_MAX;
+  a.tc_ctas = std::min(num_sms, kMaxSms);
+  a.tc_split = path.split;
+  cudaError_t err = cudaSuccess;
+  for (int left = a.B; left > 0 && err == cudaSuccess; left -= kMaxBatch) {
+    a.B = std::min(left, kMaxBatch);
+    err = launch_requests<Kernels>(a, path, max_q_len, num_sms, s);
+    a.cu += a.B;
+    a.kv_len += a.B;
+    a.c.page_table += static_cast<int64_t>(a.B) * a.c.max_pages;
+  }
+  return err;
+}
+
 // Workspace: partial sums and the row tiles to join, then what the tcgen05
 // kernel needs where a call can take it (cut blocks or not, alone or not, so
-// that a smaller call never needs more).
+// that a smaller call never needs more).  A larger batch's slices share it.
 struct Workspace {
   size_t joins, tc, tc_entries, tc_joins, tc_part, total;
 };
@@ -397,8 +413,8 @@ Workspace plan_workspace(const Args& a, int max_q_len) {
   return w;
 }
 
-bool attention_config_ok(const moe_paged_attention_config_t* c, int n_kv_heads, int head_dim) {
-  if (c->T < 0 || c->T > (1 << 28) || c->batch < 1 || c->batch > kMaxBatch || c->max_q_len < 0) return false;
+bool attention_config_ok(const moe_paged_attention_config_t* c, int max_batch, int n_kv_heads, int head_dim) {
+  if (c->T < 0 || c->T > (1 << 28) || c->batch < 1 || c->batch > max_batch || c->max_q_len < 0) return false;
   if (c->n_q_heads < 1 || c->n_q_heads % n_kv_heads != 0 || c->n_q_heads / n_kv_heads > 256) return false;
   // row and item counts are 32-bit
   const int64_t rows = static_cast<int64_t>(c->T) * (c->n_q_heads / n_kv_heads);
