@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
   const uint32_t ring = ptx::smem_u32(smem) + warp * S::kRing;
   const int ps = a.c.page_size, ps_log = 31 - __clz(ps);
   const int64_t ts = a.c.token_stride;
+  // x / group is (x per_group) >> 20 for x < group + 16 <= 272: 272 * 255 < 2^20
+  const int per_group = ((1 << 20) + a.group - 1) / a.group;
   // this lane's 16-byte chunks of a tile: token (+ RSTEP each) and chunk
   constexpr int CPR = D / 32, RSTEP = 32 / CPR, COPIES = 16 / RSTEP;
   const int crow = lane / CPR, cchunk = lane % CPR;
@@ -105,9 +107,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
   Request rq = {};
   for (int64_t at = first; at < last;) {
     // the row tile at `at`, and the piece of it that is this CTA's
-    const int b_now = find_entry(s_start, a.B, at);
-    if (b_now != b) {
-      b = b_now;
+    if (b < 0 || at >= s_start[b + 1]) {
+      b = find_entry(s_start, a.B, at);
       rq = load_request(a.cu, a.kv_len, b, a.T);
     }
     const Span sp = span_of(a, rq, kUnit);
@@ -126,6 +127,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
     const int rts = ceil_div(rq.n * a.group, kRows);
     const int kvh = tile / rts, row0 = (tile - kvh * rts) * kRows;
     const int rows = min(kRows, rq.n * a.group - row0);
+    const int tok0 = row0 / a.group, head0 = row0 - tok0 * a.group;
+    auto tok_of = [&](int r) { return ((head0 + r) * per_group) >> 20; };   // row r's token, from tok0 on
     const bool whole = u0 == 0 && u1 == sp.units;
     if (u0 == 0 && !whole) cut = JoinTile{rows, rq.row0, row0, kvh, slot, static_cast<int>((tile_end * pieces - 1) / total)};
 
@@ -133,10 +136,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
     uint4 raw[NB][KC][2];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      const int r = row0 + 8 * n + g;
       const bool live = 8 * n + g < rows;
-      const uint16_t* src = a.q + static_cast<int64_t>(rq.row0 + (live ? r / a.group : 0)) * a.qs +
-                            static_cast<int64_t>(kvh * a.group + (live ? r % a.group : 0)) * D + t * 16;
+      const int r = live ? 8 * n + g : 0, tok = tok_of(r);
+      const uint16_t* src = a.q + static_cast<int64_t>(rq.row0 + tok0 + tok) * a.qs +
+                            static_cast<int64_t>(kvh * a.group + (head0 + r - tok * a.group)) * D + t * 16;
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
           raw[n][c][i] = live ? __ldg(reinterpret_cast<const uint4*>(src + c * 64 + i * 8)) : make_uint4(0, 0, 0, 0);
     }
 
-    const int pos_min = rq.start + row0 / a.group, pos_max = rq.start + (row0 + rows - 1) / a.group;
+    const int pos_min = rq.start + tok0, pos_max = pos_min + tok_of(rows - 1);
     // units [ua, ub): the tile's rows all see all of them
     const int from = sp.window ? max(0, pos_max - sp.window + kUnit) / kUnit : 0;
     const int ua = sp.sink_blocks + max(from - sp.lo_block, 0);
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
       for (int h = 0; h < 2; ++h) {
         const int r = 8 * n + 2 * t + h;
         rf[n][h] = score_factor(a.kg, a.sm_scale * kLog2e / __shfl_sync(0xffffffffu, f, (2 * t + h) * 4));
-        pos[n][h] = r < rows ? rq.start + (row0 + r) / a.group : -1;
+        pos[n][h] = r < rows ? pos_min + tok_of(r) : -1;
         // a row that sees nothing at all needs no reference
         shift[n][h] = pos[n][h] >= 0 ? kNone : 0.f;
         l[n][h] = 0.f;
@@ -473,8 +476,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
         acc.w += x.w * f;
       }
       if (whole) {
-        const int tok = (row0 + r) / a.group, head = kvh * a.group + (row0 + r) % a.group;
-        store_row4(a, rq.row0 + tok, head, D, d, acc, mm, sum);
+        const int tok = tok_of(r), head = kvh * a.group + (head0 + r - tok * a.group);
+        store_row4(a, rq.row0 + tok0 + tok, head, D, d, acc, mm, sum);
       } else {
         float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::kPart;
         *reinterpret_cast<float4*>(part + r * D + d) = acc;

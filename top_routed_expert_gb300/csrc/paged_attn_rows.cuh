@@ -333,7 +333,7 @@ struct Path {
 // requests of 64 rows each at 3584 151 / 159, at 1024 66 / 61.
 constexpr int kTileTokens = 256;
 template <bool BLOCKS> struct TcRule {
-  static constexpr int kRows = BLOCKS ? 64 : 48;                                 // of a request and key head
+  static constexpr int kRows = 48;                                               // of a request and key head
   static constexpr int64_t kWork = BLOCKS ? int64_t(9) << 20 : int64_t(6) << 20;   // pairs
 };
 constexpr int kTcTokens = 16384;
