@@ -105,13 +105,14 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
 
   int b = -1;
   Request rq = {};
+  Span sp = {};
   for (int64_t at = first; at < last;) {
     // the row tile at `at`, and the piece of it that is this CTA's
     if (b < 0 || at >= s_start[b + 1]) {
       b = find_entry(s_start, a.B, at);
       rq = load_request(a.cu, a.kv_len, b, a.T);
+      sp = span_of(a, rq, kUnit);
     }
-    const Span sp = span_of(a, rq, kUnit);
     const int64_t in_b = at - s_start[b];
     const int width = sp.units + kTileCost;
     int tile;   // (key head, row tile)
@@ -462,11 +463,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
       float mm = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
+      const float ref = mm == -INFINITY ? 0.f : mm;   // no weights at all: each factor is 0
       float sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2_from(s_m[w][r], mm);
+        const float f = ex2(s_m[w][r] - ref);
         sum += s_l[w][r] * f;
         const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + w * (S::kRing / 4) + r * D +
                                                           (d ^ ((r & 7) << 2)));
