@@ -388,6 +388,21 @@ def test_attention_few_rows(new, total, kw, hint):
     check_attention(BlockBatch(new, total, seed=sum(total), **kw), max_q_len=max(new) if hint else 0)
 
 
+@pytest.mark.parametrize("new,total,kw", FEW)
+@pytest.mark.parametrize("window", [0, 600])
+def test_attention_few_rows_cut(new, total, kw, window):
+    """Page tables and windows of over 512 tokens: row tiles may be cut."""
+    check_attention(BlockBatch(new, total, seed=sum(total), extra_width=640 // kw.get("page", 16), **kw), window, 2, max_q_len=max(new))
+
+
+@pytest.mark.parametrize("new,total,kw", [([1, 1], [3000, 500], dict(D=64)), ([2], [1500], dict(D=256, Hkv=1)),
+                                          ([4, 3, 1], [1300, 3, 2000], dict(page=64)), ([30], [900], dict(D=128, Hq=2))])
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (130, 0), (400, 60), (477, 5), (3, 130)])
+def test_attention_few_rows_short_windows(new, total, kw, window, n_sink):
+    """Windows of up to 512 tokens in long contexts: row tiles stay whole."""
+    check_attention(BlockBatch(new, total, seed=sum(total), **kw), window, n_sink, max_q_len=max(new))
+
+
 @pytest.mark.parametrize("window,n_sink", [(1, 0), (1, 1), (16, 4), (40, 0), (64, 70), (129, 5), (10 ** 6, 3)])
 @pytest.mark.parametrize("new,total,kw", [FEW[2], FEW[5], FEW[9], FEW[7]])
 def test_attention_few_rows_window(new, total, kw, window, n_sink):

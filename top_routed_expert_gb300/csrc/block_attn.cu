@@ -35,9 +35,13 @@
 // Measured (key heads x query heads of a group x D): 12 requests at 49157 to 65536
 // tokens, 4 x 8 x 128, 397 MB in 77 us = 5.1 TB/s, of which 3 are the join and about 7
 // what every call has; each further request of 57000 tokens takes 6.1 us, 0.81 of
-// the rate of memory.  64 at 17 to 3712, 70 MB in 25.8 us; one at 3585 10.5 us; 48 drafts
-// of up to 4 tokens in a window of 1024, 8 x 4 x 64, 24.7 us; 64 at 3584, 4 x 8 x 256, 56 us.
-// No registers are spilled.
+// the rate of memory.  64 at 17 to 3712, 70 MB in 25.5 us; one at 3585 10.3 us; 48 drafts
+// of up to 4 tokens in a window of 1024, 8 x 4 x 64, 22.8 us; 64 at 3584, 4 x 8 x 256, 56 us.
+// A row tile that is short and new costs about 2300 instructions of a warp beside
+// its steps: 256 requests of 4 x 8 rows at 40 tokens (2048 row tiles) take 45 us, 36 %
+// of the issue slots (loading the next row tile's request, q, pages and first codes
+// during the join of the last one: 47).  No registers are spilled but three words at
+// D = 64 with 16 rows, outside the loop over the tokens.
 #include "block_kv.cuh"
 #include "paged_attn_rows.cuh"
 
@@ -119,12 +123,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
     if (in_b <= 0x7fffffff) tile = static_cast<int>(in_b) / width;
     else tile = static_cast<int>(in_b / width);
     const int v0 = static_cast<int>(in_b - static_cast<int64_t>(tile) * width);
-    const int v1 = static_cast<int>(min(static_cast<int64_t>(width), v0 + (last - at)));
+    // a row tile that is not cut is the CTA's in whose piece it begins
+    const int v1 = a.whole_tiles ? width : static_cast<int>(min(static_cast<int64_t>(width), v0 + (last - at)));
     const int u0 = max(v0 - kTileCost, 0), u1 = v1 - kTileCost;
     const int64_t tile_end = at + (width - v0);
     const int slot = at == first ? 0 : 1;
     at += v1 - v0;
-    if (u1 <= u0) continue;   // the next CTA begins it
+    if (u1 <= u0 || (a.whole_tiles && v0 > 0)) continue;   // the next CTA begins it, or the one before has it
     const int rts = ceil_div(rq.n * a.group, kRows);
     const int kvh = tile / rts, row0 = (tile - kvh * rts) * kRows;
     const int rows = min(kRows, rq.n * a.group - row0);

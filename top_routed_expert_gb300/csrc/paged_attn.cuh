@@ -56,6 +56,7 @@ struct BlockPaArgs : PaArgs {
   uint32_t page16, page_s;   // page strides in units of 16 bytes, and of D / 16
   int64_t scale_page, scale_head, scale_token;   // strides of the scales
   float kg, vg;                                  // factors of keys and values
+  bool whole_tiles;                              // row tiles are not cut, and nothing is joined
 };
 
 // What a row's outputs are multiplied by: 1 / sum, and the values' factor.

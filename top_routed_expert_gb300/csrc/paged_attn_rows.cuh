@@ -255,9 +255,11 @@ cudaError_t launch(const Args& a, int num_sms, cudaStream_t s) {
   cudaError_t err = ensure_kernel_attrs(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   const int ctas = ctas_for<D, NB, Args::kBlocks>(num_sms);
-  count_launches(2);
+  bool join = true;
+  if constexpr (Args::kBlocks) join = !a.whole_tiles;
+  count_launches(1 + join);
   err = launch_pdl(kernel, ctas, kWarps * 32, smem, s, a);
-  if (err != cudaSuccess) return err;
+  if (err != cudaSuccess || !join) return err;
   return Kernels::template join<D, NB>(a, ctas, s);
 }
 
@@ -330,13 +332,30 @@ struct Path {
 // Measured (us, few-row / tcgen05; 4 x 8 x 128): 32 new tokens at 3584 20.7 / 32.1, at
 // 8192 (8.2 million pairs) 30.7 / 36.3, at 16384 47.2 / 43.1, at 65536 147 / 72; 64 at 3584
 // (7.5) 29.4 / 33.0; 256 at 1024 (10) 38.5 / 34.8; 16 x 16 at 3584 79.8 / 61.5; 64
-// requests of 64 rows each at 3584 151 / 159, at 1024 66 / 61.
+// requests of 64 rows each at 3584 151 / 159, at 1024 66 / 61; 256 of 64 rows at 40 108 /
+// 62, at 300 146 / 103; 8 x 1 x 128: 256 of 40 rows at 60 127 / 134, 64 of 20 at 1000 60 / 110.
 constexpr int kTileTokens = 256;
 template <bool BLOCKS> struct TcRule {
-  static constexpr int kRows = 48;                                               // of a request and key head
+  static constexpr int kRows = 48;                                                 // of a request and key head
   static constexpr int64_t kWork = BLOCKS ? int64_t(9) << 20 : int64_t(6) << 20;   // pairs
 };
 constexpr int kTcTokens = 16384;
+
+// Over the cache in 4 bits the few-row kernel cuts no row tiles where its rows see
+// at most kWholeTokens, as far as the host knows: cutting spreads a few units over
+// more CTAs, but the join is a launch.  Measured (us, cut / whole, queued; one new
+// token, 4 x 8 x 128): 1 request at up to 128 7.4 / 5.3, at 512 7.8 / 7.7, at 1024 8.0 / 10.8;
+// 100 at 64 to 128 9.8 / 8.6, at 256 13.7 / 9.9, at 512 16.0 / 12.5, at 1024 20.3 / 20.8, at
+// 2048 28.4 / 31.6; 128 (512 row tiles for 456 CTAs) 12.8 / 12.2, 16.3 / 14.4, 19.1 / 18.3, 23.7 /
+// 25.0, 34.1 / 41.1.
+constexpr int kWholeTokens = 512;
+
+// Cached tokens that a request's rows can see, as far as the host knows.
+inline int64_t most_tokens(const PaArgs& a, int max_q_len) {
+  const int64_t all = static_cast<int64_t>(a.c.max_pages) * a.c.page_size;
+  const int64_t n = max_q_len > 0 ? std::min(max_q_len, a.T) : a.T;
+  return a.window ? std::min(all, n + a.window + a.n_sink) : all;
+}
 
 template <bool BLOCKS>
 Path path_of(const PaArgs& a, int max_q_len) {
@@ -378,6 +397,7 @@ cudaError_t launch_paged_attn(Args a, int max_q_len, int num_sms, cudaStream_t s
   a.tc_rows = path.alone ? 0 : path.tc ? TcRule<Args::kBlocks>::kRows : INT_MAX;
   a.tc_ctas = std::min(num_sms, kMaxSms);
   a.tc_split = path.split;
+  if constexpr (Args::kBlocks) a.whole_tiles = most_tokens(a, max_q_len) <= kWholeTokens;
   cudaError_t err = cudaSuccess;
   for (int left = a.B; left > 0 && err == cudaSuccess; left -= kMaxBatch) {
     a.B = std::min(left, kMaxBatch);
