@@ -40,8 +40,8 @@
 // A row tile that is short and new costs about 2300 instructions of a warp beside
 // its steps: 256 requests of 4 x 8 rows at 40 tokens (2048 row tiles) take 45 us, 36 %
 // of the issue slots (loading the next row tile's request, q, pages and first codes
-// during the join of the last one: 47).  No registers are spilled but three words at
-// D = 64 with 16 rows, outside the loop over the tokens.
+// during the join of the last one: 47).  No registers are spilled but 12 bytes at
+// D = 64 with 16 rows.
 #include "block_kv.cuh"
 #include "paged_attn_rows.cuh"
 
