@@ -98,10 +98,11 @@ __device__ __forceinline__ float largest_of(const float* x, bool& bad) {
 // The smallest E4M3 value s from 2^-9 on with top <= 6 s (448 where there is none):
 // top / 6, rounded down, is rounded up to E4M3's three bits by the addition of a
 // number whose last place is theirs; where the first rounding took that below s,
-// which 6 s < top tells exactly, the next value is s.
+// which 6 s < top tells exactly, the next value is s.  (Sizes beyond the largest scale
+// need no more than to stay there: the number added to 2^108 would be infinite.)
 __device__ __forceinline__ float block_scale(float top) {
   if (top != top) return top;
-  const float t = __fmul_rd(top, 0.16666666f);   // below 1 / 6
+  const float t = fminf(__fmul_rd(top, 0.16666666f), 512.f);   // below 1 / 6
   const float magic = __uint_as_float(max(__float_as_uint(t) & 0x7f800000u, 0x3c800000u) + 0x0a000000u);   // 2^20 times t's, or 2^-6
   float s = fminf(fmaxf(__fadd_ru(t, magic) - magic, 0.001953125f), 448.f);
   if (6.f * s < top) {
