@@ -5,9 +5,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import block_oracle as bo
 from tests.block_util import BlockBatch
 from tests.decode_util import values64
-from tests.test_gpu_block_kv import check_append, run_append
+from tests.test_gpu_block_kv import NONFINITE, check_append, check_cache, run_append
 
 pytestmark = pytest.mark.gpu
 
@@ -40,6 +41,44 @@ def test_block_maxima_of_every_size(gk, gv, layout):
     blocks[np.arange(len(top)), rng.integers(0, 16, len(top))] = top * rng.choice([-1.0, 1.0], len(top))
     x = of_blocks(rng.permutation(blocks), 4, 256)
     bt = BlockBatch([len(x)], [len(x) + 3], Hq=1, Hkv=4, D=256, seed=3, gk=gk, gv=gv)
+    bt.k.copy_(x)
+    bt.v.copy_(x)
+    check_append(bt, run_append(bt, layout=layout))
+
+
+def near_ties(rng, scales):
+    """For each scale a block whose first element is 6 of it, the others at the codes' borders or next to them."""
+    z = rng.choice([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], (len(scales), 16))
+    z *= rng.choice([1.0, 1.0, 1 + 2.0 ** -7, 1 - 2.0 ** -8], z.shape)
+    z[:, 0] = 6.0
+    return values64(torch.from_numpy(z * scales[:, None] * rng.choice([-1.0, 1.0], z.shape)).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_codes_beside_an_infinity(layout):
+    """... are the nearest too, ties to the even code."""
+    rng = np.random.default_rng(4)
+    blocks = near_ties(rng, np.repeat(bo.E4M3_SCALES, 40))
+    blocks[np.arange(len(blocks)), rng.integers(1, 16, len(blocks))] = rng.choice([-np.inf, np.inf], len(blocks))
+    x = of_blocks(rng.permutation(blocks), 4, 128)
+    bt = BlockBatch([len(x)], [len(x) + 3], Hq=1, Hkv=4, D=128, seed=4, gk=1.0, gv=1.0)
+    bt.k.copy_(x)
+    bt.v.copy_(x)
+    r = run_append(bt, layout=layout)
+    assert r["st"] == NONFINITE
+    ref = bt.oracle_cache()
+    _, written = bo.append(ref, None, values64(bt.k), values64(bt.v), None, None, None, None, bt.cu, bt.kv_len)
+    check_cache(bt, r, ref, written)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_codes_beside_elements_that_saturate(layout):
+    rng = np.random.default_rng(5)
+    blocks = near_ties(rng, np.full(2000, 448.0))
+    large = rng.choice([-1.0, 1.0], len(blocks)) * 2.0 ** rng.integers(12, 128, len(blocks))
+    blocks[np.arange(len(blocks)), rng.integers(1, 16, len(blocks))] = large
+    x = of_blocks(blocks, 4, 128)
+    bt = BlockBatch([len(x)], [len(x) + 3], Hq=1, Hkv=4, D=128, seed=5, gk=1.0, gv=1.0)
     bt.k.copy_(x)
     bt.v.copy_(x)
     check_append(bt, run_append(bt, layout=layout))

@@ -141,16 +141,20 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // two codes three, so x (24 bits) either is m sg, and then the corrected quotient
 // is m (it is off by 2^-45 before its rounding), or lies a unit of its last place
 // away, and then x / sg is over half a unit of m's from m.
-// fine: x is finite and none is over 6 sg; x inv may overflow otherwise.
+// fine: x is finite and none is over 6 sg; else what is larger, whose product with
+// inv may overflow, becomes 6 sg, the same code.  (A NaN's sg is NaN, and so are its
+// quotients.)
 template <int N>
-__device__ __forceinline__ void quotients(float (&q)[N], const float* x, float sg, float inv, bool fine) {
+__device__ __forceinline__ void quotients(float (&q)[N], float* x, float sg, float inv, bool fine) {
+  if (!fine) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = fminf(fmaxf(x[i], -6.f * sg), 6.f * sg);
+  }
   const uint64_t sg2 = pair(-sg, -sg), inv2 = pair(inv, inv);
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    const uint64_t x2 = pair(x[i], x[i + 1]);
-    uint64_t q2 = mul2(x2, inv2);
-    if (fine) q2 = fma2(fma2(q2, sg2, x2), inv2, q2);
-    unpair(q2, q[i], q[i + 1]);
+    const uint64_t x2 = pair(x[i], x[i + 1]), q2 = mul2(x2, inv2);
+    unpair(fma2(fma2(q2, sg2, x2), inv2, q2), q[i], q[i + 1]);
   }
 }
 
@@ -179,7 +183,7 @@ __device__ __forceinline__ float reciprocal(float x) {
 }
 
 // The 16 elements of a block, whose largest size is `top`, to their place.
-__device__ __forceinline__ void store_block(uint8_t* codes, uint8_t* scale, const float (&x)[16], float top, bool odd, float g,
+__device__ __forceinline__ void store_block(uint8_t* codes, uint8_t* scale, float (&x)[16], float top, bool odd, float g,
                                             float inv_g) {
   const float s = block_scale(top * inv_g), sg = s * g, inv = reciprocal(sg);
   float q[16];
