@@ -15,9 +15,6 @@
 // than its neighbours' do; the sizes of all fours of a row go through shared
 // memory then.  Query blocks are those of kv_rows.cuh.
 //
-// A request of n new tokens touches at most n/16 + 2 groups of 16 slots, so
-// request b's blocks start at cu[b]/16 + 2b, as in kv_append.cu.
-//
 // Measured: 32 x 256 tokens of 32 + 4 heads of 128, norm and rotation, 156 MB in 31.9 us
 // = 4.9 TB/s, bound by memory behind look-ups (the queries are 134 MB of that); ragged
 // prompts up to 1999 tokens of 16 + 16 heads of 64, 214 MB in 47 us = 4.5 TB/s, bound by
@@ -31,7 +28,6 @@
 namespace moe {
 namespace {
 
-constexpr int kSlots = 16;       // of a cache block
 constexpr int kThreads = kQueryThreads;
 
 // Two heads a thread for few tokens (64 single ones: 3.7 us, one head 4.0, four 4.5), else
@@ -199,7 +195,8 @@ struct Slots {
   int first, tokens, pid;   // pid: outside the cache is recorded where it is met
 };
 
-// False: nothing to do (or wrong offsets, which are recorded).
+// False: nothing to do (or wrong offsets or a length past the page table, which are
+// recorded).
 __device__ __forceinline__ bool find_slots(const BaArgs& a, int item, Slots& s) {
   const int b = warp_find_request(a.cu, a.B, item, 1, kSlots, 2);
   const Request r = load_request(a.cu, a.kv_len, b, a.T);
@@ -207,14 +204,18 @@ __device__ __forceinline__ bool find_slots(const BaArgs& a, int item, Slots& s) 
     if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     return false;
   }
-  const int at = item - (r.row0 / kSlots + 2 * b);
-  const int base = (r.start / kSlots + at) * kSlots;
-  if (r.n == 0 || at < 0 || base >= r.end) return false;   // one block too many, or before the first request
+  const int group = slot_group(r, b, item);
+  if (group < 0) return false;
+  const int in_page = a.c.page_size / kSlots, page = group >> (31 - __clz(in_page));
+  if (page >= a.c.max_pages) {   // past the page table, and maybe past what the next lines can count
+    if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+    return false;
+  }
+  const int base = group * kSlots;
   s.first = max(base, r.start);
   s.tokens = min(base + kSlots, r.end) - s.first;
   s.row0 = r.row0 + (s.first - r.start);
-  const int page = base >> (31 - __clz(a.c.page_size));
-  s.pid = page < a.c.max_pages ? a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page] : -1;
+  s.pid = a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page];
   return true;
 }
 

@@ -40,4 +40,15 @@ inline bool blockkv_pointers_ok(const moe_blockkv_cache_t* c) {
          aligned_to(c->k_scale, row) && aligned_to(c->v_scale, row) && aligned_to(c->page_table, 4);
 }
 
+// The groups of 16 slots that an append writes or a read takes are dealt to blocks:
+// request b's start at item cu[b]/16 + 2b, as its n new tokens touch at most n/16 + 2
+// of them.  The group that `item` stands for, counted from position 0; -1: none.
+// (Counted in groups: a length may be anything up to 2^31 - 1, and the position behind
+// the last group would not fit.)
+constexpr int kSlots = 16;
+__device__ __forceinline__ int slot_group(const Request& r, int b, int item) {
+  const int at = item - (r.row0 / kSlots + 2 * b), group = r.start / kSlots + at;
+  return r.n > 0 && at >= 0 && group <= (r.end - 1) / kSlots ? group : -1;
+}
+
 }  // namespace moe

@@ -15,7 +15,7 @@
 namespace moe {
 namespace {
 
-constexpr int kSlots = 16, kThreads = 256, kAtOnce = 4;   // blocks of elements that a thread has under way
+constexpr int kThreads = 256, kAtOnce = 4;   // blocks of elements that a thread has under way
 
 struct BrArgs {
   moe_blockkv_cache_t c;
