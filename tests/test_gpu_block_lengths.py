@@ -8,7 +8,7 @@ import torch
 from oracle import block_oracle as bo
 from tests.block_util import BlockBatch
 from tests.decode_util import values64
-from tests.test_gpu_block_kv import BOUNDS, check_cache, run_append
+from tests.test_gpu_block_kv import BOUNDS, check_cache, run_append, run_read
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,18 @@ def test_append(n, end, page, layout):
                     written.append((name, at, h, slot))
     check_cache(bt, r, ref, written)
     assert torch.all(r["q_out"] != 5.0)      # the queries need no page
+
+
+@pytest.mark.parametrize("end", ENDS)
+@pytest.mark.parametrize("n,page", [(1, 16), (17, 64), (300, 128)])
+def test_read(n, end, page):
+    bt = batch(n, end, page)
+    good, c = (slice(0, 20), slice(20 + n, 23 + n)), bt.oracle_cache()
+    for dtype in (torch.bfloat16, torch.float32):
+        outs, st = run_read(bt, dtype)
+        assert st == BOUNDS
+        for name, out in zip("kv", outs):
+            assert torch.all(out[20:20 + n] == 9.0)
+            for b, rows in zip((0, 2), good):
+                want = np.stack([c.values(name, b, h, bt.total[b])[bt.total[b] - bt.new[b]:] for h in range(bt.Hkv)], 1)
+                assert np.array_equal(values64(out[rows]), want)

@@ -206,7 +206,7 @@ __device__ __forceinline__ bool find_slots(const BaArgs& a, int item, Slots& s) 
   }
   const int group = slot_group(r, b, item);
   if (group < 0) return false;
-  const int in_page = a.c.page_size / kSlots, page = group >> (31 - __clz(in_page));
+  const int page = group >> (27 - __clz(a.c.page_size));   // of page_size / 16 groups
   if (page >= a.c.max_pages) {   // past the page table, and maybe past what the next lines can count
     if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     return false;

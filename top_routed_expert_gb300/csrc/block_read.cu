@@ -8,7 +8,6 @@
 // together.  Bound by memory: 0.56 bytes read and 2 (or 4) written an element; 64
 // requests of up to 3712 tokens, 4 heads of 128, 312 MB in 49.5 us = 6.3 TB/s (16 bytes an
 // access, keys before values: 72 us).
-// Request b's blocks start at cu[b]/16 + 2b, as in kv_append.cu.
 #include "block_kv.cuh"
 #include "paged_attn.cuh"
 
@@ -58,18 +57,16 @@ __global__ void __launch_bounds__(kThreads) blockkv_read_kernel(BrArgs a) {
     if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     return;
   }
-  if (r.n == 0) return;
-  const int at = item - (r.row0 / kSlots + 2 * b);
-  const int base = (r.start / kSlots + at) * kSlots;
-  if (at < 0 || base >= r.end) return;   // one block too many, or before the first request
-  const int first = max(base, r.start), tokens = min(base + kSlots, r.end) - first;
-  const int page = base >> ps_log;
+  const int group = slot_group(r, b, item);
+  if (group < 0) return;
+  const int page = group >> (ps_log - 4);   // of page_size / 16 groups
   int pid = -1;
   if (page < a.c.max_pages) pid = a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page];
   if (pid < 0 || pid >= a.c.n_pages) {
     if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     return;
   }
+  const int base = group * kSlots, first = max(base, r.start), tokens = min(base + kSlots, r.end) - first;
   const int cols = a.c.n_kv_heads * BLOCKS, n = tokens * cols;   // blocks of keys; as many of values
   const int64_t row0 = r.row0 + (first - r.start), slot0 = first & (ps - 1);
   const int64_t codes0 = pid * a.c.page_stride + slot0 * a.c.token_stride;
