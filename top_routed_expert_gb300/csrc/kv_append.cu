@@ -103,8 +103,12 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
   if (r.n == 0) return;
   const int at = item - ((r.row0 >> ps_log) + 2 * b);
   const int page = (r.start >> ps_log) + at;
+  if (at < 0 || page > (r.end - 1) >> ps_log) return;   // one block too many, or before the first request
+  if (page >= a.c.max_pages) {   // past the page table, and maybe past what positions can count (a length may be 2^31 - 1)
+    if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+    return;
+  }
   const int base = page << ps_log;
-  if (at < 0 || base >= r.end) return;   // one block too many, or before the first request
   const int lr = threadIdx.x % TPR, grp = threadIdx.x / TPR, rows = blockDim.x / TPR;
   const bool norm = a.gamma_k;
   const Place p = place_of<HALF>(lr, a.rot), pv = place_of<false>(lr, 0);
@@ -142,8 +146,7 @@ __device__ __forceinline__ void append_block(const KaArgs& a, int item, int head
   };
   fetch_next();
   if (STAGES > 1) fetch_next();
-  int pid = -1;
-  if (page < a.c.max_pages) pid = a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page];
+  const int pid = a.c.page_table[static_cast<int64_t>(b) * a.c.max_pages + page];
   Gamma gamma = {};
   if (norm) gamma = load_gamma(a.gamma_k, p);
   float2 cs[PASSES][4];
