@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NB, true>::kCtas) block_
 
     const int pos_min = rq.start + tok0, pos_max = pos_min + tok_of(rows - 1);
     // units [ua, ub): the tile's rows all see all of them
-    const int from = sp.window ? max(0, pos_max - sp.window + kUnit) / kUnit : 0;
+    const int from = sp.window && pos_max >= sp.window ? (pos_max - sp.window) / kUnit + 1 : 0;
     const int ua = sp.sink_blocks + max(from - sp.lo_block, 0);
     const int ub = max(ua, min(u1, sp.sink_blocks + max(min(pos_min + 1, sp.end), 0) / kUnit - sp.lo_block));
 
