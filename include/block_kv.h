@@ -122,7 +122,9 @@ typedef struct {
  * k_out, v_out 16-byte aligned.  A page outside the cache, a position past the
  * page table, offsets that decrease or leave [0, T] and kv_len[b] < n_b record
  * MOE_ERR_DEVICE_BOUNDS; the rows of such a page or position, or all rows of
- * such a request, are left as they were, like rows of no request.
+ * such a request, are left as they were, like rows of no request (after offsets
+ * that decrease other requests' rows may be too, and rows that two requests
+ * name then hold either's tokens).
  */
 moe_status_t moe_blockkv_read(const moe_blockkv_read_config_t* cfg, const moe_blockkv_cache_t* cache,
                               const int32_t* cu, const int32_t* kv_len, void* k_out, void* v_out,

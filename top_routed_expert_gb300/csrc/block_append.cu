@@ -36,6 +36,7 @@ constexpr int kFewTokens = 256;
 
 struct BaArgs : RowArgs {
   moe_blockkv_cache_t c;
+  int work;   // blocks but those that check offsets
   int items, key_parts, parts;   // groups of slots that the requests can touch; blocks of one for keys, and in all
   uint32_t chunks, per_chunk;    // a token's heads by the number that a thread has under way; 2^32 / chunks, rounded up
   uint32_t page16, page_s;       // page strides in units of 16 bytes, and of D / 16
@@ -432,12 +433,16 @@ __device__ __forceinline__ void append_keys_half(const BaArgs& a, const Slots& s
   if (bad) set_status(a.status, MOE_ERR_DEVICE_NONFINITE);
 }
 
-// Blocks [0, parts items): cache blocks; the rest: query blocks.  U: heads that a
-// thread has under way.
+// Blocks [0, parts items): cache blocks; then query blocks; from `work` on a few that
+// check offsets.  U: heads that a thread has under way.
 template <int D, bool HALF, int U>
 __global__ void __launch_bounds__(kThreads, 7) blockkv_append_kernel(BaArgs a) {
   pdl_enter();
   const int n_cache = a.parts * a.items, i = blockIdx.x;
+  if (i >= a.work) {
+    check_offsets(a.cu, a.B, a.T, i - a.work, a.status);
+    return;
+  }
   if (i < n_cache) {
     const int item = i / a.parts, part = i - item * a.parts;
     Slots s;
@@ -466,6 +471,8 @@ cudaError_t launch(BaArgs a, cudaStream_t s) {
   a.parts = a.key_parts + ceil_div(rounds, groups);
   int64_t blocks = static_cast<int64_t>(a.parts) * a.items;
   if (a.q) blocks += ceil_div(a.T, query_tokens<D>(a.Hq, kThreads));
+  a.work = static_cast<int>(std::min<int64_t>(blocks, 0x7fffffff));
+  blocks += ceil_div(a.B, kThreads);
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   count_launches(1);
   return launch_pdl(a.half ? blockkv_append_kernel<D, true, U> : blockkv_append_kernel<D, false, U>,

@@ -50,6 +50,11 @@ template <int D, bool F32, bool WIDE>
 __global__ void __launch_bounds__(kThreads) blockkv_read_kernel(BrArgs a) {
   constexpr int BLOCKS = D / 16;   // of a row
   pdl_enter();
+  const int items = a.T / kSlots + 2 * a.B;
+  if (static_cast<int>(blockIdx.x) >= items) {   // the last blocks
+    check_offsets(a.cu, a.B, a.T, blockIdx.x - items, a.status);
+    return;
+  }
   const int item = blockIdx.x, ps = a.c.page_size, ps_log = 31 - __clz(ps);
   const int b = warp_find_request(a.cu, a.B, item, 1, kSlots, 2);
   const Request r = load_request(a.cu, a.kv_len, b, a.T);
@@ -143,7 +148,7 @@ cudaError_t launch(BrArgs a, bool f32, cudaStream_t s) {
   const bool wide = (!a.k_out || (aligned_to(a.k_out, 32) && a.ks % per32 == 0)) &&
                     (!a.v_out || (aligned_to(a.v_out, 32) && a.vs % per32 == 0));
   count_launches(1);
-  auto go = [&](auto kernel) { return launch_pdl(kernel, a.T / kSlots + 2 * a.B, kThreads, 0, s, a); };
+  auto go = [&](auto kernel) { return launch_pdl(kernel, a.T / kSlots + 2 * a.B + ceil_div(a.B, kThreads), kThreads, 0, s, a); };
   if (f32) return wide ? go(blockkv_read_kernel<D, true, true>) : go(blockkv_read_kernel<D, true, false>);
   return wide ? go(blockkv_read_kernel<D, false, true>) : go(blockkv_read_kernel<D, false, false>);
 }

@@ -33,6 +33,7 @@ constexpr int kMaxHeads = 8;   // of a cache block
 
 struct KaArgs : RowArgs {
   moe_kv_cache_t c;
+  int work;                 // blocks but those that check offsets
   int items;                // pages that the requests can touch
   int heads, head_blocks;   // heads of a cache block; its blocks for a page
 };
@@ -258,11 +259,15 @@ template <int PASSES, int THREADS> constexpr int blocks_on_sm() {
   return THREADS == 128 ? (PASSES < 4 ? 7 : 6) : THREADS == 256 ? 3 : 1;
 }
 
-// Blocks [0, head_blocks items): cache blocks; the rest: query blocks.
+// Blocks [0, head_blocks items): cache blocks; then query blocks; from `work` on a few that check offsets.
 template <int D, int PASSES, bool HALF, int THREADS>
 __global__ void __launch_bounds__(THREADS, blocks_on_sm<PASSES, THREADS>()) kv_append_kernel(KaArgs a) {
   pdl_enter();
   const int n_cache = a.head_blocks * a.items, i = blockIdx.x;
+  if (i >= a.work) {
+    check_offsets(a.cu, a.B, a.T, i - a.work, a.status);
+    return;
+  }
   if (i < n_cache) {
     const int item = i / a.head_blocks, head0 = (i - item * a.head_blocks) * a.heads;
     append_block<D, PASSES, HALF, THREADS>(a, item, head0, min(head0 + a.heads, a.c.n_kv_heads));
@@ -289,6 +294,8 @@ cudaError_t launch(KaArgs a, int threads, int sms, cudaStream_t s) {
   a.head_blocks = ceil_div(a.c.n_kv_heads, a.heads);
   int64_t blocks = static_cast<int64_t>(a.head_blocks) * a.items;
   if (a.q) blocks += ceil_div(a.T, query_tokens<D>(a.Hq, threads));
+  a.work = static_cast<int>(std::min<int64_t>(blocks, 0x7fffffff));
+  blocks += ceil_div(a.B, threads);
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned n = static_cast<unsigned>(blocks);
   const auto kernel = a.half ? kv_append_kernel<D, PASSES, true, THREADS> : kv_append_kernel<D, PASSES, false, THREADS>;

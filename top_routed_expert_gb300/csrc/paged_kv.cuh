@@ -52,6 +52,17 @@ __device__ __forceinline__ Request load_request(const int32_t* __restrict__ cu, 
   return r;
 }
 
+// Records offsets that decrease or leave [0, T]: a thread for a request, in blocks of
+// their own, the last ones, as blocks that look for their request below may pass
+// over it when offsets are out of order (out of line and last: 0.1 us of an append of
+// 32 us; in line between cache and query blocks 0.8).
+inline __device__ __noinline__ void check_offsets(const int32_t* __restrict__ cu, int B, int T, int block, unsigned* status) {
+  const int64_t b = static_cast<int64_t>(block) * blockDim.x + threadIdx.x;
+  if (b >= B) return;
+  const int lo = cu[b], hi = cu[b + 1];
+  if (lo < 0 || hi < lo || hi > T) set_status(status, MOE_ERR_DEVICE_BOUNDS);
+}
+
 // The last b in [0, B) with cu[b] * mul / div + b * add <= x, for a
 // non-decreasing sequence with cu[0] = 0; the warp looks at 32 places at a
 // time, so 4096 requests take three dependent loads.  Every lane gets b.
