@@ -1,0 +1,59 @@
+"""Host-side checks of the binding (abi.py): a call's rows have to lie as those of
+the tensors that its configuration was made from, as the library goes by the
+configuration's strides.  No GPU."""
+import pytest
+import torch
+
+from tests import test_block_ops_host as block
+from tests.test_decode_binding_host import B, BF16, D, F32, HKV, HQ, I32, T, lib   # noqa: F401
+from top_routed_expert_gb300 import abi
+
+
+def wide(heads, dtype=BF16, more=3):
+    """Rows of `heads` heads in a buffer that has more."""
+    return torch.zeros(T, heads + more, D, dtype=dtype)[:, :heads]
+
+
+def calls(call, args, names, dense, apart, lib):   # noqa: F811
+    """args(config's rows, call's rows): dense and separate rows, each taken as configured and refused else."""
+    good = 0
+    for made in (dense, apart):
+        for given in (dense, apart):
+            if made is given:
+                call(**args(made, given))
+                good += 1
+            else:
+                with pytest.raises(ValueError, match=names[0]):
+                    call(**args(made, given))
+    assert lib.calls == good
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("name", ["k_out", "v_out"])
+def test_read(lib, dtype, name):   # noqa: F811
+    def args(made, given):
+        a = block.read_args(dtype=dtype)
+        rows = dict(k_out=a["k_out"], v_out=a["v_out"])
+        return dict(a, cfg=abi.make_blockkv_read_config(*dict(rows, **{name: made}).values(), B), **{name: given})
+    dense, apart = torch.zeros(T, HKV, D, dtype=dtype), wide(HKV, dtype)
+    calls(abi.moe_blockkv_read, args, [name], dense, apart, lib)
+    done = lib.calls
+    # the whole buffer has the slice's rows; the same strides with fewer rows, or longer ones of another shape, have not
+    abi.moe_blockkv_read(**args(apart, apart._base))
+    abi.moe_blockkv_read(**args(dense, dense.flatten(1)))
+    abi.moe_blockkv_read(**args(dense, torch.zeros(T + 4, HKV, D, dtype=dtype)))
+    for made, given in ((apart, apart[:T - 1]), (apart, apart._base[:T - 1]), (dense, apart[:, :, :D // 2]), (dense, dense[:T - 1]),
+                        (apart, torch.zeros(T, HKV + 3, D, dtype=dtype).transpose(0, 1))):
+        with pytest.raises(ValueError, match=name):
+            abi.moe_blockkv_read(**args(made, given))
+    assert lib.calls == done + 3
+
+
+def test_read_of_one_row(lib):   # noqa: F811
+    """A single row may carry any distance to a next one."""
+    a = block.read_args()
+    for made in (a["k_out"][:1], wide(HKV)[:1]):
+        cfg = abi.make_blockkv_read_config(made, made, B)
+        for given in (a["k_out"][:1], wide(HKV)[:1], a["k_out"][0]):
+            abi.moe_blockkv_read(**dict(a, cfg=cfg, k_out=given, v_out=given))
+    assert lib.calls == 6

@@ -104,8 +104,8 @@ class moe_blockkv_cache_t(ctypes.Structure):
 class moe_blockkv_read_config_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "batch", "out_dtype")]
     _fields_ += [(n, ctypes.c_int64) for n in ("k_stride", "v_stride")]
-    # of make_blockkv_read_config's tensors: (n_kv_heads, head_dim), type, bytes of a row
-    heads, dtype, row = None, None, 0
+    # of make_blockkv_read_config's tensors: (n_kv_heads, head_dim), type, elements of a row, whether rows follow each other
+    heads, dtype, row, dense = None, None, None, False
 
 
 class moe_add_norm_config_t(ctypes.Structure):
@@ -273,9 +273,25 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 # The calls below are a few microseconds long and so is what they cost here: each
 # looks at types, sizes and devices alone, written out in it.  Rows' layouts are
 # looked at by the make_ functions, which leave what no field of the C structures
-# says beside those (a structure made by hand lacks that part of the checks).
+# says beside those (a structure made by hand lacks that part of the checks); a
+# call's own rows have to lie as its configuration says.
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 _ELSEWHERE = "every tensor has to be on the current CUDA device"
+
+
+def _rows_at(t: torch.Tensor, T: int, row: int, step: int) -> bool:
+    """Whether t has T rows of `row` contiguous elements, `step` apart, whatever shape it gives them."""
+    if row == step and t.is_contiguous():
+        return t.numel() >= T * row
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 2 or shape[0] < T or (T > 1 and strides[0] != step):
+        return False
+    n = 1
+    for size, stride in zip(shape[:0:-1], strides[:0:-1]):
+        if size > 1 and stride != n:
+            return False
+        n *= size
+    return n >= row
 
 
 def _stream_of(stream, device: int) -> int:
@@ -493,8 +509,15 @@ def make_blockkv_read_config(k_out, v_out, batch) -> moe_blockkv_read_config_t:
     rows = [0 if t is None else _row_stride(t, like.dtype) for t in (k_out, v_out)]
     c = moe_blockkv_read_config_t(like.shape[0], batch, _float_type(like), *rows)
     c.heads, c.dtype = tuple(like.shape[1:]), like.dtype
-    c.row = like.shape[1] * like.shape[2] * like.element_size()
+    c.row = like.shape[1] * like.shape[2]
+    c.dense = all(t is None or step == c.row for t, step in zip((k_out, v_out), rows))
     return c
+
+
+def _read_rows(cfg, T: int, k_out, v_out) -> bool:
+    """moe_blockkv_read's outputs, where they are not simply dense."""
+    return cfg.row is None or ((k_out is None or _rows_at(k_out, T, cfg.row, cfg.k_stride))
+                               and (v_out is None or _rows_at(v_out, T, cfg.row, cfg.v_stride)))
 
 
 def moe_blockkv_read(cfg, cache, cu, kv_len, k_out, v_out, stream=None):
@@ -506,11 +529,12 @@ def moe_blockkv_read(cfg, cache, cu, kv_len, k_out, v_out, stream=None):
     B = cfg.batch
     if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
         raise ValueError(_RAGGED)
-    n, dtype = cfg.T * cfg.row, cfg.dtype
+    T, dtype = cfg.T, cfg.dtype
     if not ((cfg.heads == cache.heads or cfg.heads is None or cache.heads is None)
-            and (k_out is None or k_out.nbytes >= n and (k_out.dtype is dtype or dtype is None))
-            and (v_out is None or v_out.nbytes >= n and (v_out.dtype is dtype or dtype is None))):
-        raise ValueError("k_out and v_out: rows of the configuration's shape and type and the cache's heads")
+            and (k_out is None or k_out.dtype is dtype or dtype is None) and (v_out is None or v_out.dtype is dtype or dtype is None)
+            and (cfg.dense and (k_out is None or k_out.is_contiguous() and k_out.numel() >= T * cfg.row)
+                 and (v_out is None or v_out.is_contiguous() and v_out.numel() >= T * cfg.row) or _read_rows(cfg, T, k_out, v_out))):
+        raise ValueError("k_out and v_out: rows of the configuration's shape, type and distance and the cache's heads")
     code = load().moe_blockkv_read(cfg, cache, cu.data_ptr(), kv_len.data_ptr(), None if k_out is None else k_out.data_ptr(),
                                    None if v_out is None else v_out.data_ptr(),
                                    _current_stream(dev) if stream is None else _stream_of(stream, dev))
