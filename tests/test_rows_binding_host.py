@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from tests import test_block_ops_host as block
+from tests import test_decode_binding_host as byte
 from tests.test_decode_binding_host import B, BF16, D, F32, HKV, HQ, I32, T, lib   # noqa: F401
 from top_routed_expert_gb300 import abi
 
@@ -57,3 +58,59 @@ def test_read_of_one_row(lib):   # noqa: F811
         for given in (a["k_out"][:1], wide(HKV)[:1], a["k_out"][0]):
             abi.moe_blockkv_read(**dict(a, cfg=cfg, k_out=given, v_out=given))
     assert lib.calls == 6
+
+
+APPENDS = [(abi.moe_kv_append, byte.append_args), (abi.moe_blockkv_append, block.append_args)]
+ATTENTIONS = [(abi.moe_paged_attention, byte.attend_args), (abi.moe_blockkv_attention, block.attend_args)]
+
+
+@pytest.mark.parametrize("call,args", APPENDS)
+@pytest.mark.parametrize("name", ["q", "k", "v", "q_out"])
+def test_append(lib, call, args, name):   # noqa: F811
+    heads = HQ if name in ("q", "q_out") else HKV
+
+    def given(made, rows):
+        a = args()
+        own = dict({n: a[n] for n in ("q", "k", "v", "q_out")}, **{name: made})
+        return dict(a, cfg=abi.make_kv_append_config(*own.values(), B, rot_dim=D, n_pos=50), **{name: rows})
+    dense, apart = torch.zeros(T, heads, D, dtype=BF16), wide(heads)
+    calls(call, given, [name], dense, apart, lib)
+    done = lib.calls
+    call(**given(apart, apart._base))
+    call(**given(dense, dense.flatten(1)))
+    for made, bad in ((apart, apart._base[:T - 1]), (dense, dense.float()), (dense, dense.half()), (apart, wide(heads, F32))):
+        with pytest.raises(ValueError, match=name):
+            call(**given(made, bad))
+    assert lib.calls == done + 2
+
+
+@pytest.mark.parametrize("call,args", APPENDS)
+def test_slices_of_one_projection(lib, call, args):   # noqa: F811
+    a = args()
+    x = torch.zeros(T, (HQ + 2 * HKV) * D, dtype=BF16)
+    q, k, v = (y.unflatten(1, (-1, D)) for y in x.split([HQ * D, HKV * D, HKV * D], dim=1))
+    cfg = abi.make_kv_append_config(q, k, v, a["q_out"], B, rot_dim=D, n_pos=50)
+    call(**dict(a, cfg=cfg, q=q, k=k, v=v))
+    cfg.T = T - 2
+    call(**dict(a, cfg=cfg, q=q[:T - 2], k=k[:T - 1], v=v))
+    with pytest.raises(ValueError, match="q_out"):
+        call(**dict(a, cfg=cfg, q=q[:T - 3], k=k, v=v))
+    assert lib.calls == 2
+
+
+@pytest.mark.parametrize("call,args", ATTENTIONS)
+@pytest.mark.parametrize("name", ["q", "out"])
+def test_attention(lib, call, args, name):   # noqa: F811
+    def given(made, rows):
+        a = args()
+        own = dict({n: a[n] for n in ("q", "out")}, **{name: made})
+        return dict(a, cfg=abi.make_paged_attention_config(*own.values(), B), **{name: rows})
+    dense, apart = torch.zeros(T, HQ, D, dtype=BF16), wide(HQ)
+    calls(call, given, [name], dense, apart, lib)
+    done = lib.calls
+    call(**given(apart, apart._base))
+    call(**given(dense, dense.flatten(1)))
+    for made, bad in ((apart, apart._base[:T - 1]), (dense, dense.float()), (dense, dense.half()), (apart, wide(HQ, F32))):
+        with pytest.raises(ValueError, match=name):
+            call(**given(made, bad))
+    assert lib.calls == done + 2

@@ -80,15 +80,15 @@ class moe_kv_append_config_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "batch", "n_q_heads", "rot_dim", "rope_layout", "n_pos")]
     _fields_ += [("eps", ctypes.c_float)]
     _fields_ += [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")]
-    # of make_kv_append_config's tensors: bytes of a row of q and of k, (n_kv_heads, head_dim)
-    q_row, k_row, heads = 0, 0, None
+    # of make_kv_append_config's tensors: elements of a row of q and of k, (n_kv_heads, head_dim), whether rows follow each other
+    q_row, k_row, heads, dense = 0, 0, None, False
 
 
 class moe_paged_attention_config_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "batch", "n_q_heads", "max_q_len", "window", "n_sink")]
     _fields_ += [("sm_scale", ctypes.c_float), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
-    # of make_paged_attention_config's tensors: bytes of a row of q, head_dim
-    q_row, head_dim = 0, None
+    # of make_paged_attention_config's tensors: elements of a row of q, head_dim, whether rows follow each other
+    q_row, head_dim, dense = 0, None, False
 
 
 class moe_blockkv_cache_t(ctypes.Structure):
@@ -374,8 +374,16 @@ def make_kv_append_config(q, k, v, q_out, batch, rot_dim=0, n_pos=0, rope_layout
                                0 if q is None else _row_stride(q), _row_stride(k), _row_stride(v),
                                0 if q is None else _row_stride(q_out))
     c.heads = heads, D = tuple(k.shape[1:])
-    c.q_row, c.k_row = 2 * c.n_q_heads * D, 2 * heads * D
+    c.q_row, c.k_row = c.n_q_heads * D, heads * D
+    c.dense = c.k_stride == c.v_stride == c.k_row and c.q_stride == c.q_out_stride == c.q_row
     return c
+
+
+def _append_rows(cfg, T: int, q, k, v, q_out) -> bool:
+    """An append's rows, where they are not simply dense."""
+    return cfg.k_row == 0 or (_rows_at(k, T, cfg.k_row, cfg.k_stride) and _rows_at(v, T, cfg.k_row, cfg.v_stride) and
+                              (q is None or _rows_at(q, T, cfg.q_row, cfg.q_stride)
+                               and _rows_at(q_out, T, cfg.q_row, cfg.q_out_stride)))
 
 
 def _appending(where: str, doc: str):
@@ -392,9 +400,12 @@ def _appending(where: str, doc: str):
         if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
             raise ValueError(_RAGGED)
         T = cfg.T
-        if not (k.nbytes >= T * cfg.k_row <= v.nbytes and (cfg.heads == cache.heads or cfg.heads is None or cache.heads is None)
-                and (q is None or q.nbytes >= T * cfg.q_row <= q_out.nbytes)):
-            raise ValueError("q, k, v and q_out: rows of the configuration's shape and the cache's heads")
+        if not (k.dtype is v.dtype is _BF16 and (q is None or q.dtype is q_out.dtype is _BF16)
+                and (cfg.heads == cache.heads or cfg.heads is None or cache.heads is None)
+                and (cfg.dense and k.is_contiguous() and v.is_contiguous() and k.numel() >= T * cfg.k_row <= v.numel()
+                     and (q is None or q.is_contiguous() and q_out.is_contiguous() and q.numel() >= T * cfg.q_row <= q_out.numel())
+                     or _append_rows(cfg, T, q, k, v, q_out))):
+            raise ValueError("q, k, v and q_out: bf16 rows of the configuration's shape and distance and the cache's heads")
         if not ((gamma_k is None or gamma_k.dtype is _F32 and gamma_k.numel() >= cache.head_dim)
                 and (gamma_q is None or gamma_q.dtype is _F32 and gamma_q.numel() >= cache.head_dim)
                 and (cos_sin is None or cos_sin.dtype is _F32 and cos_sin.numel() >= cfg.n_pos * cfg.rot_dim)
@@ -424,8 +435,14 @@ def make_paged_attention_config(q, out, batch, max_q_len=0, window=0, n_sink=0,
     _need(q.shape == out.shape, "q and out: the same shape")
     c = moe_paged_attention_config_t(q.shape[0], batch, q.shape[1], max_q_len, window, n_sink,
                                      q.shape[2] ** -0.5 if sm_scale is None else sm_scale, _row_stride(q), _row_stride(out))
-    c.q_row, c.head_dim = 2 * q.shape[1] * q.shape[2], q.shape[2]
+    c.q_row, c.head_dim = q.shape[1] * q.shape[2], q.shape[2]
+    c.dense = c.q_stride == c.out_stride == c.q_row
     return c
+
+
+def _attention_rows(cfg, T: int, q, out) -> bool:
+    """An attention's rows, where they are not simply dense."""
+    return cfg.q_row == 0 or (_rows_at(q, T, cfg.q_row, cfg.q_stride) and _rows_at(out, T, cfg.q_row, cfg.out_stride))
 
 
 def moe_paged_attention_ws_bytes(cfg, cache) -> int:
@@ -444,10 +461,12 @@ def _attending(where: str, doc: str):
         if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
             raise ValueError(_RAGGED)
         T = cfg.T
-        if not (q.nbytes >= T * cfg.q_row <= out.nbytes and (cfg.head_dim is None or cfg.head_dim == cache.head_dim)
+        if not (q.dtype is out.dtype is _BF16 and (cfg.head_dim is None or cfg.head_dim == cache.head_dim)
+                and (cfg.dense and q.is_contiguous() and out.is_contiguous() and q.numel() >= T * cfg.q_row <= out.numel()
+                     or _attention_rows(cfg, T, q, out))
                 and (lse is None or lse.dtype is _F32 and lse.numel() >= T * cfg.n_q_heads)):
-            raise ValueError("q and out: rows of the configuration's shape and the cache's head size, lse: float32 "
-                             "[T, n_q_heads]")
+            raise ValueError("q and out: bf16 rows of the configuration's shape and distance and the cache's head size, lse: "
+                             "float32 [T, n_q_heads]")
         code = getattr(load(), where)(
             cfg, cache, q.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
