@@ -114,3 +114,22 @@ def test_attention(lib, call, args, name):   # noqa: F811
         with pytest.raises(ValueError, match=name):
             call(**given(made, bad))
     assert lib.calls == done + 2
+
+
+@pytest.mark.parametrize("name", ["x", "residual", "out", "sum"])
+def test_norm(lib, name):   # noqa: F811
+    dtype = BF16 if name in ("x", "out") else F32
+
+    def given(made, rows):
+        a = block.norm_args()
+        own = dict({n: a[n] for n in ("x", "residual", "out", "out8", "sum")}, **{name: made})
+        return dict(a, cfg=abi.make_add_rms_norm_config(*own.values(), group=128), **{name: rows})
+    dense, apart = torch.zeros(T, 512, dtype=dtype), torch.zeros(T, 1024, dtype=dtype)[:, :512]
+    calls(abi.moe_add_rms_norm, given, [name], dense, apart, lib)
+    done = lib.calls
+    abi.moe_add_rms_norm(**given(apart, apart._base))
+    abi.moe_add_rms_norm(**given(dense, dense.flatten()))
+    for bad in (apart._base[:T - 1], apart._base[:T - 2], torch.zeros(2 * T, 1024, dtype=dtype)[:, :504]):
+        with pytest.raises(ValueError, match=name):
+            abi.moe_add_rms_norm(**given(apart, bad))
+    assert lib.calls == done + 2

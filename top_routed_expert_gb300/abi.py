@@ -112,8 +112,8 @@ class moe_add_norm_config_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "x_dtype", "res_dtype", "out_dtype", "group")]
     _fields_ += [("eps", ctypes.c_float)]
     _fields_ += [(n, ctypes.c_int64) for n in ("x_stride", "res_stride", "sum_stride", "out_stride")]
-    # of make_add_rms_norm_config's tensors: type and strides of x, residual, out and sum
-    rows = None
+    # of make_add_rms_norm_config's tensors: types of x, residual, out and sum, whether rows follow each other
+    types, dense = None, False
 
 
 class moe_weights_t(ctypes.Structure):
@@ -574,13 +574,15 @@ def make_add_rms_norm_config(x, residual=None, out=None, out8=None, sum=None, gr
     c = moe_add_norm_config_t(T, d, _float_type(x), MOE_BF16 if residual is None else _float_type(residual),
                               MOE_BF16 if out is None else _float_type(out), group, eps, stride(x), stride(residual),
                               stride(sum), stride(out))
-    c.rows = tuple((None if t is None else t.dtype, (stride(t), 1)) for t in (x, residual, out, sum))
+    c.types = tuple(None if t is None else t.dtype for t in (x, residual, out, sum))
+    c.dense = all(stride(t) == d for t in (x, residual, out, sum))
     return c
 
 
-def _one_row(t: torch.Tensor, T: int) -> bool:
-    """A single row, which may carry any distance to a next one."""
-    return T <= 1 and t.dim() == 2 and t.stride(1) == 1
+def _norm_rows(cfg, T: int, x, residual, out, sum) -> bool:
+    """The norm's rows, where they are not simply dense."""
+    return (_rows_at(x, T, cfg.d, cfg.x_stride) and (residual is None or _rows_at(residual, T, cfg.d, cfg.res_stride))
+            and (out is None or _rows_at(out, T, cfg.d, cfg.out_stride)) and (sum is None or _rows_at(sum, T, cfg.d, cfg.sum_stride)))
 
 
 def moe_add_rms_norm(cfg, x, residual, gamma, out=None, out8=None, out8_scale=None, sum=None, stream=None):
@@ -592,13 +594,14 @@ def moe_add_rms_norm(cfg, x, residual, gamma, out=None, out8=None, out8_scale=No
         raise ValueError(_ELSEWHERE)
     T, d = cfg.T, cfg.d
     n = T * d
-    if cfg.rows is not None:
-        (xt, xs), (rt, rs), (ot, os), (st, ss) = cfg.rows
-        if not (x.dtype is xt and x.numel() >= n and (x.stride() == xs or _one_row(x, T))
-                and (residual is None or residual.dtype is rt and residual.numel() >= n
-                     and (residual.stride() == rs or _one_row(residual, T)))
-                and (out is None or out.dtype is ot and out.numel() >= n and (out.stride() == os or _one_row(out, T)))
-                and (sum is None or sum.dtype is st and sum.numel() >= n and (sum.stride() == ss or _one_row(sum, T)))):
+    if cfg.types is not None:
+        xt, rt, ot, st = cfg.types
+        if not (x.dtype is xt and (residual is None or residual.dtype is rt) and (out is None or out.dtype is ot)
+                and (sum is None or sum.dtype is st)
+                and (cfg.dense and x.is_contiguous() and x.numel() >= n
+                     and (residual is None or residual.is_contiguous() and residual.numel() >= n)
+                     and (out is None or out.is_contiguous() and out.numel() >= n)
+                     and (sum is None or sum.is_contiguous() and sum.numel() >= n) or _norm_rows(cfg, T, x, residual, out, sum))):
             raise ValueError("x, residual, out and sum: [T, d] of the configuration's types and strides")
     if not (gamma.dtype is _F32 and gamma.numel() >= d and gamma.is_contiguous()):
         raise ValueError("gamma: float32 [d]")
