@@ -133,3 +133,19 @@ def test_norm(lib, name):   # noqa: F811
         with pytest.raises(ValueError, match=name):
             abi.moe_add_rms_norm(**given(apart, bad))
     assert lib.calls == done + 2
+
+
+@pytest.mark.parametrize("call,args,names", [
+    (abi.moe_route_scores, byte.route_args, ("bias", "topk_ids", "topk_w")),
+    *((c, a, ("gamma_q", "gamma_k", "cos_sin", "positions", "cu", "kv_len")) for c, a in APPENDS),
+    *((c, a, ("cu", "kv_len", "lse", "ws")) for c, a in ATTENTIONS),
+    (abi.moe_blockkv_read, block.read_args, ("cu", "kv_len")),
+])
+def test_arrays_with_gaps(lib, call, args, names):   # noqa: F811
+    for name in names:
+        t = args()[name]
+        gaps = torch.zeros(*t.shape, 2, dtype=t.dtype)[..., 0]
+        with pytest.raises(ValueError, match=name):
+            call(**args(**{name: gaps}))
+        call(**args(**{name: gaps.contiguous()}))
+    assert lib.calls == len(names)

@@ -300,7 +300,7 @@ def _stream_of(stream, device: int) -> int:
     return stream.cuda_stream
 
 
-_RAGGED = "cu: int32 [batch + 1], kv_len: int32 [batch], batch: at most the rows of the page table"
+_RAGGED = "cu: int32 [batch + 1], kv_len: int32 [batch], both contiguous, batch: at most the rows of the page table"
 
 
 def make_route_scores_config(T, n_experts, top_k, n_groups=1, top_groups=1, group_rank=1, score=MOE_SCORE_SOFTMAX,
@@ -319,9 +319,10 @@ def moe_route_scores(cfg, logits, bias, topk_ids, topk_w, stream=None):
     T, E = cfg.T, cfg.n_experts
     if not (topk_ids.dtype is _I32 and topk_w.dtype is _F32 and topk_ids.numel() >= T * cfg.top_k <= topk_w.numel()
             and logits.dtype is (_BF16 if cfg.logit_dtype == MOE_BF16 else _F32)
-            and (bias is None or bias.dtype is _F32 and bias.numel() >= E)):
+            and topk_ids.is_contiguous() and topk_w.is_contiguous()
+            and (bias is None or bias.dtype is _F32 and bias.numel() >= E and bias.is_contiguous())):
         raise ValueError("logits: of the configuration's type, bias: float32 [E], topk_ids: int32 [T, k], topk_w: "
-                         "float32 [T, k]")
+                         "float32 [T, k], these three contiguous")
     if logits.numel() < (T - 1) * cfg.logit_stride + E:   # a view, or too short
         _need(T < 1 or (logits.dim() == 2 and logits.shape[0] >= T and logits.shape[1] >= E
                         and logits.stride(0) == cfg.logit_stride),
@@ -397,7 +398,8 @@ def _appending(where: str, doc: str):
                 and (cache.device is None or cache.device == dev)):
             raise ValueError(_ELSEWHERE)
         B = cfg.batch
-        if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
+        if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch
+                and cu.is_contiguous() and kv_len.is_contiguous()):
             raise ValueError(_RAGGED)
         T = cfg.T
         if not (k.dtype is v.dtype is _BF16 and (q is None or q.dtype is q_out.dtype is _BF16)
@@ -406,11 +408,13 @@ def _appending(where: str, doc: str):
                      and (q is None or q.is_contiguous() and q_out.is_contiguous() and q.numel() >= T * cfg.q_row <= q_out.numel())
                      or _append_rows(cfg, T, q, k, v, q_out))):
             raise ValueError("q, k, v and q_out: bf16 rows of the configuration's shape and distance and the cache's heads")
-        if not ((gamma_k is None or gamma_k.dtype is _F32 and gamma_k.numel() >= cache.head_dim)
-                and (gamma_q is None or gamma_q.dtype is _F32 and gamma_q.numel() >= cache.head_dim)
-                and (cos_sin is None or cos_sin.dtype is _F32 and cos_sin.numel() >= cfg.n_pos * cfg.rot_dim)
-                and (positions is None or positions.dtype is _I32 and positions.numel() >= T)):
-            raise ValueError("gamma_q, gamma_k: float32 [D], cos_sin: float32 [n_pos, rot_dim / 2, 2], positions: int32 [T]")
+        if not ((gamma_k is None or gamma_k.dtype is _F32 and gamma_k.numel() >= cache.head_dim and gamma_k.is_contiguous())
+                and (gamma_q is None or gamma_q.dtype is _F32 and gamma_q.numel() >= cache.head_dim and gamma_q.is_contiguous())
+                and (cos_sin is None or cos_sin.dtype is _F32 and cos_sin.numel() >= cfg.n_pos * cfg.rot_dim
+                     and cos_sin.is_contiguous())
+                and (positions is None or positions.dtype is _I32 and positions.numel() >= T and positions.is_contiguous())):
+            raise ValueError("gamma_q, gamma_k: float32 [D], cos_sin: float32 [n_pos, rot_dim / 2, 2], positions: int32 [T], "
+                             "all contiguous")
         code = getattr(load(), where)(
             cfg, cache, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
             None if gamma_q is None else gamma_q.data_ptr(), None if gamma_k is None else gamma_k.data_ptr(),
@@ -458,15 +462,17 @@ def _attending(where: str, doc: str):
                 and (cache.device is None or cache.device == dev)):
             raise ValueError(_ELSEWHERE)
         B = cfg.batch
-        if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
+        if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch
+                and cu.is_contiguous() and kv_len.is_contiguous()):
             raise ValueError(_RAGGED)
         T = cfg.T
         if not (q.dtype is out.dtype is _BF16 and (cfg.head_dim is None or cfg.head_dim == cache.head_dim)
                 and (cfg.dense and q.is_contiguous() and out.is_contiguous() and q.numel() >= T * cfg.q_row <= out.numel()
                      or _attention_rows(cfg, T, q, out))
-                and (lse is None or lse.dtype is _F32 and lse.numel() >= T * cfg.n_q_heads)):
+                and (lse is None or lse.dtype is _F32 and lse.numel() >= T * cfg.n_q_heads and lse.is_contiguous())
+                and (ws is None or ws.is_contiguous())):
             raise ValueError("q and out: bf16 rows of the configuration's shape and distance and the cache's head size, lse: "
-                             "float32 [T, n_q_heads]")
+                             "contiguous float32 [T, n_q_heads], ws: contiguous")
         code = getattr(load(), where)(
             cfg, cache, q.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
@@ -546,7 +552,8 @@ def moe_blockkv_read(cfg, cache, cu, kv_len, k_out, v_out, stream=None):
             and (v_out is None or v_out.get_device() == dev) and (cache.device is None or cache.device == dev)):
         raise ValueError(_ELSEWHERE)
     B = cfg.batch
-    if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch):
+    if not (cu.dtype is kv_len.dtype is _I32 and cu.numel() > B <= kv_len.numel() and B <= cache.batch
+            and cu.is_contiguous() and kv_len.is_contiguous()):
         raise ValueError(_RAGGED)
     T, dtype = cfg.T, cfg.dtype
     if not ((cfg.heads == cache.heads or cfg.heads is None or cache.heads is None)
