@@ -81,14 +81,16 @@ class moe_kv_append_config_t(ctypes.Structure):
     _fields_ += [("eps", ctypes.c_float)]
     _fields_ += [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")]
     # of make_kv_append_config's tensors: elements of a row of q and of k, (n_kv_heads, head_dim), whether rows follow each other
-    q_row, k_row, heads, dense = 0, 0, None, False
+    # the layouts that they have, their rows
+    q_row, k_row, heads, dense, like, rows = 0, 0, None, False, None, 0
 
 
 class moe_paged_attention_config_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "batch", "n_q_heads", "max_q_len", "window", "n_sink")]
     _fields_ += [("sm_scale", ctypes.c_float), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
     # of make_paged_attention_config's tensors: elements of a row of q, head_dim, whether rows follow each other
-    q_row, head_dim, dense = 0, None, False
+    # and the layouts that they have
+    q_row, head_dim, dense, like = 0, None, False, None
 
 
 class moe_blockkv_cache_t(ctypes.Structure):
@@ -377,7 +379,14 @@ def make_kv_append_config(q, k, v, q_out, batch, rot_dim=0, n_pos=0, rope_layout
     c.heads = heads, D = tuple(k.shape[1:])
     c.q_row, c.k_row = c.n_q_heads * D, heads * D
     c.dense = c.k_stride == c.v_stride == c.k_row and c.q_stride == c.q_out_stride == c.q_row
+    c.like, c.rows = _append_layouts(q, k, v, q_out), k.shape[0]
     return c
+
+
+def _append_layouts(q, k, v, q_out):
+    if q is None:
+        return k.shape, k.stride(), v.shape, v.stride()
+    return k.shape, k.stride(), v.shape, v.stride(), q.shape, q.stride(), q_out.shape, q_out.stride()
 
 
 def _append_rows(cfg, T: int, q, k, v, q_out) -> bool:
@@ -406,10 +415,11 @@ def _appending(where: str, doc: str):
                 and (cfg.heads == cache.heads or cfg.heads is None or cache.heads is None)
                 and (cfg.dense and k.is_contiguous() and v.is_contiguous() and k.numel() >= T * cfg.k_row <= v.numel()
                      and (q is None or q.is_contiguous() and q_out.is_contiguous() and q.numel() >= T * cfg.q_row <= q_out.numel())
-                     or _append_rows(cfg, T, q, k, v, q_out))):
+                     or _append_layouts(q, k, v, q_out) == cfg.like and T <= cfg.rows or _append_rows(cfg, T, q, k, v, q_out))):
             raise ValueError("q, k, v and q_out: bf16 rows of the configuration's shape and distance and the cache's heads")
-        if not ((gamma_k is None or gamma_k.dtype is _F32 and gamma_k.numel() >= cache.head_dim and gamma_k.is_contiguous())
-                and (gamma_q is None or gamma_q.dtype is _F32 and gamma_q.numel() >= cache.head_dim and gamma_q.is_contiguous())
+        D = cache.head_dim
+        if not ((gamma_k is None or gamma_k.dtype is _F32 and gamma_k.numel() >= D and gamma_k.is_contiguous())
+                and (gamma_q is None or gamma_q.dtype is _F32 and gamma_q.numel() >= D and gamma_q.is_contiguous())
                 and (cos_sin is None or cos_sin.dtype is _F32 and cos_sin.numel() >= cfg.n_pos * cfg.rot_dim
                      and cos_sin.is_contiguous())
                 and (positions is None or positions.dtype is _I32 and positions.numel() >= T and positions.is_contiguous())):
@@ -441,11 +451,14 @@ def make_paged_attention_config(q, out, batch, max_q_len=0, window=0, n_sink=0,
                                      q.shape[2] ** -0.5 if sm_scale is None else sm_scale, _row_stride(q), _row_stride(out))
     c.q_row, c.head_dim = q.shape[1] * q.shape[2], q.shape[2]
     c.dense = c.q_stride == c.out_stride == c.q_row
+    c.like = q.shape, q.stride(), out.shape, out.stride()
     return c
 
 
 def _attention_rows(cfg, T: int, q, out) -> bool:
     """An attention's rows, where they are not simply dense."""
+    if (q.shape, q.stride(), out.shape, out.stride()) == cfg.like and T <= q.shape[0]:
+        return True
     return cfg.q_row == 0 or (_rows_at(q, T, cfg.q_row, cfg.q_stride) and _rows_at(out, T, cfg.q_row, cfg.out_stride))
 
 
