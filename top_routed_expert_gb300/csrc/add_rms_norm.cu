@@ -272,7 +272,11 @@ extern "C" moe_status_t moe_add_rms_norm(const moe_add_norm_config_t* cfg, const
   const int pieces = cfg->d / 8, res = !residual ? 0 : cfg->res_dtype == MOE_F32 ? 2 : 1;
   cudaError_t err;
   // a pass where that gives a block 512 threads or fewer (8192 x 4096: 512 threads 52 us,
-  // 256 with two passes 58, 128 with four 59; 65536 x 512: 64 threads 48, 128 65)
+  // 256 with two passes 58, 128 with four 59; 65536 x 512: 64 threads 48, 128 65).  More
+  // passes cost spills of gamma and the next row: bytes stored with x / residual bf16 / bf16,
+  // f32 / bf16, bf16 / f32, f32 / f32 and f32 / none 16, 48, 48, 72, 16 with two passes, 0, 32, 32,
+  // 80, 0 with four.  The rate falls little: as many bytes at d = 4096, 8192, 16384 (bf16, bf16,
+  // groups of 128) 48.5, 49.5, 52.2 us.
   if (pieces <= 32) err = launch<32, 1>(a, res, sms, s);
   else if (pieces <= 64) err = launch<64, 1>(a, res, sms, s);
   else if (pieces <= 128) err = launch<128, 1>(a, res, sms, s);

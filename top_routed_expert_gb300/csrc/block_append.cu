@@ -15,13 +15,14 @@
 // than its neighbours' do; the sizes of all fours of a row go through shared
 // memory then.  Query blocks are those of kv_rows.cuh.
 //
-// Measured: 32 x 256 tokens of 32 + 4 heads of 128, norm and rotation, 156 MB in 31.9 us
-// = 4.9 TB/s, bound by memory behind look-ups (the queries are 134 MB of that); ragged
-// prompts up to 1999 tokens of 16 + 16 heads of 64, 214 MB in 47 us = 4.5 TB/s, bound by
-// the issue of instructions (67 % of the slots; with IEEE divisions and eight elements
-// a thread 72 us); 64 single tokens 3.7 us in a graph.  The interleaved layout spills 116
-// bytes of 72 registers with four heads a thread; with two heads it spills none and
-// takes 51 us, with 80 registers and six blocks on an SM 51 as well.
+// Measured: 32 x 256 tokens of 32 + 4 heads of 128, norm and rotation, 156 MB in 32.0 us
+// = 4.9 TB/s (the queries are 134 MB of that; 72 % of the issue slots, the first stall
+// that a warp is not selected, and look-ups before the rows); ragged prompts up to 1999
+// tokens of 16 + 16 heads of 64, 214 MB in 48.5 us = 4.4 TB/s, bound by the issue of
+// instructions (67 % of the slots; with IEEE divisions and eight elements a thread
+// 72 us); 64 single tokens 3.7 us in a graph.  The interleaved layout spills 144 to 152
+// bytes of 72 registers with four heads a thread; with two heads it spills 16 and
+// takes 4 us longer, with 80 registers and six blocks on an SM as well.
 #include "block_kv.cuh"
 #include "kv_rows.cuh"
 
@@ -30,8 +31,13 @@ namespace {
 
 constexpr int kThreads = kQueryThreads;
 
-// Two heads a thread for few tokens (64 single ones: 3.7 us, one head 4.0, four 4.5), else
-// four (32 x 256: 32 us, two 34).
+// Two heads a thread for few tokens (64 single ones: 3.7 us, one head 4.0, four 4.7), else
+// four (32 x 256: 32 us, two 34).  Measured in a graph (us, two / four; *: the rule takes
+// the slower), 32 + 4 heads of 128: 128 single tokens 4.7 / 5.2, 192 6.0 / 5.9*, 256 7.2 / 6.5*,
+// 384 9.7 / 8.7, 1024 23.1 / 17.7; a prompt of 512 3.9 / 5.0*, two of 1000 8.6 / 8.2; 16 + 16 of
+// 64, interleaved, 128 5.9 / 6.0, 256 8.7 / 7.9*, 1024 27 / 21; a prompt of 512 4.0 / 5.4*, two of
+// 1000 6.8 / 8.7*; 8 + 8 of 128, 64 5.1 / 4.9*, 256 11.7 / 8.9*, 384 16.2 / 11.9; 16 + 2 of 256 (two key
+// heads, so that four have nothing to do) 256 7.3 / 8.5, 4096 100 / 113*.
 constexpr int kFewTokens = 256;
 
 struct BaArgs : RowArgs {

@@ -5,12 +5,14 @@
 //
 // The rows of one (request, key head) are its new tokens times the query
 // heads of the group, row r = token r / group, head r % group; 8 or 16 rows make
-// a row tile.  The work of a row tile is cut into units of 64 cached tokens.
-// All units of the call stand in one line (request, key head, row tile,
-// token), and the persistent CTAs take equal pieces of that line, so a batch
-// of mixed lengths keeps every SM busy to the end.  A piece may end inside a
-// row tile; then all its CTAs leave partial sums and paged_attn_join adds them
-// in order (a fixed order: the same bits every time).
+// a row tile.  The work of a row tile is cut into units of cached tokens, 64 over the
+// 8-bit cache and 128 over the other.  All units of the call stand in one line
+// (request, key head, row tile, token), and the persistent CTAs take equal pieces of
+// that line, so a batch of mixed lengths keeps every SM busy to the end.  A piece
+// may end inside a row tile; then all its CTAs leave partial sums, which
+// paged_attn_join or block_attn_join adds in order (a fixed order: the same bits
+// every time).  Over the 4-bit cache row tiles of short contexts are not cut
+// (kWholeTokens): a CTA has those that begin in its piece, and nothing is joined.
 #pragma once
 
 #include <climits>
@@ -37,7 +39,7 @@ template <int D, int NB, bool BLOCKS> struct Shape {
   static constexpr int kUnit = BLOCKS ? 128 : 64;         // tokens of a unit, in equal parts for the four warps
   // What a row tile costs beside its units (finding it, q, the join of the
   // warps), in units.
-  static constexpr int kTileCost = BLOCKS ? 4 : 4;
+  static constexpr int kTileCost = 4;
   static constexpr int kTile = BLOCKS ? 8 * D : 16 * D;   // bytes of 16 tokens' keys (or values)
   static constexpr int kStage = BLOCKS ? 4 * kTile + 4 * D : 2 * kTile;
   // CTAs on an SM, by registers (O takes D NB / 4 of a thread's, q D NB / 8),
@@ -269,8 +271,10 @@ cudaError_t launch(const Args& a, int num_sms, cudaStream_t s) {
 // convert the codes half as often (64 requests of 32 rows at 3584 117 / 92 us).
 template <int D, class Kernels, class Args>
 cudaError_t launch(const Args& a, int64_t most_rows, int num_sms, cudaStream_t s) {
-  if (D == 256 || most_rows <= 8) return launch<D, 1, Kernels>(a, num_sms, s);
-  return launch<D == 256 ? 128 : D, 2, Kernels>(a, num_sms, s);
+  if constexpr (D < 256) {
+    if (most_rows > 8) return launch<D, 2, Kernels>(a, num_sms, s);
+  }
+  return launch<D, 1, Kernels>(a, num_sms, s);
 }
 
 template <int D, int NB, bool BLOCKS> size_t part_bytes() {
@@ -287,7 +291,7 @@ template <bool BLOCKS> size_t part_bytes_of(int D) {
 
 // Which kernels a call takes, from what the host knows.
 struct Path {
-  bool tc;      // the tcgen05 kernel, for requests with more than TcRule::kRows rows
+  bool tc;      // the tcgen05 kernel, for requests with more than kTcRows rows
   bool alone;   // ... and it alone
   bool split;   // ... which may cut row blocks along the cached tokens
 };
@@ -335,10 +339,8 @@ struct Path {
 // requests of 64 rows each at 3584 151 / 159, at 1024 66 / 61; 256 of 64 rows at 40 108 /
 // 62, at 300 146 / 103; 8 x 1 x 128: 256 of 40 rows at 60 127 / 134, 64 of 20 at 1000 60 / 110.
 constexpr int kTileTokens = 256;
-template <bool BLOCKS> struct TcRule {
-  static constexpr int kRows = 48;                                                 // of a request and key head
-  static constexpr int64_t kWork = BLOCKS ? int64_t(9) << 20 : int64_t(6) << 20;   // pairs
-};
+constexpr int kTcRows = 48;   // of a request and key head
+template <bool BLOCKS> constexpr int64_t kTcWork = BLOCKS ? int64_t(9) << 20 : int64_t(6) << 20;   // pairs
 constexpr int kTcTokens = 16384;
 
 // Over the cache in 4 bits the few-row kernel cuts no row tiles where its rows see
@@ -348,6 +350,16 @@ constexpr int kTcTokens = 16384;
 // 100 at 64 to 128 9.8 / 8.6, at 256 13.7 / 9.9, at 512 16.0 / 12.5, at 1024 20.3 / 20.8, at
 // 2048 28.4 / 31.6; 128 (512 row tiles for 456 CTAs) 12.8 / 12.2, 16.3 / 14.4, 19.1 / 18.3, 23.7 /
 // 25.0, 34.1 / 41.1.
+// The better side depends on the number of row tiles too, which the rule does not
+// look at: with few, or a little over what the CTAs take at once, cutting gains from
+// 256 tokens on.  Measured in a window (us, cut / whole, in a graph; *: the rule takes
+// the slower): one new token, 8 x 4 x 64, 32 tiles in 128 tokens 8.3 / 8.0, 256 8.2 / 8.7*,
+// 512 8.8 / 9.8*, 1024 9.3 / 12.9; 384 tiles 12.5 / 10.2, 13.5 / 11.3, 15.3 / 13.4, 18.5 / 18.2*;
+// 768 tiles 17.1 / 15.9, 18.8 / 17.9, 21.8 / 22.1*, 27.5 / 30.5; four (16 rows), 384 tiles
+// 15.3 / 11.7, 17.0 / 12.7, 19.1 / 15.0, 22.9 / 19.5*; one, 4 x 8 x 128, 16 tiles 8.6 / 8.7*,
+// 8.4 / 9.4*, 8.9 / 11.1*, 9.3 / 14.3; 192 tiles 12.9 / 10.7, 14.1 / 12.0, 15.3 / 14.6, 17.4 /
+// 20.2; 2 x 8 x 256, 8 tiles 9.6 / 10.3*, 9.4 / 11.6*, 9.8 / 13.9*, 10.7 / 18.5; 192 tiles
+// 15.3 / 12.6, 16.8 / 14.3, 19.9 / 17.6, 24.3 / 24.4.
 constexpr int kWholeTokens = 512;
 
 // Cached tokens that a request's rows can see, as far as the host knows.
@@ -363,7 +375,7 @@ Path path_of(const PaArgs& a, int max_q_len) {
   Path p;
   const int64_t rows = static_cast<int64_t>(a.T) * a.group * a.c.n_kv_heads;
   const int64_t tokens = std::min<int64_t>(static_cast<int64_t>(a.c.max_pages) * a.c.page_size, kTcTokens);
-  p.tc = most > TcRule<BLOCKS>::kRows && rows * (tokens + kTileTokens) >= TcRule<BLOCKS>::kWork && paged_attn_tc_supported(a.c.head_dim);
+  p.tc = most > kTcRows && rows * (tokens + kTileTokens) >= kTcWork<BLOCKS> && paged_attn_tc_supported(a.c.head_dim);
   // As many rows as if every request had max_q_len of them: they all do (or the
   // hint is wrong, and the tcgen05 kernel takes small ones too).
   p.alone = p.tc && static_cast<int64_t>(max_q_len) * a.B == a.T;
@@ -394,7 +406,7 @@ cudaError_t launch_requests(const Args& a, const Path& path, int max_q_len, int 
 template <class Kernels, class Args>
 cudaError_t launch_paged_attn(Args a, int max_q_len, int num_sms, cudaStream_t s) {
   const Path path = path_of<Args::kBlocks>(a, max_q_len);
-  a.tc_rows = path.alone ? 0 : path.tc ? TcRule<Args::kBlocks>::kRows : INT_MAX;
+  a.tc_rows = path.alone ? 0 : path.tc ? kTcRows : INT_MAX;
   a.tc_ctas = std::min(num_sms, kMaxSms);
   a.tc_split = path.split;
   if constexpr (Args::kBlocks) a.whole_tiles = most_tokens(a, max_q_len) <= kWholeTokens;
