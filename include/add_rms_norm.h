@@ -27,7 +27,7 @@ extern "C" {
 #endif
 
 typedef struct {
-  int32_t T;            /* rows, >= 0 (0 is a no-op)                                 */
+  int32_t T;            /* rows, 0..2^28 (0 is a no-op)                              */
   int32_t d;            /* elements of a row: a multiple of 8, 8..16384              */
   int32_t x_dtype;      /* MOE_BF16 or MOE_F32, each                                 */
   int32_t res_dtype;    /*   of residual and sum (ignored when residual is NULL)     */

@@ -92,20 +92,20 @@ size_t moe_blockkv_attention_ws_bytes(const moe_paged_attention_config_t* cfg, c
  * A key or value becomes e2m1(code) * e4m3(scale) exactly in f16 and q is
  * scaled by a power of two per head to f16 (exact but for elements 2^-28 below
  * the head's largest), so the products' operands are exact; scores, maxima,
- * sums and outputs are accumulated in fp32; the softmax weights w_j are rounded
- * to f16 for the product with V, to 11 bits down to 2^-22 of the row's largest,
- * smaller ones by up to 2^-33 of it.  g enters the scores' and the outputs'
- * factor.  Results do not depend on scheduling.  A NaN scale in a position
- * that a request's new tokens can see makes NaN of the rows that see it and
- * may make NaN of other rows of the same request and key head; what none of
- * them sees may hold anything.
+ * sums and outputs are accumulated in fp32, parts of a row joined by factors
+ * good to 2^-22; the softmax weights w_j are rounded to f16 for the product with
+ * V, to 11 bits down to 2^-22 of the row's largest, smaller ones by up to 2^-33
+ * of it.  g enters the scores' and the outputs' factor.  Results do not depend
+ * on scheduling.  A NaN scale in a position that a request's new tokens can see
+ * makes NaN of the rows that see it and may make NaN of other rows of the same
+ * request and key head; what none of them sees may hold anything.
  */
 moe_status_t moe_blockkv_attention(const moe_paged_attention_config_t* cfg, const moe_blockkv_cache_t* cache,
                                    const void* q, const int32_t* cu, const int32_t* kv_len, void* out, float* lse,
                                    void* ws, size_t ws_bytes, moe_stream_t stream);
 
 typedef struct {
-  int32_t T;            /* rows of k_out and v_out, >= 0 (0 is a no-op)              */
+  int32_t T;            /* rows of k_out and v_out, 0..2^28 (0 is a no-op)           */
   int32_t batch;        /* requests, 1..2^20                                        */
   int32_t out_dtype;    /* MOE_BF16 or MOE_F32                                      */
   int64_t k_stride;     /* elements between rows of k_out and of v_out (multiples of */

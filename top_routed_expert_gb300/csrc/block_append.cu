@@ -16,13 +16,13 @@
 // memory then.  Query blocks are those of kv_rows.cuh.
 //
 // Measured: 32 x 256 tokens of 32 + 4 heads of 128, norm and rotation, 156 MB in 32.0 us
-// = 4.9 TB/s (the queries are 134 MB of that; 72 % of the issue slots, the first stall
+// = 4.9 TB/s (the queries are 134 MB of that; 71 % of the issue slots, the first stall
 // that a warp is not selected, and look-ups before the rows); ragged prompts up to 1999
-// tokens of 16 + 16 heads of 64, 214 MB in 48.5 us = 4.4 TB/s, bound by the issue of
-// instructions (67 % of the slots; with IEEE divisions and eight elements a thread
-// 72 us); 64 single tokens 3.7 us in a graph.  The interleaved layout spills 144 to 152
-// bytes of 72 registers with four heads a thread; with two heads it spills 16 and
-// takes 4 us longer, with 80 registers and six blocks on an SM as well.
+// tokens of 16 + 16 heads of 64, 214 MB in 48.5 us = 4.4 TB/s, at 64 % of the issue slots
+// and with waits for loads (with IEEE divisions and eight elements a thread 72 us); 64
+// single tokens 3.7 us in a graph.  The interleaved layout spills 144 to 152 bytes of 72
+// registers with four heads a thread; with two heads it spills 16 and takes 51.8 us,
+// with 80 registers and six blocks on an SM 4 us more as well.
 #include "block_kv.cuh"
 #include "kv_rows.cuh"
 
